@@ -32,7 +32,8 @@ EP_DEVERR_BAD_INDEX = 0x1
 EP_DEVERR_CAPACITY = 0x2
 EP_DEVERR_TIMEOUT = 0x4
 EP_DEVERR_COMBINE_MISMATCH = 0x8
-EP_DT_BF16, EP_DT_FP8_E4M3, EP_DT_FP32 = 0, 1, 2
+EP_DT_BF16, EP_DT_FP8_E4M3, EP_DT_FP32, EP_DT_FP16 = 0, 1, 2, 3
+EP_MAX_WORLD, EP_MAX_TOPK, EP_MAX_ROUTE_EXPERTS = 32, 32, 1024
 
 
 class EpConfigC(ctypes.Structure):
@@ -90,6 +91,48 @@ class EpDispatchOutC(ctypes.Structure):
     ]
 
 
+class EpRouteDescC(ctypes.Structure):
+    _fields_ = [
+        ("world_size", ctypes.c_int32),
+        ("tokens", ctypes.c_int32),
+        ("num_experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("balance_coef", ctypes.c_float),
+        ("z_coef", ctypes.c_float),
+        ("row_stride", ctypes.c_int64),
+        ("rank_stride", ctypes.c_int64),
+    ]
+
+
+class EpRowsC(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("rank_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
+class EpProductDescC(ctypes.Structure):
+    _fields_ = [
+        ("ranks", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("d_count", ctypes.c_void_p),
+        ("d_offset", ctypes.c_void_p),
+        ("weight", EpRowsC),
+        ("x", EpRowsC),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -118,6 +161,13 @@ SIGNATURES = {
     "ep_moe_outputs": (_S, [_P, ctypes.POINTER(EpMoeOutC)]),
     "ep_moe_ungroup": (_S, [_P, _P, _I64, _P]),
     "ep_test_fp8_quotient_check": (_S, [_P, _P]),
+    "ep_route": (_S, [_P, _P, _P, _P, _P, _P, _P]),
+    "ep_route_backward": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "ep_balance_loss_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "ep_balance_loss": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "ep_expert_product": (_S, [_P, _P, _P, _P, _P, _P, _P]),
+    "ep_expert_product_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "ep_expert_product_backward": (_S, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "ep_layout_noalloc": (_S, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P]),
 }
 

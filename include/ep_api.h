@@ -96,7 +96,8 @@ typedef enum {
 typedef enum {
     EP_DT_BF16 = 0,
     EP_DT_FP8_E4M3 = 1,       /* OCP E4M3 ("fn"), max 448 */
-    EP_DT_FP32 = 2
+    EP_DT_FP32 = 2,
+    EP_DT_FP16 = 3            /* routing and expert products only */
 } ep_dtype_t;
 
 #define EP_MAX_WORLD 32
@@ -398,6 +399,150 @@ ep_status_t ep_layout_noalloc(int32_t world_size, int32_t num_experts,
                               int32_t *d_pos, int32_t *d_send_counts,
                               int32_t *d_recv_count, uint32_t *d_error,
                               void *stream);
+
+/* ---------------------------------------------------------------------
+ * Routing, balance loss and expert products: what stands before and between
+ * dispatch and combine in a MoE layer.  These calls need no handle; sizes
+ * and options come in a descriptor, scratch (where a call needs any) from
+ * the caller, and everything is asynchronous on `stream`.  d_error: NULL, or
+ * a device u32 (zeroed once by the caller) that gets EP_DEVERR_* bits OR-ed
+ * in.  Call them with the tensors' device current. */
+
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
+
+#define EP_MAX_ROUTE_EXPERTS 1024
+
+/* Router logits [W][T][E]: element (s,t,e) at d_logits[s * rank_stride +
+ * t * row_stride + e].  x below is the logit in fp32 with NaN read as -inf
+ * and +inf as the largest finite number; an expert with x = -inf is closed:
+ * it has probability and weight 0 and is chosen only where fewer than k
+ * experts are open.  Token t of rank s is present when t < h_num_tokens[s]. */
+typedef struct {
+    int32_t world_size;   /* W, 1..32 */
+    int32_t tokens;       /* T >= 1, W * T <= 2^30 */
+    int32_t num_experts;  /* E, 1..EP_MAX_ROUTE_EXPERTS */
+    int32_t topk;         /* k, 1..min(E, 32) */
+    int32_t dtype;        /* EP_DT_BF16, EP_DT_FP16 or EP_DT_FP32 logits */
+    int32_t score;        /* ep_score_t */
+    int32_t renormalize;  /* 1: the k weights are divided by their sum (softmax:
+                             the softmax is taken over the chosen experts) */
+    float   scale;        /* factor on the weights */
+    float   balance_coef; /* of the balance loss (loss calls only) */
+    float   z_coef;       /* of the mean squared log-sum-exp (loss calls only) */
+    int64_t row_stride;   /* elements, >= E */
+    int64_t rank_stride;  /* elements; unused when W == 1 */
+} ep_route_desc_t;
+
+/* Top-k routing.  The k experts with the largest x_e + bias_e (an fp32 add;
+ * d_bias NULL: no bias) are chosen, in descending order, ties to the lowest
+ * expert id.  The bias takes no part in the weights:
+ *   softmax:  w_j = scale * exp(x_j) / sum exp(x), the sum over the chosen
+ *             experts (renormalize) or over all
+ *   sigmoid:  w_j = scale * v_j, v_j = 1 / (1 + exp(-x_j)), divided by the sum
+ *             of the chosen v (renormalize)
+ * d_w [W][T][k] fp32 and d_idx [W][T][k] int32, dense, are dispatch's weights
+ * and indices.  Tokens that are not present get ids -1 and weights 0. */
+ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits,
+                     const float *d_bias, const int32_t *h_num_tokens,
+                     float *d_w, int32_t *d_idx, void *stream);
+
+/* The balance and z losses of a routing, with n = number of tokens present:
+ *   counts_e = choices of e among present tokens (ids outside [0, E) are
+ *              skipped and set BAD_INDEX)
+ *   probs_e  = (1/n) sum over present tokens of softmax(x)_e
+ *   d_loss[1] = sum_e (counts_e * E / (k n)) * probs_e
+ *   d_loss[2] = (1/n) sum of (log sum exp x)^2   (0 for a token that sees no
+ *               open expert)
+ *   d_loss[0] = balance_coef * d_loss[1] + z_coef * d_loss[2]
+ * All 0 when n = 0.  Sums are fp32, in an order that the sizes alone fix.
+ * d_idx [W][T][k]; d_loss [3], d_counts [E] int32, d_probs [E] fp32.
+ * d_workspace: ep_balance_loss_workspace bytes, 16-byte aligned, any
+ * contents. */
+ep_status_t ep_balance_loss_workspace(const ep_route_desc_t *d, size_t *bytes);
+ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits,
+                            const int32_t *d_idx, const int32_t *h_num_tokens,
+                            float *d_loss, int32_t *d_counts, float *d_probs,
+                            void *d_workspace, size_t workspace_bytes,
+                            uint32_t *d_error, void *stream);
+
+/* Gradient by the logits, in their type, dense [W][T][E]; 0 for tokens that
+ * are not present.  The sum of two parts, either of which may be left out:
+ *  - of the weights (d_grad_w [W][T][k] fp32 with the forward's d_idx; both
+ *    NULL: left out);
+ *  - of d_loss[0] (d_grad_loss, one fp32, with the forward's d_counts; both
+ *    NULL: left out).  counts are constants of the gradient.
+ * Ids outside [0, E) are skipped and set BAD_INDEX. */
+ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
+                              const float *d_grad_w, const int32_t *d_idx,
+                              const float *d_grad_loss, const int32_t *d_counts,
+                              const int32_t *h_num_tokens, void *d_grad_logits,
+                              uint32_t *d_error, void *stream);
+
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,
+    EP_ACT_GELU = 2,      /* v * Phi(v), the error-function form */
+    EP_ACT_SILU = 3,
+    EP_ACT_SWIGLU = 4     /* silu(first N features) * (last N of 2N features) */
+} ep_activation_t;
+
+/* Rows grouped by expert, as ep_moe_group leaves them: R segments ("ranks")
+ * of `rows` rows, and in each segment `groups` groups; group e of segment r
+ * is rows offset[r][e] .. offset[r][e] + count[r][e] - 1 (device int32 [R][groups]).
+ * Rows of a group past the segment's end are left out; d_count == NULL means one
+ * group per segment that holds all its rows.  Groups of a segment must not
+ * overlap.  Strides are in elements; every row is contiguous, every pointer is
+ * 16-byte aligned and every stride is a multiple of 8 elements. */
+typedef struct {
+    void   *ptr;
+    int64_t rank_stride;  /* unused when R == 1 */
+    int64_t row_stride;
+} ep_rows_t;
+
+typedef struct {
+    int32_t ranks;        /* R >= 1 */
+    int32_t groups;       /* groups per segment >= 1; R * groups <= 65535 */
+    int32_t rows;         /* rows per segment, 0..2^30 */
+    int32_t in_features;  /* K, multiple of 8 */
+    int32_t out_features; /* N, multiple of 8 */
+    int32_t dtype;        /* EP_DT_BF16 or EP_DT_FP16, of every tensor */
+    int32_t activation;   /* ep_activation_t */
+    int32_t reserved;     /* 0 */
+    const int32_t *d_count, *d_offset;  /* both NULL, or both [R][groups] */
+    /* weight[g][f][c], g = r * groups + e, f < wide = N (2N for SWIGLU), c < K:
+     * at weight.ptr + g * rank_stride + f * row_stride + c */
+    ep_rows_t weight;
+    ep_rows_t x;          /* [R][rows][K] */
+} ep_product_desc_t;
+
+/* For every row i of group g:
+ *   pre = x_i W_g^T + bias_g,   y_i = act(pre) + residual_i
+ * with fp32 products' sums and epilogue, one rounding per output.  d_bias:
+ * [R*groups][wide] dense or NULL; residual, pre: ptr NULL to leave out;
+ * pre gets the wide pre-activations (what the gradient needs).  Rows outside
+ * every group are not written. */
+ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
+                              const ep_rows_t *residual, const ep_rows_t *y,
+                              const ep_rows_t *pre, uint32_t *d_error,
+                              void *stream);
+
+/* The gradient, from grad = dL/dy [R][rows][N] and the forward's pre
+ * (EP_ACT_NONE: not read):
+ *   d = grad * act'(pre), rounded once to the tensors' type for the products
+ *   grad_x_i = d_i W_g;  grad_w_g = sum over g's rows of d_i^T x_i
+ *   grad_bias_g = sum over g's rows of d_i (of d before that rounding)
+ * grad_x: like x (rows outside every group are not written); d_grad_w: dense
+ * [R*groups][wide][K]; d_grad_bias: dense [R*groups][wide] or NULL.  A group
+ * without rows gets zeros.  grad_x->ptr or d_grad_w may be NULL to leave that
+ * part out.  The gradient of the residual is grad itself.  d_workspace:
+ * ep_expert_product_workspace bytes, 256-byte aligned, any contents. */
+ep_status_t ep_expert_product_workspace(const ep_product_desc_t *d, size_t *bytes);
+ep_status_t ep_expert_product_backward(const ep_product_desc_t *d,
+                                       const ep_rows_t *grad, const ep_rows_t *pre,
+                                       const ep_rows_t *grad_x, void *d_grad_w,
+                                       void *d_grad_bias, void *d_workspace,
+                                       size_t workspace_bytes, uint32_t *d_error,
+                                       void *stream);
 
 #ifdef __cplusplus
 }
