@@ -6,17 +6,34 @@
 //   grad_x    m = input,   n = row,   k = feature  A = weight^T,  B = d
 //   grad_w    m = input,   n = feature, k = row    A = x^T,       B = d^T
 // The output's contiguous dimension is always m.
+//
+// One CTA per SM walks the tiles of all groups (their row counts are on the
+// device): 128 m by up to 256 n, accumulated in tensor memory.  Weights or
+// inputs are the 128-wide operand and rows (or features) the other, so that a
+// group with few rows costs a narrow instruction (n in steps of 16) and not a
+// padded tile of 128 rows.  Warp 0 loads 64-deep slices by TMA into a ring in
+// shared memory, warp 1 issues the matrix instructions, warps 2..5 turn a
+// finished accumulator into outputs while the next one fills: two
+// accumulators of 256 columns take all of the SM's tensor memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 
-#include "ep_device.cuh"
+#include "ep_tensor.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kTile = 64, kTileK = 16;
+constexpr int kTileM = 128, kTileN = 256, kSliceK = 64;
+constexpr int kStages = 4;
+constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN * kSliceK * 2;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kChunkBytes = 64 * kSliceK * 2;      // 64 rows (or 64 columns) of one slice
+constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
+constexpr int kThreads = 192;
 
 struct Groups {
     const int32_t *count, *offset;
@@ -36,22 +53,15 @@ __device__ __forceinline__ void group_range(const Groups &gr, int g, int *first,
     *n = none ? 0 : min(c, gr.rows - o);
 }
 
-struct Operand {           // element (i, k) of a group's operand at ptr + base + i * si + k * sk
-    const void *ptr;
-    int64_t group_stride;  // by group (weights) or by segment (rows)
-    int64_t si, sk;
-    bool rows_i, rows_k;   // index i / k counts the group's rows
-};
+enum Mode { kForward, kGated, kGradX, kGradW };
 
 struct ProductParams {
     Groups gr;
-    Operand a, b;
     int M, N, K;           // N or K < 0: the group's number of rows
-    int wide_half;         // SWIGLU: features of one half, else 0
     int act;
-    bool out_by_rows;      // n counts rows (else out is per group)
-    const void *bias;
+    const void *bias;      // [G][M], or [G][2M] (gated)
     ep_rows_t residual, out, pre;
+    uint32_t *error;
 };
 
 template <typename T> __device__ __forceinline__ float f32(T v);
@@ -63,84 +73,330 @@ template <> __device__ __forceinline__ __half rounded(float v) { return __float2
 
 __device__ __forceinline__ float sigmoidf(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-__device__ __forceinline__ float activate(int act, float v) {
-    switch (act) {
-    case EP_ACT_RELU: return fmaxf(v, 0.f);
-    case EP_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case EP_ACT_SILU: return v * sigmoidf(v);
-    default: return v;
+template <typename T> struct IsBf16 { static constexpr bool value = false; };
+template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
+
+// Walks the tiles of all groups in order, 32 groups at a time: a lane holds
+// one group's range and the running number of tiles.  Every lane of the warp
+// gets the same answer.
+struct Tile {
+    int g, seg, first, rows, m, n;
+};
+struct Walker {
+    int lane, g0;
+    int64_t before, upto;      // tiles before this block of 32 groups; up to this lane's group
+    int first, rows, tiles;    // this lane's group
+
+    __device__ void load(const ProductParams &p, int mt) {
+        const int g = g0 + lane;
+        first = rows = tiles = 0;
+        if (g < p.gr.R * p.gr.per) {
+            group_range(p.gr, g, &first, &rows);
+            tiles = mt * (((p.N < 0 ? rows : p.N) + kTileN - 1) / kTileN);
+        }
+        upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+    }
+    __device__ void start(const ProductParams &p, int mt) {
+        lane = threadIdx.x & 31;
+        g0 = 0;
+        before = 0;
+        load(p, mt);
+    }
+    __device__ bool find(const ProductParams &p, int mt, int64_t index, Tile *t) {
+        for (;;) {
+            const int64_t here = __shfl_sync(0xffffffffu, upto, 31);
+            if (index < before + here) break;
+            before += here;
+            g0 += 32;
+            if (g0 >= p.gr.R * p.gr.per) return false;
+            load(p, mt);
+        }
+        const int64_t rel = index - before;
+        const int l = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;
+        const int in = (int)(rel - __shfl_sync(0xffffffffu, upto - tiles, l));
+        t->g = g0 + l;
+        t->seg = t->g / p.gr.per;
+        t->first = __shfl_sync(0xffffffffu, first, l);
+        t->rows = __shfl_sync(0xffffffffu, rows, l);
+        t->m = in % mt;
+        t->n = in / mt;
+        return true;
+    }
+};
+
+struct __align__(8) Barriers {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    int gave_up;
+};
+
+// The epilogue of 32 columns (rows, or features of grad_w) of one lane's m.
+template <typename T, Mode MODE>
+__device__ __forceinline__ void store_columns(const ProductParams &p, const Tile &t, float *v, int c0,
+                                              int columns, int m, bool live, float b0, float b1) {
+    const int64_t own = MODE == kGradW ? t.g : t.seg;
+    const int64_t row0 = (MODE == kGradW ? 0 : t.first) + t.n * (int64_t)kTileN + c0;
+    T *out = static_cast<T *>(p.out.ptr) + own * p.out.rank_stride + row0 * p.out.row_stride + m;
+    if constexpr (MODE == kGradX || MODE == kGradW) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (live && c < columns) out[c * p.out.row_stride] = rounded<T>(v[c]);
+    } else {
+        const T *res = static_cast<const T *>(p.residual.ptr) + own * p.residual.rank_stride +
+                       row0 * p.residual.row_stride + m;
+        T *pre = static_cast<T *>(p.pre.ptr) + own * p.pre.rank_stride + row0 * p.pre.row_stride + m;
+        if constexpr (MODE == kForward) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] += b0;
+            if (p.pre.ptr) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (live && c < columns) pre[c * p.pre.row_stride] = rounded<T>(v[c]);
+            }
+            switch (p.act) {
+            case EP_ACT_RELU:
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = fmaxf(v[c], 0.f);
+                break;
+            case EP_ACT_GELU:
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = 0.5f * v[c] * (1.0f + erff(v[c] * 0.70710678118654752f));
+                break;
+            case EP_ACT_SILU:
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] *= sigmoidf(v[c]);
+                break;
+            default: break;
+            }
+            if (p.residual.ptr) {
+                float r[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    r[c] = live && c < columns ? f32(res[c * p.residual.row_stride]) : 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] += r[c];
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (live && c < columns) out[c * p.out.row_stride] = rounded<T>(v[c]);
+        } else {
+            // Lanes 0-7 and 16-23 hold the gate of 8 features, lanes 8-15 and
+            // 24-31 their up half.  Of two rows, the gate's lane finishes the
+            // first and the up half's lane the second: one exchange for both.
+            const bool up = (threadIdx.x & 8) != 0;
+            const int64_t half = up ? p.M : 0;
+            const float bias = up ? b1 : b0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] += bias;
+            if (p.pre.ptr) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (live && c < columns) pre[c * p.pre.row_stride + half] = rounded<T>(v[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                const float other = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[c + 1], 8);
+                const float gate = up ? other : v[c], lin = up ? v[c + 1] : other;
+                float y = gate * sigmoidf(gate) * lin;
+                const int mine = up ? c + 1 : c;
+                if (live && mine < columns) {
+                    if (p.residual.ptr) y += f32(res[mine * p.residual.row_stride]);
+                    out[mine * p.out.row_stride] = rounded<T>(y);
+                }
+            }
+        }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) product_kernel(const ProductParams p) {
-    __shared__ float sa[2][kTileK][kTile + 1], sb[kTileK][kTile + 1];
-    const int G = p.gr.R * p.gr.per;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int mt = (p.M + kTile - 1) / kTile;
-    int64_t before = 0;
-    int64_t tile = blockIdx.x;
-    for (int g = 0; g < G; ++g) {
-        int first, rows;
-        group_range(p.gr, g, &first, &rows);
-        const int N = p.N < 0 ? rows : p.N, K = p.K < 0 ? rows : p.K;
-        const int64_t tiles = (int64_t)mt * ((N + kTile - 1) / kTile);
-        const int seg = g / p.gr.per;
-        const T *A = static_cast<const T *>(p.a.ptr) +
-                     (p.a.rows_i || p.a.rows_k ? seg : g) * p.a.group_stride +
-                     (p.a.rows_k ? first * p.a.sk : 0);
-        const T *B = static_cast<const T *>(p.b.ptr) + seg * p.b.group_stride +
-                     first * (p.b.rows_i ? p.b.si : p.b.sk);
-        for (; tile < before + tiles; tile += gridDim.x) {
-            const int m0 = (int)((tile - before) % mt) * kTile, n0 = (int)((tile - before) / mt) * kTile;
-            float acc[2][4][4] = {};
-            for (int k0 = 0; k0 < K; k0 += kTileK) {
-                for (int i = tid; i < kTile * kTileK; i += 256) {
-                    const int r = i / kTileK, c = i % kTileK;
-                    const bool kin = k0 + c < K;
-                    sa[0][c][r] = kin && m0 + r < p.M ? f32(A[(m0 + r) * p.a.si + (k0 + c) * p.a.sk]) : 0.f;
-                    if (p.wide_half)
-                        sa[1][c][r] = kin && m0 + r < p.M
-                                          ? f32(A[(p.wide_half + m0 + r) * p.a.si + (k0 + c) * p.a.sk]) : 0.f;
-                    sb[c][r] = kin && n0 + r < N ? f32(B[(n0 + r) * p.b.si + (k0 + c) * p.b.sk]) : 0.f;
-                }
-                __syncthreads();
-                for (int c = 0; c < kTileK; ++c)
-                    for (int u = 0; u < 4; ++u)
-                        for (int v = 0; v < 4; ++v) {
-                            acc[0][u][v] += sb[c][ty + 16 * u] * sa[0][c][tx + 16 * v];
-                            if (p.wide_half) acc[1][u][v] += sb[c][ty + 16 * u] * sa[1][c][tx + 16 * v];
-                        }
-                __syncthreads();
-            }
-            const int wide = p.wide_half ? 2 * p.wide_half : p.M;
-            for (int u = 0; u < 4; ++u)
-                for (int v = 0; v < 4; ++v) {
-                    const int n = n0 + ty + 16 * u, m = m0 + tx + 16 * v;
-                    if (n >= N || m >= p.M) continue;
-                    const int64_t row = p.out_by_rows ? first + n : n;
-                    const int64_t own = p.out_by_rows ? seg : g;
-                    float h0 = acc[0][u][v], h1 = acc[1][u][v];
-                    if (p.bias) {
-                        const T *bias = static_cast<const T *>(p.bias) + (int64_t)g * wide;
-                        h0 += f32(bias[m]);
-                        if (p.wide_half) h1 += f32(bias[p.wide_half + m]);
-                    }
-                    if (p.pre.ptr) {
-                        T *pre = static_cast<T *>(p.pre.ptr) + own * p.pre.rank_stride + row * p.pre.row_stride;
-                        pre[m] = rounded<T>(h0);
-                        if (p.wide_half) pre[p.wide_half + m] = rounded<T>(h1);
-                    }
-                    float y = p.wide_half ? h0 * sigmoidf(h0) * h1 : activate(p.act, h0);
-                    if (p.residual.ptr)
-                        y += f32(static_cast<const T *>(p.residual.ptr)[own * p.residual.rank_stride +
-                                                                        row * p.residual.row_stride + m]);
-                    static_cast<T *>(p.out.ptr)[own * p.out.rank_stride + row * p.out.row_stride + m] =
-                        rounded<T>(y);
-                }
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_b16, const ProductParams p) {
+    constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
+    constexpr int kFeat = MODE == kGated ? kTileM / 2 : kTileM;     // outputs along m per tile
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Barriers bars;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *gave_up = &bars.gave_up;
+    auto bar = [](uint64_t *b) { return smem_u32(b); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
         }
-        before += tiles;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], 4);
+        }
+        mbar_init(&bars.drained, 1);
+        bars.gave_up = 0;
+        mbar_init_fence();
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
     }
+    if (warp == 1) tmem_alloc(smem_u32(&bars.tmem), 512);
+    tcgen_before_sync();
+    __syncthreads();
+    tcgen_after_sync();
+    const uint32_t tmem = bars.tmem;
+
+    const int mt = (p.M + kFeat - 1) / kFeat;
+    Walker walk;
+    Tile t;
+    walk.start(p, mt);
+    bool ok = true;
+
+    if (warp == 0) {
+        uint32_t issued = 0;
+        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
+            const int n = min(kTileN, N - t.n * kTileN);
+            const bool narrow = !kBmn && n <= 48;         // 16-row boxes: at most 3 loads either way
+            const int boxes = narrow ? (n + 15) / 16 : (n + 63) / 64;
+            const uint32_t box = narrow ? kChunkBytes / 4 : kChunkBytes;
+            if (lane == 0) {
+                for (int k = 0; k < K; k += kSliceK) {
+                    const uint32_t s = issued % kStages, round = issued / kStages;
+                    if (!tensor_wait(bar(&bars.empty[s]), (round & 1u) ^ 1u, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = bar(&bars.full[s]);
+                    const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
+                    mbar_expect(full, kBytesA + boxes * box);
+                    if constexpr (MODE == kGated) {
+                        tma_load5(a, &map_a, full, k, 0, 0, t.m * (kFeat / 8), t.g);
+                    } else if constexpr (!kAmn) {
+                        tma_load3(a, &map_a, full, k, t.m * kTileM, t.g);
+                    } else {
+                        const int row = MODE == kGradW ? t.first + k : k;
+                        const int own = MODE == kGradW ? t.seg : t.g;
+                        tma_load3(a, &map_a, full, t.m * kTileM, row, own);
+                        tma_load3(a + kChunkBytes, &map_a, full, t.m * kTileM + 64, row, own);
+                    }
+                    for (int j = 0; j < boxes; ++j) {
+                        if constexpr (kBmn)
+                            tma_load3(b + j * kChunkBytes, &map_b, full, t.n * kTileN + j * 64, t.first + k, t.seg);
+                        else
+                            tma_load3(b + j * box, narrow ? &map_b16 : &map_b, full, k,
+                                      t.first + t.n * kTileN + j * (narrow ? 16 : 64), t.seg);
+                    }
+                    ++issued;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        // after a wait that ran out: no copy may outlive the CTA
+        if (!ok && lane == 0)
+            for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
+                int ignore = 0;
+                tensor_wait(bar(&bars.full[j % kStages]), (j / kStages) & 1u, &ignore);
+            }
+        __syncwarp();
+    } else if (warp == 1) {
+        constexpr uint32_t kIdesc = f16_idesc(sizeof(T) == 2 && IsBf16<T>::value, kAmn, kBmn, kTileM);
+        uint32_t slice = 0, acc = 0;
+        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
+            const int n = min(kTileN, N - t.n * kTileN);
+            if (K == 0) continue;
+            const uint32_t idesc = kIdesc | idesc_n((n + 15) & ~15);
+            const uint32_t d = tmem + (acc & 1u) * 256;
+            ok = warp_wait(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
+            tcgen_after_sync();
+            for (int k = 0; ok && k < K; k += kSliceK, ++slice) {
+                const uint32_t s = slice % kStages;
+                ok = warp_wait(bar(&bars.full[s]), (slice / kStages) & 1u, gave_up);
+                if (!ok) break;
+                tcgen_after_sync();
+                const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
+                if (MODE == kGradW && K - k < kSliceK) {
+                    // rows past the group's end: zero, whatever they held (the
+                    // 128-byte swizzle moves data within a k row only)
+                    const int live = K - k, chunks = 2 + (n + 63) / 64;
+                    for (int q = lane; q < chunks * (kSliceK - live) * 8; q += 32) {
+                        const int chunk = q / ((kSliceK - live) * 8), r = q % ((kSliceK - live) * 8);
+                        const uint32_t at = (chunk < 2 ? a + chunk * kChunkBytes : b + (chunk - 2) * kChunkBytes) +
+                                            live * 128 + r * 16;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int j = 0; j < kSliceK / 16; ++j) {
+                        const uint64_t da = kAmn ? smem_desc(a + j * 2048, kChunkBytes, 1024)
+                                                 : smem_desc(a + j * 32, 16, 1024);
+                        const uint64_t db = kBmn ? smem_desc(b + j * 2048, kChunkBytes, 1024)
+                                                 : smem_desc(b + j * 32, 16, 1024);
+                        mma_f16(d, da, db, idesc, k > 0 || j > 0);
+                    }
+                    mma_commit(bar(&bars.empty[s]));
+                    if (k + kSliceK >= K) mma_commit(bar(&bars.acc_full[acc & 1u]));
+                }
+                __syncwarp();
+            }
+            ++acc;
+        }
+        if (!ok) {                                       // let the matrix unit finish
+            int ignore = 0;
+            if (lane == 0) mma_commit(bar(&bars.drained));
+            tensor_wait(bar(&bars.drained), 0, &ignore);
+        }
+    } else {
+        const int quarter = warp & 3;                    // the TMEM lanes this warp may read
+        uint32_t acc = 0;
+        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
+            const int n = min(kTileN, N - t.n * kTileN);
+            // this lane's output index along m
+            const int in = quarter * 32 + lane;
+            const int m = t.m * kFeat + (MODE == kGated ? (in >> 4) * 8 + (in & 7) : in);
+            const bool live = m < p.M;
+            float b0 = 0.f, b1 = 0.f;
+            if ((MODE == kForward || MODE == kGated) && p.bias && live) {
+                const T *bias = static_cast<const T *>(p.bias) + (int64_t)t.g * (MODE == kGated ? 2 * p.M : p.M);
+                b0 = f32(bias[m]);
+                if (MODE == kGated) b1 = f32(bias[p.M + m]);
+            }
+            if (K > 0) {
+                ok = warp_wait(bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, gave_up);
+                if (!ok) break;
+                tcgen_after_sync();
+            }
+            const uint32_t d = tmem + (acc & 1u) * 256 + ((uint32_t)(quarter * 32) << 16);
+            for (int c = 0; c < n; c += 32) {
+                float v[32];
+                if (K > 0) {
+                    __syncwarp();
+                    tmem_load32(d + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                }
+                if (K > 0 && c + 32 >= n) {              // the accumulator may be filled again
+                    tcgen_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(&bars.acc_empty[acc & 1u]));
+                }
+                store_columns<T, MODE>(p, t, v, c, n - c, m, live, b0, b1);
+            }
+            if (K > 0) ++acc;
+        }
+    }
+    tcgen_before_sync();
+    __syncthreads();
+    tcgen_after_sync();
+    if (warp == 1) tmem_free(tmem, 512);
+    if (threadIdx.x == 0 && bars.gave_up && p.error) atomicOr(p.error, EP_DEVERR_TIMEOUT);
 }
 
 // d = grad * act'(pre) over every group's rows, rounded once for the
@@ -206,7 +462,7 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 // Rows of `width` elements: 16-byte aligned, dense rows that do not overlap.
 bool valid_rows(const ep_rows_t &r, int64_t width, bool many) {
     return r.ptr && aligned(r.ptr, 16) && r.row_stride >= width && r.row_stride % 8 == 0 &&
-           (!many || (r.rank_stride >= 0 && r.rank_stride % 8 == 0));
+           (!many || (r.rank_stride > 0 && r.rank_stride % 8 == 0));
 }
 
 int64_t wide_of(const ep_product_desc_t &d) {
@@ -239,8 +495,112 @@ template <typename F> void with_type(int dtype, F f) {
 
 ep_status_t launched() { return cudaGetLastError() == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP; }
 
-void launch_product(const ep_product_desc_t &d, const ProductParams &p, cudaStream_t st) {
-    with_type(d.dtype, [&](auto type) { product_kernel<decltype(type)><<<152 * 4, 256, 0, st>>>(p); });
+// ---- tensor maps
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static std::atomic<EncodeFn> cached{nullptr};
+    EncodeFn f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        void *sym = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeFn>(sym);
+        cached.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+bool encode(CUtensorMap *map, int dtype, void *ptr, int rank, const uint64_t *dims, const int64_t *strides,
+            const uint32_t *box) {
+    EncodeFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t d[5], s[5];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i) s[i - 1] = (cuuint64_t)strides[i] * 2;
+    }
+    return f(map, dtype == EP_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             (cuuint32_t)rank, ptr, d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [outer][rows][width] with boxes of 64 elements by `box_rows` rows.  Reads
+// past an edge give zeros.
+bool encode_rows(CUtensorMap *map, int dtype, const ep_rows_t &r, int64_t width, int64_t rows, int64_t outer,
+                 uint32_t box_rows) {
+    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)rows, (uint64_t)outer};
+    const int64_t strides[3] = {1, r.row_stride, outer > 1 ? r.rank_stride : r.row_stride};
+    const uint32_t box[3] = {kSliceK, box_rows, 1};
+    return encode(map, dtype, r.ptr, 3, dims, strides, box);
+}
+
+// Gated weights [G][2][N][K]: one box is 8 features of the gate, the same 8
+// of the up half, and so on for 64 features.
+bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, int64_t N, int64_t G) {
+    const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)G};
+    const int64_t strides[5] = {1, w.row_stride, N * w.row_stride, 8 * w.row_stride,
+                                G > 1 ? w.rank_stride : w.row_stride};
+    const uint32_t box[5] = {kSliceK, 8, 2, 8, 1};
+    return encode(map, dtype, w.ptr, 5, dims, strides, box);
+}
+
+// ---- launch
+
+int sm_count() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> cached[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    n = cached[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <typename T, Mode MODE>
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b16, const ProductParams &p,
+                   cudaStream_t st) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> configured[kMaxDevices];       // the attribute is per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(product_kernel<T, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        configured[dev].store(true, std::memory_order_release);
+    }
+    // tiles at most: every group's last tile may be a part
+    const int64_t mt = (p.M + (MODE == kGated ? 63 : 127)) / (MODE == kGated ? 64 : 128);
+    const int64_t G = (int64_t)p.gr.R * p.gr.per;
+    const int64_t nt = p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / kTileN + G : G * ((p.N + kTileN - 1) / kTileN);
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const int64_t grid = mt * nt < sms ? mt * nt : sms;
+    product_kernel<T, MODE><<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a, b, b16, p);
+    return cudaGetLastError();
+}
+
+template <Mode MODE>
+ep_status_t launch_product(int dtype, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b16,
+                           const ProductParams &p, cudaStream_t st) {
+    const cudaError_t e = dtype == EP_DT_BF16 ? launch<__nv_bfloat16, MODE>(a, b, b16, p, st)
+                                              : launch<__half, MODE>(a, b, b16, p, st);
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -266,20 +626,26 @@ ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
         return EP_ERR_INVALID_ARGS;
     ProductParams p = {};
     p.gr = groups_of(*d);
-    p.a = Operand{d->weight.ptr, d->weight.rank_stride, d->weight.row_stride, 1, false, false};
-    p.b = Operand{d->x.ptr, d->x.rank_stride, d->x.row_stride, 1, true, false};
     p.M = d->out_features;
     p.N = -1;
     p.K = d->in_features;
-    p.wide_half = d->activation == EP_ACT_SWIGLU ? d->out_features : 0;
     p.act = d->activation;
-    p.out_by_rows = true;
     p.bias = d_bias;
     p.residual = *residual;
     p.out = *y;
     p.pre = *pre;
-    launch_product(*d, p, static_cast<cudaStream_t>(stream));
-    return launched();
+    p.error = d_error;
+    const bool gated = d->activation == EP_ACT_SWIGLU;
+    const int64_t G = (int64_t)d->ranks * d->groups;
+    CUtensorMap a, b, b16;
+    if (!(gated ? encode_gated(&a, d->dtype, d->weight, p.K, p.M, G)
+                : encode_rows(&a, d->dtype, d->weight, p.K, p.M, G, kTileM)) ||
+        !encode_rows(&b, d->dtype, d->x, p.K, d->rows, d->ranks, 64) ||
+        !encode_rows(&b16, d->dtype, d->x, p.K, d->rows, d->ranks, 16))
+        return EP_ERR_GPU_OP;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return gated ? launch_product<kGated>(d->dtype, a, b, b16, p, st)
+                 : launch_product<kForward>(d->dtype, a, b, b16, p, st);
 }
 
 ep_status_t ep_expert_product_workspace(const ep_product_desc_t *d, size_t *bytes) {
@@ -314,28 +680,39 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         const dim3 grid((d->out_features + 255) / 256, gr.R * gr.per);
         with_type(d->dtype, [&](auto type) { act_grad_kernel<decltype(type)><<<grid, 256, 0, st>>>(a); });
     }
+    const int64_t G = (int64_t)d->ranks * d->groups;
+    CUtensorMap a, b, b16;
     if (grad_x->ptr && d->rows > 0) {
         ProductParams p = {};
         p.gr = gr;
-        p.a = Operand{d->weight.ptr, d->weight.rank_stride, 1, d->weight.row_stride, false, false};
-        p.b = Operand{dd.ptr, dd.rank_stride, dd.row_stride, 1, true, false};
         p.M = d->in_features;
         p.N = -1;
         p.K = (int)wide;
-        p.out_by_rows = true;
         p.out = *grad_x;
-        launch_product(*d, p, st);
+        p.error = d_error;
+        if (!encode_rows(&a, d->dtype, d->weight, d->in_features, wide, G, 64) ||
+            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, 64) ||
+            !encode_rows(&b16, d->dtype, dd, wide, d->rows, d->ranks, 16))
+            return EP_ERR_GPU_OP;
+        const ep_status_t s = launch_product<kGradX>(d->dtype, a, b, b16, p, st);
+        if (s != EP_SUCCESS) return s;
     }
+    if (d_grad_w && d->rows == 0)
+        return cudaMemsetAsync(d_grad_w, 0, (size_t)G * wide * d->in_features * 2, st) == cudaSuccess
+                   ? EP_SUCCESS : EP_ERR_GPU_OP;
     if (d_grad_w) {
         ProductParams p = {};
         p.gr = gr;
-        p.a = Operand{d->x.ptr, d->x.rank_stride, 1, d->x.row_stride, false, true};
-        p.b = Operand{dd.ptr, dd.rank_stride, 1, dd.row_stride, false, true};
         p.M = d->in_features;
         p.N = (int)wide;
         p.K = -1;
         p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
-        launch_product(*d, p, st);
+        p.error = d_error;
+        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, 64) ||
+            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, 64))
+            return EP_ERR_GPU_OP;
+        const ep_status_t s = launch_product<kGradW>(d->dtype, a, b, b, p, st);
+        if (s != EP_SUCCESS) return s;
     }
     return launched();
 }

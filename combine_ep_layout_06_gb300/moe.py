@@ -250,7 +250,8 @@ def _strided(t: torch.Tensor, name: str) -> EpRowsC:
     strides = t.stride()
     rank = strides[0] if len(strides) == 3 and t.shape[0] > 1 else 0
     row = strides[-2] if t.shape[-2] > 1 else -(-t.shape[-1] // 8) * 8
-    if strides[-1] != 1 or row < t.shape[-1] or (row | rank) % 8 or t.data_ptr() % 16:
+    if (strides[-1] != 1 or row < t.shape[-1] or (row | rank) % 8 or t.data_ptr() % 16
+            or (rank == 0 and len(strides) == 3 and t.shape[0] > 1)):
         raise ValueError(f"{name}: contiguous rows, 16-byte aligned, with strides of a multiple of 8 elements")
     return EpRowsC(t.data_ptr(), rank, row)
 
