@@ -7,14 +7,16 @@
 //   grad_w    m = input,   n = feature, k = row    A = x^T,       B = d^T
 // The output's contiguous dimension is always m.
 //
-// One CTA per SM walks the tiles of all groups (their row counts are on the
-// device): 128 m by up to 256 n, accumulated in tensor memory.  Weights or
-// inputs are the 128-wide operand and rows (or features) the other, so that a
-// group with few rows costs a narrow instruction (n in steps of 16) and not a
-// padded tile of 128 rows.  Warp 0 loads 64-deep slices by TMA into a ring in
-// shared memory, warp 1 issues the matrix instructions, warps 2..5 turn a
-// finished accumulator into outputs while the next one fills: two
-// accumulators of 256 columns take all of the SM's tensor memory.
+// Pairs of CTAs, one CTA per SM, walk the tiles of all groups (their row
+// counts are on the device): 256 m by up to 256 n, accumulated in tensor
+// memory, 128 m in each CTA.  Weights or inputs are the 256-wide operand and
+// rows (or features) the other, so that a group with few rows costs a narrow
+// instruction (n in steps of 32) and not a padded tile.  A CTA loads its own
+// 128 m and half of n, so every byte of n serves both.  In each CTA warp 0
+// loads 64-deep slices by TMA into a ring in shared memory; warp 1 of the
+// first CTA issues the pair's matrix instructions; warps 2..5 turn a finished
+// accumulator into outputs while the next one fills: two accumulators of 256
+// columns take all of the SM's tensor memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,12 +29,14 @@
 namespace ep {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kSliceK = 64;
-constexpr int kStages = 4;
-constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN * kSliceK * 2;
+constexpr int kTileM = 128, kTileN = 256, kSliceK = 64;     // m of one CTA, n of the pair
+constexpr int kStages = 6;
+constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN / 2 * kSliceK * 2;
 constexpr int kStageBytes = kBytesA + kBytesB;
 constexpr int kChunkBytes = 64 * kSliceK * 2;      // 64 rows (or 64 columns) of one slice
-constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 1024;
+constexpr int kTurnStride = 36;                    // floats per row of a warp's transposing buffer
+constexpr int kTurnBytes = 32 * kTurnStride * 4;
+constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 4 * kTurnBytes + 1024;
 constexpr int kThreads = 192;
 
 struct Groups {
@@ -129,111 +133,191 @@ struct Walker {
     }
 };
 
+// Rows (k) from `live` on of `chunks` chunks of an MN-major slice are past
+// the group's end: zero, whatever they held.  (The 128-byte swizzle moves data
+// within a k row only.)  By a whole warp; the matrix unit sees it afterwards.
+__device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live) {
+    const int per = (kSliceK - live) * 8;
+    for (int q = threadIdx.x & 31; q < chunks * per; q += 32) {
+        const uint32_t at = slice + (q / per) * kChunkBytes + live * 128 + (q % per) * 16;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
 struct __align__(8) Barriers {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kStages], empty[kStages], tail[kStages], peer_tail[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
 };
 
-// The epilogue of 32 columns (rows, or features of grad_w) of one lane's m.
-template <typename T, Mode MODE>
-__device__ __forceinline__ void store_columns(const ProductParams &p, const Tile &t, float *v, int c0,
-                                              int columns, int m, bool live, float b0, float b1) {
-    const int64_t own = MODE == kGradW ? t.g : t.seg;
-    const int64_t row0 = (MODE == kGradW ? 0 : t.first) + t.n * (int64_t)kTileN + c0;
-    T *out = static_cast<T *>(p.out.ptr) + own * p.out.rank_stride + row0 * p.out.row_stride + m;
-    if constexpr (MODE == kGradX || MODE == kGradW) {
+// Two floats as two 16-bit values.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, const float *v) {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+}
+template <typename T> __device__ __forceinline__ void add8(float *v, const uint4 &r) {
+    const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-            if (live && c < columns) out[c * p.out.row_stride] = rounded<T>(v[c]);
-    } else {
-        const T *res = static_cast<const T *>(p.residual.ptr) + own * p.residual.rank_stride +
-                       row0 * p.residual.row_stride + m;
-        T *pre = static_cast<T *>(p.pre.ptr) + own * p.pre.rank_stride + row0 * p.pre.row_stride + m;
-        if constexpr (MODE == kForward) {
+    for (int i = 0; i < 8; ++i) v[i] += f32(e[i]);
+}
+__device__ __forceinline__ void read8(float *v, const float *s) {
+    const float4 a = reinterpret_cast<const float4 *>(s)[0], b = reinterpret_cast<const float4 *>(s)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void activate8(int act, float *v) {
+    switch (act) {
+    case EP_ACT_RELU:
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] += b0;
-            if (p.pre.ptr) {
+        for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], 0.f);
+        break;
+    case EP_ACT_GELU:
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (live && c < columns) pre[c * p.pre.row_stride] = rounded<T>(v[c]);
-            }
-            switch (p.act) {
-            case EP_ACT_RELU:
+        for (int i = 0; i < 8; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+        break;
+    case EP_ACT_SILU:
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = fmaxf(v[c], 0.f);
-                break;
-            case EP_ACT_GELU:
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = 0.5f * v[c] * (1.0f + erff(v[c] * 0.70710678118654752f));
-                break;
-            case EP_ACT_SILU:
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] *= sigmoidf(v[c]);
-                break;
-            default: break;
-            }
-            if (p.residual.ptr) {
-                float r[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    r[c] = live && c < columns ? f32(res[c * p.residual.row_stride]) : 0.f;
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] += r[c];
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (live && c < columns) out[c * p.out.row_stride] = rounded<T>(v[c]);
-        } else {
-            // Lanes 0-7 and 16-23 hold the gate of 8 features, lanes 8-15 and
-            // 24-31 their up half.  Of two rows, the gate's lane finishes the
-            // first and the up half's lane the second: one exchange for both.
-            const bool up = (threadIdx.x & 8) != 0;
-            const int64_t half = up ? p.M : 0;
-            const float bias = up ? b1 : b0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] += bias;
-            if (p.pre.ptr) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (live && c < columns) pre[c * p.pre.row_stride + half] = rounded<T>(v[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                const float other = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[c + 1], 8);
-                const float gate = up ? other : v[c], lin = up ? v[c + 1] : other;
-                float y = gate * sigmoidf(gate) * lin;
-                const int mine = up ? c + 1 : c;
-                if (live && mine < columns) {
-                    if (p.residual.ptr) y += f32(res[mine * p.residual.row_stride]);
-                    out[mine * p.out.row_stride] = rounded<T>(y);
-                }
-            }
-        }
+        for (int i = 0; i < 8; ++i) v[i] *= sigmoidf(v[i]);
+        break;
+    default: break;
     }
 }
 
+// A warp's part of the epilogue.  The accumulator comes with one m per lane
+// and one n per register; a turn through shared memory gives each lane 8
+// neighbouring m of one n, so that residual, pre and out move 16 bytes at a
+// time: kTasks pairs (n, 8 m) per lane and 32 columns, lane l starting at
+// column l / kPer and block l % kPer.
+template <typename T, Mode MODE> struct Epilogue {
+    static constexpr int kPer = MODE == kGated ? 2 : 4;      // 8-blocks of outputs per column
+    static constexpr int kTasks = kPer;                      // 32 columns * kPer / 32 lanes
+    static constexpr bool kActs = MODE == kForward || MODE == kGated;
+    T *out, *pre;
+    const T *res;
+    int64_t out_stride, pre_stride, res_stride;
+    int n, M, lane;
+    bool live;                   // this lane's block of outputs is inside
+    bool pre_live;
+    uint4 next[kTasks];          // residual of the columns to come
+
+    __device__ void start(const ProductParams &p, const Tile &t, int quarter, uint32_t rank, int n_) {
+        lane = threadIdx.x & 31;
+        n = n_;
+        M = p.M;
+        const int64_t own = MODE == kGradW ? t.g : t.seg;
+        const int64_t row0 = (MODE == kGradW ? 0 : t.first) + t.n * (int64_t)kTileN;
+        // outputs of the quarter: 32 m, or 16 features (gated)
+        const int m0 = (t.m * 2 + (int)rank) * (MODE == kGated ? 64 : 128) + quarter * kPer * 8;
+        const int m = m0 + (lane % kPer) * 8;
+        live = m < M;
+        out_stride = p.out.row_stride;
+        out = static_cast<T *>(p.out.ptr) + own * p.out.rank_stride + (row0 + lane / kPer) * out_stride + m;
+        if constexpr (kActs) {
+            res_stride = p.residual.row_stride;
+            res = p.residual.ptr ? static_cast<const T *>(p.residual.ptr) + own * p.residual.rank_stride +
+                                       (row0 + lane / kPer) * res_stride + m
+                                 : nullptr;
+            // pre: four 8-blocks of accumulator lanes per column; gated: gate, up, gate, up
+            const int block = lane & 3;
+            const int64_t pm = MODE == kGated ? m0 + (block >> 1) * 8 + (block & 1) * (int64_t)M : m;
+            pre_live = MODE == kGated ? m0 + (block >> 1) * 8 < M : live;
+            pre_stride = p.pre.row_stride;
+            pre = p.pre.ptr ? static_cast<T *>(p.pre.ptr) + own * p.pre.rank_stride +
+                                  (row0 + lane / 4) * pre_stride + pm
+                            : nullptr;
+            fetch(0);
+        }
+    }
+    __device__ void fetch(int c0) {
+        if (!kActs || !res) return;
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+            const int c = c0 + i * (32 / kPer);
+            next[i] = live && c + lane / kPer < n ? *reinterpret_cast<const uint4 *>(res + c * res_stride)
+                                                  : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // v: 32 columns from c0 on of this lane's m, bias added.
+    __device__ void columns(const ProductParams &p, float *turn, const float *v, int c0) {
+        uint4 r[kTasks];
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) r[i] = next[i];
+        if (c0 + 32 < n) fetch(c0 + 32);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) turn[c * kTurnStride + lane] = v[c];
+        __syncwarp();
+        if (kActs && MODE == kGated && pre) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = i * 8 + lane / 4;
+                float f[8];
+                read8(f, turn + c * kTurnStride + (lane & 3) * 8);
+                if (pre_live && c0 + c < n) store8<T>(pre + (c0 + i * 8) * pre_stride, f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+            const int c = i * (32 / kPer) + lane / kPer;
+            const bool in = live && c0 + c < n;
+            float f[8];
+            if constexpr (MODE == kGated) {
+                float up[8];
+                read8(f, turn + c * kTurnStride + (lane & 1) * 16);
+                read8(up, turn + c * kTurnStride + (lane & 1) * 16 + 8);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = f[j] * sigmoidf(f[j]) * up[j];
+            } else {
+                read8(f, turn + c * kTurnStride + (lane & 3) * 8);
+                if constexpr (MODE == kForward) {
+                    if (pre && in) store8<T>(pre + (c0 + i * 8) * pre_stride, f);
+                    activate8(p.act, f);
+                }
+            }
+            if (kActs && res) add8<T>(f, r[i]);
+            if (in) store8<T>(out + (c0 + i * (32 / kPer)) * out_stride, f);
+        }
+        __syncwarp();
+    }
+};
+
 template <typename T, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_b16, const ProductParams p) {
     constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
-    constexpr int kFeat = MODE == kGated ? kTileM / 2 : kTileM;     // outputs along m per tile
+    constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bars;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    float *turns = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + kStages * kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     volatile int *gave_up = &bars.gave_up;
     auto bar = [](uint64_t *b) { return smem_u32(b); };
+    auto first_cta = [](uint64_t *b) { return in_cta(smem_u32(b), 0); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.full[i], 1);                 // the first CTA's hears of both CTAs' loads
             mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.tail[i], 1);
+            mbar_init(&bars.peer_tail[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 4);
+            mbar_init(&bars.acc_empty[i], 8);            // both CTAs' epilogue warps
         }
         mbar_init(&bars.drained, 1);
         bars.gave_up = 0;
@@ -241,6 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_map(&map_a);
         tma_prefetch_map(&map_b);
     }
+    __syncwarp();
+    cluster_sync();
     if (warp == 1) tmem_alloc(smem_u32(&bars.tmem), 512);
     tcgen_before_sync();
     __syncthreads();
@@ -254,13 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     if (warp == 0) {
-        uint32_t issued = 0;
-        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+        uint32_t issued = 0, tails = 0, landed = 0;       // by stage: a tail was loaded, its barrier's phase
+        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
-            const int n = min(kTileN, N - t.n * kTileN);
-            const bool narrow = !kBmn && n <= 48;         // 16-row boxes: at most 3 loads either way
-            const int boxes = narrow ? (n + 15) / 16 : (n + 63) / 64;
+            const int half = ((min(kTileN, N - t.n * kTileN) + 31) & ~31) / 2;   // this CTA's n
+            const bool narrow = !kBmn && half <= 48;      // 16-row boxes: at most 3 loads either way
+            const int boxes = narrow ? half / 16 : (half + 63) / 64;
             const uint32_t box = narrow ? kChunkBytes / 4 : kChunkBytes;
+            const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n * kTileN + (int)rank * half;
             if (lane == 0) {
                 for (int k = 0; k < K; k += kSliceK) {
                     const uint32_t s = issued % kStages, round = issued / kStages;
@@ -268,48 +355,64 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t full = bar(&bars.full[s]);
+                    // the second CTA clears the rows past a group's end before
+                    // it tells the first: that slice lands on its own barrier
+                    const bool last = MODE == kGradW && K - k < kSliceK, tail = last && rank == 1;
+                    const uint32_t full = tail ? in_cta(bar(&bars.tail[s]), 1) : first_cta(&bars.full[s]);
                     const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
-                    mbar_expect(full, kBytesA + boxes * box);
+                    const uint32_t bytes = kBytesA + boxes * box;
+                    if (rank == 0) mbar_expect(bar(&bars.full[s]), last ? bytes : 2 * bytes);
+                    if (tail) {
+                        mbar_expect(bar(&bars.tail[s]), bytes);
+                        if (tails >> s & 1u) landed ^= 1u << s;
+                        tails |= 1u << s;
+                    }
                     if constexpr (MODE == kGated) {
-                        tma_load5(a, &map_a, full, k, 0, 0, t.m * (kFeat / 8), t.g);
+                        tma_load5(a, &map_a, full, k, 0, 0, m0 / 16, t.g);
                     } else if constexpr (!kAmn) {
-                        tma_load3(a, &map_a, full, k, t.m * kTileM, t.g);
+                        tma_load3(a, &map_a, full, k, m0, t.g);
                     } else {
                         const int row = MODE == kGradW ? t.first + k : k;
                         const int own = MODE == kGradW ? t.seg : t.g;
-                        tma_load3(a, &map_a, full, t.m * kTileM, row, own);
-                        tma_load3(a + kChunkBytes, &map_a, full, t.m * kTileM + 64, row, own);
+                        tma_load3(a, &map_a, full, m0, row, own);
+                        tma_load3(a + kChunkBytes, &map_a, full, m0 + 64, row, own);
                     }
                     for (int j = 0; j < boxes; ++j) {
                         if constexpr (kBmn)
-                            tma_load3(b + j * kChunkBytes, &map_b, full, t.n * kTileN + j * 64, t.first + k, t.seg);
+                            tma_load3(b + j * kChunkBytes, &map_b, full, n0 + j * 64, t.first + k, t.seg);
                         else
                             tma_load3(b + j * box, narrow ? &map_b16 : &map_b, full, k,
-                                      t.first + t.n * kTileN + j * (narrow ? 16 : 64), t.seg);
+                                      t.first + n0 + j * (narrow ? 16 : 64), t.seg);
                     }
                     ++issued;
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        // after a wait that ran out: no copy may outlive the CTA
-        if (!ok && lane == 0)
+        // The pair ends together, and not before its copies have landed and the
+        // stages' last signals have come; after a wait that ran out, as far
+        // as they come within another wait each.
+        if (lane == 0) {
+            int ignore = 0;
+            volatile int *flag = ok ? gave_up : &ignore;
             for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
-                int ignore = 0;
-                tensor_wait(bar(&bars.full[j % kStages]), (j / kStages) & 1u, &ignore);
+                const uint32_t s = j % kStages, phase = (j / kStages) & 1u;
+                if (!ok && rank == 0) tensor_wait(bar(&bars.full[s]), phase, flag);
+                if (!ok && rank == 1 && (tails >> s & 1u)) tensor_wait(bar(&bars.tail[s]), landed >> s & 1u, flag);
+                tensor_wait(bar(&bars.empty[s]), phase, flag);
             }
+        }
         __syncwarp();
-    } else if (warp == 1) {
-        constexpr uint32_t kIdesc = f16_idesc(sizeof(T) == 2 && IsBf16<T>::value, kAmn, kBmn, kTileM);
-        uint32_t slice = 0, acc = 0;
-        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+    } else if (warp == 1 && rank == 0) {
+        constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
+        uint32_t slice = 0, acc = 0, tails = 0;
+        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
-            const int n = min(kTileN, N - t.n * kTileN);
+            const int n = (min(kTileN, N - t.n * kTileN) + 31) & ~31;
             if (K == 0) continue;
-            const uint32_t idesc = kIdesc | idesc_n((n + 15) & ~15);
+            const uint32_t idesc = kIdesc | idesc_n(n);
             const uint32_t d = tmem + (acc & 1u) * 256;
-            ok = warp_wait(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
+            ok = warp_wait<true>(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
             tcgen_after_sync();
             for (int k = 0; ok && k < K; k += kSliceK, ++slice) {
                 const uint32_t s = slice % kStages;
@@ -318,17 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tcgen_after_sync();
                 const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
                 if (MODE == kGradW && K - k < kSliceK) {
-                    // rows past the group's end: zero, whatever they held (the
-                    // 128-byte swizzle moves data within a k row only)
-                    const int live = K - k, chunks = 2 + (n + 63) / 64;
-                    for (int q = lane; q < chunks * (kSliceK - live) * 8; q += 32) {
-                        const int chunk = q / ((kSliceK - live) * 8), r = q % ((kSliceK - live) * 8);
-                        const uint32_t at = (chunk < 2 ? a + chunk * kChunkBytes : b + (chunk - 2) * kChunkBytes) +
-                                            live * 128 + r * 16;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
-                    }
-                    fence_async_smem();
-                    __syncwarp();
+                    clear_rows(a, 2 + (n / 2 + 63) / 64, K - k);
+                    ok = warp_wait<true>(bar(&bars.peer_tail[s]), tails >> s & 1u, gave_up);
+                    if (!ok) break;
+                    tails ^= 1u << s;
                 }
                 if (lane == 0) {
 #pragma unroll
@@ -339,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  : smem_desc(b + j * 32, 16, 1024);
                         mma_f16(d, da, db, idesc, k > 0 || j > 0);
                     }
-                    mma_commit(bar(&bars.empty[s]));
-                    if (k + kSliceK >= K) mma_commit(bar(&bars.acc_full[acc & 1u]));
+                    mma_commit_pair(bar(&bars.empty[s]));
+                    if (k + kSliceK >= K) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
                 }
                 __syncwarp();
             }
@@ -351,21 +447,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mma_commit(bar(&bars.drained));
             tensor_wait(bar(&bars.drained), 0, &ignore);
         }
+    } else if (warp == 1) {
+        if (MODE == kGradW) {
+            uint32_t slice = 0, tails = 0;
+            for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
+                const int slices = (t.rows + kSliceK - 1) / kSliceK, live = t.rows % kSliceK;
+                slice += slices;
+                if (live == 0) continue;
+                const int n = (min(kTileN, p.N - t.n * kTileN) + 31) & ~31;
+                const uint32_t s = (slice - 1) % kStages;
+                ok = warp_wait(bar(&bars.tail[s]), tails >> s & 1u, gave_up);
+                if (!ok) break;
+                tails ^= 1u << s;
+                clear_rows(ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, live);
+                if (lane == 0) cluster_arrive(first_cta(&bars.peer_tail[s]));
+            }
+        }
     } else {
         const int quarter = warp & 3;                    // the TMEM lanes this warp may read
+        float *turn = turns + (warp - 2) * (kTurnBytes / 4);
         uint32_t acc = 0;
-        for (int64_t i = blockIdx.x; ok && walk.find(p, mt, i, &t); i += gridDim.x) {
+        Epilogue<T, MODE> ep;
+        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
             const int n = min(kTileN, N - t.n * kTileN);
-            // this lane's output index along m
-            const int in = quarter * 32 + lane;
-            const int m = t.m * kFeat + (MODE == kGated ? (in >> 4) * 8 + (in & 7) : in);
-            const bool live = m < p.M;
-            float b0 = 0.f, b1 = 0.f;
-            if ((MODE == kForward || MODE == kGated) && p.bias && live) {
-                const T *bias = static_cast<const T *>(p.bias) + (int64_t)t.g * (MODE == kGated ? 2 * p.M : p.M);
-                b0 = f32(bias[m]);
-                if (MODE == kGated) b1 = f32(bias[p.M + m]);
+            ep.start(p, t, quarter, rank, n);
+            float bias = 0.f;
+            if ((MODE == kForward || MODE == kGated) && p.bias) {
+                const int in = quarter * 32 + lane;      // this lane's row of the accumulator
+                const int m = (t.m * 2 + (int)rank) * (MODE == kGated ? 64 : 128) +
+                              (MODE == kGated ? (in >> 4) * 8 + (in & 7) : in);
+                const T *b = static_cast<const T *>(p.bias) + (int64_t)t.g * (MODE == kGated ? 2 * p.M : p.M);
+                if (m < p.M) bias = f32(b[MODE == kGated && (in & 8) ? p.M + m : m]);
             }
             if (K > 0) {
                 ok = warp_wait(bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, gave_up);
@@ -376,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < n; c += 32) {
                 float v[32];
                 if (K > 0) {
-                    __syncwarp();
                     tmem_load32(d + c, v);
                 } else {
 #pragma unroll
@@ -385,15 +497,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (K > 0 && c + 32 >= n) {              // the accumulator may be filled again
                     tcgen_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(&bars.acc_empty[acc & 1u]));
+                    if (lane == 0) cluster_arrive(first_cta(&bars.acc_empty[acc & 1u]));
                 }
-                store_columns<T, MODE>(p, t, v, c, n - c, m, live, b0, b1);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += bias;
+                ep.columns(p, turn, v, c);
             }
             if (K > 0) ++acc;
         }
     }
+    __syncwarp();
     tcgen_before_sync();
-    __syncthreads();
+    cluster_sync();              // neither CTA's memory is read or signalled any more
     tcgen_after_sync();
     if (warp == 1) tmem_free(tmem, 512);
     if (threadIdx.x == 0 && bars.gave_up && p.error) atomicOr(p.error, EP_DEVERR_TIMEOUT);
@@ -585,12 +700,13 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap
         configured[dev].store(true, std::memory_order_release);
     }
     // tiles at most: every group's last tile may be a part
-    const int64_t mt = (p.M + (MODE == kGated ? 63 : 127)) / (MODE == kGated ? 64 : 128);
+    constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;
+    const int64_t mt = (p.M + kFeat - 1) / kFeat;
     const int64_t G = (int64_t)p.gr.R * p.gr.per;
     const int64_t nt = p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / kTileN + G : G * ((p.N + kTileN - 1) / kTileN);
-    const int sms = sm_count();
-    if (sms < 1) return cudaErrorInvalidDevice;
-    const int64_t grid = mt * nt < sms ? mt * nt : sms;
+    const int pairs = sm_count() / 2;
+    if (pairs < 1) return cudaErrorInvalidDevice;
+    const int64_t grid = 2 * (mt * nt < pairs ? mt * nt : pairs);
     product_kernel<T, MODE><<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a, b, b16, p);
     return cudaGetLastError();
 }
