@@ -84,7 +84,8 @@ template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; }
 // one group's range and the running number of tiles.  Every lane of the warp
 // gets the same answer.
 struct Tile {
-    int g, seg, first, rows, m, n;
+    int g, seg, first, rows, m;
+    int n0, n;             // columns: first and number
 };
 struct Walker {
     int lane, g0;
@@ -128,7 +129,13 @@ struct Walker {
         t->first = __shfl_sync(0xffffffffu, first, l);
         t->rows = __shfl_sync(0xffffffffu, rows, l);
         t->m = in % mt;
-        t->n = in / mt;
+        // equal parts of N instead of full tiles and a rest: a narrow rest would
+        // load as much of the other operand for less work
+        const int N = p.N < 0 ? t->rows : p.N;
+        const int parts = (N + kTileN - 1) / kTileN;
+        const int width = ((N + parts - 1) / parts + 31) & ~31;
+        t->n0 = in / mt * width;
+        t->n = min(width, N - t->n0);
         return true;
     }
 };
@@ -211,12 +218,12 @@ template <typename T, Mode MODE> struct Epilogue {
     bool pre_live;
     uint4 next[kTasks];          // residual of the columns to come
 
-    __device__ void start(const ProductParams &p, const Tile &t, int quarter, uint32_t rank, int n_) {
+    __device__ void start(const ProductParams &p, const Tile &t, int quarter, uint32_t rank) {
         lane = threadIdx.x & 31;
-        n = n_;
+        n = t.n;
         M = p.M;
         const int64_t own = MODE == kGradW ? t.g : t.seg;
-        const int64_t row0 = (MODE == kGradW ? 0 : t.first) + t.n * (int64_t)kTileN;
+        const int64_t row0 = (MODE == kGradW ? 0 : t.first) + (int64_t)t.n0;
         // outputs of the quarter: 32 m, or 16 features (gated)
         const int m0 = (t.m * 2 + (int)rank) * (MODE == kGated ? 64 : 128) + quarter * kPer * 8;
         const int m = m0 + (lane % kPer) * 8;
@@ -294,7 +301,7 @@ template <typename T, Mode MODE> struct Epilogue {
 template <typename T, Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_b16, const ProductParams p) {
+                   const __grid_constant__ CUtensorMap map_b32, const ProductParams p) {
     constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
     constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
     extern __shared__ unsigned char smem_raw[];
@@ -340,27 +347,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     if (warp == 0) {
-        uint32_t issued = 0, tails = 0, landed = 0;       // by stage: a tail was loaded, its barrier's phase
+        uint32_t issued = 0, s = 0, phase = 0;            // slices, the next one's stage and its round's parity
+        uint32_t tails = 0, landed = 0;                   // by stage: a tail was loaded, its barrier's phase
+        const uint32_t full0 = first_cta(&bars.full[0]);
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
-            const int half = ((min(kTileN, N - t.n * kTileN) + 31) & ~31) / 2;   // this CTA's n
-            const bool narrow = !kBmn && half <= 48;      // 16-row boxes: at most 3 loads either way
-            const int boxes = narrow ? half / 16 : (half + 63) / 64;
-            const uint32_t box = narrow ? kChunkBytes / 4 : kChunkBytes;
-            const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n * kTileN + (int)rank * half;
+            const int K = p.K < 0 ? t.rows : p.K;
+            const int half = ((t.n + 31) & ~31) / 2;      // this CTA's n
+            // a copy costs the loading thread about as much whatever its size:
+            // one of 128 rows, or up to three of 32
+            const bool narrow = !kBmn && half <= 96;
+            const int boxes = kBmn ? (half + 63) / 64 : narrow ? (half + 31) / 32 : 1;
+            const uint32_t box = kBmn ? kChunkBytes : narrow ? kChunkBytes / 2 : kBytesB;
+            const uint32_t bytes = kBytesA + boxes * box;
+            const CUtensorMap *mb = narrow ? &map_b32 : &map_b;
+            const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n0 + (int)rank * half;
             if (lane == 0) {
                 for (int k = 0; k < K; k += kSliceK) {
-                    const uint32_t s = issued % kStages, round = issued / kStages;
-                    if (!tensor_wait(bar(&bars.empty[s]), (round & 1u) ^ 1u, gave_up)) {
+                    if (!tensor_wait(bar(&bars.empty[s]), phase ^ 1u, gave_up)) {
                         ok = false;
                         break;
                     }
                     // the second CTA clears the rows past a group's end before
                     // it tells the first: that slice lands on its own barrier
                     const bool last = MODE == kGradW && K - k < kSliceK, tail = last && rank == 1;
-                    const uint32_t full = tail ? in_cta(bar(&bars.tail[s]), 1) : first_cta(&bars.full[s]);
+                    const uint32_t full = tail ? in_cta(bar(&bars.tail[s]), 1) : full0 + s * 8;
                     const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
-                    const uint32_t bytes = kBytesA + boxes * box;
                     if (rank == 0) mbar_expect(bar(&bars.full[s]), last ? bytes : 2 * bytes);
                     if (tail) {
                         mbar_expect(bar(&bars.tail[s]), bytes);
@@ -379,12 +390,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     for (int j = 0; j < boxes; ++j) {
                         if constexpr (kBmn)
-                            tma_load3(b + j * kChunkBytes, &map_b, full, n0 + j * 64, t.first + k, t.seg);
+                            tma_load3(b + j * kChunkBytes, mb, full, n0 + j * 64, t.first + k, t.seg);
                         else
-                            tma_load3(b + j * box, narrow ? &map_b16 : &map_b, full, k,
-                                      t.first + n0 + j * (narrow ? 16 : 64), t.seg);
+                            tma_load3(b + j * box, mb, full, k, t.first + n0 + j * 32, t.seg);
                     }
                     ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -396,50 +410,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int ignore = 0;
             volatile int *flag = ok ? gave_up : &ignore;
             for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
-                const uint32_t s = j % kStages, phase = (j / kStages) & 1u;
-                if (!ok && rank == 0) tensor_wait(bar(&bars.full[s]), phase, flag);
-                if (!ok && rank == 1 && (tails >> s & 1u)) tensor_wait(bar(&bars.tail[s]), landed >> s & 1u, flag);
-                tensor_wait(bar(&bars.empty[s]), phase, flag);
+                const uint32_t q = j % kStages, round = (j / kStages) & 1u;
+                if (!ok && rank == 0) tensor_wait(bar(&bars.full[q]), round, flag);
+                if (!ok && rank == 1 && (tails >> q & 1u)) tensor_wait(bar(&bars.tail[q]), landed >> q & 1u, flag);
+                tensor_wait(bar(&bars.empty[q]), round, flag);
             }
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
-        uint32_t slice = 0, acc = 0, tails = 0;
+        // descriptors: 16 k on is 32 bytes (K-major) or 16 rows (MN-major) on
+        constexpr uint64_t kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;
+        const uint64_t a0 = smem_desc(ring, kAmn ? kChunkBytes : 16, 1024);
+        const uint64_t b0 = smem_desc(ring + kBytesA, kBmn ? kChunkBytes : 16, 1024);
+        uint32_t s = 0, phase = 0, acc = 0, tails = 0;
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
-            const int n = (min(kTileN, N - t.n * kTileN) + 31) & ~31;
+            const int K = p.K < 0 ? t.rows : p.K;
+            const int n = (t.n + 31) & ~31;
             if (K == 0) continue;
             const uint32_t idesc = kIdesc | idesc_n(n);
             const uint32_t d = tmem + (acc & 1u) * 256;
             ok = warp_wait<true>(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
             tcgen_after_sync();
-            for (int k = 0; ok && k < K; k += kSliceK, ++slice) {
-                const uint32_t s = slice % kStages;
-                ok = warp_wait(bar(&bars.full[s]), (slice / kStages) & 1u, gave_up);
-                if (!ok) break;
-                tcgen_after_sync();
-                const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
-                if (MODE == kGradW && K - k < kSliceK) {
-                    clear_rows(a, 2 + (n / 2 + 63) / 64, K - k);
-                    ok = warp_wait<true>(bar(&bars.peer_tail[s]), tails >> s & 1u, gave_up);
-                    if (!ok) break;
-                    tails ^= 1u << s;
-                }
-                if (lane == 0) {
+            // One thread issues everything: the pair's next instructions have
+            // to be queued before the last ones end, so its loop is kept short.
+            int left = ok ? (MODE == kGradW ? K / kSliceK : (K + kSliceK - 1) / kSliceK) : 0;
+            bool add = false;
+            if (lane == 0) {
+                for (; left > 0; --left) {
+                    if (!tensor_wait(bar(&bars.full[s]), phase, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < kSliceK / 16; ++j) {
-                        const uint64_t da = kAmn ? smem_desc(a + j * 2048, kChunkBytes, 1024)
-                                                 : smem_desc(a + j * 32, 16, 1024);
-                        const uint64_t db = kBmn ? smem_desc(b + j * 2048, kChunkBytes, 1024)
-                                                 : smem_desc(b + j * 32, 16, 1024);
-                        mma_f16(d, da, db, idesc, k > 0 || j > 0);
+                        mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, add);
+                        add = true;
                     }
                     mma_commit_pair(bar(&bars.empty[s]));
-                    if (k + kSliceK >= K) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
-                __syncwarp();
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (MODE == kGradW && ok && K % kSliceK) {
+                s = __shfl_sync(0xffffffffu, s, 0);
+                phase = __shfl_sync(0xffffffffu, phase, 0);
+                ok = warp_wait(bar(&bars.full[s]), phase, gave_up);
+                if (ok) {
+                    clear_rows(ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, K % kSliceK);
+                    ok = warp_wait<true>(bar(&bars.peer_tail[s]), tails >> s & 1u, gave_up);
+                    tails ^= 1u << s;
+                }
+                if (ok && lane == 0) {
+                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+#pragma unroll
+                    for (int j = 0; j < kSliceK / 16; ++j)
+                        mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, K > kSliceK || j > 0);
+                    mma_commit_pair(bar(&bars.empty[s]));
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok && lane == 0) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
             ++acc;
         }
         if (!ok) {                                       // let the matrix unit finish
@@ -454,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int slices = (t.rows + kSliceK - 1) / kSliceK, live = t.rows % kSliceK;
                 slice += slices;
                 if (live == 0) continue;
-                const int n = (min(kTileN, p.N - t.n * kTileN) + 31) & ~31;
+                const int n = (t.n + 31) & ~31;
                 const uint32_t s = (slice - 1) % kStages;
                 ok = warp_wait(bar(&bars.tail[s]), tails >> s & 1u, gave_up);
                 if (!ok) break;
@@ -469,9 +507,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t acc = 0;
         Epilogue<T, MODE> ep;
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int N = p.N < 0 ? t.rows : p.N, K = p.K < 0 ? t.rows : p.K;
-            const int n = min(kTileN, N - t.n * kTileN);
-            ep.start(p, t, quarter, rank, n);
+            const int K = p.K < 0 ? t.rows : p.K, n = t.n;
+            ep.start(p, t, quarter, rank);
             float bias = 0.f;
             if ((MODE == kForward || MODE == kGated) && p.bias) {
                 const int in = quarter * 32 + lane;      // this lane's row of the accumulator
@@ -685,7 +722,7 @@ int sm_count() {
 }
 
 template <typename T, Mode MODE>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b16, const ProductParams &p,
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b32, const ProductParams &p,
                    cudaStream_t st) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> configured[kMaxDevices];       // the attribute is per device
@@ -707,15 +744,15 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap
     const int pairs = sm_count() / 2;
     if (pairs < 1) return cudaErrorInvalidDevice;
     const int64_t grid = 2 * (mt * nt < pairs ? mt * nt : pairs);
-    product_kernel<T, MODE><<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a, b, b16, p);
+    product_kernel<T, MODE><<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a, b, b32, p);
     return cudaGetLastError();
 }
 
 template <Mode MODE>
-ep_status_t launch_product(int dtype, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b16,
+ep_status_t launch_product(int dtype, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b32,
                            const ProductParams &p, cudaStream_t st) {
-    const cudaError_t e = dtype == EP_DT_BF16 ? launch<__nv_bfloat16, MODE>(a, b, b16, p, st)
-                                              : launch<__half, MODE>(a, b, b16, p, st);
+    const cudaError_t e = dtype == EP_DT_BF16 ? launch<__nv_bfloat16, MODE>(a, b, b32, p, st)
+                                              : launch<__half, MODE>(a, b, b32, p, st);
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
@@ -753,15 +790,15 @@ ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
     p.error = d_error;
     const bool gated = d->activation == EP_ACT_SWIGLU;
     const int64_t G = (int64_t)d->ranks * d->groups;
-    CUtensorMap a, b, b16;
+    CUtensorMap a, b, b32;
     if (!(gated ? encode_gated(&a, d->dtype, d->weight, p.K, p.M, G)
                 : encode_rows(&a, d->dtype, d->weight, p.K, p.M, G, kTileM)) ||
-        !encode_rows(&b, d->dtype, d->x, p.K, d->rows, d->ranks, 64) ||
-        !encode_rows(&b16, d->dtype, d->x, p.K, d->rows, d->ranks, 16))
+        !encode_rows(&b, d->dtype, d->x, p.K, d->rows, d->ranks, kTileN / 2) ||
+        !encode_rows(&b32, d->dtype, d->x, p.K, d->rows, d->ranks, 32))
         return EP_ERR_GPU_OP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return gated ? launch_product<kGated>(d->dtype, a, b, b16, p, st)
-                 : launch_product<kForward>(d->dtype, a, b, b16, p, st);
+    return gated ? launch_product<kGated>(d->dtype, a, b, b32, p, st)
+                 : launch_product<kForward>(d->dtype, a, b, b32, p, st);
 }
 
 ep_status_t ep_expert_product_workspace(const ep_product_desc_t *d, size_t *bytes) {
@@ -797,7 +834,7 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         with_type(d->dtype, [&](auto type) { act_grad_kernel<decltype(type)><<<grid, 256, 0, st>>>(a); });
     }
     const int64_t G = (int64_t)d->ranks * d->groups;
-    CUtensorMap a, b, b16;
+    CUtensorMap a, b, b32;
     if (grad_x->ptr && d->rows > 0) {
         ProductParams p = {};
         p.gr = gr;
@@ -807,10 +844,10 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         p.out = *grad_x;
         p.error = d_error;
         if (!encode_rows(&a, d->dtype, d->weight, d->in_features, wide, G, 64) ||
-            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, 64) ||
-            !encode_rows(&b16, d->dtype, dd, wide, d->rows, d->ranks, 16))
+            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
+            !encode_rows(&b32, d->dtype, dd, wide, d->rows, d->ranks, 32))
             return EP_ERR_GPU_OP;
-        const ep_status_t s = launch_product<kGradX>(d->dtype, a, b, b16, p, st);
+        const ep_status_t s = launch_product<kGradX>(d->dtype, a, b, b32, p, st);
         if (s != EP_SUCCESS) return s;
     }
     if (d_grad_w && d->rows == 0)

@@ -13,26 +13,30 @@ namespace ep {
 
 constexpr uint64_t kTensorWaitNs = 1000000000ull;
 
-// Waits for `parity` of an mbarrier, for a second at most.  `gave_up` is the
-// CTA's shared flag: set by the wait that runs out, and seen by the others.
 // PEER: the barrier is signalled by ordinary instructions of the other CTA
 // of the pair (copies and matrix instructions need no cluster-wide order).
 template <bool PEER = false>
-__device__ __forceinline__ bool tensor_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+__device__ __forceinline__ bool tensor_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (PEER)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Waits for `parity` of an mbarrier, for a second at most.  `gave_up` is the
+// CTA's shared flag: set by the wait that runs out, and seen by the others.
+template <bool PEER>
+__device__ __noinline__ bool tensor_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     uint64_t t0 = 0;
     for (uint32_t it = 0; it < (1u << 26); ++it) {
-        uint32_t ok;
-        if constexpr (PEER)
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        else
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-        if (ok) return true;
+        if (tensor_try<PEER>(bar, parity)) return true;
         if ((it & 63) == 63) {
             if (*gave_up) return false;
             const uint64_t now = globaltimer_ns();
@@ -42,6 +46,10 @@ __device__ __forceinline__ bool tensor_wait(uint32_t bar, uint32_t parity, volat
     }
     *gave_up = 1;
     return false;
+}
+template <bool PEER = false>
+__device__ __forceinline__ bool tensor_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    return tensor_try<PEER>(bar, parity) || tensor_wait_long<PEER>(bar, parity, gave_up);
 }
 // The same by a whole warp, with one answer for all its lanes.
 template <bool PEER = false>
