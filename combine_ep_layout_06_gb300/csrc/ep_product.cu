@@ -29,14 +29,11 @@
 namespace ep {
 namespace {
 
-constexpr int kTileM = 128, kTileN = 256, kSliceK = 64;     // m of one CTA, n of the pair
-constexpr int kStages = 6;
-constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN / 2 * kSliceK * 2;
-constexpr int kStageBytes = kBytesA + kBytesB;
-constexpr int kChunkBytes = 64 * kSliceK * 2;      // 64 rows (or 64 columns) of one slice
+constexpr int kTileM = 128, kTileN = 256;          // m of one CTA, n of the pair
+constexpr int kRingBytes = 6 * 32768, kMaxStages = 6;
 constexpr int kTurnStride = 36;                    // floats per row of a warp's transposing buffer
 constexpr int kTurnBytes = 32 * kTurnStride * 4;
-constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + 4 * kTurnBytes + 1024;
+constexpr size_t kSmemBytes = (size_t)kRingBytes + 4 * kTurnBytes + 1024;
 constexpr int kThreads = 192;
 
 struct Groups {
@@ -59,6 +56,17 @@ __device__ __forceinline__ void group_range(const Groups &gr, int g, int *first,
 
 enum Mode { kForward, kGated, kGradX, kGradW };
 
+// Slices of the ring.  One copy brings 64 elements (the swizzle's 128 bytes)
+// by up to 256 rows.  Rows of k (grad_w) come 128 at a time, which halves its
+// copies; elsewhere k runs along the 64 elements.
+template <Mode MODE> struct Ring {
+    static constexpr int kSliceK = MODE == kGradW ? 128 : 64;
+    static constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN / 2 * kSliceK * 2;
+    static constexpr int kStageBytes = kBytesA + kBytesB;
+    static constexpr int kStages = kRingBytes / kStageBytes;
+    static constexpr int kChunkBytes = 64 * kSliceK * 2;      // 64 m (or n) of an MN-major slice
+};
+
 struct ProductParams {
     Groups gr;
     int M, N, K;           // N or K < 0: the group's number of rows
@@ -75,7 +83,9 @@ template <typename T> __device__ __forceinline__ T rounded(float v);
 template <> __device__ __forceinline__ __nv_bfloat16 rounded(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rounded(float v) { return __float2half_rn(v); }
 
-__device__ __forceinline__ float sigmoidf(float v) { return 1.0f / (1.0f + expf(-v)); }
+// Within a few units of the last place of fp32 (more of 2^-24 |v|): far below
+// the 16-bit rounding of every result it goes into.
+__device__ __forceinline__ float sigmoidf(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 template <typename T> struct IsBf16 { static constexpr bool value = false; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
@@ -144,6 +154,7 @@ struct Walker {
 // the group's end: zero, whatever they held.  (The 128-byte swizzle moves data
 // within a k row only.)  By a whole warp; the matrix unit sees it afterwards.
 __device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live) {
+    constexpr int kSliceK = Ring<kGradW>::kSliceK, kChunkBytes = Ring<kGradW>::kChunkBytes;
     const int per = (kSliceK - live) * 8;
     for (int q = threadIdx.x & 31; q < chunks * per; q += 32) {
         const uint32_t at = slice + (q / per) * kChunkBytes + live * 128 + (q % per) * 16;
@@ -154,7 +165,7 @@ __device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live)
 }
 
 struct __align__(8) Barriers {
-    uint64_t full[kStages], empty[kStages], tail[kStages], peer_tail[kStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
 };
@@ -303,11 +314,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_b32, const ProductParams p) {
     constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
+    constexpr int kSliceK = Ring<MODE>::kSliceK, kStages = Ring<MODE>::kStages;
+    constexpr int kBytesA = Ring<MODE>::kBytesA, kBytesB = Ring<MODE>::kBytesB;
+    constexpr int kStageBytes = Ring<MODE>::kStageBytes, kChunkBytes = Ring<MODE>::kChunkBytes;
     constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bars;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    float *turns = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + kStages * kStageBytes);
+    float *turns = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + kRingBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -357,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // one of 128 rows, or up to three of 32
             const bool narrow = !kBmn && half <= 96;
             const int boxes = kBmn ? (half + 63) / 64 : narrow ? (half + 31) / 32 : 1;
-            const uint32_t box = kBmn ? kChunkBytes : narrow ? kChunkBytes / 2 : kBytesB;
+            const uint32_t box = kBmn ? kChunkBytes : narrow ? 32 * kSliceK * 2 : kBytesB;
             const uint32_t bytes = kBytesA + boxes * box;
             const CUtensorMap *mb = narrow ? &map_b32 : &map_b;
             const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n0 + (int)rank * half;
@@ -552,61 +566,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // d = grad * act'(pre) over every group's rows, rounded once for the
-// products, and its column sums before that rounding.  One block takes 256
-// features of one group, thread t feature t, rows in order.
+// products, and its column sums before that rounding.  Bound by memory: grad
+// and pre are read once, d is written once.  A block takes 256 features and
+// one of `splits` parts of a group's rows; a lane holds 8 features (16 bytes),
+// the 8 warps take rows in turn.  Column sums are joined in a fixed order:
+// warps in shared memory, parts by sum_parts_kernel.
 struct ActGradParams {
     Groups gr;
-    int N, act;
+    int N, act, splits;
     ep_rows_t grad, pre, d;
-    void *grad_bias;        // [G][wide] or null
+    float *part;            // [splits][G][wide] column sums, or null
     bool write;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
-    const int g = blockIdx.y, seg = g / p.gr.per;
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= p.N) return;
+constexpr int kActWarps = 8, kActCols = 256, kActRows = 4;
+
+__device__ __forceinline__ float act_slope(int act, float v) {
+    if (act == EP_ACT_RELU) return v > 0.f ? 1.f : 0.f;
+    if (act == EP_ACT_GELU)      // Phi(v) + v phi(v), phi(v) = exp(-v^2/2) / sqrt(2 pi)
+        return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+    if (act == EP_ACT_SILU) {
+        const float s = sigmoidf(v);
+        return s * (1.0f + v * (1.0f - s));
+    }
+    return 1.f;
+}
+
+template <typename T> __device__ __forceinline__ void unpack8(float *v, const uint4 &r) {
+    const T *e = reinterpret_cast<const T *>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f32(e[i]);
+}
+
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradParams p) {
+    __shared__ float sums[kActWarps][GATED ? 2 : 1][kActCols + 4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = blockIdx.y, seg = g / p.gr.per, split = blockIdx.z;
+    const int c = blockIdx.x * kActCols + lane * 8;
+    const bool live = c < p.N;
     int first, rows;
     group_range(p.gr, g, &first, &rows);
-    const bool gated = p.act == EP_ACT_SWIGLU;
-    float s0 = 0.f, s1 = 0.f;
-    for (int i = first; i < first + rows; ++i) {
-        const float gy = f32(static_cast<const T *>(p.grad.ptr)[seg * p.grad.rank_stride + i * p.grad.row_stride + c]);
-        float d0 = gy, d1 = 0.f;
-        if (p.act != EP_ACT_NONE) {
-            const T *pre = static_cast<const T *>(p.pre.ptr) + seg * p.pre.rank_stride + i * p.pre.row_stride;
-            const float v = f32(pre[c]);
-            if (p.act == EP_ACT_RELU) {
-                d0 = v > 0.f ? gy : 0.f;
-            } else if (p.act == EP_ACT_GELU) {
-                // Phi(v) + v phi(v), phi(v) = exp(-v^2/2) / sqrt(2 pi)
-                d0 = gy * (0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
-                           v * expf(-0.5f * v * v) * 0.39894228040143268f);
-            } else {
-                const float s = sigmoidf(v), slope = s * (1.0f + v * (1.0f - s));
-                if (gated) {
-                    const float up = f32(pre[p.N + c]);
-                    d0 = gy * up * slope;
-                    d1 = gy * v * s;
-                } else {
-                    d0 = gy * slope;
+    const int per = (rows + p.splits - 1) / p.splits;
+    const int r1 = first + min(rows, (split + 1) * per);
+    const T *grad = static_cast<const T *>(p.grad.ptr) + seg * p.grad.rank_stride + c;
+    const T *pre = static_cast<const T *>(p.pre.ptr) + seg * p.pre.rank_stride + c;
+    T *d = static_cast<T *>(p.d.ptr) + seg * p.d.rank_stride + c;
+    float s0[8] = {}, s1[8] = {};
+    const bool reads_pre = p.act != EP_ACT_NONE;
+    for (int64_t r = first + split * per + warp; live && r < r1; r += kActWarps * kActRows) {
+        uint4 gv[kActRows], v0[kActRows], v1[kActRows];
+#pragma unroll
+        for (int u = 0; u < kActRows; ++u) {
+            const int64_t i = r + u * kActWarps;
+            if (i >= r1) continue;
+            gv[u] = ld_stream16(grad + i * p.grad.row_stride);
+            if (reads_pre) v0[u] = ld_stream16(pre + i * p.pre.row_stride);
+            if (GATED) v1[u] = ld_stream16(pre + i * p.pre.row_stride + p.N);
+        }
+#pragma unroll
+        for (int u = 0; u < kActRows; ++u) {
+            const int64_t i = r + u * kActWarps;
+            if (i >= r1) continue;
+            float y[8], v[8], d0[8], d1[8];
+            unpack8<T>(y, gv[u]);
+            if (GATED) {
+                float up[8];
+                unpack8<T>(v, v0[u]);
+                unpack8<T>(up, v1[u]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float s = sigmoidf(v[j]);
+                    d0[j] = y[j] * up[j] * (s * (1.0f + v[j] * (1.0f - s)));
+                    d1[j] = y[j] * v[j] * s;
+                    s1[j] += d1[j];
                 }
+            } else if (reads_pre) {
+                unpack8<T>(v, v0[u]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d0[j] = y[j] * act_slope(p.act, v[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d0[j] = y[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s0[j] += d0[j];
+            if (p.write) {
+                store8<T>(d + i * p.d.row_stride, d0);
+                if (GATED) store8<T>(d + i * p.d.row_stride + p.N, d1);
             }
         }
-        if (p.write) {
-            T *d = static_cast<T *>(p.d.ptr) + seg * p.d.rank_stride + i * p.d.row_stride;
-            d[c] = rounded<T>(d0);
-            if (gated) d[p.N + c] = rounded<T>(d1);
-        }
-        s0 += d0;
-        s1 += d1;
     }
-    if (p.grad_bias) {
-        T *gb = static_cast<T *>(p.grad_bias) + (int64_t)g * (gated ? 2 * p.N : p.N);
-        gb[c] = rounded<T>(s0);
-        if (gated) gb[p.N + c] = rounded<T>(s1);
+    if (!p.part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sums[warp][0][lane * 8 + j] = s0[j];
+        if (GATED) sums[warp][GATED ? 1 : 0][lane * 8 + j] = s1[j];
     }
+    __syncthreads();
+    const int64_t G = (int64_t)p.gr.R * p.gr.per, wide = GATED ? 2 * (int64_t)p.N : p.N;
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        const int col = blockIdx.x * kActCols + threadIdx.x;
+        float s = 0.f;
+        for (int w = 0; w < kActWarps; ++w) s += sums[w][h][threadIdx.x];
+        if (col < p.N) p.part[(split * G + g) * wide + h * (int64_t)p.N + col] = s;
+    }
+}
+
+// grad_bias = the parts' sums, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int splits, int64_t n, T *out) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int k = 0; k < splits; ++k) s += part[k * n + i];
+    out[i] = rounded<T>(s);
+}
+
+// Parts of a group's rows in act_grad_kernel: about 64 rows each, going by
+// the average group, at most 32.
+int act_splits(const ep_product_desc_t &d) {
+    const int64_t average = d.rows / d.groups;
+    const int64_t parts = (average + 63) / 64;
+    return (int)(parts < 1 ? 1 : parts > 32 ? 32 : parts);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -692,7 +774,7 @@ bool encode_rows(CUtensorMap *map, int dtype, const ep_rows_t &r, int64_t width,
                  uint32_t box_rows) {
     const uint64_t dims[3] = {(uint64_t)width, (uint64_t)rows, (uint64_t)outer};
     const int64_t strides[3] = {1, r.row_stride, outer > 1 ? r.rank_stride : r.row_stride};
-    const uint32_t box[3] = {kSliceK, box_rows, 1};
+    const uint32_t box[3] = {64, box_rows, 1};
     return encode(map, dtype, r.ptr, 3, dims, strides, box);
 }
 
@@ -702,7 +784,7 @@ bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, in
     const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)G};
     const int64_t strides[5] = {1, w.row_stride, N * w.row_stride, 8 * w.row_stride,
                                 G > 1 ? w.rank_stride : w.row_stride};
-    const uint32_t box[5] = {kSliceK, 8, 2, 8, 1};
+    const uint32_t box[5] = {64, 8, 2, 8, 1};
     return encode(map, dtype, w.ptr, 5, dims, strides, box);
 }
 
@@ -756,7 +838,15 @@ ep_status_t launch_product(int dtype, const CUtensorMap &a, const CUtensorMap &b
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
+// The gradient's workspace: d in the tensors' type (not needed where act' is
+// 1), then the parts of the bias gradient.
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+size_t rounded_d_bytes(const ep_product_desc_t &d) {
+    return d.activation == EP_ACT_NONE ? 0 : align256((size_t)d.ranks * d.rows * (size_t)wide_of(d) * 2);
+}
+size_t part_bytes(const ep_product_desc_t &d) {
+    return align256((size_t)act_splits(d) * d.ranks * d.groups * (size_t)wide_of(d) * 4);
+}
 
 }  // namespace
 }  // namespace ep
@@ -803,8 +893,7 @@ ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
 
 ep_status_t ep_expert_product_workspace(const ep_product_desc_t *d, size_t *bytes) {
     if (!valid(d) || !bytes) return EP_ERR_INVALID_ARGS;
-    *bytes = d->activation == EP_ACT_NONE
-                 ? 0 : align256((size_t)d->ranks * d->rows * (size_t)wide_of(*d) * 2);
+    *bytes = rounded_d_bytes(*d) + part_bytes(*d);
     return EP_SUCCESS;
 }
 
@@ -829,9 +918,20 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
     const Groups gr = groups_of(*d);
     const ep_rows_t dd = act ? ep_rows_t{d_workspace, d->rows * wide, wide} : *grad;
     if (act || d_grad_bias) {
-        ActGradParams a = {gr, d->out_features, d->activation, *grad, *pre, dd, d_grad_bias, act};
-        const dim3 grid((d->out_features + 255) / 256, gr.R * gr.per);
-        with_type(d->dtype, [&](auto type) { act_grad_kernel<decltype(type)><<<grid, 256, 0, st>>>(a); });
+        float *part = d_grad_bias ? reinterpret_cast<float *>(static_cast<char *>(d_workspace) + rounded_d_bytes(*d))
+                                  : nullptr;
+        const int splits = act_splits(*d), G = gr.R * gr.per;
+        const ActGradParams q = {gr, d->out_features, d->activation, splits, *grad, *pre, dd, part, act};
+        const dim3 grid((d->out_features + kActCols - 1) / kActCols, G, splits);
+        with_type(d->dtype, [&](auto type) {
+            using T = decltype(type);
+            if (d->activation == EP_ACT_SWIGLU) act_grad_kernel<T, true><<<grid, kActWarps * 32, 0, st>>>(q);
+            else act_grad_kernel<T, false><<<grid, kActWarps * 32, 0, st>>>(q);
+            const int64_t n = G * wide;
+            if (part)
+                sum_parts_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, splits, n,
+                                                                                 static_cast<T *>(d_grad_bias));
+        });
     }
     const int64_t G = (int64_t)d->ranks * d->groups;
     CUtensorMap a, b, b32;
@@ -861,8 +961,9 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         p.K = -1;
         p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
         p.error = d_error;
-        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, 64) ||
-            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, 64))
+        constexpr int kRows = Ring<kGradW>::kSliceK;
+        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kRows) ||
+            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kRows))
             return EP_ERR_GPU_OP;
         const ep_status_t s = launch_product<kGradW>(d->dtype, a, b, b, p, st);
         if (s != EP_SUCCESS) return s;
