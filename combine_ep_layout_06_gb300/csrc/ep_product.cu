@@ -14,7 +14,7 @@
 // instruction (n in steps of 32) and not a padded tile.  A CTA loads its own
 // 128 m and half of n, so every byte of n serves both.  In each CTA warp 0
 // loads 64-deep slices by TMA into a ring in shared memory; warp 1 of the
-// first CTA issues the pair's matrix instructions; warps 2..5 turn a finished
+// first CTA issues the pair's matrix instructions; warps 2..9 turn a finished
 // accumulator into outputs while the next one fills: two accumulators of 256
 // columns take all of the SM's tensor memory.
 #include <cuda.h>
@@ -31,10 +31,10 @@ namespace {
 
 constexpr int kTileM = 128, kTileN = 256;          // m of one CTA, n of the pair
 constexpr int kRingBytes = 6 * 32768, kMaxStages = 6;
-constexpr int kTurnStride = 36;                    // floats per row of a warp's transposing buffer
-constexpr int kTurnBytes = 32 * kTurnStride * 4;
-constexpr size_t kSmemBytes = (size_t)kRingBytes + 4 * kTurnBytes + 1024;
-constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 8;
+constexpr int kTurnBytes = 32 * 32 * 4;            // a warp's transposing buffer
+constexpr size_t kSmemBytes = (size_t)kRingBytes + kEpilogueWarps * kTurnBytes + 1024;
+constexpr int kThreads = 64 + kEpilogueWarps * 32;
 
 struct Groups {
     const int32_t *count, *offset;
@@ -150,16 +150,17 @@ struct Walker {
     }
 };
 
-// Rows (k) from `live` on of `chunks` chunks of an MN-major slice are past
-// the group's end: zero, whatever they held.  (The 128-byte swizzle moves data
-// within a k row only.)  By a whole warp; the matrix unit sees it afterwards.
+// The last slice of a group's rows (k): the instructions that it needs take
+// 16 rows each, so rows from `live` to the next multiple of 16 are set to zero,
+// whatever they held, in all `chunks` chunks.  (The 128-byte swizzle moves
+// data within a k row only.)  By a whole warp; the matrix unit sees it
+// afterwards.
 __device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live) {
-    constexpr int kSliceK = Ring<kGradW>::kSliceK, kChunkBytes = Ring<kGradW>::kChunkBytes;
-    const int per = (kSliceK - live) * 8;
-    for (int q = threadIdx.x & 31; q < chunks * per; q += 32) {
-        const uint32_t at = slice + (q / per) * kChunkBytes + live * 128 + (q % per) * 16;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(at), "r"(0) : "memory");
-    }
+    const int lane = threadIdx.x & 31, end = (live + 15) & ~15;
+    for (int r = live + lane / 8; r < end; r += 4)
+        for (int c = 0; c < chunks; ++c)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                         :: "r"(slice + c * Ring<kGradW>::kChunkBytes + r * 128 + lane % 8 * 16), "r"(0) : "memory");
     fence_async_smem();
     __syncwarp();
 }
@@ -189,8 +190,15 @@ template <typename T> __device__ __forceinline__ void add8(float *v, const uint4
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += f32(e[i]);
 }
-__device__ __forceinline__ void read8(float *v, const float *s) {
-    const float4 a = reinterpret_cast<const float4 *>(s)[0], b = reinterpret_cast<const float4 *>(s)[1];
+// A warp's transposing buffer: row c (a column of the accumulator) of 32
+// floats, its 16-byte blocks in the order block ^ (c & 7), so that neither the
+// writes along a row nor the reads of blocks down the rows meet in a bank.
+__device__ __forceinline__ float *turn_at(float *turn, int c, int i) {
+    return turn + c * 32 + (((i >> 2) ^ (c & 7)) << 2) + (i & 3);
+}
+__device__ __forceinline__ void read8(float *v, float *turn, int c, int i) {
+    const float4 a = *reinterpret_cast<const float4 *>(turn_at(turn, c, i));
+    const float4 b = *reinterpret_cast<const float4 *>(turn_at(turn, c, i + 4));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -212,6 +220,10 @@ __device__ __forceinline__ void activate8(int act, float *v) {
     }
 }
 
+// A quarter of the accumulator's lanes belongs to two warps, which take turns
+// of 32 columns.
+constexpr int kColumnStep = 32 * (kEpilogueWarps / 4);
+
 // A warp's part of the epilogue.  The accumulator comes with one m per lane
 // and one n per register; a turn through shared memory gives each lane 8
 // neighbouring m of one n, so that residual, pre and out move 16 bytes at a
@@ -229,7 +241,7 @@ template <typename T, Mode MODE> struct Epilogue {
     bool pre_live;
     uint4 next[kTasks];          // residual of the columns to come
 
-    __device__ void start(const ProductParams &p, const Tile &t, int quarter, uint32_t rank) {
+    __device__ void start(const ProductParams &p, const Tile &t, int quarter, uint32_t rank, int c0) {
         lane = threadIdx.x & 31;
         n = t.n;
         M = p.M;
@@ -254,7 +266,7 @@ template <typename T, Mode MODE> struct Epilogue {
             pre = p.pre.ptr ? static_cast<T *>(p.pre.ptr) + own * p.pre.rank_stride +
                                   (row0 + lane / 4) * pre_stride + pm
                             : nullptr;
-            fetch(0);
+            fetch(c0);
         }
     }
     __device__ void fetch(int c0) {
@@ -271,16 +283,16 @@ template <typename T, Mode MODE> struct Epilogue {
         uint4 r[kTasks];
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) r[i] = next[i];
-        if (c0 + 32 < n) fetch(c0 + 32);
+        if (c0 + kColumnStep < n) fetch(c0 + kColumnStep);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) turn[c * kTurnStride + lane] = v[c];
+        for (int c = 0; c < 32; ++c) *turn_at(turn, c, lane) = v[c];
         __syncwarp();
         if (kActs && MODE == kGated && pre) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = i * 8 + lane / 4;
                 float f[8];
-                read8(f, turn + c * kTurnStride + (lane & 3) * 8);
+                read8(f, turn, c, (lane & 3) * 8);
                 if (pre_live && c0 + c < n) store8<T>(pre + (c0 + i * 8) * pre_stride, f);
             }
         }
@@ -291,12 +303,12 @@ template <typename T, Mode MODE> struct Epilogue {
             float f[8];
             if constexpr (MODE == kGated) {
                 float up[8];
-                read8(f, turn + c * kTurnStride + (lane & 1) * 16);
-                read8(up, turn + c * kTurnStride + (lane & 1) * 16 + 8);
+                read8(f, turn, c, (lane & 1) * 16);
+                read8(up, turn, c, (lane & 1) * 16 + 8);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = f[j] * sigmoidf(f[j]) * up[j];
             } else {
-                read8(f, turn + c * kTurnStride + (lane & 3) * 8);
+                read8(f, turn, c, (lane & 3) * 8);
                 if constexpr (MODE == kForward) {
                     if (pre && in) store8<T>(pre + (c0 + i * 8) * pre_stride, f);
                     activate8(p.act, f);
@@ -338,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 8);            // both CTAs' epilogue warps
+            mbar_init(&bars.acc_empty[i], 2 * kEpilogueWarps);   // both CTAs' epilogue warps
         }
         mbar_init(&bars.drained, 1);
         bars.gave_up = 0;
@@ -483,7 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < kSliceK / 16; ++j)
-                        mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, K > kSliceK || j > 0);
+                        if (j * 16 < K % kSliceK)
+                            mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, K > kSliceK || j > 0);
                     mma_commit_pair(bar(&bars.empty[s]));
                 }
                 if (++s == kStages) {
@@ -517,12 +530,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         const int quarter = warp & 3;                    // the TMEM lanes this warp may read
+        const int c0 = (warp - 2) / 4 * 32;              // its first columns
         float *turn = turns + (warp - 2) * (kTurnBytes / 4);
         uint32_t acc = 0;
         Epilogue<T, MODE> ep;
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int K = p.K < 0 ? t.rows : p.K, n = t.n;
-            ep.start(p, t, quarter, rank);
+            ep.start(p, t, quarter, rank, c0);
             float bias = 0.f;
             if ((MODE == kForward || MODE == kGated) && p.bias) {
                 const int in = quarter * 32 + lane;      // this lane's row of the accumulator
@@ -537,7 +551,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tcgen_after_sync();
             }
             const uint32_t d = tmem + (acc & 1u) * 256 + ((uint32_t)(quarter * 32) << 16);
-            for (int c = 0; c < n; c += 32) {
+            if (K > 0 && c0 >= n) {                      // no columns for this warp
+                tcgen_before_sync();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(first_cta(&bars.acc_empty[acc & 1u]));
+            }
+            for (int c = c0; c < n; c += kColumnStep) {
                 float v[32];
                 if (K > 0) {
                     tmem_load32(d + c, v);
@@ -545,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 }
-                if (K > 0 && c + 32 >= n) {              // the accumulator may be filled again
+                if (K > 0 && c + kColumnStep >= n) {              // the accumulator may be filled again
                     tcgen_before_sync();
                     __syncwarp();
                     if (lane == 0) cluster_arrive(first_cta(&bars.acc_empty[acc & 1u]));
