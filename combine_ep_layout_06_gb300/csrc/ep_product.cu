@@ -13,7 +13,7 @@
 // rows (or features) the other, so that a group with few rows costs a narrow
 // instruction (n in steps of 32) and not a padded tile.  A CTA loads its own
 // 128 m and half of n, so every byte of n serves both.  In each CTA warp 0
-// loads 64-deep slices by TMA into a ring in shared memory; warp 1 of the
+// loads 128-deep slices by TMA into a ring in shared memory; warp 1 of the
 // first CTA issues the pair's matrix instructions; warps 2..9 turn a finished
 // accumulator into outputs while the next one fills: two accumulators of 256
 // columns take all of the SM's tensor memory.
@@ -30,7 +30,16 @@ namespace ep {
 namespace {
 
 constexpr int kTileM = 128, kTileN = 256;          // m of one CTA, n of the pair
-constexpr int kRingBytes = 6 * 32768, kMaxStages = 6;
+// A slice is 128 deep (k): two 16 KB halves of each operand.  K-major (x, a
+// weight's rows): 128 rows of 64 k each.  MN-major (the gradients' transposed
+// operands): 64 m or n each, 128 rows of k.  A copy brings the 128 bytes that
+// the swizzle spans by up to 128 rows, and costs the loading thread about as
+// much whatever its size: 64-deep slices of 8 KB copies held grad_w of 16384
+// rows at 311 us, these take 250.
+constexpr int kSliceK = 128, kStages = 3;
+constexpr int kHalfBytes = 128 * 128;
+constexpr int kBytesA = 2 * kHalfBytes, kStageBytes = 4 * kHalfBytes;
+constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kEpilogueWarps = 8;
 constexpr int kTurnBytes = 32 * 32 * 4;            // a warp's transposing buffer
 constexpr size_t kSmemBytes = (size_t)kRingBytes + kEpilogueWarps * kTurnBytes + 1024;
@@ -55,17 +64,6 @@ __device__ __forceinline__ void group_range(const Groups &gr, int g, int *first,
 }
 
 enum Mode { kForward, kGated, kGradX, kGradW };
-
-// Slices of the ring.  One copy brings 64 elements (the swizzle's 128 bytes)
-// by up to 256 rows.  Rows of k (grad_w) come 128 at a time, which halves its
-// copies; elsewhere k runs along the 64 elements.
-template <Mode MODE> struct Ring {
-    static constexpr int kSliceK = MODE == kGradW ? 128 : 64;
-    static constexpr int kBytesA = kTileM * kSliceK * 2, kBytesB = kTileN / 2 * kSliceK * 2;
-    static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kStages = kRingBytes / kStageBytes;
-    static constexpr int kChunkBytes = 64 * kSliceK * 2;      // 64 m (or n) of an MN-major slice
-};
 
 struct ProductParams {
     Groups gr;
@@ -160,13 +158,13 @@ __device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live)
     for (int r = live + lane / 8; r < end; r += 4)
         for (int c = 0; c < chunks; ++c)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
-                         :: "r"(slice + c * Ring<kGradW>::kChunkBytes + r * 128 + lane % 8 * 16), "r"(0) : "memory");
+                         :: "r"(slice + c * kHalfBytes + r * 128 + lane % 8 * 16), "r"(0) : "memory");
     fence_async_smem();
     __syncwarp();
 }
 
 struct __align__(8) Barriers {
-    uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer_tail[kMaxStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kStages], empty[kStages], tail[kStages], peer_tail[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int gave_up;
 };
@@ -326,9 +324,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_b32, const ProductParams p) {
     constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
-    constexpr int kSliceK = Ring<MODE>::kSliceK, kStages = Ring<MODE>::kStages;
-    constexpr int kBytesA = Ring<MODE>::kBytesA, kBytesB = Ring<MODE>::kBytesB;
-    constexpr int kStageBytes = Ring<MODE>::kStageBytes, kChunkBytes = Ring<MODE>::kChunkBytes;
     constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bars;
@@ -379,12 +374,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int K = p.K < 0 ? t.rows : p.K;
             const int half = ((t.n + 31) & ~31) / 2;      // this CTA's n
-            // a copy costs the loading thread about as much whatever its size:
-            // one of 128 rows, or up to three of 32
+            // rows of B: one copy of 128, or up to three of 32
             const bool narrow = !kBmn && half <= 96;
             const int boxes = kBmn ? (half + 63) / 64 : narrow ? (half + 31) / 32 : 1;
-            const uint32_t box = kBmn ? kChunkBytes : narrow ? 32 * kSliceK * 2 : kBytesB;
-            const uint32_t bytes = kBytesA + boxes * box;
+            const uint32_t box = narrow ? kHalfBytes / 4 : kHalfBytes;
             const CUtensorMap *mb = narrow ? &map_b32 : &map_b;
             const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n0 + (int)rank * half;
             if (lane == 0) {
@@ -393,6 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
+                    const int halves = K - k > 64 ? 2 : 1;        // of a K-major operand
+                    const uint32_t bytes = (kAmn ? 2 : halves) * kHalfBytes + (kBmn ? 1 : halves) * boxes * box;
                     // the second CTA clears the rows past a group's end before
                     // it tells the first: that slice lands on its own barrier
                     const bool last = MODE == kGradW && K - k < kSliceK, tail = last && rank == 1;
@@ -404,21 +399,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (tails >> s & 1u) landed ^= 1u << s;
                         tails |= 1u << s;
                     }
-                    if constexpr (MODE == kGated) {
-                        tma_load5(a, &map_a, full, k, 0, 0, m0 / 16, t.g);
-                    } else if constexpr (!kAmn) {
-                        tma_load3(a, &map_a, full, k, m0, t.g);
-                    } else {
+                    if constexpr (kAmn) {
                         const int row = MODE == kGradW ? t.first + k : k;
                         const int own = MODE == kGradW ? t.seg : t.g;
                         tma_load3(a, &map_a, full, m0, row, own);
-                        tma_load3(a + kChunkBytes, &map_a, full, m0 + 64, row, own);
+                        tma_load3(a + kHalfBytes, &map_a, full, m0 + 64, row, own);
                     }
-                    for (int j = 0; j < boxes; ++j) {
-                        if constexpr (kBmn)
-                            tma_load3(b + j * kChunkBytes, mb, full, n0 + j * 64, t.first + k, t.seg);
-                        else
-                            tma_load3(b + j * box, mb, full, k, t.first + n0 + j * 32, t.seg);
+                    if constexpr (kBmn) {
+                        for (int j = 0; j < boxes; ++j)
+                            tma_load3(b + j * kHalfBytes, mb, full, n0 + j * 64, t.first + k, t.seg);
+                    }
+                    for (int h = 0; h < halves; ++h) {
+                        if constexpr (MODE == kGated)
+                            tma_load5(a + h * kHalfBytes, &map_a, full, k + h * 64, 0, 0, m0 / 16, t.g);
+                        else if constexpr (!kAmn)
+                            tma_load3(a + h * kHalfBytes, &map_a, full, k + h * 64, m0, t.g);
+                        if constexpr (!kBmn)
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load3(b + h * kHalfBytes + j * box, mb, full, k + h * 64, t.first + n0 + j * 32,
+                                          t.seg);
                     }
                     ++issued;
                     if (++s == kStages) {
@@ -445,10 +444,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
-        // descriptors: 16 k on is 32 bytes (K-major) or 16 rows (MN-major) on
-        constexpr uint64_t kStepA = (kAmn ? 2048 : 32) >> 4, kStepB = (kBmn ? 2048 : 32) >> 4;
-        const uint64_t a0 = smem_desc(ring, kAmn ? kChunkBytes : 16, 1024);
-        const uint64_t b0 = smem_desc(ring + kBytesA, kBmn ? kChunkBytes : 16, 1024);
+        // descriptors; step j is 16 k on: 32 bytes of a row and the other half
+        // after four (K-major), or 16 rows (MN-major)
+        const uint64_t a0 = smem_desc(ring, kAmn ? kHalfBytes : 16, 1024);
+        const uint64_t b0 = smem_desc(ring + kBytesA, kBmn ? kHalfBytes : 16, 1024);
+        auto step = [](bool mn, int j) -> uint64_t {
+            return (mn ? j * 2048 : j / 4 * kHalfBytes + j % 4 * 32) >> 4;
+        };
         uint32_t s = 0, phase = 0, acc = 0, tails = 0;
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int K = p.K < 0 ? t.rows : p.K;
@@ -460,20 +462,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tcgen_after_sync();
             // One thread issues everything: the pair's next instructions have
             // to be queued before the last ones end, so its loop is kept short.
-            int left = ok ? (MODE == kGradW ? K / kSliceK : (K + kSliceK - 1) / kSliceK) : 0;
-            bool add = false;
+            const int end = !ok ? 0 : MODE == kGradW ? K / kSliceK * kSliceK : K;
             if (lane == 0) {
-                for (; left > 0; --left) {
+                for (int k = 0; k < end; k += kSliceK) {
                     if (!tensor_wait(bar(&bars.full[s]), phase, gave_up)) {
                         ok = false;
                         break;
                     }
                     const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
 #pragma unroll
-                    for (int j = 0; j < kSliceK / 16; ++j) {
-                        mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, add);
-                        add = true;
-                    }
+                    for (int j = 0; j < kSliceK / 16; ++j)
+                        if (j == 0 || k + j * 16 < K)
+                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, k > 0 || j > 0);
                     mma_commit_pair(bar(&bars.empty[s]));
                     if (++s == kStages) {
                         s = 0;
@@ -496,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kSliceK / 16; ++j)
                         if (j * 16 < K % kSliceK)
-                            mma_f16(d, da + j * kStepA, db + j * kStepB, idesc, K > kSliceK || j > 0);
+                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, K > kSliceK || j > 0);
                     mma_commit_pair(bar(&bars.empty[s]));
                 }
                 if (++s == kStages) {
@@ -962,7 +962,7 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         p.K = (int)wide;
         p.out = *grad_x;
         p.error = d_error;
-        if (!encode_rows(&a, d->dtype, d->weight, d->in_features, wide, G, 64) ||
+        if (!encode_rows(&a, d->dtype, d->weight, d->in_features, wide, G, kSliceK) ||
             !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
             !encode_rows(&b32, d->dtype, dd, wide, d->rows, d->ranks, 32))
             return EP_ERR_GPU_OP;
@@ -980,9 +980,8 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
         p.K = -1;
         p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
         p.error = d_error;
-        constexpr int kRows = Ring<kGradW>::kSliceK;
-        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kRows) ||
-            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kRows))
+        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kSliceK) ||
+            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kSliceK))
             return EP_ERR_GPU_OP;
         const ep_status_t s = launch_product<kGradW>(d->dtype, a, b, b, p, st);
         if (s != EP_SUCCESS) return s;
