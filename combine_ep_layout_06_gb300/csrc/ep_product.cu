@@ -136,13 +136,18 @@ struct Walker {
         t->seg = t->g / p.gr.per;
         t->first = __shfl_sync(0xffffffffu, first, l);
         t->rows = __shfl_sync(0xffffffffu, rows, l);
-        t->m = in % mt;
+        // bands of at most 16 m-tiles: what runs at a time, some 76 tiles, spans
+        // about as much of n as of m (8192 x 8192 x 8192: 712 -> 680 us)
+        const int bands = (mt + 15) / 16, band = (mt + bands - 1) / bands;
         // equal parts of N instead of full tiles and a rest: a narrow rest would
         // load as much of the other operand for less work
         const int N = p.N < 0 ? t->rows : p.N;
         const int parts = (N + kTileN - 1) / kTileN;
         const int width = ((N + parts - 1) / parts + 31) & ~31;
-        t->n0 = in / mt * width;
+        const int b = in / (band * parts), in_band = in - b * band * parts;
+        const int wide = min(band, mt - b * band);
+        t->m = b * band + in_band % wide;
+        t->n0 = in_band / wide * width;
         t->n = min(width, N - t->n0);
         return true;
     }
@@ -370,6 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         uint32_t issued = 0, s = 0, phase = 0;            // slices, the next one's stage and its round's parity
         uint32_t tails = 0, landed = 0;                   // by stage: a tail was loaded, its barrier's phase
+        const bool elected = elect_one();
         const uint32_t full0 = first_cta(&bars.full[0]);
         for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
             const int K = p.K < 0 ? t.rows : p.K;
@@ -380,12 +386,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t box = narrow ? kHalfBytes / 4 : kHalfBytes;
             const CUtensorMap *mb = narrow ? &map_b32 : &map_b;
             const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n0 + (int)rank * half;
-            if (lane == 0) {
-                for (int k = 0; k < K; k += kSliceK) {
-                    if (!tensor_wait(bar(&bars.empty[s]), phase ^ 1u, gave_up)) {
-                        ok = false;
-                        break;
-                    }
+            for (int k = 0; k < K; k += kSliceK) {
+                if (!tensor_wait(bar(&bars.empty[s]), phase ^ 1u, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                if (elected) {
                     const int halves = K - k > 64 ? 2 : 1;        // of a K-major operand
                     const uint32_t bytes = (kAmn ? 2 : halves) * kHalfBytes + (kBmn ? 1 : halves) * boxes * box;
                     // the second CTA clears the rows past a group's end before
@@ -394,11 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const uint32_t full = tail ? in_cta(bar(&bars.tail[s]), 1) : full0 + s * 8;
                     const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
                     if (rank == 0) mbar_expect(bar(&bars.full[s]), last ? bytes : 2 * bytes);
-                    if (tail) {
-                        mbar_expect(bar(&bars.tail[s]), bytes);
-                        if (tails >> s & 1u) landed ^= 1u << s;
-                        tails |= 1u << s;
-                    }
+                    if (tail) mbar_expect(bar(&bars.tail[s]), bytes);
                     if constexpr (kAmn) {
                         const int row = MODE == kGradW ? t.first + k : k;
                         const int own = MODE == kGradW ? t.seg : t.g;
@@ -419,14 +421,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 tma_load3(b + h * kHalfBytes + j * box, mb, full, k + h * 64, t.first + n0 + j * 32,
                                           t.seg);
                     }
-                    ++issued;
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                }
+                if (MODE == kGradW && rank == 1 && K - k < kSliceK) {
+                    if (tails >> s & 1u) landed ^= 1u << s;
+                    tails |= 1u << s;
+                }
+                ++issued;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = __all_sync(0xffffffffu, ok);
         }
         // The pair ends together, and not before its copies have landed and the
         // stages' last signals have come; after a wait that ran out, as far
@@ -444,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
+        const bool elected = elect_one();
         // descriptors; step j is 16 k on: 32 bytes of a row and the other half
         // after four (K-major), or 16 rows (MN-major)
         const uint64_t a0 = smem_desc(ring, kAmn ? kHalfBytes : 16, 1024);
@@ -460,38 +467,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + (acc & 1u) * 256;
             ok = warp_wait<true>(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
             tcgen_after_sync();
-            // One thread issues everything: the pair's next instructions have
-            // to be queued before the last ones end, so its loop is kept short.
+            // One thread issues everything, and has to queue the next slice's
+            // instructions before the last one's end: the loop is kept short.
             const int end = !ok ? 0 : MODE == kGradW ? K / kSliceK * kSliceK : K;
-            if (lane == 0) {
-                for (int k = 0; k < end; k += kSliceK) {
-                    if (!tensor_wait(bar(&bars.full[s]), phase, gave_up)) {
-                        ok = false;
-                        break;
-                    }
+            for (int k = 0; k < end; k += kSliceK) {
+                if (!tensor_wait(bar(&bars.full[s]), phase, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                if (elected) {
                     const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < kSliceK / 16; ++j)
                         if (j == 0 || k + j * 16 < K)
                             mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, k > 0 || j > 0);
                     mma_commit_pair(bar(&bars.empty[s]));
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = __all_sync(0xffffffffu, ok);
             if (MODE == kGradW && ok && K % kSliceK) {
-                s = __shfl_sync(0xffffffffu, s, 0);
-                phase = __shfl_sync(0xffffffffu, phase, 0);
                 ok = warp_wait(bar(&bars.full[s]), phase, gave_up);
                 if (ok) {
                     clear_rows(ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, K % kSliceK);
                     ok = warp_wait<true>(bar(&bars.peer_tail[s]), tails >> s & 1u, gave_up);
                     tails ^= 1u << s;
                 }
-                if (ok && lane == 0) {
+                if (ok && elected) {
                     const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int j = 0; j < kSliceK / 16; ++j)
@@ -504,12 +509,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     phase ^= 1u;
                 }
             }
-            if (ok && lane == 0) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
+            if (ok && elected) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
             ++acc;
         }
         if (!ok) {                                       // let the matrix unit finish
             int ignore = 0;
-            if (lane == 0) mma_commit(bar(&bars.drained));
+            if (elected) mma_commit(bar(&bars.drained));
             tensor_wait(bar(&bars.drained), 0, &ignore);
         }
     } else if (warp == 1) {

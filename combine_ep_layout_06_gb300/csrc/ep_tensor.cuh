@@ -56,6 +56,14 @@ template <bool PEER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     return __all_sync(0xffffffffu, tensor_wait<PEER>(bar, parity, gave_up));
 }
+// One lane of the warp, the same one each time.  Code that only it runs,
+// inside control flow that the whole warp follows, keeps its operands in
+// uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes)
                  : "memory");
