@@ -1,10 +1,13 @@
 // Top-k routing, the balance and z losses, and the gradient of both by the
 // router logits.
 //
-// One warp per token: the row of E logits lies in registers, lane l holding
-// experts l, l + 32, ...  Softmax statistics are warp reductions in fp32.
-// Top-k is k rounds of a warp-wide maximum over order-preserving integer
-// keys; a tie goes to the lowest expert id by a second, minimum reduction.
+// A token's row of E logits lies in the registers of LANES neighbouring lanes,
+// 8 (or, past 256 experts, 16 or 32) neighbouring experts each, so that lane
+// order is expert order and a warp holds 32 / LANES tokens: with 8 experts a
+// thread has a token to itself.  Softmax statistics are fp32 reductions over
+// those lanes.  Top-k takes the largest remaining key k times over; a lane
+// keeps its two best keys at hand and looks through its own again when both
+// are taken.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -17,13 +20,14 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
-constexpr int kLossWarps = 8;
+constexpr int kLossWarps = 32;
 
 struct RouteParams {
     const void *logits;
     int64_t row_stride, rank_stride;
     TokenCounts nt;
     int W, T, E, k;
+    bool vec;                // rows of logits (and of their gradient) in 16-byte pieces
     float scale;
     const float *bias;       // forward
     float *w;                // forward
@@ -64,28 +68,74 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Reductions over the LANES lanes of a token.
+template <int LANES> __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int LANES> __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
+template <int LANES> __device__ __forceinline__ uint32_t row_max_key(uint32_t v) {
+    if constexpr (LANES == 32) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// exp of a difference of logits, within 2^-22 (1 + |d| / 2) of it: the callers'
+// sums and 1e-5 tolerances are far above.
+__device__ __forceinline__ float exp_diff(float d) { return __expf(d); }
 
 template <typename T>
 __device__ __forceinline__ const T *logit_row(const RouteParams &p, int s, int t) {
     return static_cast<const T *>(p.logits) + s * p.rank_stride + t * p.row_stride;
 }
 
+// Experts l * VPL .. l * VPL + VPL - 1 of a row; -inf past the last expert.
 template <typename T, int VPL>
-__device__ __forceinline__ void load_row(const RouteParams &p, const T *row, int lane, float *x) {
+__device__ __forceinline__ void load_row(const RouteParams &p, const T *row, int l, float *x) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (p.vec) {             // E is a multiple of 8: every piece is inside or outside
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < p.E ? sane_logit(to_f32(row[e])) : -INFINITY;
+        for (int c = 0; c < VPL; c += kPer) {
+            const int e = l * VPL + c;
+            if (e < p.E) {
+                const uint4 v = ld_stream16(row + e);
+                const T *s = reinterpret_cast<const T *>(&v);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x[c + i] = sane_logit(to_f32(s[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x[c + i] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = l * VPL + i;
+            x[i] = e < p.E ? sane_logit(to_f32(row[e])) : -INFINITY;
+        }
+    }
+}
+template <typename T, int VPL>
+__device__ __forceinline__ void store_row(const RouteParams &p, T *row, int l, const float *d) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (p.vec) {
+#pragma unroll
+        for (int c = 0; c < VPL; c += kPer) {
+            const int e = l * VPL + c;
+            __align__(16) T s[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) s[i] = from_f32<T>(d[c + i]);
+            if (e < p.E) *reinterpret_cast<uint4 *>(row + e) = *reinterpret_cast<const uint4 *>(s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (l * VPL + i < p.E) row[l * VPL + i] = from_f32<T>(d[i]);
     }
 }
 
@@ -99,171 +149,198 @@ struct RowStats {
     __device__ float lse() const { return open ? m - logf(inv_sum) : 0.f; }
 };
 
-// Softmax over the warp's row: probabilities in place of x (all 0 when no
+// Softmax over a token's row: probabilities in place of x (all 0 when no
 // expert is open).
-template <int VPL>
+template <int LANES, int VPL>
 __device__ __forceinline__ RowStats softmax_row(float *x) {
-    float m = -INFINITY;
+    float m = x[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
-    if (m == -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) x[i] = 0.f;
-        return RowStats{0.f, 1.f, false};
-    }
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
+    m = row_max<LANES>(m);
+    const bool open = m > -INFINITY;
+    if (!open) m = 0.f;                      // every exponential is then 0
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        x[i] = expf(x[i] - m);
+        x[i] = exp_diff(x[i] - m);
         sum += x[i];
     }
-    sum = warp_sum(sum);
-    const float inv = 1.0f / sum;
+    sum = row_sum<LANES>(sum);
+    const float inv = open ? 1.0f / sum : 1.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] *= inv;
-    return RowStats{m, inv, true};
+    return RowStats{m, inv, open};
 }
 
-// Softmax over the chosen experts (lane j < k holds x_j of choice j).
-__device__ __forceinline__ float chosen_softmax(float xj, bool mine) {
-    const float m = warp_max(mine ? xj : -INFINITY);
-    const float e = mine && m > -INFINITY ? expf(xj - m) : 0.f;
-    const float sum = warp_sum(e);
-    return sum > 0.f ? e / sum : 0.f;
-}
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-template <typename T, int VPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool softmax,
-                                                                 bool renorm) {
-    const int lane = threadIdx.x & 31;
-    const int64_t tok = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-    if (tok >= (int64_t)p.W * p.T) return;
-    const int s = (int)(tok / p.T), t = (int)(tok - (int64_t)s * p.T);
-    if (t >= p.nt.n[s]) {
-        if (lane < p.k) {
-            p.w[tok * p.k + lane] = 0.f;
-            p.idx_out[tok * p.k + lane] = -1;
-        }
-        return;
+// A token's place: lane l of its LANES, token t of rank blockIdx.y.
+template <int LANES> struct Place {
+    int l, s, t;
+    int64_t tok;
+    bool in, present;
+    __device__ explicit Place(const RouteParams &p, int warps) {
+        constexpr int kTokens = 32 / LANES;              // of a warp
+        const int lane = threadIdx.x & 31;
+        l = lane % LANES;
+        s = blockIdx.y;
+        t = (blockIdx.x * warps + (threadIdx.x >> 5)) * kTokens + lane / LANES;
+        tok = (int64_t)s * p.T + t;
+        in = t < p.T;
+        present = t < p.nt.n[s];
     }
-    float x[VPL];
-    uint32_t key[VPL];
-    load_row<T, VPL>(p, logit_row<T>(p, s, t), lane, x);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < p.E ? order_key(p.bias ? x[i] + p.bias[e] : x[i]) : 0u;
-    }
-    int mine_e = 0;
-    float mine_x = -INFINITY;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t best = 0;
-        int be = 0;
-        float bx = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                be = lane + 32 * i;
-                bx = x[i];
-            }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)be : 0xffffffffu);
-        const float xe = __shfl_sync(0xffffffffu, bx, e & 31);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if ((uint32_t)(lane + 32 * i) == e) key[i] = 0;
-        if (lane == j) {
-            mine_e = (int)e;
-            mine_x = xe;
-        }
-    }
-    const bool mine = lane < p.k;
-    float v;
+};
+
+// Choice j of a token is held by lane j % LANES of its lanes, in slot
+// j / LANES; with 32 choices at most and at most 8 * LANES experts below 32
+// lanes, min(8, 32 / LANES) slots are enough.
+template <int LANES> __host__ __device__ constexpr int slots_of() { return 32 / LANES < 8 ? 32 / LANES : 8; }
+
+// Scores of the chosen experts from their logits c[] (mine: slot is a choice)
+// and the row's statistics.  v[]: scale 1.  For the sigmoid *sum is what
+// renormalising divides by.
+template <int LANES, int SLOTS>
+__device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const RowStats &st, const float *c,
+                                              const bool *mine, float *v, float *sum) {
+    *sum = 0.f;
     if (softmax && renorm) {
-        v = chosen_softmax(mine_x, mine);
-    } else if (softmax) {
-        const RowStats st = softmax_row<VPL>(x);
-        v = mine ? st.prob(mine_x) : 0.f;
-    } else {
-        v = mine ? sigmoid(mine_x) : 0.f;
-        if (renorm) {
-            const float sum = warp_sum(v);
-            v = sum > 0.f ? v / sum : 0.f;
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) m = fmaxf(m, mine[q] ? c[q] : -INFINITY);
+        m = row_max<LANES>(m);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            v[q] = mine[q] && m > -INFINITY ? expf(c[q] - m) : 0.f;
+            *sum += v[q];
         }
-    }
-    if (mine) {
-        p.w[tok * p.k + lane] = v * p.scale;
-        p.idx_out[tok * p.k + lane] = mine_e;
+        *sum = row_sum<LANES>(*sum);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) v[q] = *sum > 0.f ? v[q] / *sum : 0.f;
+    } else if (softmax) {
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) v[q] = mine[q] ? st.prob(c[q]) : 0.f;
+    } else {
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            v[q] = mine[q] ? sigmoid(c[q]) : 0.f;
+            *sum += v[q];
+        }
+        if (renorm) *sum = row_sum<LANES>(*sum);
     }
 }
 
-template <typename T, int VPL>
+template <typename T, int LANES, int VPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool softmax,
+                                                                 bool renorm) {
+    constexpr int SLOTS = slots_of<LANES>();
+    const Place<LANES> at(p, kRouteWarps);
+    const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
+    float x[VPL];
+    if (at.present) {
+        load_row<T, VPL>(p, row, at.l, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) x[i] = -INFINITY;
+    }
+    // this lane's best and second best key: the larger one, or the earlier expert
+    uint32_t key[VPL], best = 0, second = 0;
+    int be = 0, se = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = at.l * VPL + i;
+        key[i] = e < p.E ? order_key(p.bias ? x[i] + p.bias[e] : x[i]) : 0u;
+        const bool first = key[i] > best, next = key[i] > second;
+        second = first ? best : next ? key[i] : second;
+        se = first ? be : next ? i : se;
+        best = first ? key[i] : best;
+        be = first ? i : be;
+    }
+    const uint32_t lanes = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
+    int id[SLOTS];
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) id[q] = -1;
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t top = row_max_key<LANES>(best);
+        const uint32_t who = __ballot_sync(0xffffffffu, best == top) & lanes;
+        const int winner = __ffs(who) - 1;               // the first lane has the first expert
+        const int e = __shfl_sync(0xffffffffu, at.l * VPL + be, winner);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q)
+            if (j == q * LANES + at.l) id[q] = e;
+        bool again = false;
+        if ((threadIdx.x & 31) == winner) {
+            again = second == 0;
+            if (!again) {
+                best = second;
+                be = se;
+                second = 0;
+            }
+        }
+        if (__any_sync(0xffffffffu, again)) {
+            // both keys are taken: the best two after the one taken last (equal
+            // keys in the order of the experts)
+            if (again) {
+                const uint32_t last = best;
+                const int le = be;
+                best = second = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    const bool open = key[i] < last || (key[i] == last && i > le);
+                    const uint32_t v = open ? key[i] : 0u;
+                    const bool first = v > best, next = v > second;
+                    second = first ? best : next ? v : second;
+                    se = first ? be : next ? i : se;
+                    best = first ? v : best;
+                    be = first ? i : be;
+                }
+            }
+        }
+    }
+    float c[SLOTS], v[SLOTS], sum;
+    bool mine[SLOTS];
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+        mine[q] = at.present && q * LANES + at.l < p.k;
+        c[q] = mine[q] ? sane_logit(to_f32(row[id[q]])) : -INFINITY;
+    }
+    RowStats st = {0.f, 1.f, false};
+    if (softmax && !renorm) st = softmax_row<LANES, VPL>(x);
+    chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+        const int j = q * LANES + at.l;
+        if (!softmax && renorm) v[q] = sum > 0.f ? v[q] / sum : 0.f;
+        if (at.in && j < p.k) {
+            p.w[at.tok * p.k + j] = mine[q] ? v[q] * p.scale : 0.f;
+            p.idx_out[at.tok * p.k + j] = mine[q] ? id[q] : -1;
+        }
+    }
+}
+
+// The weights' gradient is nonzero at the chosen experts (and, for a softmax
+// that is not renormalised, dense): the row meets in shared memory, where the
+// chosen experts' terms are added to the dense part, one choice after the
+// other where an expert was chosen twice.
+template <typename T, int LANES, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const RouteParams p, bool softmax, bool renorm) {
-    const int lane = threadIdx.x & 31;
-    const int64_t tok = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-    if (tok >= (int64_t)p.W * p.T) return;
-    const int s = (int)(tok / p.T), t = (int)(tok - (int64_t)s * p.T);
-    T *out = static_cast<T *>(p.grad_logits) + tok * p.E;
-    if (t >= p.nt.n[s]) {
-        for (int e = lane; e < p.E; e += 32) out[e] = from_f32<T>(0.f);
-        return;
-    }
-    const T *row = logit_row<T>(p, s, t);
+    constexpr int SLOTS = slots_of<LANES>();
+    constexpr int kTokens = 32 / LANES, kRow = LANES * VPL;
+    __shared__ __align__(16) float rows[kRouteWarps * kTokens][kRow + 4];
+    const Place<LANES> at(p, kRouteWarps);
+    const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
     float d[VPL], pr[VPL];
     RowStats st = {0.f, 1.f, false};
-    const bool dense = p.grad_loss || (p.grad_w && softmax && !renorm);
-    if (dense) {
-        load_row<T, VPL>(p, row, lane, pr);
-        st = softmax_row<VPL>(pr);
-    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = 0.f;
-    if (p.grad_w) {
-        int id = -1;
-        float g = 0.f, xj = -INFINITY;
-        if (lane < p.k) {
-            id = p.idx[tok * p.k + lane];
-            if ((uint32_t)id < (uint32_t)p.E) {
-                g = p.grad_w[tok * p.k + lane] * p.scale;
-                xj = sane_logit(to_f32(row[id]));
-            } else {
-                id = -1;
-                if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
-            }
-        }
-        const bool mine = id >= 0;
-        float dj, inner = 0.f;
-        if (softmax && renorm) {
-            const float v = chosen_softmax(xj, mine);
-            dj = v * (g - warp_sum(g * v));
-        } else if (softmax) {
-            const float v = mine ? st.prob(xj) : 0.f;
-            inner = warp_sum(g * v);
-            dj = v * g;
+    if (p.grad_loss || (softmax && !renorm)) {
+        if (at.present) {
+            load_row<T, VPL>(p, row, at.l, pr);
         } else {
-            const float v = mine ? sigmoid(xj) : 0.f;
-            float dv = g;
-            if (renorm) {
-                const float sum = warp_sum(v), dot = warp_sum(g * v);
-                dv = sum > 0.f ? (g - dot / sum) / sum : 0.f;
-            }
-            dj = dv * v * (1.0f - v);
-        }
-        for (int j = 0; j < p.k; ++j) {
-            const int e = __shfl_sync(0xffffffffu, id, j);
-            const float de = __shfl_sync(0xffffffffu, dj, j);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (e == lane + 32 * i) d[i] += de;
+            for (int i = 0; i < VPL; ++i) pr[i] = -INFINITY;
         }
-        if (softmax && !renorm) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * inner;
-        }
+        st = softmax_row<LANES, VPL>(pr);
     }
     if (p.grad_loss) {
         const float gl = *p.grad_loss * p.inv_n, lse = st.lse();
@@ -271,60 +348,156 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         float f[VPL], dot = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 32 * i;
+            const int e = at.l * VPL + i;
             f[i] = e < p.E ? (float)p.counts[e] * share : 0.f;
             dot += pr[i] * f[i];
         }
-        dot = warp_sum(dot);
+        dot = row_sum<LANES>(dot);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            d[i] += pr[i] * ((f[i] - dot) * p.balance_coef + 2.0f * p.z_coef * lse) * gl;
+            d[i] = pr[i] * ((f[i] - dot) * p.balance_coef + 2.0f * p.z_coef * lse) * gl;
     }
+    if (p.grad_w) {
+        int id[SLOTS];
+        float g[SLOTS], c[SLOTS], v[SLOTS], dv[SLOTS], sum, dot = 0.f;
+        bool mine[SLOTS];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < p.E) out[e] = from_f32<T>(d[i]);
+        for (int q = 0; q < SLOTS; ++q) {
+            const int j = q * LANES + at.l;
+            id[q] = -1;
+            g[q] = 0.f;
+            c[q] = -INFINITY;
+            if (at.present && j < p.k) {
+                id[q] = p.idx[at.tok * p.k + j];
+                if ((uint32_t)id[q] < (uint32_t)p.E) {
+                    g[q] = p.grad_w[at.tok * p.k + j] * p.scale;
+                    c[q] = sane_logit(to_f32(row[id[q]]));
+                } else {
+                    id[q] = -1;
+                    if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+                }
+            }
+            mine[q] = id[q] >= 0;
+        }
+        chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
+        if (softmax || renorm) dot = row_sum<LANES>(dot);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            if (softmax) {
+                dv[q] = renorm ? v[q] * (g[q] - dot) : v[q] * g[q];
+            } else {
+                float s = g[q];
+                if (renorm) s = sum > 0.f ? (g[q] - dot / sum) / sum : 0.f;
+                dv[q] = s * v[q] * (1.0f - v[q]);
+            }
+        }
+        if (softmax && !renorm) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * dot;
+        }
+        float *r = rows[threadIdx.x / LANES];
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4)
+            *reinterpret_cast<float4 *>(r + at.l * VPL + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        __syncwarp();
+        // one lane a token: in order.  32: at once, unless an expert comes twice.
+        bool twice = LANES < 32;
+        if (LANES == 32) {
+            const uint32_t same = __match_any_sync(0xffffffffu, mine[0] ? id[0] : -1 - (int)(threadIdx.x & 31));
+            twice = __any_sync(0xffffffffu, (same & (same - 1u)) != 0);
+        }
+        if (!twice) {
+            if (mine[0]) r[id[0]] += dv[0];
+        } else {
+            for (int j = 0; j < p.k; ++j) {
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q)
+                    if (j == q * LANES + at.l && mine[q]) r[id[q]] += dv[q];
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(r + at.l * VPL + i);
+            d[i] = f.x;
+            d[i + 1] = f.y;
+            d[i + 2] = f.z;
+            d[i + 3] = f.w;
+        }
     }
+    if (!at.in) return;
+    if (!at.present) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) d[i] = 0.f;
+    }
+    store_row<T, VPL>(p, static_cast<T *>(p.grad_logits) + at.tok * p.E, at.l, d);
 }
 
 // Losses, pass 1: every block sums softmax probabilities and lse^2 of its
-// tokens (a warp's tokens in registers, then the warps in order) and counts
-// choices in shared memory.
-template <typename T, int VPL>
-__global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const RouteParams p) {
+// tokens (a lane's tokens in registers, then lanes and warps in order) and
+// counts choices in shared memory.  Bound by instructions (about 100 a warp
+// and token of 256 experts), so one block of 32 warps per SM.
+template <typename T, int LANES, int VPL>
+__global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const RouteParams p, int tokens_per_warp) {
     extern __shared__ float sh[];                 // [kLossWarps][E + 1], then [E] counts
+    constexpr int kTokens = 32 / LANES;
     int32_t *cnt = reinterpret_cast<int32_t *>(sh + kLossWarps * (p.E + 1));
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
     float acc[VPL], z = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+    // this warp's tokens: a run of all ranks' tokens
     const int64_t total = (int64_t)p.W * p.T;
-    for (int64_t tok = (int64_t)blockIdx.x * kLossWarps + warp; tok < total;
-         tok += (int64_t)gridDim.x * kLossWarps) {
-        const int s = (int)(tok / p.T), t = (int)(tok - (int64_t)s * p.T);
-        if (t >= p.nt.n[s]) continue;
-        if (lane < p.k) {
-            const int id = p.idx[tok * p.k + lane];
-            if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&cnt[id], 1);
-            else if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+    const int64_t tok0 = ((int64_t)blockIdx.x * kLossWarps + warp) * tokens_per_warp;
+    int s = (int)(tok0 / p.T), t0 = (int)(tok0 - (int64_t)s * p.T);
+    for (int i0 = 0; i0 < tokens_per_warp; i0 += kTokens) {
+        int t = t0 + i0 + lane / LANES, r = s;
+        while (t >= p.T && r < p.W) {
+            t -= p.T;
+            ++r;
         }
+        const bool present = i0 + lane / LANES < tokens_per_warp && tok0 + i0 + lane / LANES < total && t < p.nt.n[r];
         float x[VPL];
-        load_row<T, VPL>(p, logit_row<T>(p, s, t), lane, x);
-        const float lse = softmax_row<VPL>(x).lse();
-        z += lse * lse;
+        if (present) {
+            const int64_t tok = (int64_t)r * p.T + t;
+            for (int j = l; j < p.k; j += LANES) {
+                const int id = p.idx[tok * p.k + j];
+                if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&cnt[id], 1);
+                else if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+            }
+            load_row<T, VPL>(p, logit_row<T>(p, r, t), l, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) x[i] = -INFINITY;
+        }
+        const float lse = softmax_row<LANES, VPL>(x).lse();
+        z += l == 0 ? lse * lse : 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) acc[i] += x[i];
     }
-    float *mine = sh + warp * (p.E + 1);
+    // the warp's tokens of other lanes with the same experts
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < p.E) mine[lane + 32 * i] = acc[i];
+    for (int o = 16; o >= LANES; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    }
+    z = row_sum<32>(z);
+    float *mine = sh + warp * (p.E + 1);
+    if (lane < LANES) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (l * VPL + i < p.E) mine[l * VPL + i] = acc[i];
+    }
     if (lane == 0) mine[p.E] = z;
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
         float sum = 0.f;
+#pragma unroll 8
         for (int w = 0; w < kLossWarps; ++w) sum += sh[w * (p.E + 1) + e];
         p.part[(int64_t)blockIdx.x * (p.E + 1) + e] = sum;
         if (e < p.E) p.part_count[(int64_t)blockIdx.x * p.E + e] = cnt[e];
@@ -369,8 +542,8 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
         __syncthreads();
     }
     if (warp == 0) {
-        balance = warp_sum(balance);
-        z = warp_sum(z);
+        balance = row_sum<32>(balance);
+        z = row_sum<32>(z);
         if (lane == 0) {
             p.loss[0] = p.balance_coef * balance + p.z_coef * z;
             p.loss[1] = balance;
@@ -385,15 +558,16 @@ int loss_blocks(const ep_route_desc_t &d) {
     return (int)(want < 152 ? want : 152);
 }
 
-// Calls f(T(), integral VPL) for the logits' type and the row length.
+// Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
 template <int V> struct Int { static constexpr int value = V; };
 template <typename T, typename F> void with_row(int E, F f) {
-    if (E <= 32) f(T(), Int<1>());
-    else if (E <= 64) f(T(), Int<2>());
-    else if (E <= 128) f(T(), Int<4>());
-    else if (E <= 256) f(T(), Int<8>());
-    else if (E <= 512) f(T(), Int<16>());
-    else f(T(), Int<32>());
+    if (E <= 8) f(T(), Int<1>(), Int<8>());
+    else if (E <= 32) f(T(), Int<4>(), Int<8>());
+    else if (E <= 64) f(T(), Int<8>(), Int<8>());
+    else if (E <= 128) f(T(), Int<16>(), Int<8>());
+    else if (E <= 256) f(T(), Int<32>(), Int<8>());
+    else if (E <= 512) f(T(), Int<32>(), Int<16>());
+    else f(T(), Int<32>(), Int<32>());
 }
 template <typename F> void with_types(int dtype, int E, F f) {
     if (dtype == EP_DT_BF16) with_row<__nv_bfloat16>(E, f);
@@ -436,13 +610,18 @@ bool make_params(const ep_route_desc_t *d, const void *logits, const int32_t *h_
     p->balance_coef = d->balance_coef;
     p->z_coef = d->z_coef;
     p->inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+    const int size = d->dtype == EP_DT_FP32 ? 4 : 2;
+    p->vec = d->num_experts % 8 == 0 && aligned(logits, 16) && d->row_stride * size % 16 == 0 &&
+             p->rank_stride * size % 16 == 0;
     return true;
 }
 
 ep_status_t launched() { return cudaGetLastError() == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP; }
 
-unsigned token_blocks(const RouteParams &p) {
-    return (unsigned)(((int64_t)p.W * p.T + kRouteWarps - 1) / kRouteWarps);
+// One block per 4 warps of tokens of a rank.
+template <int LANES> dim3 token_grid(const RouteParams &p) {
+    constexpr int kTokens = kRouteWarps * (32 / LANES);
+    return dim3((unsigned)((p.T + kTokens - 1) / kTokens), (unsigned)p.W);
 }
 
 }  // namespace
@@ -464,9 +643,10 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits, const float
     p.idx_out = d_idx;
     const bool softmax = d->score == EP_SCORE_SOFTMAX, renorm = d->renormalize != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    with_types(d->dtype, p.E, [&](auto type, auto vpl) {
-        route_kernel<decltype(type), decltype(vpl)::value>
-            <<<token_blocks(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
+    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+        constexpr int kLanes = decltype(lanes)::value;
+        route_kernel<decltype(type), kLanes, decltype(vpl)::value>
+            <<<token_grid<kLanes>(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
     });
     return launched();
 }
@@ -494,9 +674,11 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
     p.error = d_error;
     const bool softmax = d->score == EP_SCORE_SOFTMAX, renorm = d->renormalize != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    with_types(d->dtype, p.E, [&](auto type, auto vpl) {
-        route_backward_kernel<decltype(type), decltype(vpl)::value>
-            <<<token_blocks(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
+    p.vec = p.vec && aligned(d_grad_logits, 16);
+    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+        constexpr int kLanes = decltype(lanes)::value;
+        route_backward_kernel<decltype(type), kLanes, decltype(vpl)::value>
+            <<<token_grid<kLanes>(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
     });
     return launched();
 }
@@ -530,11 +712,16 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     p.part = static_cast<float *>(d_workspace);
     p.part_count = reinterpret_cast<int32_t *>(p.part + (size_t)blocks * (p.E + 1));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const size_t sh = ((size_t)kLossWarps * (p.E + 1) + p.E) * 4;    // 36 KB at most
-    with_types(d->dtype, p.E, [&](auto type, auto vpl) {
-        balance_partial_kernel<decltype(type), decltype(vpl)::value>
-            <<<blocks, kLossWarps * 32, sh, st>>>(p);
+    const size_t sh = ((size_t)kLossWarps * (p.E + 1) + p.E) * 4;    // 135 KB at most
+    const int64_t warps = (int64_t)blocks * kLossWarps;
+    const int per_warp = (int)(((int64_t)p.W * p.T + warps - 1) / warps);
+    cudaError_t e = cudaSuccess;
+    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+        auto kernel = balance_partial_kernel<decltype(type), decltype(lanes)::value, decltype(vpl)::value>;
+        if (sh > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e == cudaSuccess) kernel<<<blocks, kLossWarps * 32, sh, st>>>(p, per_warp);
     });
+    if (e != cudaSuccess) return EP_ERR_GPU_OP;
     balance_final_kernel<<<1, 1024, 0, st>>>(p, blocks);
     return launched();
 }

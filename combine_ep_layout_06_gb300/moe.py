@@ -9,11 +9,19 @@ Marshalling only: every step runs in the CUDA kernels of libep_gb300.so.  The
 formulas are those of include/ep_api.h.  Every call is asynchronous on
 ``stream`` (default: the current one); what it allocates belongs to that
 stream.  Device-side problems (an expert id out of range, a wait that gave up)
-set bits that ``moe_error`` reads.
+set bits that ``moe_error`` reads.  The first call on a device creates its
+error word and may load device code: make it before any stream capture.
+
+A single-token call takes a few microseconds on the GPU, so the host's part is
+kept short: what shapes, strides and options alone decide is checked once and
+remembered by their values (never by a tensor's address or identity), and C
+descriptors are packed as bytes.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -28,19 +36,29 @@ _PRODUCT_DTYPES = {torch.bfloat16: _lib.EP_DT_BF16, torch.float16: _lib.EP_DT_FP
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 
+# the descriptors' layouts (native alignment), as bytes
+_ROUTE_DESC = struct.Struct("7i3f2q")
+_ROWS = struct.Struct("Pqq")
+_PRODUCT_HEAD = struct.Struct("8i")
+_PRODUCT_TAIL = struct.Struct("PPPqqPqq")
+assert _ROUTE_DESC.size == ctypes.sizeof(EpRouteDescC)
+assert _ROWS.size == ctypes.sizeof(EpRowsC)
+assert _PRODUCT_HEAD.size + _PRODUCT_TAIL.size == ctypes.sizeof(EpProductDescC)
+_NO_ROWS = _ROWS.pack(0, 0, 0)
+
 _lock = threading.Lock()
-_error_words = {}                  # device index -> the device's error word
+_error_words = {}                  # device index -> (the device's error word, its address)
 
 
-def _error_word(index: int) -> torch.Tensor:
+def _error_word(index: int):
     t = _error_words.get(index)
     if t is None:
         with _lock:
             t = _error_words.get(index)
             if t is None:
-                t = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
+                word = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
                 torch.cuda.current_stream(index).synchronize()   # zero for every stream
-                _error_words[index] = t
+                t = _error_words[index] = (word, word.data_ptr())
     return t
 
 
@@ -51,7 +69,7 @@ def moe_error(device=None) -> int:
     if index is None:
         index = torch.cuda.current_device()
     torch.cuda.synchronize(index)
-    t = _error_word(index)
+    t = _error_word(index)[0]
     bits = int(t.item())
     if bits:
         t.zero_()
@@ -59,50 +77,46 @@ def moe_error(device=None) -> int:
     return bits
 
 
-class _On:
-    """Makes the tensors' device and the call's stream current."""
+@functools.lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(_lib.load(), name)
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
+
+def _on_stream(call):
+    """``stream`` of a call: what it allocates and launches goes there, with
+    the first tensor's device current."""
+    @functools.wraps(call)
+    def wrapper(first, *args, stream=None, **options):
+        if first is None or not first.is_cuda:
+            raise ValueError(f"{call.__name__}: tensors must be on a CUDA device")
+        index = first.get_device()
+        if stream is None:
+            if torch._C._cuda_getDevice() == index:
+                return call(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **options)
+            with torch.cuda.device(index):
+                return call(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **options)
+        if stream.device != first.device:
             raise ValueError("the stream is on another device than the tensors")
-        self.guard = None
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.index = device.index
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _on_gpu(t: torch.Tensor, what: str):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on a CUDA device")
+        with torch.cuda.stream(stream):
+            return call(first, *args, stream=stream.cuda_stream, **options)
+    return wrapper
 
 
 def _same_device(like: torch.Tensor, **tensors):
+    index = like.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != like.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} must be on {like.device}")
 
 
 # ------------------------------------------------------------ routing
 
-def _route_desc(logits, topk, num_tokens, score="softmax", renormalize=True, scale=1.0,
-                balance_coef=0.0, z_coef=0.0):
-    """Descriptor, token counts, and the (W, T) that a [T][E] or [W][T][E]
-    tensor of logits stands for."""
-    _on_gpu(logits, "logits")
-    if logits.dim() not in (2, 3) or logits.dtype not in _ROUTE_DTYPES:
+@functools.lru_cache(maxsize=1024)
+def _route_plan(shape, strides, dtype, topk, num_tokens, score, renormalize, scale, balance_coef, z_coef):
+    """Descriptor, token counts, lead shape, T, E and the losses' scratch
+    bytes for [T][E] or [W][T][E] logits."""
+    if len(shape) not in (2, 3) or dtype not in _ROUTE_DTYPES:
         raise ValueError("logits must be bf16, fp16 or fp32 [T][E] or [W][T][E]")
-    shape = tuple(logits.shape)
     W, T, E = shape if len(shape) == 3 else (1, *shape)
     if not 1 <= E <= _lib.EP_MAX_ROUTE_EXPERTS:
         raise ValueError(f"1 to {_lib.EP_MAX_ROUTE_EXPERTS} experts, not {E}")
@@ -112,25 +126,33 @@ def _route_desc(logits, topk, num_tokens, score="softmax", renormalize=True, sca
         raise ValueError(f"topk must be 1 to {min(E, _lib.EP_MAX_TOPK)}, not {topk}")
     if score not in _SCORES:
         raise ValueError(f"score {score!r}: one of {sorted(_SCORES)}")
-    strides = logits.stride()
     if (strides[-1] != 1 and E > 1) or (strides[-2] < E and T > 1):
         raise ValueError("the rows of logits must be contiguous and must not overlap")
     if num_tokens is None:
-        counts = [T] * W
-    else:
-        counts = [int(n) for n in num_tokens]
-        if len(counts) != W or min(counts) < 0 or max(counts) > T:
-            raise ValueError(f"num_tokens must be {W} counts of 0 to {T}")
-    desc = EpRouteDescC(W, T, E, topk, _ROUTE_DTYPES[logits.dtype], _SCORES[score], int(bool(renormalize)),
-                        scale, balance_coef, z_coef, max(strides[-2], E), strides[0] if W > 1 else 0)
-    return desc, (ctypes.c_int32 * W)(*counts), W, T, E
+        num_tokens = (T,) * W
+    if len(num_tokens) != W or min(num_tokens) < 0 or max(num_tokens) > T:
+        raise ValueError(f"num_tokens must be {W} counts of 0 to {T}")
+    desc = _ROUTE_DESC.pack(W, T, E, topk, _ROUTE_DTYPES[dtype], _SCORES[score], int(bool(renormalize)),
+                            scale, balance_coef, z_coef, max(strides[-2], E), strides[0] if W > 1 else 0)
+    need = ctypes.c_size_t(0)
+    if T:
+        check(_entry("ep_balance_loss_workspace")(desc, ctypes.byref(need)), "ep_balance_loss_workspace")
+    return desc, struct.pack(f"{W}i", *num_tokens), tuple(shape[:-1]), T, E, need.value
+
+
+def _plan(logits, topk, num_tokens, score="softmax", renormalize=True, scale=1.0, balance_coef=0.0, z_coef=0.0):
+    if num_tokens is not None:
+        num_tokens = tuple(map(int, num_tokens))
+    return _route_plan(logits.shape, logits.stride(), logits.dtype, topk, num_tokens, score, renormalize,
+                       float(scale), float(balance_coef), float(z_coef))
 
 
 def _dense(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
 
 
+@_on_stream
 def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormalize: bool = True,
           scale: float = 1.0, bias: Optional[torch.Tensor] = None,
           num_tokens: Optional[Sequence[int]] = None, stream=None):
@@ -141,49 +163,42 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormaliz
     logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
     [...][topk], as ``EpDispatchCombineOp.dispatch`` takes them; tokens
     t >= num_tokens[w] get weights 0 and indices -1."""
-    desc, counts, W, T, E = _route_desc(logits, topk, num_tokens, score, renormalize, scale)
+    desc, counts, lead, T, E, _ = _plan(logits, topk, num_tokens, score, renormalize, scale)
     if bias is not None:
         _same_device(logits, bias=bias)
         _dense(bias, torch.float32, (E,), "bias")
-    lead = logits.shape[:-1]
-    with _On(logits.device, stream) as st:
-        w = torch.empty((*lead, topk), dtype=torch.float32, device=logits.device)
-        idx = torch.empty((*lead, topk), dtype=torch.int32, device=logits.device)
-        if T == 0:
-            return w, idx
-        check(_lib.load().ep_route(ctypes.byref(desc), logits.data_ptr(),
-                                   None if bias is None else bias.data_ptr(), counts, w.data_ptr(),
-                                   idx.data_ptr(), st), "ep_route")
+    device = logits.device
+    w = torch.empty((*lead, topk), dtype=torch.float32, device=device)
+    idx = torch.empty((*lead, topk), dtype=torch.int32, device=device)
+    if T:
+        check(_entry("ep_route")(desc, logits.data_ptr(), None if bias is None else bias.data_ptr(), counts,
+                                 w.data_ptr(), idx.data_ptr(), stream), "ep_route")
     return w, idx
 
 
-def _backward(grad_weights, logits, indices, topk, grad_loss, counts, num_tokens, stream, **options):
-    desc, nt, W, T, E = _route_desc(logits, topk, num_tokens, **options)
-    _same_device(logits, grad_weights=grad_weights, indices=indices, grad_loss=grad_loss, counts=counts)
-    lead = logits.shape[:-1]
+def _backward(grad_weights, logits, indices, topk, grad_loss, loss_counts, num_tokens, stream, *options):
+    desc, counts, lead, T, E, _ = _plan(logits, topk, num_tokens, *options)
+    _same_device(logits, grad_weights=grad_weights, indices=indices, grad_loss=grad_loss, counts=loss_counts)
+    gw = idx = gl = lc = None
     if grad_weights is not None:
         _dense(grad_weights, torch.float32, (*lead, topk), "grad_weights")
         _dense(indices, torch.int32, (*lead, topk), "indices")
+        gw, idx = grad_weights.data_ptr(), indices.data_ptr()
     if grad_loss is not None:
-        if counts is None:
+        if loss_counts is None:
             raise ValueError("grad_loss needs the counts of balance_loss")
         if grad_loss.dtype != torch.float32 or grad_loss.numel() != 1:
             raise ValueError("grad_loss must be one fp32 value on the device")
-        _dense(counts, torch.int32, (E,), "counts")
-    with _On(logits.device, stream) as st:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        if T == 0:
-            return out
-        check(_lib.load().ep_route_backward(
-            ctypes.byref(desc), logits.data_ptr(),
-            None if grad_weights is None else grad_weights.data_ptr(),
-            None if grad_weights is None else indices.data_ptr(),
-            None if grad_loss is None else grad_loss.data_ptr(),
-            None if grad_loss is None else counts.data_ptr(), nt, out.data_ptr(),
-            _error_word(logits.device.index).data_ptr(), st), "ep_route_backward")
+        _dense(loss_counts, torch.int32, (E,), "counts")
+        gl, lc = grad_loss.data_ptr(), loss_counts.data_ptr()
+    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if T:
+        check(_entry("ep_route_backward")(desc, logits.data_ptr(), gw, idx, gl, lc, counts, out.data_ptr(),
+                                          _error_word(logits.get_device())[1], stream), "ep_route_backward")
     return out
 
 
+@_on_stream
 def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, indices: torch.Tensor, *,
                    score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
                    num_tokens: Optional[Sequence[int]] = None, grad_loss: Optional[torch.Tensor] = None,
@@ -193,110 +208,114 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, indices: to
     With grad_loss (one fp32 value) and counts, the gradient of
     ``balance_loss`` with these coefficients is added in the same pass."""
     return _backward(grad_weights, logits, indices, indices.shape[-1], grad_loss, counts, num_tokens,
-                     stream, score=score, renormalize=renormalize, scale=scale,
-                     balance_coef=balance_coef, z_coef=z_coef)
+                     stream, score, renormalize, scale, balance_coef, z_coef)
 
 
+@_on_stream
 def balance_loss(logits: torch.Tensor, indices: torch.Tensor, *, balance_coef: float = 1.0,
                  z_coef: float = 0.0, num_tokens: Optional[Sequence[int]] = None, stream=None):
     """Balance and z losses of a routing.  Returns (loss fp32 [3]: total,
     balance, z; counts int32 [E]: how often each expert was chosen; probs fp32
     [E]: mean router probability), over the tokens t < num_tokens[w]."""
     topk = indices.shape[-1]
-    desc, nt, W, T, E = _route_desc(logits, topk, num_tokens, balance_coef=balance_coef, z_coef=z_coef)
+    desc, nt, lead, T, E, need = _plan(logits, topk, num_tokens, "softmax", True, 1.0, balance_coef, z_coef)
     _same_device(logits, indices=indices)
-    _dense(indices, torch.int32, (*logits.shape[:-1], topk), "indices")
-    L = _lib.load()
-    dev = logits.device
-    with _On(dev, stream) as st:
-        loss = torch.empty(3, dtype=torch.float32, device=dev)
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-        probs = torch.empty(E, dtype=torch.float32, device=dev)
-        if T == 0:
-            return loss.zero_(), counts.zero_(), probs.zero_()
-        need = ctypes.c_size_t(0)
-        check(L.ep_balance_loss_workspace(ctypes.byref(desc), ctypes.byref(need)), "ep_balance_loss_workspace")
-        scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        check(L.ep_balance_loss(ctypes.byref(desc), logits.data_ptr(), indices.data_ptr(), nt,
-                                loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), scratch.data_ptr(),
-                                need.value, _error_word(dev.index).data_ptr(), st), "ep_balance_loss")
+    _dense(indices, torch.int32, (*lead, topk), "indices")
+    device = logits.device
+    loss = torch.empty(3, dtype=torch.float32, device=device)
+    counts = torch.empty(E, dtype=torch.int32, device=device)
+    probs = torch.empty(E, dtype=torch.float32, device=device)
+    if T == 0:
+        return loss.zero_(), counts.zero_(), probs.zero_()
+    scratch = torch.empty(need, dtype=torch.uint8, device=device)
+    check(_entry("ep_balance_loss")(desc, logits.data_ptr(), indices.data_ptr(), nt, loss.data_ptr(),
+                                    counts.data_ptr(), probs.data_ptr(), scratch.data_ptr(), need,
+                                    _error_word(logits.get_device())[1], stream), "ep_balance_loss")
     return loss, counts, probs
 
 
+@_on_stream
 def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, counts: torch.Tensor, topk: int, *,
                           balance_coef: float = 1.0, z_coef: float = 0.0,
                           num_tokens: Optional[Sequence[int]] = None, stream=None) -> torch.Tensor:
     """Gradient of ``balance_loss``'s total by the logits; grad_loss is one
     fp32 value on the device, counts those that ``balance_loss`` returned."""
-    if grad_loss is None:
-        raise ValueError("grad_loss must be one fp32 value on the device")
     return _backward(None, logits, None, topk, grad_loss, counts, num_tokens, stream,
-                     balance_coef=balance_coef, z_coef=z_coef)
+                     "softmax", True, 1.0, balance_coef, z_coef)
 
 
 # ------------------------------------------------------------ products
 
-def _rows(t: Optional[torch.Tensor], like, width: int, name: str) -> EpRowsC:
+@functools.lru_cache(maxsize=1024)
+def _strides_of(shape, strides, name):
+    """(rank stride, row stride) of rows that the kernels can read."""
+    rank = strides[0] if len(strides) == 3 and shape[0] > 1 else 0
+    row = strides[-2] if shape[-2] > 1 else -(-shape[-1] // 8) * 8
+    if (strides[-1] != 1 or row < shape[-1] or (row | rank) % 8
+            or (rank == 0 and len(strides) == 3 and shape[0] > 1)):
+        raise ValueError(f"{name}: contiguous rows, with strides of a multiple of 8 elements")
+    return rank, row
+
+
+def _strided(t: torch.Tensor, name: str):
+    rank, row = _strides_of(t.shape, t.stride(), name)
+    ptr = t.data_ptr()
+    if ptr % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    return ptr, rank, row
+
+
+def _rows(t: torch.Tensor, like, width: int, name: str) -> bytes:
     """A [rows][width] or [R][rows][width] tensor of x's type and rows."""
-    if t is None:
-        return EpRowsC(None, 0, 0)
-    shape = tuple(t.shape)
-    if t.dtype != like.dtype or shape[:-1] != tuple(like.shape[:-1]) or shape[-1] != width:
+    if t.dtype != like.dtype or t.shape[:-1] != like.shape[:-1] or t.shape[-1] != width:
         raise ValueError(f"{name} must be {like.dtype} {[*like.shape[:-1], width]}")
-    return _strided(t, name)
+    return _ROWS.pack(*_strided(t, name))
 
 
-def _strided(t: torch.Tensor, name: str) -> EpRowsC:
-    strides = t.stride()
-    rank = strides[0] if len(strides) == 3 and t.shape[0] > 1 else 0
-    row = strides[-2] if t.shape[-2] > 1 else -(-t.shape[-1] // 8) * 8
-    if (strides[-1] != 1 or row < t.shape[-1] or (row | rank) % 8 or t.data_ptr() % 16
-            or (rank == 0 and len(strides) == 3 and t.shape[0] > 1)):
-        raise ValueError(f"{name}: contiguous rows, 16-byte aligned, with strides of a multiple of 8 elements")
-    return EpRowsC(t.data_ptr(), rank, row)
-
-
-def _product_desc(x, weight, count, offset, activation):
-    _on_gpu(x, "x")
-    if x.dtype not in _PRODUCT_DTYPES or x.dim() not in (2, 3):
+@functools.lru_cache(maxsize=1024)
+def _product_plan(xshape, wshape, dtype, wdtype, activation, grouped):
+    """The descriptor's head, rows, N, wide, groups, and the gradient's
+    workspace bytes."""
+    if dtype not in _PRODUCT_DTYPES or len(xshape) not in (2, 3):
         raise ValueError("x must be bf16 or fp16 [rows][K] or [R][rows][K]")
-    shape = tuple(x.shape)
-    R, rows, K = shape if len(shape) == 3 else (1, *shape)
+    R, rows, K = xshape if len(xshape) == 3 else (1, *xshape)
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation {activation!r}: one of {sorted(_ACTIVATIONS)}")
-    if weight.dtype != x.dtype or weight.dim() != 3 or weight.shape[2] != K:
-        raise ValueError(f"weight must be {x.dtype} [groups][features][{K}]")
-    G, wide = weight.shape[0], weight.shape[1]
+    if wdtype != dtype or len(wshape) != 3 or wshape[2] != K:
+        raise ValueError(f"weight must be {dtype} [groups][features][{K}]")
+    G, wide = wshape[0], wshape[1]
     N = wide // 2 if activation == "swiglu" else wide
     if K % 8 or K == 0 or N % 8 or N == 0 or (activation == "swiglu" and wide % 2):
         raise ValueError("feature counts must be multiples of 8")
     if R < 1 or G % R or G == 0:
         raise ValueError(f"{G} groups do not divide over {R} ranks")
+    if not grouped and G != R:
+        raise ValueError("without count and offset there is one group per rank")
+    head = _PRODUCT_HEAD.pack(R, G // R, rows, K, N, _PRODUCT_DTYPES[dtype], _ACTIVATIONS[activation], 0)
+    # pointers of the right kind: the size depends on the head alone
+    fake = head + _PRODUCT_TAIL.pack(16 if grouped else 0, 16 if grouped else 0, 16, 8 * wide * K, K, 16, 8 * rows * K or 8, K)
+    need = ctypes.c_size_t(0)
+    check(_entry("ep_expert_product_workspace")(fake, ctypes.byref(need)), "ep_expert_product_workspace")
+    return head, rows, N, wide, G, need.value
+
+
+def _product_desc(x, weight, count, offset, activation):
+    head, rows, N, wide, G, need = _product_plan(x.shape, weight.shape, x.dtype, weight.dtype, activation,
+                                                 count is not None)
     _same_device(x, weight=weight, count=count, offset=offset)
     if (count is None) != (offset is None):
         raise ValueError("count and offset come together")
-    if count is None:
-        if G != R:
-            raise ValueError("without count and offset there is one group per rank")
-    else:
-        for name, t in (("count", count), ("offset", offset)):
-            if t.dtype != torch.int32 or t.numel() != G or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous int32 [{R}][{G // R}]")
-    desc = EpProductDescC(R, G // R, rows, K, N, _PRODUCT_DTYPES[x.dtype], _ACTIVATIONS[activation], 0,
-                          None if count is None else count.data_ptr(),
-                          None if offset is None else offset.data_ptr(),
-                          _strided(weight, "weight"), _strided(x, "x") if rows else EpRowsC(None, 0, 0))
-    return desc, N, wide
+    c = o = 0
+    if count is not None:
+        if (count.dtype != torch.int32 or offset.dtype != torch.int32 or count.numel() != G or offset.numel() != G
+                or not count.is_contiguous() or not offset.is_contiguous()):
+            raise ValueError(f"count and offset must be contiguous int32 of {G} groups")
+        c, o = count.data_ptr(), offset.data_ptr()
+    desc = head + _PRODUCT_TAIL.pack(c, o, *_strided(weight, "weight"), *(_strided(x, "x") if rows else (0, 0, 0)))
+    return desc, rows, N, wide, G, need
 
 
-def _bias(bias, x, G, wide):
-    if bias is None:
-        return None
-    _same_device(x, bias=bias)
-    _dense(bias, x.dtype, (G, wide), "bias")
-    return bias.data_ptr()
-
-
+@_on_stream
 def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.Tensor] = None,
                    offset: Optional[torch.Tensor] = None, *, bias: Optional[torch.Tensor] = None,
                    activation: str = "none", residual: Optional[torch.Tensor] = None,
@@ -310,22 +329,32 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.
     features].  residual and out: [...][N].  Returns y, or (y, pre) with
     save_pre: what ``expert_product_backward`` needs.  Rows outside every
     group are unspecified (untouched in ``out``)."""
-    desc, N, wide = _product_desc(x, weight, count, offset, activation)
-    _same_device(x, residual=residual, out=out)
-    b = _bias(bias, x, weight.shape[0], wide)
-    res = _rows(residual, x, N, "residual")
+    desc, rows, N, wide, G, _ = _product_desc(x, weight, count, offset, activation)
+    b, res, pre, p = None, _NO_ROWS, None, _NO_ROWS
+    if bias is not None:
+        _same_device(x, bias=bias)
+        _dense(bias, x.dtype, (G, wide), "bias")
+        b = bias.data_ptr()
+    if residual is not None:
+        _same_device(x, residual=residual)
+        res = _rows(residual, x, N, "residual")
     lead = x.shape[:-1]
-    with _On(x.device, stream) as st:
-        y = torch.empty((*lead, N), dtype=x.dtype, device=x.device) if out is None else out
-        pre = torch.empty((*lead, wide), dtype=x.dtype, device=x.device) if save_pre else None
-        if desc.rows:
-            check(_lib.load().ep_expert_product(
-                ctypes.byref(desc), b, ctypes.byref(res), ctypes.byref(_rows(y, x, N, "out")),
-                ctypes.byref(_rows(pre, x, wide, "pre")), _error_word(x.device.index).data_ptr(), st),
-                "ep_expert_product")
+    if out is None:
+        y = torch.empty((*lead, N), dtype=x.dtype, device=x.device)
+    else:
+        _same_device(x, out=out)
+        y = out
+    o = _rows(y, x, N, "out")
+    if save_pre:
+        pre = torch.empty((*lead, wide), dtype=x.dtype, device=x.device)
+        p = _rows(pre, x, wide, "pre")
+    if rows:
+        check(_entry("ep_expert_product")(desc, b, res, o, p, _error_word(x.get_device())[1], stream),
+              "ep_expert_product")
     return (y, pre) if save_pre else y
 
 
+@_on_stream
 def expert_product_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                             count: Optional[torch.Tensor] = None, offset: Optional[torch.Tensor] = None, *,
                             pre: Optional[torch.Tensor] = None, activation: str = "none",
@@ -334,22 +363,18 @@ def expert_product_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.T
     None) from grad = dL/dy.  pre: the forward's (not needed for "none").  The
     residual's gradient is grad itself.  Rows of grad_x outside every group
     are unspecified; a group without rows gets zero gradients."""
-    desc, N, wide = _product_desc(x, weight, count, offset, activation)
+    desc, rows, N, wide, G, need = _product_desc(x, weight, count, offset, activation)
     _same_device(x, grad=grad, pre=pre)
     if pre is None and activation != "none":
         raise ValueError(f"the gradient of {activation!r} needs pre")
     g = _rows(grad, x, N, "grad")
-    p = _rows(pre, x, wide, "pre")
-    L = _lib.load()
-    with _On(x.device, stream) as st:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(weight.shape, dtype=x.dtype, device=x.device)
-        db = torch.empty((weight.shape[0], wide), dtype=x.dtype, device=x.device) if bias_grad else None
-        need = ctypes.c_size_t(0)
-        check(L.ep_expert_product_workspace(ctypes.byref(desc), ctypes.byref(need)), "ep_expert_product_workspace")
-        scratch = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        check(L.ep_expert_product_backward(
-            ctypes.byref(desc), ctypes.byref(g), ctypes.byref(p), ctypes.byref(_rows(dx, x, x.shape[-1], "x")),
-            dw.data_ptr(), None if db is None else db.data_ptr(), scratch.data_ptr(), need.value,
-            _error_word(x.device.index).data_ptr(), st), "ep_expert_product_backward")
+    p = _NO_ROWS if pre is None else _rows(pre, x, wide, "pre")
+    device = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+    dw = torch.empty(weight.shape, dtype=x.dtype, device=device)
+    db = torch.empty((G, wide), dtype=x.dtype, device=device) if bias_grad else None
+    scratch = torch.empty(need, dtype=torch.uint8, device=device)
+    check(_entry("ep_expert_product_backward")(
+        desc, g, p, _rows(dx, x, x.shape[-1], "x"), dw.data_ptr(), None if db is None else db.data_ptr(),
+        scratch.data_ptr(), need, _error_word(x.get_device())[1], stream), "ep_expert_product_backward")
     return dx, dw, db
