@@ -20,7 +20,9 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
-constexpr int kLossWarps = 32;
+// Warps of a block of the losses: as many as an SM takes with 8 experts a lane;
+// longer rows need more registers.
+__host__ __device__ constexpr int loss_warps(int experts_per_lane) { return experts_per_lane == 8 ? 32 : 8; }
 
 struct RouteParams {
     const void *logits;
@@ -28,6 +30,8 @@ struct RouteParams {
     TokenCounts nt;
     int W, T, E, k;
     bool vec;                // rows of logits (and of their gradient) in 16-byte pieces
+    bool vec_e;              // per-expert inputs in 16-byte pieces
+    int rounds;              // backward: runs of tokens of a warp
     float scale;
     const float *bias;       // forward
     float *w;                // forward
@@ -40,6 +44,8 @@ struct RouteParams {
     float balance_coef, z_coef, inv_n;
     float *part;             // loss: [blocks][E + 1] partial sums
     int32_t *part_count;     // loss: [blocks][E]
+    float *tail;             // loss: [final blocks + 1] shares of the loss, z
+    uint32_t *ticket;        // loss: final blocks that are done
     float *loss, *probs;
     int32_t *counts_out;
     uint32_t *error;
@@ -58,14 +64,14 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return
 // NaN reads as -inf (closed), +inf as the largest finite number, so that
 // differences of logits are never inf - inf between open experts.
 __device__ __forceinline__ float sane_logit(float v) {
-    return v != v ? -INFINITY : fminf(v, FLT_MAX);
+    return fminf(fmaxf(v, -INFINITY), FLT_MAX);     // fmaxf drops a NaN
 }
 
 // Unsigned integers in the order of the floats (-0 counts as +0).  Every
 // value, -inf included, maps above 0, which marks "no candidate".
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Reductions over the LANES lanes of a token.
@@ -85,41 +91,55 @@ template <int LANES> __device__ __forceinline__ uint32_t row_max_key(uint32_t v)
     for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// exp of a difference of logits, within 2^-22 (1 + |d| / 2) of it: the callers'
-// sums and 1e-5 tolerances are far above.
-__device__ __forceinline__ float exp_diff(float d) { return __expf(d); }
+// exp of a difference of logits (<= 0) as a power of two: relative error below
+// 2^-22 + |d| 2^-23, results below 2^-126 are 0.  Terms with a large |d| weigh
+// exp(d) of the largest one.
+__device__ __forceinline__ float exp_diff(float d) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.44269504088896341f));
+    return r;
+}
 
 template <typename T>
 __device__ __forceinline__ const T *logit_row(const RouteParams &p, int s, int t) {
     return static_cast<const T *>(p.logits) + s * p.rank_stride + t * p.row_stride;
 }
 
-// Experts l * VPL .. l * VPL + VPL - 1 of a row; -inf past the last expert.
-template <typename T, int VPL>
-__device__ __forceinline__ void load_row(const RouteParams &p, const T *row, int l, float *x) {
-    constexpr int kPer = 16 / sizeof(T);
-    if (p.vec) {             // E is a multiple of 8: every piece is inside or outside
+// Experts l * VPL .. l * VPL + VPL - 1 of a row, as they lie in memory, and
+// as fp32 with -inf past the last expert.  Two steps, so that the next row's
+// load can be on its way while a row is worked on.
+template <typename T, int VPL> struct RawRow {
+    static constexpr int kPer = 16 / sizeof(T);
+    uint4 v[VPL / kPer];
+
+    __device__ __forceinline__ void load(const RouteParams &p, const T *row, int l, bool present) {
+        if (!present) {
+            const T shut = from_f32<T>(-INFINITY);
+            T *s = reinterpret_cast<T *>(v);
 #pragma unroll
-        for (int c = 0; c < VPL; c += kPer) {
-            const int e = l * VPL + c;
-            if (e < p.E) {
-                const uint4 v = ld_stream16(row + e);
-                const T *s = reinterpret_cast<const T *>(&v);
+            for (int i = 0; i < VPL; ++i) s[i] = shut;
+        } else if (p.vec) {  // E is a multiple of 8: every piece is inside or outside
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[c + i] = sane_logit(to_f32(s[i]));
-            } else {
+            for (int c = 0; c < VPL / kPer; ++c)
+                if (l * VPL + c * kPer < p.E) v[c] = ld_stream16(row + l * VPL + c * kPer);
+        } else {
+            T *s = reinterpret_cast<T *>(v);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[c + i] = -INFINITY;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = l * VPL + i;
-            x[i] = e < p.E ? sane_logit(to_f32(row[e])) : -INFINITY;
+            for (int i = 0; i < VPL; ++i)
+                if (l * VPL + i < p.E) s[i] = row[l * VPL + i];
         }
     }
-}
+    __device__ __forceinline__ void values(const RouteParams &p, int l, float *x) const {
+        const T *s = reinterpret_cast<const T *>(v);
+        if ((l + 1) * VPL <= p.E) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) x[i] = sane_logit(to_f32(s[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) x[i] = l * VPL + i < p.E ? sane_logit(to_f32(s[i])) : -INFINITY;
+        }
+    }
+};
 template <typename T, int VPL>
 __device__ __forceinline__ void store_row(const RouteParams &p, T *row, int l, const float *d) {
     constexpr int kPer = 16 / sizeof(T);
@@ -174,17 +194,18 @@ __device__ __forceinline__ RowStats softmax_row(float *x) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// A token's place: lane l of its LANES, token t of rank blockIdx.y.
+// A token's place: lane l of its LANES, token t of rank blockIdx.y.  A warp
+// takes `rounds` runs of 32 / LANES tokens.
 template <int LANES> struct Place {
+    static constexpr int kTokens = 32 / LANES;           // of a warp and round
     int l, s, t;
     int64_t tok;
     bool in, present;
-    __device__ explicit Place(const RouteParams &p, int warps) {
-        constexpr int kTokens = 32 / LANES;              // of a warp
+    __device__ Place(const RouteParams &p, int warps, int rounds, int round) {
         const int lane = threadIdx.x & 31;
         l = lane % LANES;
         s = blockIdx.y;
-        t = (blockIdx.x * warps + (threadIdx.x >> 5)) * kTokens + lane / LANES;
+        t = ((blockIdx.x * warps + (threadIdx.x >> 5)) * rounds + round) * kTokens + lane / LANES;
         tok = (int64_t)s * p.T + t;
         in = t < p.T;
         present = t < p.nt.n[s];
@@ -210,7 +231,7 @@ __device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const R
         m = row_max<LANES>(m);
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
-            v[q] = mine[q] && m > -INFINITY ? expf(c[q] - m) : 0.f;
+            v[q] = mine[q] && m > -INFINITY ? exp_diff(c[q] - m) : 0.f;
             *sum += v[q];
         }
         *sum = row_sum<LANES>(*sum);
@@ -233,32 +254,46 @@ template <typename T, int LANES, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool softmax,
                                                                  bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
-    const Place<LANES> at(p, kRouteWarps);
+    const Place<LANES> at(p, kRouteWarps, 1, 0);
+    if (!__any_sync(0xffffffffu, at.present)) {          // nobody here
+        for (int j = at.l; at.in && j < p.k; j += LANES) {
+            p.w[at.tok * p.k + j] = 0.f;
+            p.idx_out[at.tok * p.k + j] = -1;
+        }
+        return;
+    }
     const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
-    float x[VPL];
-    if (at.present) {
-        load_row<T, VPL>(p, row, at.l, x);
+    RawRow<T, VPL> raw;
+    raw.load(p, row, at.l, at.present);
+    float x[VPL], y[VPL];
+    const int e0 = at.l * VPL;
+    if (p.bias && p.vec_e && e0 < p.E) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += 4) {
+            const float4 b = *reinterpret_cast<const float4 *>(p.bias + e0 + i);
+            y[i] = b.x; y[i + 1] = b.y; y[i + 2] = b.z; y[i + 3] = b.w;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) x[i] = -INFINITY;
+        for (int i = 0; i < VPL; ++i) y[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
     }
+    raw.values(p, at.l, x);
     // this lane's best and second best key: the larger one, or the earlier expert
     uint32_t key[VPL], best = 0, second = 0;
     int be = 0, se = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int e = at.l * VPL + i;
-        key[i] = e < p.E ? order_key(p.bias ? x[i] + p.bias[e] : x[i]) : 0u;
+        key[i] = e0 + i < p.E ? order_key(x[i] + y[i]) : 0u;
         const bool first = key[i] > best, next = key[i] > second;
-        second = first ? best : next ? key[i] : second;
+        second = max(second, min(best, key[i]));
         se = first ? be : next ? i : se;
-        best = first ? key[i] : best;
+        best = max(best, key[i]);
         be = first ? i : be;
     }
     const uint32_t lanes = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
     int id[SLOTS];
 #pragma unroll
-    for (int q = 0; q < SLOTS; ++q) id[q] = -1;
+    for (int q = 0; q < SLOTS; ++q) id[q] = 0;
     for (int j = 0; j < p.k; ++j) {
         const uint32_t top = row_max_key<LANES>(best);
         const uint32_t who = __ballot_sync(0xffffffffu, best == top) & lanes;
@@ -288,9 +323,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
                     const bool open = key[i] < last || (key[i] == last && i > le);
                     const uint32_t v = open ? key[i] : 0u;
                     const bool first = v > best, next = v > second;
-                    second = first ? best : next ? v : second;
+                    second = max(second, min(best, v));
                     se = first ? be : next ? i : se;
-                    best = first ? v : best;
+                    best = max(best, v);
                     be = first ? i : be;
                 }
             }
@@ -320,130 +355,140 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 // The weights' gradient is nonzero at the chosen experts (and, for a softmax
 // that is not renormalised, dense): the row meets in shared memory, where the
 // chosen experts' terms are added to the dense part, one choice after the
-// other where an expert was chosen twice.
+// other where an expert was chosen twice.  The experts' loads, the same for
+// all tokens, stay in registers over a warp's tokens.
 template <typename T, int LANES, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const RouteParams p, bool softmax, bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
     constexpr int kTokens = 32 / LANES, kRow = LANES * VPL;
     __shared__ __align__(16) float rows[kRouteWarps * kTokens][kRow + 4];
-    const Place<LANES> at(p, kRouteWarps);
-    const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
-    float d[VPL], pr[VPL];
-    RowStats st = {0.f, 1.f, false};
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) d[i] = 0.f;
-    if (p.grad_loss || (softmax && !renorm)) {
-        if (at.present) {
-            load_row<T, VPL>(p, row, at.l, pr);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) pr[i] = -INFINITY;
-        }
-        st = softmax_row<LANES, VPL>(pr);
-    }
+    const bool dense = p.grad_loss || (softmax && !renorm);
+    const int e0 = (int)(threadIdx.x & 31) % LANES * VPL;
+    float f[VPL], gl = 0.f;
     if (p.grad_loss) {
-        const float gl = *p.grad_loss * p.inv_n, lse = st.lse();
-        const float share = p.inv_n * ((float)p.E / (float)p.k);
-        float f[VPL], dot = 0.f;
+        gl = *p.grad_loss * p.inv_n;
+        const float share = p.inv_n * ((float)p.E / (float)p.k) * p.balance_coef;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = at.l * VPL + i;
-            f[i] = e < p.E ? (float)p.counts[e] * share : 0.f;
-            dot += pr[i] * f[i];
-        }
-        dot = row_sum<LANES>(dot);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            d[i] = pr[i] * ((f[i] - dot) * p.balance_coef + 2.0f * p.z_coef * lse) * gl;
+        for (int i = 0; i < VPL; ++i) f[i] = e0 + i < p.E ? (float)p.counts[e0 + i] * share : 0.f;
     }
-    if (p.grad_w) {
-        int id[SLOTS];
-        float g[SLOTS], c[SLOTS], v[SLOTS], dv[SLOTS], sum, dot = 0.f;
-        bool mine[SLOTS];
-#pragma unroll
-        for (int q = 0; q < SLOTS; ++q) {
-            const int j = q * LANES + at.l;
-            id[q] = -1;
-            g[q] = 0.f;
-            c[q] = -INFINITY;
-            if (at.present && j < p.k) {
-                id[q] = p.idx[at.tok * p.k + j];
-                if ((uint32_t)id[q] < (uint32_t)p.E) {
-                    g[q] = p.grad_w[at.tok * p.k + j] * p.scale;
-                    c[q] = sane_logit(to_f32(row[id[q]]));
-                } else {
-                    id[q] = -1;
-                    if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
-                }
-            }
-            mine[q] = id[q] >= 0;
-        }
-        chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
-#pragma unroll
-        for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
-        if (softmax || renorm) dot = row_sum<LANES>(dot);
-#pragma unroll
-        for (int q = 0; q < SLOTS; ++q) {
-            if (softmax) {
-                dv[q] = renorm ? v[q] * (g[q] - dot) : v[q] * g[q];
-            } else {
-                float s = g[q];
-                if (renorm) s = sum > 0.f ? (g[q] - dot / sum) / sum : 0.f;
-                dv[q] = s * v[q] * (1.0f - v[q]);
-            }
-        }
-        if (softmax && !renorm) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * dot;
-        }
-        float *r = rows[threadIdx.x / LANES];
-#pragma unroll
-        for (int i = 0; i < VPL; i += 4)
-            *reinterpret_cast<float4 *>(r + at.l * VPL + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-        __syncwarp();
-        // one lane a token: in order.  32: at once, unless an expert comes twice.
-        bool twice = LANES < 32;
-        if (LANES == 32) {
-            const uint32_t same = __match_any_sync(0xffffffffu, mine[0] ? id[0] : -1 - (int)(threadIdx.x & 31));
-            twice = __any_sync(0xffffffffu, (same & (same - 1u)) != 0);
-        }
-        if (!twice) {
-            if (mine[0]) r[id[0]] += dv[0];
-        } else {
-            for (int j = 0; j < p.k; ++j) {
-#pragma unroll
-                for (int q = 0; q < SLOTS; ++q)
-                    if (j == q * LANES + at.l && mine[q]) r[id[q]] += dv[q];
-                __syncwarp();
-            }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < VPL; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(r + at.l * VPL + i);
-            d[i] = f.x;
-            d[i + 1] = f.y;
-            d[i + 2] = f.z;
-            d[i + 3] = f.w;
-        }
-    }
-    if (!at.in) return;
-    if (!at.present) {
+    for (int round = 0; round < p.rounds; ++round) {
+        const Place<LANES> at(p, kRouteWarps, p.rounds, round);
+        float d[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = 0.f;
+        if (__any_sync(0xffffffffu, at.present)) {
+            const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
+            float pr[VPL];
+            RowStats st = {0.f, 1.f, false};
+            int id[SLOTS];
+            float g[SLOTS];
+            if (p.grad_w) {
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) {
+                    const int j = q * LANES + at.l;
+                    const bool mine = at.present && j < p.k;
+                    id[q] = mine ? p.idx[at.tok * p.k + j] : 0;
+                    g[q] = mine ? p.grad_w[at.tok * p.k + j] * p.scale : 0.f;
+                }
+            }
+            if (dense) {
+                RawRow<T, VPL> raw;
+                raw.load(p, row, at.l, at.present);
+                raw.values(p, at.l, pr);
+                st = softmax_row<LANES, VPL>(pr);
+            }
+            if (p.grad_loss) {
+                const float lse = 2.0f * p.z_coef * st.lse();
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) dot += pr[i] * f[i];
+                dot = row_sum<LANES>(dot);
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) d[i] = pr[i] * ((f[i] - dot) + lse) * gl;
+            }
+            if (p.grad_w) {
+                float c[SLOTS], v[SLOTS], dv[SLOTS], sum, dot = 0.f;
+                bool mine[SLOTS];
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) {
+                    mine[q] = at.present && q * LANES + at.l < p.k;
+                    if (mine[q] && (uint32_t)id[q] >= (uint32_t)p.E) {
+                        mine[q] = false;
+                        g[q] = 0.f;
+                        if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+                    }
+                    c[q] = mine[q] ? sane_logit(to_f32(row[id[q]])) : -INFINITY;
+                }
+                chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
+                if (softmax || renorm) dot = row_sum<LANES>(dot);
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) {
+                    if (softmax) {
+                        dv[q] = renorm ? v[q] * (g[q] - dot) : v[q] * g[q];
+                    } else {
+                        float s = g[q];
+                        if (renorm) s = sum > 0.f ? (g[q] - dot / sum) / sum : 0.f;
+                        dv[q] = s * v[q] * (1.0f - v[q]);
+                    }
+                }
+                if (softmax && !renorm) {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * dot;
+                }
+                float *r = rows[threadIdx.x / LANES];
+                // one lane of several choices: in order.  One choice a lane: at
+                // once, unless two lanes find each other at an expert's place.
+                bool twice = LANES < 32;
+                if (LANES == 32) {
+                    int *mark = reinterpret_cast<int *>(r);
+                    if (mine[0]) mark[id[0]] = at.l;
+                    __syncwarp();
+                    twice = __any_sync(0xffffffffu, mine[0] && mark[id[0]] != at.l);
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < VPL; i += 4)
+                    *reinterpret_cast<float4 *>(r + e0 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                __syncwarp();
+                if (!twice) {
+                    if (mine[0]) r[id[0]] += dv[0];
+                } else {
+                    for (int j = 0; j < p.k; ++j) {
+#pragma unroll
+                        for (int q = 0; q < SLOTS; ++q)
+                            if (j == q * LANES + at.l && mine[q]) r[id[q]] += dv[q];
+                        __syncwarp();
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < VPL; i += 4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(r + e0 + i);
+                    d[i] = b.x; d[i + 1] = b.y; d[i + 2] = b.z; d[i + 3] = b.w;
+                }
+                __syncwarp();
+            }
+            if (!at.present) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) d[i] = 0.f;
+            }
+        }
+        if (at.in) store_row<T, VPL>(p, static_cast<T *>(p.grad_logits) + at.tok * p.E, at.l, d);
     }
-    store_row<T, VPL>(p, static_cast<T *>(p.grad_logits) + at.tok * p.E, at.l, d);
 }
 
 // Losses, pass 1: every block sums softmax probabilities and lse^2 of its
 // tokens (a lane's tokens in registers, then lanes and warps in order) and
-// counts choices in shared memory.  Bound by instructions (about 100 a warp
-// and token of 256 experts), so one block of 32 warps per SM.
+// counts choices in shared memory.  Bound by instructions and the rows' latency:
+// 32 warps per SM, each with its next row on the way.
 template <typename T, int LANES, int VPL>
-__global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const RouteParams p, int tokens_per_warp) {
+__global__ void __launch_bounds__(loss_warps(VPL) * 32)
+    balance_partial_kernel(const RouteParams p, int tokens_per_warp) {
     extern __shared__ float sh[];                 // [kLossWarps][E + 1], then [E] counts
-    constexpr int kTokens = 32 / LANES;
+    constexpr int kTokens = 32 / LANES, kLossWarps = loss_warps(VPL);
     int32_t *cnt = reinterpret_cast<int32_t *>(sh + kLossWarps * (p.E + 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
@@ -454,15 +499,15 @@ __global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const 
     // this warp's tokens: a run of all ranks' tokens
     const int64_t total = (int64_t)p.W * p.T;
     const int64_t tok0 = ((int64_t)blockIdx.x * kLossWarps + warp) * tokens_per_warp;
-    int s = (int)(tok0 / p.T), t0 = (int)(tok0 - (int64_t)s * p.T);
-    for (int i0 = 0; i0 < tokens_per_warp; i0 += kTokens) {
-        int t = t0 + i0 + lane / LANES, r = s;
+    int r = (int)(tok0 / p.T), t = (int)(tok0 - (int64_t)r * p.T) + lane / LANES, i = lane / LANES;
+    RawRow<T, VPL> raw, ahead;
+    bool present = false;
+    auto fetch = [&] {                           // the row of this lane's token i; then on to the next
         while (t >= p.T && r < p.W) {
             t -= p.T;
             ++r;
         }
-        const bool present = i0 + lane / LANES < tokens_per_warp && tok0 + i0 + lane / LANES < total && t < p.nt.n[r];
-        float x[VPL];
+        present = i < tokens_per_warp && tok0 + i < total && t < p.nt.n[r];
         if (present) {
             const int64_t tok = (int64_t)r * p.T + t;
             for (int j = l; j < p.k; j += LANES) {
@@ -470,15 +515,21 @@ __global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const 
                 if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&cnt[id], 1);
                 else if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
             }
-            load_row<T, VPL>(p, logit_row<T>(p, r, t), l, x);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) x[i] = -INFINITY;
         }
+        ahead.load(p, present ? logit_row<T>(p, r, t) : nullptr, l, present);
+        t += kTokens;
+        i += kTokens;
+    };
+    fetch();
+    for (int i0 = 0; i0 < tokens_per_warp; i0 += kTokens) {
+        raw = ahead;
+        if (i0 + kTokens < tokens_per_warp) fetch();
+        float x[VPL];
+        raw.values(p, l, x);
         const float lse = softmax_row<LANES, VPL>(x).lse();
         z += l == 0 ? lse * lse : 0.f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += x[i];
+        for (int j = 0; j < VPL; ++j) acc[j] += x[j];
     }
     // the warp's tokens of other lanes with the same experts
 #pragma unroll
@@ -502,61 +553,75 @@ __global__ void __launch_bounds__(kLossWarps * 32) balance_partial_kernel(const 
         p.part[(int64_t)blockIdx.x * (p.E + 1) + e] = sum;
         if (e < p.E) p.part_count[(int64_t)blockIdx.x * p.E + e] = cnt[e];
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
 }
 
-// Losses, pass 2: one block joins the blocks' sums; lanes are experts, warp w
-// takes blocks w, w + 32, ..., and the warps' sums are added in order.
+// Losses, pass 2: a block joins the parts of 32 experts; lanes are experts,
+// warp w takes parts w, w + 32, ..., and the warps' sums are added in order.  The
+// last block to finish adds up the loss.
 __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p, int blocks) {
     __shared__ float sh[32][33];
     __shared__ int32_t sc[32][33];
+    __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float balance = 0.f, z = 0.f;                 // warp 0's
-    for (int e0 = 0; e0 <= p.E; e0 += 32) {
-        const int e = e0 + lane;
-        float sum = 0.f;
-        int32_t c = 0;
-        if (e <= p.E)
-            for (int b = warp; b < blocks; b += 32) {
-                sum += p.part[(int64_t)b * (p.E + 1) + e];
-                if (e < p.E) c += p.part_count[(int64_t)b * p.E + e];
-            }
-        sh[warp][lane] = sum;
-        sc[warp][lane] = c;
-        __syncthreads();
-        if (warp == 0 && e <= p.E) {
-            sum = 0.f;
-            c = 0;
-            for (int w = 0; w < 32; ++w) {
-                sum += sh[w][lane];
-                c += sc[w][lane];
-            }
-            sum *= p.inv_n;
-            if (e < p.E) {
-                p.probs[e] = sum;
-                p.counts_out[e] = c;
-                balance += (float)c * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
-            } else {
-                z = sum;
-            }
-        }
-        __syncthreads();
+    const int e = blockIdx.x * 32 + lane;
+    grid_dependency_wait();
+    float sum = 0.f;
+    int32_t c = 0;
+#pragma unroll 5
+    for (int b = warp; b < blocks; b += 32) {
+        if (e <= p.E) sum += p.part[(int64_t)b * (p.E + 1) + e];
+        if (e < p.E) c += p.part_count[(int64_t)b * p.E + e];
     }
+    sh[warp][lane] = sum;
+    sc[warp][lane] = c;
+    __syncthreads();
     if (warp == 0) {
+        sum = 0.f;
+        c = 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) {
+            sum += sh[w][lane];
+            c += sc[w][lane];
+        }
+        sum *= p.inv_n;
+        float balance = 0.f;
+        if (e < p.E) {
+            p.probs[e] = sum;
+            p.counts_out[e] = c;
+            balance = (float)c * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
+        } else if (e == p.E) {
+            p.tail[gridDim.x] = sum;                     // z
+        }
         balance = row_sum<32>(balance);
-        z = row_sum<32>(z);
-        if (lane == 0) {
-            p.loss[0] = p.balance_coef * balance + p.z_coef * z;
-            p.loss[1] = balance;
-            p.loss[2] = z;
+        if (lane == 0) p.tail[blockIdx.x] = balance;
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) last = atom_add_acq_rel_gpu(p.ticket, 1u) == gridDim.x - 1;
+        __syncwarp();
+        if (last) {
+            __threadfence();
+            float total = 0.f;
+            for (int i = lane; i < (int)gridDim.x; i += 32) total += __ldcg(p.tail + i);
+            total = row_sum<32>(total);
+            if (lane == 0) {
+                const float z = __ldcg(p.tail + gridDim.x);
+                p.loss[0] = p.balance_coef * total + p.z_coef * z;
+                p.loss[1] = total;
+                p.loss[2] = z;
+            }
         }
     }
 }
 
 int loss_blocks(const ep_route_desc_t &d) {
     const int64_t tokens = (int64_t)d.world_size * d.tokens;
-    const int64_t want = (tokens + kLossWarps - 1) / kLossWarps;
-    return (int)(want < 152 ? want : 152);
+    const int warps = loss_warps(d.num_experts <= 256 ? 8 : 16);
+    const int64_t want = (tokens + warps - 1) / warps, most = 152 * 32 / warps;
+    return (int)(want < most ? want : most);
 }
+
+int final_blocks(const ep_route_desc_t &d) { return d.num_experts / 32 + 1; }
 
 // Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
 template <int V> struct Int { static constexpr int value = V; };
@@ -619,9 +684,9 @@ bool make_params(const ep_route_desc_t *d, const void *logits, const int32_t *h_
 ep_status_t launched() { return cudaGetLastError() == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP; }
 
 // One block per 4 warps of tokens of a rank.
-template <int LANES> dim3 token_grid(const RouteParams &p) {
-    constexpr int kTokens = kRouteWarps * (32 / LANES);
-    return dim3((unsigned)((p.T + kTokens - 1) / kTokens), (unsigned)p.W);
+template <int LANES> dim3 token_grid(const RouteParams &p, int rounds) {
+    const int tokens = kRouteWarps * (32 / LANES) * rounds;
+    return dim3((unsigned)((p.T + tokens - 1) / tokens), (unsigned)p.W);
 }
 
 }  // namespace
@@ -639,6 +704,7 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits, const float
     if (!d_w || !d_idx || !aligned(d_w, 4) || !aligned(d_idx, 4) || !aligned(d_bias, 4))
         return EP_ERR_INVALID_ARGS;
     p.bias = d_bias;
+    p.vec_e = p.E % 8 == 0 && aligned(d_bias, 16);
     p.w = d_w;
     p.idx_out = d_idx;
     const bool softmax = d->score == EP_SCORE_SOFTMAX, renorm = d->renormalize != 0;
@@ -646,7 +712,7 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits, const float
     with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
         route_kernel<decltype(type), kLanes, decltype(vpl)::value>
-            <<<token_grid<kLanes>(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
+            <<<token_grid<kLanes>(p, 1), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
     });
     return launched();
 }
@@ -677,15 +743,19 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
     p.vec = p.vec && aligned(d_grad_logits, 16);
     with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
+        // enough warps for all SMs (32 each) before a warp takes a second run
+        const int64_t runs = (int64_t)p.W * p.T * kLanes / 32;
+        p.rounds = (int)(runs < 152 * 32 ? 1 : runs < 4 * 152 * 32 ? runs / (152 * 32) : 4);
         route_backward_kernel<decltype(type), kLanes, decltype(vpl)::value>
-            <<<token_grid<kLanes>(p), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
+            <<<token_grid<kLanes>(p, p.rounds), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
     });
     return launched();
 }
 
 ep_status_t ep_balance_loss_workspace(const ep_route_desc_t *d, size_t *bytes) {
     if (!valid(d) || !bytes) return EP_ERR_INVALID_ARGS;
-    *bytes = (size_t)loss_blocks(*d) * (2 * (size_t)d->num_experts + 1) * 4;
+    // parts of the sums and counts, shares of the loss, z, the ticket
+    *bytes = ((size_t)loss_blocks(*d) * (2 * (size_t)d->num_experts + 1) + final_blocks(*d) + 2) * 4;
     return EP_SUCCESS;
 }
 
@@ -711,19 +781,22 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     p.error = d_error;
     p.part = static_cast<float *>(d_workspace);
     p.part_count = reinterpret_cast<int32_t *>(p.part + (size_t)blocks * (p.E + 1));
+    const int last = final_blocks(*d);
+    p.tail = reinterpret_cast<float *>(p.part_count + (size_t)blocks * p.E);
+    p.ticket = reinterpret_cast<uint32_t *>(p.tail + last + 1);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const size_t sh = ((size_t)kLossWarps * (p.E + 1) + p.E) * 4;    // 135 KB at most
-    const int64_t warps = (int64_t)blocks * kLossWarps;
-    const int per_warp = (int)(((int64_t)p.W * p.T + warps - 1) / warps);
-    cudaError_t e = cudaSuccess;
     with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
-        auto kernel = balance_partial_kernel<decltype(type), decltype(lanes)::value, decltype(vpl)::value>;
-        if (sh > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e == cudaSuccess) kernel<<<blocks, kLossWarps * 32, sh, st>>>(p, per_warp);
+        constexpr int kWarps = loss_warps(decltype(vpl)::value);
+        const size_t sh = ((size_t)kWarps * (p.E + 1) + p.E) * 4;    // 37 KB at most
+        const int64_t warps = (int64_t)blocks * kWarps;
+        const int per_warp = (int)(((int64_t)p.W * p.T + warps - 1) / warps);
+        balance_partial_kernel<decltype(type), decltype(lanes)::value, decltype(vpl)::value>
+            <<<blocks, kWarps * 32, sh, st>>>(p, per_warp);
     });
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return EP_ERR_GPU_OP;
-    balance_final_kernel<<<1, 1024, 0, st>>>(p, blocks);
-    return launched();
+    e = launch_after_previous(balance_final_kernel, last, 1024, 0, st, p, blocks);
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 }  // extern "C"
