@@ -2,7 +2,7 @@
 // router logits.
 //
 // A token's row of E logits lies in the registers of LANES neighbouring lanes,
-// 8 (or, past 256 experts, 16 or 32) neighbouring experts each, so that lane
+// 8 to 32 neighbouring experts each, so that lane
 // order is expert order and a warp holds 32 / LANES tokens: with 8 experts a
 // thread has a token to itself.  Softmax statistics are fp32 reductions over
 // those lanes.  Top-k takes the largest remaining key k times over; a lane
@@ -20,9 +20,8 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
-// Warps of a block of the losses: as many as an SM takes with 8 experts a lane;
-// longer rows need more registers.
-__host__ __device__ constexpr int loss_warps(int experts_per_lane) { return experts_per_lane == 8 ? 32 : 8; }
+// Warps of a block of the losses, one block per SM: what the registers allow.
+__host__ __device__ constexpr int loss_warps(int experts_per_lane) { return 256 / experts_per_lane; }
 
 struct RouteParams {
     const void *logits;
@@ -81,6 +80,11 @@ template <int LANES> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 template <int LANES> __device__ __forceinline__ float row_max(float v) {
+    if constexpr (LANES == 32) {
+        float r;
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
@@ -166,7 +170,8 @@ struct RowStats {
     float m, inv_sum;
     bool open;                   // some expert is open
     __device__ float prob(float x) const { return open ? expf(x - m) * inv_sum : 0.f; }
-    __device__ float lse() const { return open ? m - logf(inv_sum) : 0.f; }
+    // |error| of the logarithm: 2^-22, next to an lse of order 1 or more
+    __device__ float lse() const { return open ? m - __logf(inv_sum) : 0.f; }
 };
 
 // Softmax over a token's row: probabilities in place of x (all 0 when no
@@ -186,7 +191,7 @@ __device__ __forceinline__ RowStats softmax_row(float *x) {
         sum += x[i];
     }
     sum = row_sum<LANES>(sum);
-    const float inv = open ? 1.0f / sum : 1.f;
+    const float inv = open ? __fdividef(1.0f, sum) : 1.f;      // 1 <= sum <= E
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] *= inv;
     return RowStats{m, inv, open};
@@ -372,32 +377,67 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
         for (int i = 0; i < VPL; ++i) f[i] = e0 + i < p.E ? (float)p.counts[e0 + i] * share : 0.f;
     }
+    // one round ahead: the rows, the choices and their weights' gradients
+    RawRow<T, VPL> raw;
+    int id_next[SLOTS];
+    float g_next[SLOTS];
+    auto fetch = [&](int round) {
+        const Place<LANES> at(p, kRouteWarps, p.rounds, round);
+        if (dense) raw.load(p, at.present ? logit_row<T>(p, at.s, at.t) : nullptr, at.l, at.present);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            const int j = q * LANES + at.l;
+            const bool mine = p.grad_w && at.present && j < p.k;
+            id_next[q] = mine ? p.idx[at.tok * p.k + j] : 0;
+            g_next[q] = mine ? p.grad_w[at.tok * p.k + j] : 0.f;
+        }
+    };
+    fetch(0);
     for (int round = 0; round < p.rounds; ++round) {
         const Place<LANES> at(p, kRouteWarps, p.rounds, round);
-        float d[VPL];
+        float d[VPL], pr[VPL], g[SLOTS];
+        int id[SLOTS];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = 0.f;
-        if (__any_sync(0xffffffffu, at.present)) {
-            const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
-            float pr[VPL];
-            RowStats st = {0.f, 1.f, false};
-            int id[SLOTS];
-            float g[SLOTS];
-            if (p.grad_w) {
 #pragma unroll
-                for (int q = 0; q < SLOTS; ++q) {
-                    const int j = q * LANES + at.l;
-                    const bool mine = at.present && j < p.k;
-                    id[q] = mine ? p.idx[at.tok * p.k + j] : 0;
-                    g[q] = mine ? p.grad_w[at.tok * p.k + j] * p.scale : 0.f;
+        for (int q = 0; q < SLOTS; ++q) {
+            id[q] = id_next[q];
+            g[q] = g_next[q] * p.scale;
+        }
+        if (dense) raw.values(p, at.l, pr);
+        if (round + 1 < p.rounds) fetch(round + 1);
+        if (__any_sync(0xffffffffu, at.present)) {
+            RowStats st = {0.f, 1.f, false};
+            float *r = rows[threadIdx.x / LANES];
+            float c[SLOTS];
+            bool mine[SLOTS];
+#pragma unroll
+            for (int q = 0; q < SLOTS; ++q) {
+                mine[q] = p.grad_w && at.present && q * LANES + at.l < p.k;
+                if (mine[q] && (uint32_t)id[q] >= (uint32_t)p.E) {
+                    mine[q] = false;
+                    g[q] = 0.f;
+                    if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
                 }
+                c[q] = -INFINITY;
             }
-            if (dense) {
-                RawRow<T, VPL> raw;
-                raw.load(p, row, at.l, at.present);
-                raw.values(p, at.l, pr);
-                st = softmax_row<LANES, VPL>(pr);
+            // the chosen logits: from the row where it is at hand
+            if (p.grad_w && dense) {
+#pragma unroll
+                for (int i = 0; i < VPL; i += 4)
+                    *reinterpret_cast<float4 *>(r + e0 + i) = make_float4(pr[i], pr[i + 1], pr[i + 2], pr[i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q)
+                    if (mine[q]) c[q] = r[id[q]];
+                __syncwarp();
+            } else if (p.grad_w) {
+                const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q)
+                    if (mine[q]) c[q] = sane_logit(to_f32(row[id[q]]));
             }
+            if (dense) st = softmax_row<LANES, VPL>(pr);
             if (p.grad_loss) {
                 const float lse = 2.0f * p.z_coef * st.lse();
                 float dot = 0.f;
@@ -408,18 +448,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 for (int i = 0; i < VPL; ++i) d[i] = pr[i] * ((f[i] - dot) + lse) * gl;
             }
             if (p.grad_w) {
-                float c[SLOTS], v[SLOTS], dv[SLOTS], sum, dot = 0.f;
-                bool mine[SLOTS];
-#pragma unroll
-                for (int q = 0; q < SLOTS; ++q) {
-                    mine[q] = at.present && q * LANES + at.l < p.k;
-                    if (mine[q] && (uint32_t)id[q] >= (uint32_t)p.E) {
-                        mine[q] = false;
-                        g[q] = 0.f;
-                        if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
-                    }
-                    c[q] = mine[q] ? sane_logit(to_f32(row[id[q]])) : -INFINITY;
-                }
+                float v[SLOTS], dv[SLOTS], sum, dot = 0.f;
                 chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
@@ -438,11 +467,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
                     for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * dot;
                 }
-                float *r = rows[threadIdx.x / LANES];
-                // one lane of several choices: in order.  One choice a lane: at
-                // once, unless two lanes find each other at an expert's place.
-                bool twice = LANES < 32;
-                if (LANES == 32) {
+                // several choices a lane: in order.  One choice a lane: at once,
+                // unless two lanes find each other at an expert's place.
+                bool twice = p.k > LANES;
+                if (!twice) {
                     int *mark = reinterpret_cast<int *>(r);
                     if (mine[0]) mark[id[0]] = at.l;
                     __syncwarp();
@@ -478,6 +506,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         }
         if (at.in) store_row<T, VPL>(p, static_cast<T *>(p.grad_logits) + at.tok * p.E, at.l, d);
     }
+}
+
+__device__ __forceinline__ void store_loss(const RouteParams &p, float balance, float z) {
+    p.loss[0] = p.balance_coef * balance + p.z_coef * z;
+    p.loss[1] = balance;
+    p.loss[2] = z;
 }
 
 // Losses, pass 1: every block sums softmax probabilities and lse^2 of its
@@ -546,6 +580,31 @@ __global__ void __launch_bounds__(loss_warps(VPL) * 32)
     }
     if (lane == 0) mine[p.E] = z;
     __syncthreads();
+    if (gridDim.x == 1) {                        // few tokens: no second pass
+        __shared__ float shares[33];             // of the loss, by warp; z
+        float balance = 0.f;
+        for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+            float sum = 0.f;
+#pragma unroll 8
+            for (int w = 0; w < kLossWarps; ++w) sum += sh[w * (p.E + 1) + e];
+            sum *= p.inv_n;
+            if (e < p.E) {
+                p.probs[e] = sum;
+                p.counts_out[e] = cnt[e];
+                balance += (float)cnt[e] * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
+            } else {
+                shares[32] = sum;
+            }
+        }
+        balance = row_sum<32>(balance);
+        if (lane == 0) shares[warp] = balance;
+        __syncthreads();
+        if (warp == 0) {
+            const float total = row_sum<32>(lane < kLossWarps ? shares[lane] : 0.f);
+            if (lane == 0) store_loss(p, total, shares[32]);
+        }
+        return;
+    }
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
         float sum = 0.f;
 #pragma unroll 8
@@ -606,9 +665,7 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
             total = row_sum<32>(total);
             if (lane == 0) {
                 const float z = __ldcg(p.tail + gridDim.x);
-                p.loss[0] = p.balance_coef * total + p.z_coef * z;
-                p.loss[1] = total;
-                p.loss[2] = z;
+                store_loss(p, total, z);
             }
         }
     }
@@ -616,28 +673,32 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
 
 int loss_blocks(const ep_route_desc_t &d) {
     const int64_t tokens = (int64_t)d.world_size * d.tokens;
-    const int warps = loss_warps(d.num_experts <= 256 ? 8 : 16);
-    const int64_t want = (tokens + warps - 1) / warps, most = 152 * 32 / warps;
-    return (int)(want < most ? want : most);
+    // one block, without a second pass, costs an SM about 4 us for 2^15 logits
+    const int64_t want = tokens * d.num_experts <= 1 << 15 ? 1 : (tokens + 31) / 32;
+    return (int)(want < 152 ? want : 152);
 }
 
 int final_blocks(const ep_route_desc_t &d) { return d.num_experts / 32 + 1; }
 
 // Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
+// Reductions cost a warp the same for one token or several, so for the losses
+// (WIDE) a lane takes 16 experts of a long row (32768 x 256: 11.2 against 12.3
+// us); top-k, which searches a lane's experts, and the gradient, which needs the
+// registers, take 8 (gradient: 19 against 26 us).
 template <int V> struct Int { static constexpr int value = V; };
-template <typename T, typename F> void with_row(int E, F f) {
+template <bool WIDE, typename T, typename F> void with_row(int E, F f) {
     if (E <= 8) f(T(), Int<1>(), Int<8>());
     else if (E <= 32) f(T(), Int<4>(), Int<8>());
     else if (E <= 64) f(T(), Int<8>(), Int<8>());
-    else if (E <= 128) f(T(), Int<16>(), Int<8>());
-    else if (E <= 256) f(T(), Int<32>(), Int<8>());
+    else if (E <= 128) f(T(), Int<WIDE ? 8 : 16>(), Int<WIDE ? 16 : 8>());
+    else if (E <= 256) f(T(), Int<WIDE ? 16 : 32>(), Int<WIDE ? 16 : 8>());
     else if (E <= 512) f(T(), Int<32>(), Int<16>());
     else f(T(), Int<32>(), Int<32>());
 }
-template <typename F> void with_types(int dtype, int E, F f) {
-    if (dtype == EP_DT_BF16) with_row<__nv_bfloat16>(E, f);
-    else if (dtype == EP_DT_FP16) with_row<__half>(E, f);
-    else with_row<float>(E, f);
+template <bool WIDE, typename F> void with_types(int dtype, int E, F f) {
+    if (dtype == EP_DT_BF16) with_row<WIDE, __nv_bfloat16>(E, f);
+    else if (dtype == EP_DT_FP16) with_row<WIDE, __half>(E, f);
+    else with_row<WIDE, float>(E, f);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -709,7 +770,7 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits, const float
     p.idx_out = d_idx;
     const bool softmax = d->score == EP_SCORE_SOFTMAX, renorm = d->renormalize != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+    with_types<false>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
         route_kernel<decltype(type), kLanes, decltype(vpl)::value>
             <<<token_grid<kLanes>(p, 1), kRouteWarps * 32, 0, st>>>(p, softmax, renorm);
@@ -741,7 +802,7 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
     const bool softmax = d->score == EP_SCORE_SOFTMAX, renorm = d->renormalize != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     p.vec = p.vec && aligned(d_grad_logits, 16);
-    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+    with_types<false>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
         // enough warps for all SMs (32 each) before a warp takes a second run
         const int64_t runs = (int64_t)p.W * p.T * kLanes / 32;
@@ -785,7 +846,7 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     p.tail = reinterpret_cast<float *>(p.part_count + (size_t)blocks * p.E);
     p.ticket = reinterpret_cast<uint32_t *>(p.tail + last + 1);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    with_types(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
+    with_types<true>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kWarps = loss_warps(decltype(vpl)::value);
         const size_t sh = ((size_t)kWarps * (p.E + 1) + p.E) * 4;    // 37 KB at most
         const int64_t warps = (int64_t)blocks * kWarps;
@@ -795,6 +856,7 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     });
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return EP_ERR_GPU_OP;
+    if (blocks == 1) return EP_SUCCESS;
     e = launch_after_previous(balance_final_kernel, last, 1024, 0, st, p, blocks);
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
