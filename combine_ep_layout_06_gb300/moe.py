@@ -82,31 +82,27 @@ def _entry(name: str):
     return getattr(_lib.load(), name)
 
 
-def _on_stream(call):
-    """``stream`` of a call: what it allocates and launches goes there, with
-    the first tensor's device current."""
-    @functools.wraps(call)
-    def wrapper(first, *args, stream=None, **options):
-        if first is None or not first.is_cuda:
-            raise ValueError(f"{call.__name__}: tensors must be on a CUDA device")
-        index = first.get_device()
-        if stream is None:
-            if torch._C._cuda_getDevice() == index:
-                return call(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **options)
-            with torch.cuda.device(index):
-                return call(first, *args, stream=torch._C._cuda_getCurrentRawStream(index), **options)
-        if stream.device != first.device:
-            raise ValueError("the stream is on another device than the tensors")
-        with torch.cuda.stream(stream):
-            return call(first, *args, stream=stream.cuda_stream, **options)
-    return wrapper
+# set once torch has CUDA; a machine without a GPU has only tensors to refuse
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _same_device(like: torch.Tensor, **tensors):
-    index = like.get_device()
-    for name, t in tensors.items():
+def _elsewhere(tensor, stream):
+    """Context in which a call runs whose tensors' device is not the current
+    one, or that names a stream: what it allocates and launches goes there."""
+    if tensor is None or not tensor.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        return torch.cuda.device(tensor.get_device())
+    if stream.device != tensor.device:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _check_device(index, what, *tensors):
+    for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must be on {like.device}")
+            raise ValueError(f"{what} must be on cuda:{index}")
 
 
 # ------------------------------------------------------------ routing
@@ -144,7 +140,7 @@ def _plan(logits, topk, num_tokens, score="softmax", renormalize=True, scale=1.0
     if num_tokens is not None:
         num_tokens = tuple(map(int, num_tokens))
     return _route_plan(logits.shape, logits.stride(), logits.dtype, topk, num_tokens, score, renormalize,
-                       float(scale), float(balance_coef), float(z_coef))
+                       scale, balance_coef, z_coef)
 
 
 def _dense(t, dtype, shape, name):
@@ -152,7 +148,6 @@ def _dense(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}")
 
 
-@_on_stream
 def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormalize: bool = True,
           scale: float = 1.0, bias: Optional[torch.Tensor] = None,
           num_tokens: Optional[Sequence[int]] = None, stream=None):
@@ -163,22 +158,35 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormaliz
     logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
     [...][topk], as ``EpDispatchCombineOp.dispatch`` takes them; tokens
     t >= num_tokens[w] get weights 0 and indices -1."""
+    index = logits.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _elsewhere(logits, stream):
+            return route(logits, topk, score=score, renormalize=renormalize, scale=scale, bias=bias,
+                         num_tokens=num_tokens)
     desc, counts, lead, T, E, _ = _plan(logits, topk, num_tokens, score, renormalize, scale)
+    b = None
     if bias is not None:
-        _same_device(logits, bias=bias)
+        _check_device(index, "bias", bias)
         _dense(bias, torch.float32, (E,), "bias")
+        b = bias.data_ptr()
     device = logits.device
     w = torch.empty((*lead, topk), dtype=torch.float32, device=device)
     idx = torch.empty((*lead, topk), dtype=torch.int32, device=device)
     if T:
-        check(_entry("ep_route")(desc, logits.data_ptr(), None if bias is None else bias.data_ptr(), counts,
-                                 w.data_ptr(), idx.data_ptr(), stream), "ep_route")
+        status = _entry("ep_route")(desc, logits.data_ptr(), b, counts, w.data_ptr(), idx.data_ptr(),
+                                    _raw_stream(index))
+        if status:
+            check(status, "ep_route")
     return w, idx
 
 
 def _backward(grad_weights, logits, indices, topk, grad_loss, loss_counts, num_tokens, stream, *options):
+    index = logits.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _elsewhere(logits, stream):
+            return _backward(grad_weights, logits, indices, topk, grad_loss, loss_counts, num_tokens, None, *options)
     desc, counts, lead, T, E, _ = _plan(logits, topk, num_tokens, *options)
-    _same_device(logits, grad_weights=grad_weights, indices=indices, grad_loss=grad_loss, counts=loss_counts)
+    _check_device(index, "gradients, indices and counts", grad_weights, indices, grad_loss, loss_counts)
     gw = idx = gl = lc = None
     if grad_weights is not None:
         _dense(grad_weights, torch.float32, (*lead, topk), "grad_weights")
@@ -193,12 +201,13 @@ def _backward(grad_weights, logits, indices, topk, grad_loss, loss_counts, num_t
         gl, lc = grad_loss.data_ptr(), loss_counts.data_ptr()
     out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     if T:
-        check(_entry("ep_route_backward")(desc, logits.data_ptr(), gw, idx, gl, lc, counts, out.data_ptr(),
-                                          _error_word(logits.get_device())[1], stream), "ep_route_backward")
+        status = _entry("ep_route_backward")(desc, logits.data_ptr(), gw, idx, gl, lc, counts, out.data_ptr(),
+                                             _error_word(index)[1], _raw_stream(index))
+        if status:
+            check(status, "ep_route_backward")
     return out
 
 
-@_on_stream
 def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, indices: torch.Tensor, *,
                    score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
                    num_tokens: Optional[Sequence[int]] = None, grad_loss: Optional[torch.Tensor] = None,
@@ -207,19 +216,24 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, indices: to
     """Gradient of ``route``'s weights by the logits, dense and in their type.
     With grad_loss (one fp32 value) and counts, the gradient of
     ``balance_loss`` with these coefficients is added in the same pass."""
+    if grad_weights is None:
+        raise ValueError("grad_weights is needed: balance_loss_backward is the loss's gradient alone")
     return _backward(grad_weights, logits, indices, indices.shape[-1], grad_loss, counts, num_tokens,
                      stream, score, renormalize, scale, balance_coef, z_coef)
 
 
-@_on_stream
 def balance_loss(logits: torch.Tensor, indices: torch.Tensor, *, balance_coef: float = 1.0,
                  z_coef: float = 0.0, num_tokens: Optional[Sequence[int]] = None, stream=None):
     """Balance and z losses of a routing.  Returns (loss fp32 [3]: total,
     balance, z; counts int32 [E]: how often each expert was chosen; probs fp32
     [E]: mean router probability), over the tokens t < num_tokens[w]."""
+    index = logits.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _elsewhere(logits, stream):
+            return balance_loss(logits, indices, balance_coef=balance_coef, z_coef=z_coef, num_tokens=num_tokens)
     topk = indices.shape[-1]
     desc, nt, lead, T, E, need = _plan(logits, topk, num_tokens, "softmax", True, 1.0, balance_coef, z_coef)
-    _same_device(logits, indices=indices)
+    _check_device(index, "indices", indices)
     _dense(indices, torch.int32, (*lead, topk), "indices")
     device = logits.device
     loss = torch.empty(3, dtype=torch.float32, device=device)
@@ -228,18 +242,21 @@ def balance_loss(logits: torch.Tensor, indices: torch.Tensor, *, balance_coef: f
     if T == 0:
         return loss.zero_(), counts.zero_(), probs.zero_()
     scratch = torch.empty(need, dtype=torch.uint8, device=device)
-    check(_entry("ep_balance_loss")(desc, logits.data_ptr(), indices.data_ptr(), nt, loss.data_ptr(),
-                                    counts.data_ptr(), probs.data_ptr(), scratch.data_ptr(), need,
-                                    _error_word(logits.get_device())[1], stream), "ep_balance_loss")
+    status = _entry("ep_balance_loss")(desc, logits.data_ptr(), indices.data_ptr(), nt, loss.data_ptr(),
+                                       counts.data_ptr(), probs.data_ptr(), scratch.data_ptr(), need,
+                                       _error_word(index)[1], _raw_stream(index))
+    if status:
+        check(status, "ep_balance_loss")
     return loss, counts, probs
 
 
-@_on_stream
 def balance_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, counts: torch.Tensor, topk: int, *,
                           balance_coef: float = 1.0, z_coef: float = 0.0,
                           num_tokens: Optional[Sequence[int]] = None, stream=None) -> torch.Tensor:
     """Gradient of ``balance_loss``'s total by the logits; grad_loss is one
     fp32 value on the device, counts those that ``balance_loss`` returned."""
+    if grad_loss is None:
+        raise ValueError("grad_loss must be one fp32 value on the device")
     return _backward(None, logits, None, topk, grad_loss, counts, num_tokens, stream,
                      "softmax", True, 1.0, balance_coef, z_coef)
 
@@ -257,25 +274,21 @@ def _strides_of(shape, strides, name):
     return rank, row
 
 
-def _strided(t: torch.Tensor, name: str):
-    rank, row = _strides_of(t.shape, t.stride(), name)
+def _rows(t: torch.Tensor, dtype, lead, width: int, name: str) -> bytes:
+    """A given [rows][width] or [R][rows][width] tensor."""
+    shape = t.shape
+    if t.dtype != dtype or shape[:-1] != lead or shape[-1] != width:
+        raise ValueError(f"{name} must be {dtype} {[*lead, width]}")
     ptr = t.data_ptr()
     if ptr % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
-    return ptr, rank, row
-
-
-def _rows(t: torch.Tensor, like, width: int, name: str) -> bytes:
-    """A [rows][width] or [R][rows][width] tensor of x's type and rows."""
-    if t.dtype != like.dtype or t.shape[:-1] != like.shape[:-1] or t.shape[-1] != width:
-        raise ValueError(f"{name} must be {like.dtype} {[*like.shape[:-1], width]}")
-    return _ROWS.pack(*_strided(t, name))
+    return _ROWS.pack(ptr, *_strides_of(shape, t.stride(), name))
 
 
 @functools.lru_cache(maxsize=1024)
-def _product_plan(xshape, wshape, dtype, wdtype, activation, grouped):
-    """The descriptor's head, rows, N, wide, groups, and the gradient's
-    workspace bytes."""
+def _product_plan(xshape, xstrides, wshape, wstrides, dtype, wdtype, activation, grouped):
+    """The descriptor's head, the strides of weight and x, R's lead shape,
+    rows, N, wide, groups, and the gradient's workspace bytes."""
     if dtype not in _PRODUCT_DTYPES or len(xshape) not in (2, 3):
         raise ValueError("x must be bf16 or fp16 [rows][K] or [R][rows][K]")
     R, rows, K = xshape if len(xshape) == 3 else (1, *xshape)
@@ -291,31 +304,34 @@ def _product_plan(xshape, wshape, dtype, wdtype, activation, grouped):
         raise ValueError(f"{G} groups do not divide over {R} ranks")
     if not grouped and G != R:
         raise ValueError("without count and offset there is one group per rank")
+    ws = _strides_of(wshape, wstrides, "weight")
+    xs = _strides_of(xshape, xstrides, "x") if rows else (0, 0)
     head = _PRODUCT_HEAD.pack(R, G // R, rows, K, N, _PRODUCT_DTYPES[dtype], _ACTIVATIONS[activation], 0)
-    # pointers of the right kind: the size depends on the head alone
-    fake = head + _PRODUCT_TAIL.pack(16 if grouped else 0, 16 if grouped else 0, 16, 8 * wide * K, K, 16, 8 * rows * K or 8, K)
+    # with pointers of the right kind: the size depends on the head alone
+    some = 16 if grouped else 0
     need = ctypes.c_size_t(0)
-    check(_entry("ep_expert_product_workspace")(fake, ctypes.byref(need)), "ep_expert_product_workspace")
-    return head, rows, N, wide, G, need.value
+    check(_entry("ep_expert_product_workspace")(head + _PRODUCT_TAIL.pack(some, some, 16, *ws, 16, *xs),
+                                                ctypes.byref(need)), "ep_expert_product_workspace")
+    return head, ws, xs, tuple(xshape[:-1]), rows, N, wide, G, need.value
 
 
-def _product_desc(x, weight, count, offset, activation):
-    head, rows, N, wide, G, need = _product_plan(x.shape, weight.shape, x.dtype, weight.dtype, activation,
-                                                 count is not None)
-    _same_device(x, weight=weight, count=count, offset=offset)
-    if (count is None) != (offset is None):
-        raise ValueError("count and offset come together")
+def _product_desc(plan, index, x, weight, count, offset):
+    head, ws, xs, _, rows, _, _, G, _ = plan
     c = o = 0
     if count is not None:
+        _check_device(index, "weight, count and offset", weight, count, offset)
         if (count.dtype != torch.int32 or offset.dtype != torch.int32 or count.numel() != G or offset.numel() != G
                 or not count.is_contiguous() or not offset.is_contiguous()):
             raise ValueError(f"count and offset must be contiguous int32 of {G} groups")
         c, o = count.data_ptr(), offset.data_ptr()
-    desc = head + _PRODUCT_TAIL.pack(c, o, *_strided(weight, "weight"), *(_strided(x, "x") if rows else (0, 0, 0)))
-    return desc, rows, N, wide, G, need
+    else:
+        _check_device(index, "weight", weight)
+    w, p = weight.data_ptr(), x.data_ptr() if rows else 0
+    if (w | p) % 16:
+        raise ValueError("x and weight must be 16-byte aligned")
+    return head + _PRODUCT_TAIL.pack(c, o, w, *ws, p, *xs)
 
 
-@_on_stream
 def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.Tensor] = None,
                    offset: Optional[torch.Tensor] = None, *, bias: Optional[torch.Tensor] = None,
                    activation: str = "none", residual: Optional[torch.Tensor] = None,
@@ -329,32 +345,42 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.
     features].  residual and out: [...][N].  Returns y, or (y, pre) with
     save_pre: what ``expert_product_backward`` needs.  Rows outside every
     group are unspecified (untouched in ``out``)."""
-    desc, rows, N, wide, G, _ = _product_desc(x, weight, count, offset, activation)
+    index = x.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _elsewhere(x, stream):
+            return expert_product(x, weight, count, offset, bias=bias, activation=activation, residual=residual,
+                                  save_pre=save_pre, out=out)
+    if (count is None) != (offset is None):
+        raise ValueError("count and offset come together")
+    dtype = x.dtype
+    plan = _product_plan(x.shape, x.stride(), weight.shape, weight.stride(), dtype, weight.dtype, activation,
+                         count is not None)
+    _, _, _, lead, rows, N, wide, G, _ = plan
+    desc = _product_desc(plan, index, x, weight, count, offset)
     b, res, pre, p = None, _NO_ROWS, None, _NO_ROWS
     if bias is not None:
-        _same_device(x, bias=bias)
-        _dense(bias, x.dtype, (G, wide), "bias")
+        _check_device(index, "bias", bias)
+        _dense(bias, dtype, (G, wide), "bias")
         b = bias.data_ptr()
     if residual is not None:
-        _same_device(x, residual=residual)
-        res = _rows(residual, x, N, "residual")
-    lead = x.shape[:-1]
+        _check_device(index, "residual", residual)
+        res = _rows(residual, dtype, lead, N, "residual")
     if out is None:
-        y = torch.empty((*lead, N), dtype=x.dtype, device=x.device)
+        y = torch.empty((*lead, N), dtype=dtype, device=x.device)
+        o = _ROWS.pack(y.data_ptr(), rows * N, N)
     else:
-        _same_device(x, out=out)
-        y = out
-    o = _rows(y, x, N, "out")
+        _check_device(index, "out", out)
+        y, o = out, _rows(out, dtype, lead, N, "out")
     if save_pre:
-        pre = torch.empty((*lead, wide), dtype=x.dtype, device=x.device)
-        p = _rows(pre, x, wide, "pre")
+        pre = torch.empty((*lead, wide), dtype=dtype, device=x.device)
+        p = _ROWS.pack(pre.data_ptr(), rows * wide, wide)
     if rows:
-        check(_entry("ep_expert_product")(desc, b, res, o, p, _error_word(x.get_device())[1], stream),
-              "ep_expert_product")
+        status = _entry("ep_expert_product")(desc, b, res, o, p, _error_word(index)[1], _raw_stream(index))
+        if status:
+            check(status, "ep_expert_product")
     return (y, pre) if save_pre else y
 
 
-@_on_stream
 def expert_product_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                             count: Optional[torch.Tensor] = None, offset: Optional[torch.Tensor] = None, *,
                             pre: Optional[torch.Tensor] = None, activation: str = "none",
@@ -363,18 +389,31 @@ def expert_product_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.T
     None) from grad = dL/dy.  pre: the forward's (not needed for "none").  The
     residual's gradient is grad itself.  Rows of grad_x outside every group
     are unspecified; a group without rows gets zero gradients."""
-    desc, rows, N, wide, G, need = _product_desc(x, weight, count, offset, activation)
-    _same_device(x, grad=grad, pre=pre)
+    index = x.get_device()
+    if stream is not None or index < 0 or index != _current_device():
+        with _elsewhere(x, stream):
+            return expert_product_backward(grad, x, weight, count, offset, pre=pre, activation=activation,
+                                           bias_grad=bias_grad)
+    if (count is None) != (offset is None):
+        raise ValueError("count and offset come together")
+    dtype = x.dtype
+    plan = _product_plan(x.shape, x.stride(), weight.shape, weight.stride(), dtype, weight.dtype, activation,
+                         count is not None)
+    _, _, _, lead, rows, N, wide, G, need = plan
+    desc = _product_desc(plan, index, x, weight, count, offset)
     if pre is None and activation != "none":
         raise ValueError(f"the gradient of {activation!r} needs pre")
-    g = _rows(grad, x, N, "grad")
-    p = _NO_ROWS if pre is None else _rows(pre, x, wide, "pre")
-    device = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device)
-    dw = torch.empty(weight.shape, dtype=x.dtype, device=device)
-    db = torch.empty((G, wide), dtype=x.dtype, device=device) if bias_grad else None
+    _check_device(index, "grad and pre", grad, pre)
+    g = _rows(grad, dtype, lead, N, "grad")
+    p = _NO_ROWS if pre is None else _rows(pre, dtype, lead, wide, "pre")
+    device, K = x.device, weight.shape[2]
+    dx = torch.empty((*lead, K), dtype=dtype, device=device)
+    dw = torch.empty((G, wide, K), dtype=dtype, device=device)
+    db = torch.empty((G, wide), dtype=dtype, device=device) if bias_grad else None
     scratch = torch.empty(need, dtype=torch.uint8, device=device)
-    check(_entry("ep_expert_product_backward")(
-        desc, g, p, _rows(dx, x, x.shape[-1], "x"), dw.data_ptr(), None if db is None else db.data_ptr(),
-        scratch.data_ptr(), need, _error_word(x.get_device())[1], stream), "ep_expert_product_backward")
+    status = _entry("ep_expert_product_backward")(
+        desc, g, p, _ROWS.pack(dx.data_ptr(), rows * K, K), dw.data_ptr(), None if db is None else db.data_ptr(),
+        scratch.data_ptr(), need, _error_word(index)[1], _raw_stream(index))
+    if status:
+        check(status, "ep_expert_product_backward")
     return dx, dw, db
