@@ -136,8 +136,16 @@ template <typename T, int VPL> struct RawRow {
     __device__ __forceinline__ void values(const RouteParams &p, int l, float *x) const {
         const T *s = reinterpret_cast<const T *>(v);
         if ((l + 1) * VPL <= p.E) {
+            float odd = 0.f;                     // a NaN as soon as one logit is not finite
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) x[i] = sane_logit(to_f32(s[i]));
+            for (int i = 0; i < VPL; ++i) {
+                x[i] = to_f32(s[i]);
+                odd = fmaf(x[i], 0.f, odd);
+            }
+            if (odd != odd) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) x[i] = sane_logit(x[i]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) x[i] = l * VPL + i < p.E ? sane_logit(to_f32(s[i])) : -INFINITY;
@@ -241,7 +249,7 @@ __device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const R
         }
         *sum = row_sum<LANES>(*sum);
 #pragma unroll
-        for (int q = 0; q < SLOTS; ++q) v[q] = *sum > 0.f ? v[q] / *sum : 0.f;
+        for (int q = 0; q < SLOTS; ++q) v[q] = *sum > 0.f ? __fdividef(v[q], *sum) : 0.f;     // 1 <= sum <= k
     } else if (softmax) {
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) v[q] = mine[q] ? st.prob(c[q]) : 0.f;
@@ -287,8 +295,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     uint32_t key[VPL], best = 0, second = 0;
     int be = 0, se = 0;
 #pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = order_key(x[i] + y[i]);
+    if (e0 + VPL > p.E) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e0 + i >= p.E) key[i] = 0;
+    }
+#pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        key[i] = e0 + i < p.E ? order_key(x[i] + y[i]) : 0u;
         const bool first = key[i] > best, next = key[i] > second;
         second = max(second, min(best, key[i]));
         se = first ? be : next ? i : se;
@@ -303,7 +317,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         const uint32_t top = row_max_key<LANES>(best);
         const uint32_t who = __ballot_sync(0xffffffffu, best == top) & lanes;
         const int winner = __ffs(who) - 1;               // the first lane has the first expert
-        const int e = __shfl_sync(0xffffffffu, at.l * VPL + be, winner);
+        const int e = __shfl_sync(0xffffffffu, e0 + be, winner);
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q)
             if (j == q * LANES + at.l) id[q] = e;
