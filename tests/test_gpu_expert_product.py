@@ -180,6 +180,60 @@ def test_strided_tensors_and_another_stream():
     check(d, 128, 136, wide, rows, torch.float16, "swiglu", views=views, stream=torch.cuda.Stream())
 
 
+def test_offsets_past_32_bits():
+    """Segments 2^31 elements apart: every tensor's last segment ends beyond
+    what 32 bits of elements (or of bytes) reach."""
+    gap = 1 << 31
+    R, rows, K, N = 2, 70, 64, 72
+    d, wide, rows = make(R, 2, [[30, 40], [9, 61]], K, N, torch.bfloat16, "silu", seed=11, rows=rows)
+
+    def far(t):
+        big = torch.empty(gap + t[1].numel(), dtype=t.dtype, device="cuda")
+        v = torch.as_strided(big, t.shape, (gap, t.shape[2], 1))
+        v.copy_(t)
+        return v
+    x, res, out = far(d["x"]), far(d["residual"]), far(torch.zeros((R, rows, N), dtype=torch.bfloat16))
+    a = {n: t.cuda() for n, t in d.items()}
+    y = ep.expert_product(x, a["weight"], a["count"], a["offset"], activation="silu", residual=res, out=out)
+    want = ep.expert_product(a["x"], a["weight"], a["count"], a["offset"], activation="silu", residual=a["residual"])
+    assert torch.equal(y, want)
+    del res, out, y
+    pre, grad = far(d["pre"]), far(d["grad"])
+    got = ep.expert_product_backward(grad, x, a["weight"], a["count"], a["offset"], pre=pre, activation="silu", bias_grad=True)
+    want = ep.expert_product_backward(a["grad"], a["x"], a["weight"], a["count"], a["offset"], pre=a["pre"],
+                                      activation="silu", bias_grad=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_residual_in_place_and_graph_replay():
+    """out may be the residual itself; a captured call replays."""
+    d, wide, rows = make(1, 3, [[100, 0, 57]], 256, 320, torch.bfloat16, "gelu", seed=12)
+    a = {n: t.cuda() for n, t in d.items()}
+    args = (a["x"], a["weight"], a["count"], a["offset"])
+    want = ep.expert_product(*args, activation="gelu", residual=a["residual"])
+    same = a["residual"].clone()
+    assert ep.expert_product(*args, activation="gelu", residual=same, out=same) is same
+    assert torch.equal(same, want)
+    grads = ep.expert_product_backward(a["grad"], *args, pre=a["pre"], activation="gelu", bias_grad=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ep.expert_product(*args, activation="gelu", residual=a["residual"])
+        g = ep.expert_product_backward(a["grad"], *args, pre=a["pre"], activation="gelu", bias_grad=True)
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, want) and all(torch.equal(p, q) for p, q in zip(g, grads))
+
+
+def test_many_small_groups():
+    """More groups than the tile walk looks at in one go, most of them empty."""
+    g = torch.Generator().manual_seed(13)
+    counts = [[int(c) for c in torch.randint(0, 4, (150,), generator=g) * (torch.rand(150, generator=g) < 0.4)]
+              for _ in range(2)]
+    d, wide, rows = make(2, 150, counts, 64, 72, torch.bfloat16, "swiglu", seed=14)
+    check(d, 64, 72, wide, rows, torch.bfloat16, "swiglu")
+
+
 def test_one_group_of_all_rows():
     """No count and offset: a plain product, 2-D rows."""
     d, wide, rows = make(1, 1, [[333]], 264, 392, torch.bfloat16, "gelu", seed=4)

@@ -245,6 +245,31 @@ def test_strided_logits_streams_and_no_tokens():
     assert w.shape == (2, 0, 8) and idx.shape == (2, 0, 8)
 
 
+def test_offsets_past_32_bits_and_graph_replay():
+    gap = 1 << 31
+    x = draw_logits(2, 40, 64, torch.bfloat16, seed=21).cuda()
+    big = torch.empty(gap + x[1].numel(), dtype=x.dtype, device="cuda")
+    far = torch.as_strided(big, x.shape, (gap, 64, 1))
+    far.copy_(x)
+    w, idx = ep.route(x, 6)
+    assert all(torch.equal(a, b) for a, b in zip(ep.route(far, 6), (w, idx)))
+    loss = ep.balance_loss(x, idx, z_coef=0.1)
+    assert all(torch.equal(a, b) for a, b in zip(ep.balance_loss(far, idx, z_coef=0.1), loss))
+    one = torch.ones((), device="cuda")
+    d = ep.route_backward(w, x, idx, grad_loss=one, counts=loss[1], balance_coef=1.0, z_coef=0.1)
+    assert torch.equal(ep.route_backward(w, far, idx, grad_loss=one, counts=loss[1], balance_coef=1.0, z_coef=0.1), d)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w2, idx2 = ep.route(x, 6)
+        loss2 = ep.balance_loss(x, idx2, z_coef=0.1)
+        d2 = ep.route_backward(w2, x, idx2, grad_loss=one, counts=loss2[1], balance_coef=1.0, z_coef=0.1)
+    for _ in range(2):
+        d2.zero_()
+        graph.replay()
+        assert torch.equal(w, w2) and torch.equal(idx, idx2) and torch.equal(d, d2)
+        assert all(torch.equal(a, b) for a, b in zip(loss, loss2))
+
+
 def test_ids_out_of_range_are_skipped_and_reported():
     x = draw_logits(1, 5, 20, torch.float32, seed=2).cuda()
     w, idx = ep.route(x, 4)
