@@ -63,7 +63,7 @@ __device__ __forceinline__ void group_range(const Groups &gr, int g, int *first,
     *n = none ? 0 : min(c, gr.rows - o);
 }
 
-enum Mode { kForward, kGated, kGradX, kGradW };
+enum Mode { kForward, kGated, kGradX, kGradW, kNone };
 
 struct ProductParams {
     Groups gr;
@@ -324,23 +324,333 @@ template <typename T, Mode MODE> struct Epilogue {
     }
 };
 
-template <typename T, Mode MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_b32, const ProductParams p) {
-    constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
-    constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
+// One product's inputs and outputs.
+struct Work {
+    CUtensorMap a, b, b32;   // b32: rows of a K-major B, 32 at a time
+    ProductParams p;
+};
+
+// What the roles share.  A role works through one product's tiles after the
+// other's and carries its place in the ring and in the accumulators along;
+// `next` is this pair's next tile, counted from the product's first.
+struct Cta {
+    Barriers *bars;
+    uint32_t ring, tmem, rank;
+    float *turns;
+    int64_t pairs;
+    volatile int *gave_up;
+
+    static __device__ uint32_t bar(uint64_t *b) { return smem_u32(b); }
+    static __device__ uint32_t first_cta(uint64_t *b) { return in_cta(smem_u32(b), 0); }
+};
+
+template <Mode MODE> struct Shape {
+    static constexpr bool kAmn = MODE == kGradX || MODE == kGradW, kBmn = MODE == kGradW;
+    static constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;     // outputs along m per tile
+    static __device__ int m_tiles(const ProductParams &p) { return (p.M + kFeat - 1) / kFeat; }
+};
+
+__device__ __forceinline__ void advance(uint32_t &s, uint32_t &phase) {
+    if (++s == kStages) {
+        s = 0;
+        phase ^= 1u;
+    }
+}
+
+// ---- warp 0 of each CTA: copies
+
+struct Loader {
+    uint32_t issued = 0, s = 0, phase = 0;    // slices; the next one's stage and its round's parity
+    uint32_t tails = 0, landed = 0;           // by stage: a tail was loaded, its barrier's phase
+    int64_t next;
+
+    template <Mode MODE> __device__ bool run(const Cta &c, const Work &w) {
+        constexpr bool kAmn = Shape<MODE>::kAmn, kBmn = Shape<MODE>::kBmn;
+        Barriers &bars = *c.bars;
+        const ProductParams &p = w.p;
+        const bool elected = elect_one();
+        const uint32_t full0 = c.first_cta(&bars.full[0]);
+        const int mt = Shape<MODE>::m_tiles(p);
+        bool ok = true;
+        Walker walk;
+        Tile t;
+        walk.start(p, mt);
+        for (; ok && walk.find(p, mt, next, &t); next += c.pairs) {
+            const int K = p.K < 0 ? t.rows : p.K;
+            const int half = ((t.n + 31) & ~31) / 2;      // this CTA's n
+            // rows of B: one copy of 128, or up to three of 32
+            const bool narrow = !kBmn && half <= 96;
+            const int boxes = kBmn ? (half + 63) / 64 : narrow ? (half + 31) / 32 : 1;
+            const uint32_t box = narrow ? kHalfBytes / 4 : kHalfBytes;
+            const CUtensorMap *mb = narrow ? &w.b32 : &w.b;
+            const int m0 = (t.m * 2 + (int)c.rank) * kTileM, n0 = t.n0 + (int)c.rank * half;
+            for (int k = 0; k < K; k += kSliceK) {
+                if (!tensor_wait(c.bar(&bars.empty[s]), phase ^ 1u, c.gave_up)) {
+                    ok = false;
+                    break;
+                }
+                if (elected) {
+                    const int halves = K - k > 64 ? 2 : 1;        // of a K-major operand
+                    const uint32_t bytes = (kAmn ? 2 : halves) * kHalfBytes + (kBmn ? 1 : halves) * boxes * box;
+                    // the second CTA clears the rows past a group's end before
+                    // it tells the first: that slice lands on its own barrier
+                    const bool last = MODE == kGradW && K - k < kSliceK, tail = last && c.rank == 1;
+                    const uint32_t full = tail ? in_cta(c.bar(&bars.tail[s]), 1) : full0 + s * 8;
+                    const uint32_t a = c.ring + s * kStageBytes, b = a + kBytesA;
+                    if (c.rank == 0) mbar_expect(c.bar(&bars.full[s]), last ? bytes : 2 * bytes);
+                    if (tail) mbar_expect(c.bar(&bars.tail[s]), bytes);
+                    if constexpr (kAmn) {
+                        const int row = MODE == kGradW ? t.first + k : k;
+                        const int own = MODE == kGradW ? t.seg : t.g;
+                        tma_load3(a, &w.a, full, m0, row, own);
+                        tma_load3(a + kHalfBytes, &w.a, full, m0 + 64, row, own);
+                    }
+                    if constexpr (kBmn) {
+                        for (int j = 0; j < boxes; ++j)
+                            tma_load3(b + j * kHalfBytes, mb, full, n0 + j * 64, t.first + k, t.seg);
+                    }
+                    for (int h = 0; h < halves; ++h) {
+                        if constexpr (MODE == kGated)
+                            tma_load5(a + h * kHalfBytes, &w.a, full, k + h * 64, 0, 0, m0 / 16, t.g);
+                        else if constexpr (!kAmn)
+                            tma_load3(a + h * kHalfBytes, &w.a, full, k + h * 64, m0, t.g);
+                        if constexpr (!kBmn)
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load3(b + h * kHalfBytes + j * box, mb, full, k + h * 64, t.first + n0 + j * 32,
+                                          t.seg);
+                    }
+                }
+                if (MODE == kGradW && c.rank == 1 && K - k < kSliceK) {
+                    if (tails >> s & 1u) landed ^= 1u << s;
+                    tails |= 1u << s;
+                }
+                ++issued;
+                advance(s, phase);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        next -= walk.before;
+        return ok;
+    }
+
+    // The pair ends together, and not before its copies have landed and the
+    // stages' last signals have come; after a wait that ran out, as far as they
+    // come within another wait each.
+    __device__ void finish(const Cta &c, bool ok) {
+        if ((threadIdx.x & 31) == 0) {
+            Barriers &bars = *c.bars;
+            int ignore = 0;
+            volatile int *flag = ok ? c.gave_up : &ignore;
+            for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
+                const uint32_t q = j % kStages, round = (j / kStages) & 1u;
+                if (!ok && c.rank == 0) tensor_wait(c.bar(&bars.full[q]), round, flag);
+                if (!ok && c.rank == 1 && (tails >> q & 1u))
+                    tensor_wait(c.bar(&bars.tail[q]), landed >> q & 1u, flag);
+                tensor_wait(c.bar(&bars.empty[q]), round, flag);
+            }
+        }
+        __syncwarp();
+    }
+};
+
+// ---- warp 1 of the first CTA: matrix instructions
+
+struct Multiplier {
+    uint32_t s = 0, phase = 0, acc = 0, tails = 0;
+    int64_t next;
+
+    template <typename T, Mode MODE> __device__ bool run(const Cta &c, const Work &w) {
+        constexpr bool kAmn = Shape<MODE>::kAmn, kBmn = Shape<MODE>::kBmn;
+        constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
+        Barriers &bars = *c.bars;
+        const ProductParams &p = w.p;
+        const bool elected = elect_one();
+        // descriptors; step j is 16 k on: 32 bytes of a row and the other half
+        // after four (K-major), or 16 rows (MN-major)
+        const uint64_t a0 = smem_desc(c.ring, kAmn ? kHalfBytes : 16, 1024);
+        const uint64_t b0 = smem_desc(c.ring + kBytesA, kBmn ? kHalfBytes : 16, 1024);
+        auto step = [](bool mn, int j) -> uint64_t {
+            return (mn ? j * 2048 : j / 4 * kHalfBytes + j % 4 * 32) >> 4;
+        };
+        const int mt = Shape<MODE>::m_tiles(p);
+        bool ok = true;
+        Walker walk;
+        Tile t;
+        walk.start(p, mt);
+        for (; ok && walk.find(p, mt, next, &t); next += c.pairs) {
+            const int K = p.K < 0 ? t.rows : p.K;
+            const int n = (t.n + 31) & ~31;
+            if (K == 0) continue;
+            const uint32_t idesc = kIdesc | idesc_n(n);
+            const uint32_t d = c.tmem + (acc & 1u) * 256;
+            ok = warp_wait<true>(c.bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, c.gave_up);
+            tcgen_after_sync();
+            // One thread issues everything, and has to queue the next slice's
+            // instructions before the last one's end: the loop is kept short.
+            const int end = !ok ? 0 : MODE == kGradW ? K / kSliceK * kSliceK : K;
+            for (int k = 0; k < end; k += kSliceK) {
+                if (!tensor_wait(c.bar(&bars.full[s]), phase, c.gave_up)) {
+                    ok = false;
+                    break;
+                }
+                if (elected) {
+                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+#pragma unroll
+                    for (int j = 0; j < kSliceK / 16; ++j)
+                        if (j == 0 || k + j * 16 < K)
+                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, k > 0 || j > 0);
+                    mma_commit_pair(c.bar(&bars.empty[s]));
+                }
+                advance(s, phase);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (MODE == kGradW && ok && K % kSliceK) {
+                ok = warp_wait(c.bar(&bars.full[s]), phase, c.gave_up);
+                if (ok) {
+                    clear_rows(c.ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, K % kSliceK);
+                    ok = warp_wait<true>(c.bar(&bars.peer_tail[s]), tails >> s & 1u, c.gave_up);
+                    tails ^= 1u << s;
+                }
+                if (ok && elected) {
+                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+#pragma unroll
+                    for (int j = 0; j < kSliceK / 16; ++j)
+                        if (j * 16 < K % kSliceK)
+                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, K > kSliceK || j > 0);
+                    mma_commit_pair(c.bar(&bars.empty[s]));
+                }
+                advance(s, phase);
+            }
+            if (ok && elected) mma_commit_pair(c.bar(&bars.acc_full[acc & 1u]));
+            ++acc;
+        }
+        next -= walk.before;
+        return ok;
+    }
+    __device__ void finish(const Cta &c, bool ok) {
+        if (ok) return;                                  // else let the matrix unit finish
+        int ignore = 0;
+        if (elect_one()) mma_commit(c.bar(&c.bars->drained));
+        tensor_wait(c.bar(&c.bars->drained), 0, &ignore);
+    }
+};
+
+// ---- warp 1 of the second CTA: clears its part of a group's last rows
+
+struct Clearer {
+    uint32_t slice = 0, tails = 0;
+    int64_t next;
+
+    template <Mode MODE> __device__ bool run(const Cta &c, const Work &w) {
+        Barriers &bars = *c.bars;
+        const ProductParams &p = w.p;
+        const int mt = Shape<MODE>::m_tiles(p);
+        bool ok = true;
+        Walker walk;
+        Tile t;
+        walk.start(p, mt);
+        for (; ok && walk.find(p, mt, next, &t); next += c.pairs) {
+            const int K = p.K < 0 ? t.rows : p.K, live = K % kSliceK;
+            slice += (K + kSliceK - 1) / kSliceK;
+            if (MODE != kGradW || live == 0) continue;
+            const int n = (t.n + 31) & ~31;
+            const uint32_t s = (slice - 1) % kStages;
+            ok = warp_wait(c.bar(&bars.tail[s]), tails >> s & 1u, c.gave_up);
+            if (!ok) break;
+            tails ^= 1u << s;
+            clear_rows(c.ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, live);
+            if ((threadIdx.x & 31) == 0) cluster_arrive(c.first_cta(&bars.peer_tail[s]));
+        }
+        next -= walk.before;
+        return ok;
+    }
+};
+
+// ---- warps 2..9: outputs
+
+struct Finisher {
+    uint32_t acc = 0;
+    int64_t next;
+
+    template <typename T, Mode MODE> __device__ bool run(const Cta &c, const Work &w) {
+        Barriers &bars = *c.bars;
+        const ProductParams &p = w.p;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int quarter = warp & 3;                    // the TMEM lanes this warp may read
+        const int c0 = (warp - 2) / 4 * 32;              // its first columns
+        float *turn = c.turns + (warp - 2) * (kTurnBytes / 4);
+        const int mt = Shape<MODE>::m_tiles(p);
+        bool ok = true;
+        Epilogue<T, MODE> ep;
+        Walker walk;
+        Tile t;
+        walk.start(p, mt);
+        for (; ok && walk.find(p, mt, next, &t); next += c.pairs) {
+            const int K = p.K < 0 ? t.rows : p.K, n = t.n;
+            ep.start(p, t, quarter, c.rank, c0);
+            float bias = 0.f;
+            if ((MODE == kForward || MODE == kGated) && p.bias) {
+                const int in = quarter * 32 + lane;      // this lane's row of the accumulator
+                const int m = (t.m * 2 + (int)c.rank) * (MODE == kGated ? 64 : 128) +
+                              (MODE == kGated ? (in >> 4) * 8 + (in & 7) : in);
+                const T *b = static_cast<const T *>(p.bias) + (int64_t)t.g * (MODE == kGated ? 2 * p.M : p.M);
+                if (m < p.M) bias = f32(b[MODE == kGated && (in & 8) ? p.M + m : m]);
+            }
+            if (K > 0) {
+                ok = warp_wait(c.bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, c.gave_up);
+                if (!ok) break;
+                tcgen_after_sync();
+            }
+            const uint32_t d = c.tmem + (acc & 1u) * 256 + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t free = c.first_cta(&bars.acc_empty[acc & 1u]);
+            if (K > 0 && c0 >= n) {                      // no columns for this warp
+                tcgen_before_sync();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(free);
+            }
+            for (int col = c0; col < n; col += kColumnStep) {
+                float v[32];
+                if (K > 0) {
+                    tmem_load32(d + col, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                }
+                if (K > 0 && col + kColumnStep >= n) {   // the accumulator may be filled again
+                    tcgen_before_sync();
+                    __syncwarp();
+                    if (lane == 0) cluster_arrive(free);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += bias;
+                ep.columns(p, turn, v, col);
+            }
+            if (K > 0) ++acc;
+        }
+        next -= walk.before;
+        return ok;
+    }
+};
+
+// One product (FIRST), or two in a row (then SECOND), either of which may be
+// left out (null).
+template <typename T, Mode FIRST, Mode SECOND>
+__device__ __forceinline__ void run_products(const Work *first, const Work *second, uint32_t *error) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bars;
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    float *turns = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + kRingBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    volatile int *gave_up = &bars.gave_up;
-    auto bar = [](uint64_t *b) { return smem_u32(b); };
-    auto first_cta = [](uint64_t *b) { return in_cta(smem_u32(b), 0); };
+    const int warp = threadIdx.x >> 5;
+    Cta c;
+    c.bars = &bars;
+    c.ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    c.turns = reinterpret_cast<float *>(smem_raw + (c.ring - smem_u32(smem_raw)) + kRingBytes);
+    c.rank = cluster_rank();
+    c.pairs = gridDim.x >> 1;
+    c.gave_up = &bars.gave_up;
+    const int64_t pair = blockIdx.x >> 1;
 
+    // The next kernel on the stream may get ready as this one's CTAs leave; this
+    // one does so before it waits for the kernel before it.
+    grid_dependents_may_launch();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 1);                 // the first CTA's hears of both CTAs' loads
@@ -355,8 +665,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(&bars.drained, 1);
         bars.gave_up = 0;
         mbar_init_fence();
-        tma_prefetch_map(&map_a);
-        tma_prefetch_map(&map_b);
+        const Work *w = first ? first : second;
+        tma_prefetch_map(&w->a);
+        tma_prefetch_map(&w->b);
     }
     __syncwarp();
     cluster_sync();
@@ -364,229 +675,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tcgen_before_sync();
     __syncthreads();
     tcgen_after_sync();
-    const uint32_t tmem = bars.tmem;
+    c.tmem = bars.tmem;
+    grid_dependency_wait();
 
-    const int mt = (p.M + kFeat - 1) / kFeat;
-    Walker walk;
-    Tile t;
-    walk.start(p, mt);
     bool ok = true;
-
     if (warp == 0) {
-        uint32_t issued = 0, s = 0, phase = 0;            // slices, the next one's stage and its round's parity
-        uint32_t tails = 0, landed = 0;                   // by stage: a tail was loaded, its barrier's phase
-        const bool elected = elect_one();
-        const uint32_t full0 = first_cta(&bars.full[0]);
-        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int K = p.K < 0 ? t.rows : p.K;
-            const int half = ((t.n + 31) & ~31) / 2;      // this CTA's n
-            // rows of B: one copy of 128, or up to three of 32
-            const bool narrow = !kBmn && half <= 96;
-            const int boxes = kBmn ? (half + 63) / 64 : narrow ? (half + 31) / 32 : 1;
-            const uint32_t box = narrow ? kHalfBytes / 4 : kHalfBytes;
-            const CUtensorMap *mb = narrow ? &map_b32 : &map_b;
-            const int m0 = (t.m * 2 + (int)rank) * kTileM, n0 = t.n0 + (int)rank * half;
-            for (int k = 0; k < K; k += kSliceK) {
-                if (!tensor_wait(bar(&bars.empty[s]), phase ^ 1u, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                if (elected) {
-                    const int halves = K - k > 64 ? 2 : 1;        // of a K-major operand
-                    const uint32_t bytes = (kAmn ? 2 : halves) * kHalfBytes + (kBmn ? 1 : halves) * boxes * box;
-                    // the second CTA clears the rows past a group's end before
-                    // it tells the first: that slice lands on its own barrier
-                    const bool last = MODE == kGradW && K - k < kSliceK, tail = last && rank == 1;
-                    const uint32_t full = tail ? in_cta(bar(&bars.tail[s]), 1) : full0 + s * 8;
-                    const uint32_t a = ring + s * kStageBytes, b = a + kBytesA;
-                    if (rank == 0) mbar_expect(bar(&bars.full[s]), last ? bytes : 2 * bytes);
-                    if (tail) mbar_expect(bar(&bars.tail[s]), bytes);
-                    if constexpr (kAmn) {
-                        const int row = MODE == kGradW ? t.first + k : k;
-                        const int own = MODE == kGradW ? t.seg : t.g;
-                        tma_load3(a, &map_a, full, m0, row, own);
-                        tma_load3(a + kHalfBytes, &map_a, full, m0 + 64, row, own);
-                    }
-                    if constexpr (kBmn) {
-                        for (int j = 0; j < boxes; ++j)
-                            tma_load3(b + j * kHalfBytes, mb, full, n0 + j * 64, t.first + k, t.seg);
-                    }
-                    for (int h = 0; h < halves; ++h) {
-                        if constexpr (MODE == kGated)
-                            tma_load5(a + h * kHalfBytes, &map_a, full, k + h * 64, 0, 0, m0 / 16, t.g);
-                        else if constexpr (!kAmn)
-                            tma_load3(a + h * kHalfBytes, &map_a, full, k + h * 64, m0, t.g);
-                        if constexpr (!kBmn)
-                            for (int j = 0; j < boxes; ++j)
-                                tma_load3(b + h * kHalfBytes + j * box, mb, full, k + h * 64, t.first + n0 + j * 32,
-                                          t.seg);
-                    }
-                }
-                if (MODE == kGradW && rank == 1 && K - k < kSliceK) {
-                    if (tails >> s & 1u) landed ^= 1u << s;
-                    tails |= 1u << s;
-                }
-                ++issued;
-                if (++s == kStages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        // The pair ends together, and not before its copies have landed and the
-        // stages' last signals have come; after a wait that ran out, as far
-        // as they come within another wait each.
-        if (lane == 0) {
-            int ignore = 0;
-            volatile int *flag = ok ? gave_up : &ignore;
-            for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
-                const uint32_t q = j % kStages, round = (j / kStages) & 1u;
-                if (!ok && rank == 0) tensor_wait(bar(&bars.full[q]), round, flag);
-                if (!ok && rank == 1 && (tails >> q & 1u)) tensor_wait(bar(&bars.tail[q]), landed >> q & 1u, flag);
-                tensor_wait(bar(&bars.empty[q]), round, flag);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1 && rank == 0) {
-        constexpr uint32_t kIdesc = f16_idesc(IsBf16<T>::value, kAmn, kBmn, 2 * kTileM);
-        const bool elected = elect_one();
-        // descriptors; step j is 16 k on: 32 bytes of a row and the other half
-        // after four (K-major), or 16 rows (MN-major)
-        const uint64_t a0 = smem_desc(ring, kAmn ? kHalfBytes : 16, 1024);
-        const uint64_t b0 = smem_desc(ring + kBytesA, kBmn ? kHalfBytes : 16, 1024);
-        auto step = [](bool mn, int j) -> uint64_t {
-            return (mn ? j * 2048 : j / 4 * kHalfBytes + j % 4 * 32) >> 4;
-        };
-        uint32_t s = 0, phase = 0, acc = 0, tails = 0;
-        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int K = p.K < 0 ? t.rows : p.K;
-            const int n = (t.n + 31) & ~31;
-            if (K == 0) continue;
-            const uint32_t idesc = kIdesc | idesc_n(n);
-            const uint32_t d = tmem + (acc & 1u) * 256;
-            ok = warp_wait<true>(bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, gave_up);
-            tcgen_after_sync();
-            // One thread issues everything, and has to queue the next slice's
-            // instructions before the last one's end: the loop is kept short.
-            const int end = !ok ? 0 : MODE == kGradW ? K / kSliceK * kSliceK : K;
-            for (int k = 0; k < end; k += kSliceK) {
-                if (!tensor_wait(bar(&bars.full[s]), phase, gave_up)) {
-                    ok = false;
-                    break;
-                }
-                if (elected) {
-                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
-#pragma unroll
-                    for (int j = 0; j < kSliceK / 16; ++j)
-                        if (j == 0 || k + j * 16 < K)
-                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, k > 0 || j > 0);
-                    mma_commit_pair(bar(&bars.empty[s]));
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (MODE == kGradW && ok && K % kSliceK) {
-                ok = warp_wait(bar(&bars.full[s]), phase, gave_up);
-                if (ok) {
-                    clear_rows(ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, K % kSliceK);
-                    ok = warp_wait<true>(bar(&bars.peer_tail[s]), tails >> s & 1u, gave_up);
-                    tails ^= 1u << s;
-                }
-                if (ok && elected) {
-                    const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
-#pragma unroll
-                    for (int j = 0; j < kSliceK / 16; ++j)
-                        if (j * 16 < K % kSliceK)
-                            mma_f16(d, da + step(kAmn, j), db + step(kBmn, j), idesc, K > kSliceK || j > 0);
-                    mma_commit_pair(bar(&bars.empty[s]));
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (ok && elected) mma_commit_pair(bar(&bars.acc_full[acc & 1u]));
-            ++acc;
-        }
-        if (!ok) {                                       // let the matrix unit finish
-            int ignore = 0;
-            if (elected) mma_commit(bar(&bars.drained));
-            tensor_wait(bar(&bars.drained), 0, &ignore);
-        }
+        Loader r;
+        r.next = pair;
+        if (first) ok = r.run<FIRST>(c, *first);
+        if constexpr (SECOND != kNone)
+            if (ok && second) ok = r.run<SECOND>(c, *second);
+        r.finish(c, ok);
+    } else if (warp == 1 && c.rank == 0) {
+        Multiplier r;
+        r.next = pair;
+        if (first) ok = r.run<T, FIRST>(c, *first);
+        if constexpr (SECOND != kNone)
+            if (ok && second) ok = r.run<T, SECOND>(c, *second);
+        r.finish(c, ok);
     } else if (warp == 1) {
-        if (MODE == kGradW) {
-            uint32_t slice = 0, tails = 0;
-            for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-                const int slices = (t.rows + kSliceK - 1) / kSliceK, live = t.rows % kSliceK;
-                slice += slices;
-                if (live == 0) continue;
-                const int n = (t.n + 31) & ~31;
-                const uint32_t s = (slice - 1) % kStages;
-                ok = warp_wait(bar(&bars.tail[s]), tails >> s & 1u, gave_up);
-                if (!ok) break;
-                tails ^= 1u << s;
-                clear_rows(ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, live);
-                if (lane == 0) cluster_arrive(first_cta(&bars.peer_tail[s]));
-            }
+        if constexpr (SECOND != kNone) {
+            Clearer r;
+            r.next = pair;
+            if (first) ok = r.run<FIRST>(c, *first);
+            if (ok && second) ok = r.run<SECOND>(c, *second);
         }
     } else {
-        const int quarter = warp & 3;                    // the TMEM lanes this warp may read
-        const int c0 = (warp - 2) / 4 * 32;              // its first columns
-        float *turn = turns + (warp - 2) * (kTurnBytes / 4);
-        uint32_t acc = 0;
-        Epilogue<T, MODE> ep;
-        for (int64_t i = pair; ok && walk.find(p, mt, i, &t); i += pairs) {
-            const int K = p.K < 0 ? t.rows : p.K, n = t.n;
-            ep.start(p, t, quarter, rank, c0);
-            float bias = 0.f;
-            if ((MODE == kForward || MODE == kGated) && p.bias) {
-                const int in = quarter * 32 + lane;      // this lane's row of the accumulator
-                const int m = (t.m * 2 + (int)rank) * (MODE == kGated ? 64 : 128) +
-                              (MODE == kGated ? (in >> 4) * 8 + (in & 7) : in);
-                const T *b = static_cast<const T *>(p.bias) + (int64_t)t.g * (MODE == kGated ? 2 * p.M : p.M);
-                if (m < p.M) bias = f32(b[MODE == kGated && (in & 8) ? p.M + m : m]);
-            }
-            if (K > 0) {
-                ok = warp_wait(bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, gave_up);
-                if (!ok) break;
-                tcgen_after_sync();
-            }
-            const uint32_t d = tmem + (acc & 1u) * 256 + ((uint32_t)(quarter * 32) << 16);
-            if (K > 0 && c0 >= n) {                      // no columns for this warp
-                tcgen_before_sync();
-                __syncwarp();
-                if (lane == 0) cluster_arrive(first_cta(&bars.acc_empty[acc & 1u]));
-            }
-            for (int c = c0; c < n; c += kColumnStep) {
-                float v[32];
-                if (K > 0) {
-                    tmem_load32(d + c, v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                }
-                if (K > 0 && c + kColumnStep >= n) {              // the accumulator may be filled again
-                    tcgen_before_sync();
-                    __syncwarp();
-                    if (lane == 0) cluster_arrive(first_cta(&bars.acc_empty[acc & 1u]));
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += bias;
-                ep.columns(p, turn, v, c);
-            }
-            if (K > 0) ++acc;
-        }
+        Finisher r;
+        r.next = pair;
+        if (first) ok = r.run<T, FIRST>(c, *first);
+        if constexpr (SECOND != kNone)
+            if (ok && second) ok = r.run<T, SECOND>(c, *second);
     }
     __syncwarp();
     tcgen_before_sync();
     cluster_sync();              // neither CTA's memory is read or signalled any more
     tcgen_after_sync();
-    if (warp == 1) tmem_free(tmem, 512);
-    if (threadIdx.x == 0 && bars.gave_up && p.error) atomicOr(p.error, EP_DEVERR_TIMEOUT);
+    if (warp == 1) tmem_free(c.tmem, 512);
+    if (threadIdx.x == 0 && bars.gave_up && error) atomicOr(error, EP_DEVERR_TIMEOUT);
+}
+
+template <typename T, Mode MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ Work w) {
+    run_products<T, MODE, kNone>(&w, nullptr, w.p.error);
+}
+
+// Both gradients in one launch: the pairs that finish grad_x's tiles go on
+// with grad_w's.
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gradient_kernel(const __grid_constant__ Work x, const __grid_constant__ Work w, bool has_x, bool has_w) {
+    run_products<T, kGradX, kGradW>(has_x ? &x : nullptr, has_w ? &w : nullptr, w.p.error);
 }
 
 // d = grad * act'(pre) over every group's rows, rounded once for the
@@ -600,6 +740,7 @@ struct ActGradParams {
     int N, act, splits;
     ep_rows_t grad, pre, d;
     float *part;            // [splits][G][wide] column sums, or null
+    void *grad_bias;        // [G][wide], with one part a group
     bool write;
 };
 
@@ -633,6 +774,7 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
     group_range(p.gr, g, &first, &rows);
     const int per = (rows + p.splits - 1) / p.splits;
     const int r1 = first + min(rows, (split + 1) * per);
+    grid_dependents_may_launch();
     const T *grad = static_cast<const T *>(p.grad.ptr) + seg * p.grad.rank_stride + c;
     const T *pre = static_cast<const T *>(p.pre.ptr) + seg * p.pre.rank_stride + c;
     T *d = static_cast<T *>(p.d.ptr) + seg * p.d.rank_stride + c;
@@ -681,7 +823,7 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
             }
         }
     }
-    if (!p.part) return;
+    if (!p.part && !p.grad_bias) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         sums[warp][0][lane * 8 + j] = s0[j];
@@ -693,7 +835,9 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
         const int col = blockIdx.x * kActCols + threadIdx.x;
         float s = 0.f;
         for (int w = 0; w < kActWarps; ++w) s += sums[w][h][threadIdx.x];
-        if (col < p.N) p.part[(split * G + g) * wide + h * (int64_t)p.N + col] = s;
+        if (col >= p.N) continue;
+        if (p.part) p.part[(split * G + g) * wide + h * (int64_t)p.N + col] = s;
+        else static_cast<T *>(p.grad_bias)[g * wide + h * (int64_t)p.N + col] = rounded<T>(s);
     }
 }
 
@@ -814,12 +958,11 @@ bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, in
 
 // ---- launch
 
-int sm_count() {
-    constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = 64;
+
+int sm_count(int dev) {
     static std::atomic<int> cached[kMaxDevices];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-    n = cached[dev].load(std::memory_order_relaxed);
+    int n = cached[dev].load(std::memory_order_relaxed);
     if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         cached[dev].store(n, std::memory_order_relaxed);
@@ -827,39 +970,40 @@ int sm_count() {
     return n;
 }
 
-template <typename T, Mode MODE>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b32, const ProductParams &p,
-                   cudaStream_t st) {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> configured[kMaxDevices];       // the attribute is per device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!configured[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(product_kernel<T, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        configured[dev].store(true, std::memory_order_release);
-    }
-    // tiles at most: every group's last tile may be a part
-    constexpr int kFeat = MODE == kGated ? kTileM : 2 * kTileM;
-    const int64_t mt = (p.M + kFeat - 1) / kFeat;
+// Tiles at most: every group's last tile may be a part.
+template <Mode MODE> int64_t most_tiles(const ProductParams &p) {
+    const int64_t mt = (p.M + Shape<MODE>::kFeat - 1) / Shape<MODE>::kFeat;
     const int64_t G = (int64_t)p.gr.R * p.gr.per;
-    const int64_t nt = p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / kTileN + G : G * ((p.N + kTileN - 1) / kTileN);
-    const int pairs = sm_count() / 2;
-    if (pairs < 1) return cudaErrorInvalidDevice;
-    const int64_t grid = 2 * (mt * nt < pairs ? mt * nt : pairs);
-    product_kernel<T, MODE><<<(unsigned)grid, kThreads, kSmemBytes, st>>>(a, b, b32, p);
-    return cudaGetLastError();
+    return mt * (p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / kTileN + G : G * ((p.N + kTileN - 1) / kTileN));
 }
 
-template <Mode MODE>
-ep_status_t launch_product(int dtype, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &b32,
-                           const ProductParams &p, cudaStream_t st) {
-    const cudaError_t e = dtype == EP_DT_BF16 ? launch<__nv_bfloat16, MODE>(a, b, b32, p, st)
-                                              : launch<__half, MODE>(a, b, b32, p, st);
-    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
+// One CTA per SM, in pairs, as a programmatic dependent of the kernel before.
+template <typename... Params, typename... Args>
+ep_status_t launch_pairs(std::atomic<bool> *configured, void (*kernel)(Params...), int64_t tiles, cudaStream_t st,
+                         Args &&...args) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EP_ERR_GPU_OP;
+    if (!configured[dev].load(std::memory_order_acquire)) {        // the attribute is per device
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
+            return EP_ERR_GPU_OP;
+        configured[dev].store(true, std::memory_order_release);
+    }
+    const int pairs = sm_count(dev) / 2;
+    if (pairs < 1) return EP_ERR_GPU_OP;
+    const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
+    return launch_after_previous(kernel, grid, kThreads, kSmemBytes, st, static_cast<Args &&>(args)...) == cudaSuccess
+               ? EP_SUCCESS : EP_ERR_GPU_OP;
+}
+
+template <typename T, Mode MODE> ep_status_t launch_product(const Work &w, cudaStream_t st) {
+    static std::atomic<bool> configured[kMaxDevices];
+    return launch_pairs(configured, product_kernel<T, MODE>, most_tiles<MODE>(w.p), st, w);
+}
+template <typename T>
+ep_status_t launch_gradients(const Work &x, const Work &w, bool has_x, bool has_w, cudaStream_t st) {
+    static std::atomic<bool> configured[kMaxDevices];
+    const int64_t tiles = (has_x ? most_tiles<kGradX>(x.p) : 0) + (has_w ? most_tiles<kGradW>(w.p) : 0);
+    return launch_pairs(configured, gradient_kernel<T>, tiles, st, x, w, has_x, has_w);
 }
 
 // The gradient's workspace: d in the tensors' type (not needed where act' is
@@ -891,7 +1035,8 @@ ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
         (residual->ptr && !valid_rows(*residual, d->out_features, many)) ||
         (pre->ptr && !valid_rows(*pre, wide_of(*d), many)))
         return EP_ERR_INVALID_ARGS;
-    ProductParams p = {};
+    Work w = {};
+    ProductParams &p = w.p;
     p.gr = groups_of(*d);
     p.M = d->out_features;
     p.N = -1;
@@ -902,17 +1047,16 @@ ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
     p.out = *y;
     p.pre = *pre;
     p.error = d_error;
-    const bool gated = d->activation == EP_ACT_SWIGLU;
+    const bool gated = d->activation == EP_ACT_SWIGLU, bf16 = d->dtype == EP_DT_BF16;
     const int64_t G = (int64_t)d->ranks * d->groups;
-    CUtensorMap a, b, b32;
-    if (!(gated ? encode_gated(&a, d->dtype, d->weight, p.K, p.M, G)
-                : encode_rows(&a, d->dtype, d->weight, p.K, p.M, G, kTileM)) ||
-        !encode_rows(&b, d->dtype, d->x, p.K, d->rows, d->ranks, kTileN / 2) ||
-        !encode_rows(&b32, d->dtype, d->x, p.K, d->rows, d->ranks, 32))
+    if (!(gated ? encode_gated(&w.a, d->dtype, d->weight, p.K, p.M, G)
+                : encode_rows(&w.a, d->dtype, d->weight, p.K, p.M, G, kTileM)) ||
+        !encode_rows(&w.b, d->dtype, d->x, p.K, d->rows, d->ranks, kTileN / 2) ||
+        !encode_rows(&w.b32, d->dtype, d->x, p.K, d->rows, d->ranks, 32))
         return EP_ERR_GPU_OP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return gated ? launch_product<kGated>(d->dtype, a, b, b32, p, st)
-                 : launch_product<kForward>(d->dtype, a, b, b32, p, st);
+    if (gated) return bf16 ? launch_product<__nv_bfloat16, kGated>(w, st) : launch_product<__half, kGated>(w, st);
+    return bf16 ? launch_product<__nv_bfloat16, kForward>(w, st) : launch_product<__half, kForward>(w, st);
 }
 
 ep_status_t ep_expert_product_workspace(const ep_product_desc_t *d, size_t *bytes) {
@@ -941,56 +1085,54 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Groups gr = groups_of(*d);
     const ep_rows_t dd = act ? ep_rows_t{d_workspace, d->rows * wide, wide} : *grad;
+    const int splits = act_splits(*d);
+    const int64_t G = (int64_t)d->ranks * d->groups;
+    float *part = d_grad_bias && splits > 1
+                      ? reinterpret_cast<float *>(static_cast<char *>(d_workspace) + rounded_d_bytes(*d)) : nullptr;
     if (act || d_grad_bias) {
-        float *part = d_grad_bias ? reinterpret_cast<float *>(static_cast<char *>(d_workspace) + rounded_d_bytes(*d))
-                                  : nullptr;
-        const int splits = act_splits(*d), G = gr.R * gr.per;
-        const ActGradParams q = {gr, d->out_features, d->activation, splits, *grad, *pre, dd, part, act};
-        const dim3 grid((d->out_features + kActCols - 1) / kActCols, G, splits);
+        const ActGradParams q = {gr, d->out_features, d->activation, splits, *grad, *pre, dd, part,
+                                 part ? nullptr : d_grad_bias, act};
+        const dim3 grid((d->out_features + kActCols - 1) / kActCols, (unsigned)G, splits);
         with_type(d->dtype, [&](auto type) {
             using T = decltype(type);
             if (d->activation == EP_ACT_SWIGLU) act_grad_kernel<T, true><<<grid, kActWarps * 32, 0, st>>>(q);
             else act_grad_kernel<T, false><<<grid, kActWarps * 32, 0, st>>>(q);
-            const int64_t n = G * wide;
-            if (part)
-                sum_parts_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, splits, n,
-                                                                                 static_cast<T *>(d_grad_bias));
         });
     }
-    const int64_t G = (int64_t)d->ranks * d->groups;
-    CUtensorMap a, b, b32;
-    if (grad_x->ptr && d->rows > 0) {
-        ProductParams p = {};
-        p.gr = gr;
-        p.M = d->in_features;
-        p.N = -1;
-        p.K = (int)wide;
-        p.out = *grad_x;
-        p.error = d_error;
-        if (!encode_rows(&a, d->dtype, d->weight, d->in_features, wide, G, kSliceK) ||
-            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
-            !encode_rows(&b32, d->dtype, dd, wide, d->rows, d->ranks, 32))
+    const bool has_x = grad_x->ptr && d->rows > 0, has_w = d_grad_w && d->rows > 0;
+    if (has_x || has_w) {
+        Work x = {}, w = {};
+        x.p.gr = gr;
+        x.p.M = d->in_features;
+        x.p.N = -1;
+        x.p.K = (int)wide;
+        x.p.out = *grad_x;
+        w.p.gr = gr;
+        w.p.M = d->in_features;
+        w.p.N = (int)wide;
+        w.p.K = -1;
+        w.p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
+        x.p.error = w.p.error = d_error;
+        if ((has_x && (!encode_rows(&x.a, d->dtype, d->weight, d->in_features, wide, G, kSliceK) ||
+                       !encode_rows(&x.b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
+                       !encode_rows(&x.b32, d->dtype, dd, wide, d->rows, d->ranks, 32))) ||
+            (has_w && (!encode_rows(&w.a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kSliceK) ||
+                       !encode_rows(&w.b, d->dtype, dd, wide, d->rows, d->ranks, kSliceK))))
             return EP_ERR_GPU_OP;
-        const ep_status_t s = launch_product<kGradX>(d->dtype, a, b, b32, p, st);
+        const ep_status_t s = d->dtype == EP_DT_BF16 ? launch_gradients<__nv_bfloat16>(x, w, has_x, has_w, st)
+                                                     : launch_gradients<__half>(x, w, has_x, has_w, st);
         if (s != EP_SUCCESS) return s;
-    }
-    if (d_grad_w && d->rows == 0)
-        return cudaMemsetAsync(d_grad_w, 0, (size_t)G * wide * d->in_features * 2, st) == cudaSuccess
-                   ? EP_SUCCESS : EP_ERR_GPU_OP;
-    if (d_grad_w) {
-        ProductParams p = {};
-        p.gr = gr;
-        p.M = d->in_features;
-        p.N = (int)wide;
-        p.K = -1;
-        p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
-        p.error = d_error;
-        if (!encode_rows(&a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kSliceK) ||
-            !encode_rows(&b, d->dtype, dd, wide, d->rows, d->ranks, kSliceK))
+    } else if (d_grad_w) {
+        if (cudaMemsetAsync(d_grad_w, 0, (size_t)G * wide * d->in_features * 2, st) != cudaSuccess)
             return EP_ERR_GPU_OP;
-        const ep_status_t s = launch_product<kGradW>(d->dtype, a, b, b, p, st);
-        if (s != EP_SUCCESS) return s;
     }
+    if (part)
+        with_type(d->dtype, [&](auto type) {
+            using T = decltype(type);
+            const int64_t n = G * wide;
+            sum_parts_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, splits, n,
+                                                                             static_cast<T *>(d_grad_bias));
+        });
     return launched();
 }
 
