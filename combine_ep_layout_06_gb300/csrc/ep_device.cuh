@@ -210,10 +210,10 @@ __device__ __forceinline__ void bulk_wait_all() {
 // stream: its CTAs may be scheduled while that kernel finishes and must call
 // grid_dependency_wait() before reading anything it (or earlier work) wrote.
 template <typename... Params, typename... Args>
-cudaError_t launch_after_previous(void (*kernel)(Params...), unsigned blocks, unsigned threads,
+cudaError_t launch_after_previous(void (*kernel)(Params...), dim3 blocks, unsigned threads,
                                   size_t dyn, cudaStream_t st, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = blocks;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = dyn;
     cfg.stream = st;
