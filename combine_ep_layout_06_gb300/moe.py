@@ -8,7 +8,8 @@ gradient as a ``*_backward`` call.
 Marshalling only: every step runs in the CUDA kernels of libep_gb300.so.  The
 formulas are those of include/ep_api.h.  Every call is asynchronous on
 ``stream`` (default: the current one); what it allocates belongs to that
-stream.  Device-side problems (an expert id out of range, a wait that gave up)
+stream.  Inputs that another stream made have to be ready there, and to live
+until the call's work is done (``Tensor.record_stream``).  Device-side problems (an expert id out of range, a wait that gave up)
 set bits that ``moe_error`` reads.  The first call on a device creates its
 error word and may load device code: make it before any stream capture.
 
@@ -344,7 +345,8 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.
     with weight [G][2N][K] (the gate's features first); bias: [G][weight's
     features].  residual and out: [...][N].  Returns y, or (y, pre) with
     save_pre: what ``expert_product_backward`` needs.  Rows outside every
-    group are unspecified (untouched in ``out``)."""
+    group are unspecified (untouched in ``out``).  out may be the residual
+    itself and overlaps no other input."""
     index = x.get_device()
     if stream is not None or index < 0 or index != _current_device():
         with _elsewhere(x, stream):

@@ -520,7 +520,11 @@ typedef struct {
  * with fp32 products' sums and epilogue, one rounding per output.  d_bias:
  * [R*groups][wide] dense or NULL; residual, pre: ptr NULL to leave out;
  * pre gets the wide pre-activations (what the gradient needs).  Rows outside
- * every group are not written. */
+ * every group are not written.  y may be the residual itself; otherwise y and
+ * pre overlap nothing that the call reads.  The kernel is launched as a
+ * programmatic dependent of the kernel before it on the stream and waits for
+ * it before its first read or write; so are the gradient's, and ep_route's and
+ * ep_route_backward's from 2^22 logits on. */
 ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
                               const ep_rows_t *residual, const ep_rows_t *y,
                               const ep_rows_t *pre, uint32_t *d_error,

@@ -245,6 +245,35 @@ def test_one_group_of_all_rows():
     assert dx.shape == x.shape and dw.shape == w.shape and db is None
 
 
+def test_gradient_parts_can_be_left_out():
+    """The C entry with grad_x or grad_w NULL gives the same other parts."""
+    import ctypes
+
+    from combine_ep_layout_06_gb300 import _lib
+    d, wide, rows = make(1, 3, [[70, 0, 131]], 72, 136, torch.bfloat16, "silu", seed=15)
+    a = {n: t.cuda() for n, t in d.items()}
+    dx, dw, db = ep.expert_product_backward(a["grad"], a["x"], a["weight"], a["count"], a["offset"], pre=a["pre"],
+                                            activation="silu", bias_grad=True)
+    L = _lib.load()
+
+    def r(t):
+        return _lib.EpRowsC(t.data_ptr() if t is not None else None, 0, t.shape[-1] if t is not None else 0)
+    desc = _lib.EpProductDescC(1, 3, rows, 72, 136, _lib.EP_DT_BF16, 3, 0, a["count"].data_ptr(),
+                               a["offset"].data_ptr(), _lib.EpRowsC(a["weight"].data_ptr(), wide * 72, 72), r(a["x"]))
+    need = ctypes.c_size_t(0)
+    assert L.ep_expert_product_workspace(ctypes.byref(desc), ctypes.byref(need)) == 0
+    scratch = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for want_x, want_w, want_b in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1)):
+        x2, w2, b2 = (torch.zeros_like(t) if on else None for t, on in ((dx, want_x), (dw, want_w), (db, want_b)))
+        assert L.ep_expert_product_backward(
+            ctypes.byref(desc), ctypes.byref(r(a["grad"])), ctypes.byref(r(a["pre"])), ctypes.byref(r(x2)),
+            w2.data_ptr() if want_w else None, b2.data_ptr() if want_b else None, scratch.data_ptr(), need.value,
+            None, stream) == 0
+        for got, want in ((x2, dx), (w2, dw), (b2, db)):
+            assert got is None or torch.equal(got, want)
+
+
 def test_no_rows():
     w = torch.randn((3, 64, 32)).to(torch.bfloat16).cuda()
     x = torch.empty((1, 0, 32), dtype=torch.bfloat16, device="cuda")
