@@ -68,6 +68,7 @@ enum Mode { kForward, kGated, kGradX, kGradW, kNone };
 struct ProductParams {
     Groups gr;
     int M, N, K;           // N or K < 0: the group's number of rows
+    int tile_n;            // columns of a tile: kTileN, 128 or 64
     int act;
     const void *bias;      // [G][M], or [G][2M] (gated)
     ep_rows_t residual, out, pre;
@@ -105,7 +106,7 @@ struct Walker {
         first = rows = tiles = 0;
         if (g < p.gr.R * p.gr.per) {
             group_range(p.gr, g, &first, &rows);
-            tiles = mt * (((p.N < 0 ? rows : p.N) + kTileN - 1) / kTileN);
+            tiles = mt * (((p.N < 0 ? rows : p.N) + p.tile_n - 1) / p.tile_n);
         }
         upto = tiles;
 #pragma unroll
@@ -142,7 +143,7 @@ struct Walker {
         // equal parts of N instead of full tiles and a rest: a narrow rest would
         // load as much of the other operand for less work
         const int N = p.N < 0 ? t->rows : p.N;
-        const int parts = (N + kTileN - 1) / kTileN;
+        const int parts = (N + p.tile_n - 1) / p.tile_n;
         const int width = ((N + parts - 1) / parts + 31) & ~31;
         const int b = in / (band * parts), in_band = in - b * band * parts;
         const int wide = min(band, mt - b * band);
@@ -609,12 +610,14 @@ struct Finisher {
                 if (lane == 0) cluster_arrive(free);
             }
             for (int col = c0; col < n; col += kColumnStep) {
+                uint32_t r[32];
                 float v[32];
                 if (K > 0) {
-                    tmem_load32(d + col, v);
+                    tmem_load32(d + col, r);
+                    tmem_wait(r);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
                 }
                 if (K > 0 && col + kColumnStep >= n) {   // the accumulator may be filled again
                     tcgen_before_sync();
@@ -622,7 +625,7 @@ struct Finisher {
                     if (lane == 0) cluster_arrive(free);
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += bias;
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) + bias;
                 ep.columns(p, turn, v, col);
             }
             if (K > 0) ++acc;
@@ -970,40 +973,61 @@ int sm_count(int dev) {
     return n;
 }
 
-// Tiles at most: every group's last tile may be a part.
-template <Mode MODE> int64_t most_tiles(const ProductParams &p) {
+// Tiles of `columns` columns at most: every group's last tile may be a part.
+template <Mode MODE> int64_t most_tiles(const ProductParams &p, int columns) {
     const int64_t mt = (p.M + Shape<MODE>::kFeat - 1) / Shape<MODE>::kFeat;
     const int64_t G = (int64_t)p.gr.R * p.gr.per;
-    return mt * (p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / kTileN + G : G * ((p.N + kTileN - 1) / kTileN));
+    return mt * (p.N < 0 ? (int64_t)p.gr.R * p.gr.rows / columns + G : G * ((p.N + columns - 1) / columns));
+}
+
+// Full tiles, or narrower ones while those still find a pair of SMs each: they
+// load more for the same work, but outputs (most of a short tile's time) are
+// finished by more SMs.  2670 rows of 4 groups x 1688 -> 96 with gelu and
+// residual: 12 tiles 21.7 us, 43 tiles 12.6 us; past one tile a pair it turns
+// (9448 rows of 24 groups x 120 -> 64 gated: 8.9 us, in two rounds 10.8).
+template <Mode MODE> int64_t choose_tile(ProductParams &p, int64_t pairs) {
+    p.tile_n = kTileN;
+    while (p.tile_n > 64 && most_tiles<MODE>(p, p.tile_n / 2) <= pairs) p.tile_n /= 2;
+    return most_tiles<MODE>(p, p.tile_n);
 }
 
 // One CTA per SM, in pairs, as a programmatic dependent of the kernel before.
 template <typename... Params, typename... Args>
-ep_status_t launch_pairs(std::atomic<bool> *configured, void (*kernel)(Params...), int64_t tiles, cudaStream_t st,
-                         Args &&...args) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EP_ERR_GPU_OP;
+ep_status_t launch_pairs(int dev, std::atomic<bool> *configured, void (*kernel)(Params...), int64_t grid,
+                         cudaStream_t st, Args &&...args) {
     if (!configured[dev].load(std::memory_order_acquire)) {        // the attribute is per device
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) != cudaSuccess)
             return EP_ERR_GPU_OP;
         configured[dev].store(true, std::memory_order_release);
     }
-    const int pairs = sm_count(dev) / 2;
-    if (pairs < 1) return EP_ERR_GPU_OP;
-    const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_after_previous(kernel, grid, kThreads, kSmemBytes, st, static_cast<Args &&>(args)...) == cudaSuccess
+    return launch_after_previous(kernel, 2 * (unsigned)grid, kThreads, kSmemBytes, st, static_cast<Args &&>(args)...) ==
+                   cudaSuccess
                ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
-template <typename T, Mode MODE> ep_status_t launch_product(const Work &w, cudaStream_t st) {
+// The current device and its pairs of SMs; 0 when there is none.
+int device_pairs(int *dev) {
+    if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return 0;
+    return sm_count(*dev) / 2;
+}
+
+template <typename T, Mode MODE> ep_status_t launch_product(Work &w, cudaStream_t st) {
     static std::atomic<bool> configured[kMaxDevices];
-    return launch_pairs(configured, product_kernel<T, MODE>, most_tiles<MODE>(w.p), st, w);
+    int dev;
+    const int pairs = device_pairs(&dev);
+    if (pairs < 1) return EP_ERR_GPU_OP;
+    const int64_t tiles = choose_tile<MODE>(w.p, pairs);
+    return launch_pairs(dev, configured, product_kernel<T, MODE>, tiles < pairs ? tiles : pairs, st, w);
 }
 template <typename T>
-ep_status_t launch_gradients(const Work &x, const Work &w, bool has_x, bool has_w, cudaStream_t st) {
+ep_status_t launch_gradients(Work &x, Work &w, bool has_x, bool has_w, cudaStream_t st) {
     static std::atomic<bool> configured[kMaxDevices];
-    const int64_t tiles = (has_x ? most_tiles<kGradX>(x.p) : 0) + (has_w ? most_tiles<kGradW>(w.p) : 0);
-    return launch_pairs(configured, gradient_kernel<T>, tiles, st, x, w, has_x, has_w);
+    int dev;
+    const int pairs = device_pairs(&dev);
+    if (pairs < 1) return EP_ERR_GPU_OP;
+    int64_t tiles = has_x ? choose_tile<kGradX>(x.p, has_w ? pairs / 2 : pairs) : 0;
+    if (has_w) tiles += choose_tile<kGradW>(w.p, pairs - tiles);
+    return launch_pairs(dev, configured, gradient_kernel<T>, tiles < pairs ? tiles : pairs, st, x, w, has_x, has_w);
 }
 
 // The gradient's workspace: d in the tensors' type (not needed where act' is
