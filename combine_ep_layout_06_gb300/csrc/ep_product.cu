@@ -651,9 +651,6 @@ __device__ __forceinline__ void run_products(const Work *first, const Work *seco
     c.gave_up = &bars.gave_up;
     const int64_t pair = blockIdx.x >> 1;
 
-    // The next kernel on the stream may get ready as this one's CTAs leave; this
-    // one does so before it waits for the kernel before it.
-    grid_dependents_may_launch();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 1);                 // the first CTA's hears of both CTAs' loads
@@ -679,7 +676,10 @@ __device__ __forceinline__ void run_products(const Work *first, const Work *seco
     __syncthreads();
     tcgen_after_sync();
     c.tmem = bars.tmem;
+    // This far while the kernel before ends.  Only then may the next one start
+    // to get ready: it may count on all that came before this kernel.
     grid_dependency_wait();
+    grid_dependents_may_launch();
 
     bool ok = true;
     if (warp == 0) {

@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
                                                                  bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
     const Place<LANES> at(p, kRouteWarps, 1, 0);
-    grid_dependents_may_launch();
     grid_dependency_wait();
+    grid_dependents_may_launch();     // the next kernel may count on all before this one
     if (!__any_sync(0xffffffffu, at.present)) {          // nobody here
         for (int j = at.l; at.in && j < p.k; j += LANES) {
             p.w[at.tok * p.k + j] = 0.f;
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const bool dense = p.grad_loss || (softmax && !renorm);
     const int e0 = (int)(threadIdx.x & 31) % LANES * VPL;
     float f[VPL], gl = 0.f;
-    grid_dependents_may_launch();
     grid_dependency_wait();
+    grid_dependents_may_launch();     // the next kernel may count on all before this one
     if (p.grad_loss) {
         gl = *p.grad_loss * p.inv_n;
         const float share = p.inv_n * ((float)p.E / (float)p.k) * p.balance_coef;
@@ -690,7 +690,8 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
 
 int loss_blocks(const ep_route_desc_t &d) {
     const int64_t tokens = (int64_t)d.world_size * d.tokens;
-    // one block, without a second pass, costs an SM about 4 us for 2^15 logits
+    // one block, without a second pass: 19 712 logits 8.6 us in one launch
+    // against 4.9 + 4.1 us in two
     const int64_t want = tokens * d.num_experts <= 1 << 15 ? 1 : (tokens + 31) / 32;
     return (int)(want < 152 ? want : 152);
 }

@@ -69,3 +69,45 @@ def test_example_runs(capsys):
     lines = capsys.readouterr().out.strip().splitlines()
     first, last = (float(s.split("error ")[1].split(",")[0]) for s in (lines[0], lines[-1]))
     assert last < first                       # it learns
+
+
+@pytest.mark.parametrize("W,T,H", [(2, 64, 256), (4, 600, 512)])
+def test_back_to_back_calls_are_ordered(W, T, H):
+    """Kernels get ready while the one before them ends; each must still see
+    all that came before it: a chain product -> route -> dispatch -> combine on
+    changing inputs, with nothing waited for in between, gives the bits of the
+    same chain with the GPU waited for after every call."""
+    E, k, F = 4 * W, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(*shape):
+        return (torch.randn(shape, generator=g, device="cuda") * 0.2).to(torch.bfloat16)
+    w1, w2, router = rand(1, F, H), rand(1, H, F), rand(1, E, H)
+    op = ep.EpDispatchCombineOp(ep.EpDispatchCombineConfig(W, E, k, H, T))
+
+    def chain(x, wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        h = ep.expert_product(x.view(1, W * T, H), w1, activation="silu")
+        pause()
+        y = ep.expert_product(h, w2, residual=x.view(1, W * T, H))
+        pause()
+        logits = ep.expert_product(y, router).view(W, T, E)
+        pause()
+        weights, idx = ep.route(logits, k)
+        pause()
+        op.dispatch(y.view(W, T, H), weights, None, idx)
+        pause()
+        op.identity_expert()
+        pause()
+        out, _ = op.combine()
+        pause()
+        dx, dw, _ = ep.expert_product_backward(out.view(1, W * T, H), h, w2)
+        pause()
+        return out, dx, dw
+    inputs = [rand(W, T, H) for _ in range(12)]
+    want = [chain(x, True) for x in inputs]
+    got = [chain(x, False) for x in inputs]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert op.get_error() == (0, 0) and ep.moe_error() == 0
