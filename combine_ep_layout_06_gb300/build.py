@@ -1,9 +1,11 @@
-"""Build libep_gb300.so in-tree with nvcc for sm_103a (no cmake).
+"""Build libep_gb300.so in-tree with nvcc for sm_103a (no cmake), and
+_moe.so, the Python binding of the routing, loss and product calls.
 
 Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
 one shared library with the CUDA runtime linked statically, so that loading
-it needs only the driver.  Usage: ``python -m combine_ep_layout_06_gb300.build
-[--ptxas-verbose]``.
+it needs only the driver.  The binding is one C++ file against torch's
+headers, compiled next to them and linked to that library.  Usage: ``python -m
+combine_ep_layout_06_gb300.build [--ptxas-verbose]``.
 """
 from __future__ import annotations
 
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libep_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "moe_binding.cpp")
+BINDING = os.path.join(BUILD, "_moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-O2", f"-I{os.path.join(ROOT, 'include')}",
@@ -43,10 +48,46 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return all(os.path.getmtime(d) <= t for d in _deps()) and \
+        os.path.getmtime(BINDING_SRC) <= os.path.getmtime(BINDING)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _compile_binding() -> str:
+    import torch
+    cxx = shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: it is required to build the Python binding")
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(BUILD, "moe_binding.o")
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", BINDING_SRC, "-o", obj],
+         f"g++ failed on {BINDING_SRC}")
+    return obj
+
+
+def _link_binding(obj: str):
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    _run([shutil.which("g++"), "-shared", "-o", tmp, obj, f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python",
+          "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"],
+         "link of the Python binding failed")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
@@ -68,8 +109,10 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, sources()))
+        binding = binding.result()
     if ptxas_verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -80,6 +123,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
