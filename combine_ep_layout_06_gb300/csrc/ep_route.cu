@@ -95,14 +95,22 @@ template <int LANES> __device__ __forceinline__ uint32_t row_max_key(uint32_t v)
     for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-// exp of a difference of logits (<= 0) as a power of two: relative error below
-// 2^-22 + |d| 2^-23, results below 2^-126 are 0.  Terms with a large |d| weigh
-// exp(d) of the largest one.
-__device__ __forceinline__ float exp_diff(float d) {
+template <int LANES> __device__ __forceinline__ uint32_t row_min(uint32_t v) {
+    if constexpr (LANES == 32) return __reduce_min_sync(0xffffffffu, v);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+// 2^v within 2^-22, results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float v) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.44269504088896341f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// exp of a difference of logits (<= 0): relative error below 2^-22 + |d| 2^-23.
+// Terms with a large |d| weigh exp(d) of the largest one.
+__device__ __forceinline__ float exp_diff(float d) { return exp2_approx(d * kLog2e); }
 
 template <typename T>
 __device__ __forceinline__ const T *logit_row(const RouteParams &p, int s, int t) {
@@ -152,17 +160,30 @@ template <typename T, int VPL> struct RawRow {
         }
     }
 };
+// Two values as they lie in memory, in 32 bits (16-bit types).
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(__half, float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 template <typename T, int VPL>
 __device__ __forceinline__ void store_row(const RouteParams &p, T *row, int l, const float *d) {
-    constexpr int kPer = 16 / sizeof(T);
     if (p.vec) {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int c = 0; c < VPL; c += kPer) {
-            const int e = l * VPL + c;
-            __align__(16) T s[kPer];
+            for (int c = 0; c < VPL; c += 4)
+                if (l * VPL + c < p.E)
+                    *reinterpret_cast<float4 *>(row + l * VPL + c) = make_float4(d[c], d[c + 1], d[c + 2], d[c + 3]);
+        } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s[i] = from_f32<T>(d[c + i]);
-            if (e < p.E) *reinterpret_cast<uint4 *>(row + e) = *reinterpret_cast<const uint4 *>(s);
+            for (int c = 0; c < VPL; c += 8)
+                if (l * VPL + c < p.E)
+                    *reinterpret_cast<uint4 *>(row + l * VPL + c) =
+                        make_uint4(pack2(T(), d[c], d[c + 1]), pack2(T(), d[c + 2], d[c + 3]),
+                                   pack2(T(), d[c + 4], d[c + 5]), pack2(T(), d[c + 6], d[c + 7]));
         }
     } else {
 #pragma unroll
@@ -175,50 +196,72 @@ __device__ __forceinline__ void store_row(const RouteParams &p, T *row, int l, c
 // Probabilities are taken from the pair: m + log(sum) in one number would
 // lose the sum's digits where |m| is large.
 struct RowStats {
-    float m, inv_sum;
+    float m, scaled, inv_sum;    // scaled: m log2(e)
     bool open;                   // some expert is open
-    __device__ float prob(float x) const { return open ? expf(x - m) * inv_sum : 0.f; }
+
+    // Rows of ordinary size take exp(x - m) as 2^(x log2(e) - scaled), one
+    // multiply-add; scaled's rounding is a factor that all terms share.
+    __device__ bool near() const { return fabsf(m) <= 1e30f; }
+    __device__ float prob(float x) const {
+        if (!open) return 0.f;
+        return (near() ? exp2_approx(fmaf(x, kLog2e, -scaled)) : exp_diff(x - m)) * inv_sum;
+    }
     // |error| of the logarithm: 2^-22, next to an lse of order 1 or more
     __device__ float lse() const { return open ? m - __logf(inv_sum) : 0.f; }
 };
 
-// Softmax over a token's row: probabilities in place of x (all 0 when no
-// expert is open).
+// Statistics of a token's row but for the sum; exp(x - max) in place of x (all
+// 0 when no expert is open).
 template <int LANES, int VPL>
-__device__ __forceinline__ RowStats softmax_row(float *x) {
+__device__ __forceinline__ RowStats row_exps(float *x) {
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) m = fmaxf(m, x[i]);
     m = row_max<LANES>(m);
-    const bool open = m > -INFINITY;
-    if (!open) m = 0.f;                      // every exponential is then 0
-    float sum = 0.f;
+    RowStats st = {m, 0.f, 1.f, m > -INFINITY};
+    if (!st.open) st.m = 0.f;                // every exponential is then 0
+    st.scaled = st.m * kLog2e;
+    if (st.near()) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        x[i] = exp_diff(x[i] - m);
-        sum += x[i];
+        for (int i = 0; i < VPL; ++i) x[i] = exp2_approx(fmaf(x[i], kLog2e, -st.scaled));
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) x[i] = exp_diff(x[i] - st.m);
     }
-    sum = row_sum<LANES>(sum);
-    const float inv = open ? __fdividef(1.0f, sum) : 1.f;      // 1 <= sum <= E
+    return st;
+}
+// 1 <= sum <= E for an open row.
+__device__ __forceinline__ float inverse(const RowStats &st, float sum) {
+    return st.open ? __fdividef(1.0f, sum) : 1.f;
+}
+template <int VPL> __device__ __forceinline__ float lane_sum(const float *x) {
+    float sum = x[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) x[i] *= inv;
-    return RowStats{m, inv, open};
+    for (int i = 1; i < VPL; ++i) sum += x[i];
+    return sum;
+}
+// The whole: exponentials in place of x, their inverse sum in the statistics.
+template <int LANES, int VPL>
+__device__ __forceinline__ RowStats softmax_row(float *x) {
+    RowStats st = row_exps<LANES, VPL>(x);
+    st.inv_sum = inverse(st, row_sum<LANES>(lane_sum<VPL>(x)));
+    return st;
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // A token's place: lane l of its LANES, token t of rank blockIdx.y.  A warp
-// takes `rounds` runs of 32 / LANES tokens.
+// takes `rounds` runs of 32 / LANES tokens; this is the first.
 template <int LANES> struct Place {
     static constexpr int kTokens = 32 / LANES;           // of a warp and round
     int l, s, t;
     int64_t tok;
     bool in, present;
-    __device__ Place(const RouteParams &p, int warps, int rounds, int round) {
+    __device__ Place(const RouteParams &p, int warps, int rounds) {
         const int lane = threadIdx.x & 31;
         l = lane % LANES;
         s = blockIdx.y;
-        t = ((blockIdx.x * warps + (threadIdx.x >> 5)) * rounds + round) * kTokens + lane / LANES;
+        t = (blockIdx.x * warps + (threadIdx.x >> 5)) * rounds * kTokens + lane / LANES;
         tok = (int64_t)s * p.T + t;
         in = t < p.T;
         present = t < p.nt.n[s];
@@ -267,7 +310,7 @@ template <typename T, int LANES, int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool softmax,
                                                                  bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
-    const Place<LANES> at(p, kRouteWarps, 1, 0);
+    const Place<LANES> at(p, kRouteWarps, 1);
     grid_dependency_wait();
     grid_dependents_may_launch();     // the next kernel may count on all before this one
     if (!__any_sync(0xffffffffu, at.present)) {          // nobody here
@@ -311,20 +354,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         best = max(best, key[i]);
         be = first ? i : be;
     }
-    const uint32_t lanes = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
     int id[SLOTS];
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) id[q] = 0;
     for (int j = 0; j < p.k; ++j) {
         const uint32_t top = row_max_key<LANES>(best);
-        const uint32_t who = __ballot_sync(0xffffffffu, best == top) & lanes;
-        const int winner = __ffs(who) - 1;               // the first lane has the first expert
-        const int e = __shfl_sync(0xffffffffu, e0 + be, winner);
+        const int mine = e0 + be;                        // of equal keys the first expert's
+        const int e = (int)row_min<LANES>(best == top ? (uint32_t)mine : 0xffffffffu);
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q)
             if (j == q * LANES + at.l) id[q] = e;
         bool again = false;
-        if ((threadIdx.x & 31) == winner) {
+        if (e == mine && best == top) {
             again = second == 0;
             if (!again) {
                 best = second;
@@ -359,7 +400,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         mine[q] = at.present && q * LANES + at.l < p.k;
         c[q] = mine[q] ? sane_logit(to_f32(row[id[q]])) : -INFINITY;
     }
-    RowStats st = {0.f, 1.f, false};
+    RowStats st = {0.f, 0.f, 1.f, false};
     if (softmax && !renorm) st = softmax_row<LANES, VPL>(x);
     chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
 #pragma unroll
@@ -396,25 +437,31 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         for (int i = 0; i < VPL; ++i) f[i] = e0 + i < p.E ? (float)p.counts[e0 + i] * share : 0.f;
     }
     // one round ahead: the rows, the choices and their weights' gradients
+    const Place<LANES> at(p, kRouteWarps, p.rounds);
+    const int present = p.nt.n[at.s];
+    const T *row = logit_row<T>(p, at.s, 0) + at.t * p.row_stride;
+    T *out = static_cast<T *>(p.grad_logits) + at.tok * p.E;
+    const int32_t *idx = p.idx + at.tok * p.k;
+    const float *gw = p.grad_w + at.tok * p.k;
     RawRow<T, VPL> raw;
     int id_next[SLOTS];
     float g_next[SLOTS];
-    auto fetch = [&](int round) {
-        const Place<LANES> at(p, kRouteWarps, p.rounds, round);
-        if (dense) raw.load(p, at.present ? logit_row<T>(p, at.s, at.t) : nullptr, at.l, at.present);
+    auto fetch = [&](int t) {                 // token t of the rank, at row, idx and gw
+        if (dense) raw.load(p, row, at.l, t < present);
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
             const int j = q * LANES + at.l;
-            const bool mine = p.grad_w && at.present && j < p.k;
-            id_next[q] = mine ? p.idx[at.tok * p.k + j] : 0;
-            g_next[q] = mine ? p.grad_w[at.tok * p.k + j] : 0.f;
+            const bool mine = p.grad_w && t < present && j < p.k;
+            id_next[q] = mine ? idx[j] : 0;
+            g_next[q] = mine ? gw[j] : 0.f;
         }
     };
-    fetch(0);
-    for (int round = 0; round < p.rounds; ++round) {
-        const Place<LANES> at(p, kRouteWarps, p.rounds, round);
+    int t = at.t;
+    fetch(t);
+    for (int round = 0; round < p.rounds; ++round, t += kTokens, out += (int64_t)kTokens * p.E) {
         float d[VPL], pr[VPL], g[SLOTS];
         int id[SLOTS];
+        const T *here = row;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) d[i] = 0.f;
 #pragma unroll
@@ -423,15 +470,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             g[q] = g_next[q] * p.scale;
         }
         if (dense) raw.values(p, at.l, pr);
-        if (round + 1 < p.rounds) fetch(round + 1);
-        if (__any_sync(0xffffffffu, at.present)) {
-            RowStats st = {0.f, 1.f, false};
+        if (round + 1 < p.rounds) {
+            row += kTokens * p.row_stride;
+            idx += kTokens * p.k;
+            gw += kTokens * p.k;
+            fetch(t + kTokens);
+        }
+        if (__any_sync(0xffffffffu, t < present)) {
+            const bool is = t < present;
+            RowStats st = {0.f, 0.f, 1.f, false};
             float *r = rows[threadIdx.x / LANES];
             float c[SLOTS];
             bool mine[SLOTS];
 #pragma unroll
             for (int q = 0; q < SLOTS; ++q) {
-                mine[q] = p.grad_w && at.present && q * LANES + at.l < p.k;
+                mine[q] = p.grad_w && is && q * LANES + at.l < p.k;
                 if (mine[q] && (uint32_t)id[q] >= (uint32_t)p.E) {
                     mine[q] = false;
                     g[q] = 0.f;
@@ -450,20 +503,27 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                     if (mine[q]) c[q] = r[id[q]];
                 __syncwarp();
             } else if (p.grad_w) {
-                const T *row = logit_row<T>(p, at.s, at.present ? at.t : 0);
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q)
-                    if (mine[q]) c[q] = sane_logit(to_f32(row[id[q]]));
+                    if (mine[q]) c[q] = sane_logit(to_f32(here[id[q]]));
             }
-            if (dense) st = softmax_row<LANES, VPL>(pr);
             if (p.grad_loss) {
-                const float lse = 2.0f * p.z_coef * st.lse();
-                float dot = 0.f;
+                // p (f - <p, f> + 2 z lse), with p = exp / sum: both sums at once
+                st = row_exps<LANES, VPL>(pr);
+                float sum = lane_sum<VPL>(pr), dot = 0.f;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) dot += pr[i] * f[i];
-                dot = row_sum<LANES>(dot);
+                for (int i = 0; i < VPL; ++i) dot = fmaf(pr[i], f[i], dot);
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) d[i] = pr[i] * ((f[i] - dot) + lse) * gl;
+                for (int o = LANES / 2; o > 0; o >>= 1) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                }
+                st.inv_sum = inverse(st, sum);
+                const float shift = 2.0f * p.z_coef * st.lse() - dot * st.inv_sum, factor = st.inv_sum * gl;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) d[i] = pr[i] * factor * (f[i] + shift);
+            } else if (dense) {
+                st = softmax_row<LANES, VPL>(pr);
             }
             if (p.grad_w) {
                 float v[SLOTS], dv[SLOTS], sum, dot = 0.f;
@@ -482,8 +542,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                     }
                 }
                 if (softmax && !renorm) {
+                    const float slope = dot * st.inv_sum;
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * dot;
+                    for (int i = 0; i < VPL; ++i) d[i] = fmaf(-pr[i], slope, d[i]);
                 }
                 // several choices a lane: in order.  One choice a lane: at once,
                 // unless two lanes find each other at an expert's place.
@@ -517,12 +578,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 }
                 __syncwarp();
             }
-            if (!at.present) {
+            if (!is) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) d[i] = 0.f;
             }
         }
-        if (at.in) store_row<T, VPL>(p, static_cast<T *>(p.grad_logits) + at.tok * p.E, at.l, d);
+        if (t < p.T) store_row<T, VPL>(p, out, at.l, d);
     }
 }
 
@@ -578,10 +639,11 @@ __global__ void __launch_bounds__(loss_warps(VPL) * 32)
         if (i0 + kTokens < tokens_per_warp) fetch();
         float x[VPL];
         raw.values(p, l, x);
-        const float lse = softmax_row<LANES, VPL>(x).lse();
+        const RowStats st = softmax_row<LANES, VPL>(x);
+        const float lse = st.lse();
         z += l == 0 ? lse * lse : 0.f;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) acc[j] += x[j];
+        for (int j = 0; j < VPL; ++j) acc[j] = fmaf(x[j], st.inv_sum, acc[j]);
     }
     // the warp's tokens of other lanes with the same experts
 #pragma unroll
