@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             if (j == q * LANES + at.l) id[q] = e;
         bool again = false;
         if (e == mine && best == top) {
-            again = second == 0;
+            again = second == 0 && j + 1 < p.k;
             if (!again) {
                 best = second;
                 be = se;
@@ -374,21 +374,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             }
         }
         if (__any_sync(0xffffffffu, again)) {
-            // both keys are taken: the best two after the one taken last (equal
+            // both keys are taken: the best one after the one taken last (equal
             // keys in the order of the experts)
             if (again) {
                 const uint32_t last = best;
                 const int le = be;
-                best = second = 0;
+                best = 0;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
                     const bool open = key[i] < last || (key[i] == last && i > le);
-                    const uint32_t v = open ? key[i] : 0u;
-                    const bool first = v > best, next = v > second;
-                    second = max(second, min(best, v));
-                    se = first ? be : next ? i : se;
-                    best = max(best, v);
-                    be = first ? i : be;
+                    if (open && key[i] > best) {
+                        best = key[i];
+                        be = i;
+                    }
                 }
             }
         }
@@ -593,18 +591,39 @@ __device__ __forceinline__ void store_loss(const RouteParams &p, float balance, 
     p.loss[2] = z;
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+}
+
 // Losses, pass 1: every block sums softmax probabilities and lse^2 of its
 // tokens (a lane's tokens in registers, then lanes and warps in order) and
-// counts choices in shared memory.  Bound by instructions and the rows' latency:
-// 32 warps per SM, each with its next row on the way.
+// counts choices in shared memory; the 4 blocks of a cluster join their sums,
+// each a quarter of the experts, through distributed shared memory.  Few tokens
+// are one cluster's, which also finishes the losses.  Bound by instructions and
+// the rows' latency: one block per SM, each lane with its next row on the way.
+constexpr int kLossCluster = 4;
+
 template <typename T, int LANES, int VPL>
-__global__ void __launch_bounds__(loss_warps(VPL) * 32)
+__global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(loss_warps(VPL) * 32)
     balance_partial_kernel(const RouteParams p, int tokens_per_warp) {
     extern __shared__ float sh[];                 // [kLossWarps][E + 1], then [E] counts
-    constexpr int kTokens = 32 / LANES, kLossWarps = loss_warps(VPL);
+    constexpr int kTokens = 32 / LANES, kLossWarps = loss_warps(VPL), SLOTS = slots_of<LANES>();
+    __shared__ float shares[32], joined[kLossCluster + 1];   // of the loss by warp, by block; z
     int32_t *cnt = reinterpret_cast<int32_t *>(sh + kLossWarps * (p.E + 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
+    grid_dependency_wait();
+    grid_dependents_may_launch();     // the next kernel may count on all before this one
     __syncthreads();
     float acc[VPL], z = 0.f;
 #pragma unroll
@@ -614,28 +633,36 @@ __global__ void __launch_bounds__(loss_warps(VPL) * 32)
     const int64_t tok0 = ((int64_t)blockIdx.x * kLossWarps + warp) * tokens_per_warp;
     int r = (int)(tok0 / p.T), t = (int)(tok0 - (int64_t)r * p.T) + lane / LANES, i = lane / LANES;
     RawRow<T, VPL> raw, ahead;
-    bool present = false;
+    int ids[SLOTS];                              // -1: no choice of a present token here
     auto fetch = [&] {                           // the row of this lane's token i; then on to the next
         while (t >= p.T && r < p.W) {
             t -= p.T;
             ++r;
         }
-        present = i < tokens_per_warp && tok0 + i < total && t < p.nt.n[r];
-        if (present) {
-            const int64_t tok = (int64_t)r * p.T + t;
-            for (int j = l; j < p.k; j += LANES) {
-                const int id = p.idx[tok * p.k + j];
-                if ((uint32_t)id < (uint32_t)p.E) atomicAdd(&cnt[id], 1);
-                else if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+        const bool present = i < tokens_per_warp && tok0 + i < total && t < p.nt.n[r];
+        ahead.load(p, present ? logit_row<T>(p, r, t) : nullptr, l, present);
+        const int64_t first = ((int64_t)r * p.T + t) * p.k;
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            const int j = q * LANES + l;
+            ids[q] = -1;
+            if (present && j < p.k) {
+                ids[q] = p.idx[first + j];
+                if ((uint32_t)ids[q] >= (uint32_t)p.E) ids[q] = p.E;
             }
         }
-        ahead.load(p, present ? logit_row<T>(p, r, t) : nullptr, l, present);
         t += kTokens;
         i += kTokens;
     };
     fetch();
     for (int i0 = 0; i0 < tokens_per_warp; i0 += kTokens) {
         raw = ahead;
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+            if (ids[q] < 0) continue;
+            if (ids[q] < p.E) atomicAdd(&cnt[ids[q]], 1);
+            else if (p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
+        }
         if (i0 + kTokens < tokens_per_warp) fetch();
         float x[VPL];
         raw.values(p, l, x);
@@ -649,56 +676,77 @@ __global__ void __launch_bounds__(loss_warps(VPL) * 32)
 #pragma unroll
     for (int o = 16; o >= LANES; o >>= 1) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        for (int j = 0; j < VPL; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
     }
     z = row_sum<32>(z);
     float *mine = sh + warp * (p.E + 1);
     if (lane < LANES) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (l * VPL + i < p.E) mine[l * VPL + i] = acc[i];
+        for (int j = 0; j < VPL; ++j)
+            if (l * VPL + j < p.E) mine[l * VPL + j] = acc[j];
     }
     if (lane == 0) mine[p.E] = z;
     __syncthreads();
-    if (gridDim.x == 1) {                        // few tokens: no second pass
-        __shared__ float shares[33];             // of the loss, by warp; z
-        float balance = 0.f;
-        for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
-            float sum = 0.f;
-#pragma unroll 8
-            for (int w = 0; w < kLossWarps; ++w) sum += sh[w * (p.E + 1) + e];
-            sum *= p.inv_n;
-            if (e < p.E) {
-                p.probs[e] = sum;
-                p.counts_out[e] = cnt[e];
-                balance += (float)cnt[e] * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
-            } else {
-                shares[32] = sum;
-            }
-        }
-        balance = row_sum<32>(balance);
-        if (lane == 0) shares[warp] = balance;
-        __syncthreads();
-        if (warp == 0) {
-            const float total = row_sum<32>(lane < kLossWarps ? shares[lane] : 0.f);
-            if (lane == 0) store_loss(p, total, shares[32]);
-        }
-        return;
-    }
+    // the block's sums, in the first warp's place
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
         float sum = 0.f;
 #pragma unroll 8
         for (int w = 0; w < kLossWarps; ++w) sum += sh[w * (p.E + 1) + e];
-        p.part[(int64_t)blockIdx.x * (p.E + 1) + e] = sum;
-        if (e < p.E) p.part_count[(int64_t)blockIdx.x * p.E + e] = cnt[e];
+        sh[e] = sum;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+    __syncwarp();
+    cluster_sync();
+    const uint32_t rank = cluster_rank();
+    const int per = (p.E + kLossCluster) / kLossCluster;     // of E + 1 sums
+    const int e1 = min(p.E + 1, (int)(rank + 1) * per);
+    const bool whole = gridDim.x == kLossCluster;
+    const int64_t part = blockIdx.x / kLossCluster;
+    float balance = 0.f;
+    for (int e = rank * per + threadIdx.x; e < e1; e += blockDim.x) {
+        float sum = 0.f;
+        int32_t c = 0;
+#pragma unroll
+        for (uint32_t b = 0; b < kLossCluster; ++b) {
+            sum += ld_cluster_f32(in_cta(smem_u32(sh + e), b));
+            if (e < p.E) c += ld_cluster_s32(in_cta(smem_u32(cnt + e), b));
+        }
+        if (!whole) {
+            p.part[part * (p.E + 1) + e] = sum;
+            if (e < p.E) p.part_count[part * p.E + e] = c;
+        } else if (e < p.E) {
+            sum *= p.inv_n;
+            p.probs[e] = sum;
+            p.counts_out[e] = c;
+            balance += (float)c * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
+        } else {
+            st_cluster_f32(in_cta(smem_u32(joined + kLossCluster), 0), sum * p.inv_n);
+        }
+    }
+    if (whole) {
+        __syncwarp();
+        balance = row_sum<32>(balance);
+        if (lane == 0) shares[warp] = balance;
+        __syncthreads();
+        if (warp == 0) {
+            balance = row_sum<32>(lane < kLossWarps ? shares[lane] : 0.f);
+            if (lane == 0) st_cluster_f32(in_cta(smem_u32(joined + rank), 0), balance);
+        }
+    } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *p.ticket = 0;
+    }
+    __syncwarp();
+    cluster_sync();                              // no block's shared memory is read any more
+    if (whole && rank == 0 && threadIdx.x == 0) {
+        balance = 0.f;
+        for (int b = 0; b < kLossCluster; ++b) balance += joined[b];
+        store_loss(p, balance, joined[kLossCluster]);
+    }
 }
 
 // Losses, pass 2: a block joins the parts of 32 experts; lanes are experts,
 // warp w takes parts w, w + 32, ..., and the warps' sums are added in order.  The
 // last block to finish adds up the loss.
-__global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p, int blocks) {
+__global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p, int parts) {
     __shared__ float sh[32][33];
     __shared__ int32_t sc[32][33];
     __shared__ bool last;
@@ -706,8 +754,9 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
     const int e = blockIdx.x * 32 + lane;
     float sum = 0.f;
     int32_t c = 0;
-#pragma unroll 5
-    for (int b = warp; b < blocks; b += 32) {
+    grid_dependency_wait();
+#pragma unroll 2
+    for (int b = warp; b < parts; b += 32) {
         if (e <= p.E) sum += p.part[(int64_t)b * (p.E + 1) + e];
         if (e < p.E) c += p.part_count[(int64_t)b * p.E + e];
     }
@@ -750,12 +799,12 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p
     }
 }
 
-int loss_blocks(const ep_route_desc_t &d) {
+// Clusters of the losses' first pass.  One, without a second pass, up to 2^17
+// logits; else one per 128 tokens, up to the 36 that fit the SMs.
+int loss_clusters(const ep_route_desc_t &d) {
     const int64_t tokens = (int64_t)d.world_size * d.tokens;
-    // one block, without a second pass: 19 712 logits 8.6 us in one launch
-    // against 4.9 + 4.1 us in two
-    const int64_t want = tokens * d.num_experts <= 1 << 15 ? 1 : (tokens + 31) / 32;
-    return (int)(want < 152 ? want : 152);
+    const int64_t want = tokens * d.num_experts <= 1 << 17 ? 1 : (tokens + 127) / 128;
+    return (int)(want < 36 ? want : 36);
 }
 
 int final_blocks(const ep_route_desc_t &d) { return d.num_experts / 32 + 1; }
@@ -823,14 +872,13 @@ bool make_params(const ep_route_desc_t *d, const void *logits, const int32_t *h_
 }
 
 // Launches as a programmatic dependent of the kernel before where the kernel
-// is long enough to gain by it: the gradient of 32768 x 256 logits takes 18.2
-// instead of 20.5 us a call, but the launch itself costs the host about a
-// microsecond more, which is what a short call's time goes by (131072 x 8:
-// 11.1 instead of 9.8 us).
+// is long enough to gain by it (131072 x 8 logits: 5.8 instead of 6.2 us a
+// call, the gradient of 32768 x 256 18.1 instead of 20.5); a one-token call's
+// time goes by the host, whose launch it makes a microsecond longer.
 template <typename... Params, typename... Args>
 cudaError_t launch(const RouteParams &p, void (*kernel)(Params...), dim3 blocks, unsigned threads, size_t dyn,
                    cudaStream_t st, Args &&...args) {
-    if ((int64_t)p.W * p.T * p.E >= 1 << 22)
+    if ((int64_t)p.W * p.T * p.E >= 1 << 18)
         return launch_after_previous(kernel, blocks, threads, dyn, st, static_cast<Args &&>(args)...);
     kernel<<<blocks, threads, dyn, st>>>(static_cast<Args &&>(args)...);
     return cudaGetLastError();
@@ -910,7 +958,7 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
 ep_status_t ep_balance_loss_workspace(const ep_route_desc_t *d, size_t *bytes) {
     if (!valid(d) || !bytes) return EP_ERR_INVALID_ARGS;
     // parts of the sums and counts, shares of the loss, z, the ticket
-    *bytes = ((size_t)loss_blocks(*d) * (2 * (size_t)d->num_experts + 1) + final_blocks(*d) + 2) * 4;
+    *bytes = ((size_t)loss_clusters(*d) * (2 * (size_t)d->num_experts + 1) + final_blocks(*d) + 2) * 4;
     return EP_SUCCESS;
 }
 
@@ -928,32 +976,31 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
         return EP_ERR_INVALID_ARGS;
     ep_balance_loss_workspace(d, &need);
     if (workspace_bytes < need) return EP_ERR_INVALID_ARGS;
-    const int blocks = loss_blocks(*d);
+    const int clusters = loss_clusters(*d);
     p.idx = d_idx;
     p.loss = d_loss;
     p.counts_out = d_counts;
     p.probs = d_probs;
     p.error = d_error;
     p.part = static_cast<float *>(d_workspace);
-    p.part_count = reinterpret_cast<int32_t *>(p.part + (size_t)blocks * (p.E + 1));
+    p.part_count = reinterpret_cast<int32_t *>(p.part + (size_t)clusters * (p.E + 1));
     const int last = final_blocks(*d);
-    p.tail = reinterpret_cast<float *>(p.part_count + (size_t)blocks * p.E);
+    p.tail = reinterpret_cast<float *>(p.part_count + (size_t)clusters * p.E);
     p.ticket = reinterpret_cast<uint32_t *>(p.tail + last + 1);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     with_types<true>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kWarps = loss_warps(decltype(vpl)::value);
         const size_t sh = ((size_t)kWarps * (p.E + 1) + p.E) * 4;    // 37 KB at most
-        const int64_t warps = (int64_t)blocks * kWarps;
+        const int64_t warps = (int64_t)clusters * kLossCluster * kWarps;
         const int per_warp = (int)(((int64_t)p.W * p.T + warps - 1) / warps);
-        balance_partial_kernel<decltype(type), decltype(lanes)::value, decltype(vpl)::value>
-            <<<blocks, kWarps * 32, sh, st>>>(p, per_warp);
-        e = cudaGetLastError();
+        e = launch_after_previous(
+            balance_partial_kernel<decltype(type), decltype(lanes)::value, decltype(vpl)::value>,
+            clusters * kLossCluster, kWarps * 32, sh, st, p, per_warp);
     });
     if (e != cudaSuccess) return EP_ERR_GPU_OP;
-    if (blocks == 1) return EP_SUCCESS;
-    balance_final_kernel<<<last, 1024, 0, st>>>(p, blocks);
-    e = cudaGetLastError();
+    if (clusters == 1) return EP_SUCCESS;
+    e = launch_after_previous(balance_final_kernel, last, 1024, 0, st, p, clusters);
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 

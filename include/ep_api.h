@@ -523,8 +523,8 @@ typedef struct {
  * every group are not written.  y may be the residual itself; otherwise y and
  * pre overlap nothing that the call reads.  The kernel is launched as a
  * programmatic dependent of the kernel before it on the stream and waits for
- * it before its first read or write; so are the gradient's, and ep_route's and
- * ep_route_backward's from 2^22 logits on. */
+ * it before its first read or write; so are the gradient's, the balance
+ * loss's, and ep_route's and ep_route_backward's from 2^18 logits on. */
 ep_status_t ep_expert_product(const ep_product_desc_t *d, const void *d_bias,
                               const ep_rows_t *residual, const ep_rows_t *y,
                               const ep_rows_t *pre, uint32_t *d_error,
