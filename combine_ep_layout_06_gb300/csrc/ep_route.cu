@@ -41,10 +41,8 @@ struct RouteParams {
     const int32_t *counts;   // backward
     void *grad_logits;       // backward
     float balance_coef, z_coef, inv_n;
-    float *part;             // loss: [blocks][E + 1] partial sums
-    int32_t *part_count;     // loss: [blocks][E]
-    float *tail;             // loss: [final blocks + 1] shares of the loss, z
-    uint32_t *ticket;        // loss: final blocks that are done
+    float *part;             // loss: [clusters][E + 1] partial sums
+    int32_t *part_count;     // loss: [clusters][E]
     float *loss, *probs;
     int32_t *counts_out;
     uint32_t *error;
@@ -731,8 +729,6 @@ __global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(loss_warp
             balance = row_sum<32>(lane < kLossWarps ? shares[lane] : 0.f);
             if (lane == 0) st_cluster_f32(in_cta(smem_u32(joined + rank), 0), balance);
         }
-    } else if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *p.ticket = 0;
     }
     __syncwarp();
     cluster_sync();                              // no block's shared memory is read any more
@@ -743,59 +739,65 @@ __global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(loss_warp
     }
 }
 
-// Losses, pass 2: a block joins the parts of 32 experts; lanes are experts,
-// warp w takes parts w, w + 32, ..., and the warps' sums are added in order.  The
-// last block to finish adds up the loss.
-__global__ void __launch_bounds__(1024) balance_final_kernel(const RouteParams p, int parts) {
-    __shared__ float sh[32][33];
-    __shared__ int32_t sc[32][33];
-    __shared__ bool last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
-    float sum = 0.f;
-    int32_t c = 0;
+// Losses, pass 2: one cluster of 8 blocks joins the parts, each block an
+// eighth of the experts (128 at most) by 8 slices of the parts, sums in order;
+// the loss's shares meet in the first block.
+constexpr int kFinalCluster = 8, kFinalColumns = EP_MAX_ROUTE_EXPERTS / kFinalCluster;
+
+__global__ void __cluster_dims__(kFinalCluster, 1, 1) __launch_bounds__(1024)
+    balance_final_kernel(const RouteParams p, int parts) {
+    constexpr int kSlices = 1024 / kFinalColumns;
+    __shared__ float sh[kSlices][kFinalColumns], shares[kFinalColumns / 32], joined[kFinalCluster + 1];
+    __shared__ int32_t sc[kSlices][kFinalColumns];
+    const uint32_t rank = cluster_rank();
+    const int column = threadIdx.x % kFinalColumns, slice = threadIdx.x / kFinalColumns;
+    const int per = (p.E + kFinalCluster - 1) / kFinalCluster;
+    const int e = column < per && (int)rank * per + column < p.E ? (int)rank * per + column : -1;
     grid_dependency_wait();
-#pragma unroll 2
-    for (int b = warp; b < parts; b += 32) {
-        if (e <= p.E) sum += p.part[(int64_t)b * (p.E + 1) + e];
-        if (e < p.E) c += p.part_count[(int64_t)b * p.E + e];
-    }
-    sh[warp][lane] = sum;
-    sc[warp][lane] = c;
-    __syncthreads();
-    if (warp == 0) {
-        sum = 0.f;
-        c = 0;
-#pragma unroll
-        for (int w = 0; w < 32; ++w) {
-            sum += sh[w][lane];
-            c += sc[w][lane];
+    float sum = 0.f, z = 0.f;
+    int32_t c = 0;
+    if (e >= 0) {
+#pragma unroll 5
+        for (int b = slice; b < parts; b += kSlices) {
+            sum += p.part[(int64_t)b * (p.E + 1) + e];
+            c += p.part_count[(int64_t)b * p.E + e];
         }
-        sum *= p.inv_n;
+    }
+    if (rank == 0 && threadIdx.x < 32) {
+        for (int b = threadIdx.x; b < parts; b += 32) z += p.part[(int64_t)b * (p.E + 1) + p.E];
+        z = row_sum<32>(z) * p.inv_n;
+    }
+    sh[slice][column] = sum;
+    sc[slice][column] = c;
+    __syncthreads();
+    if (slice == 0) {
+#pragma unroll
+        for (int s = 1; s < kSlices; ++s) {
+            sum += sh[s][column];
+            c += sc[s][column];
+        }
         float balance = 0.f;
-        if (e < p.E) {
+        if (e >= 0) {
+            sum *= p.inv_n;
             p.probs[e] = sum;
             p.counts_out[e] = c;
             balance = (float)c * (p.inv_n * ((float)p.E / (float)p.k)) * sum;
-        } else if (e == p.E) {
-            p.tail[gridDim.x] = sum;                     // z
         }
         balance = row_sum<32>(balance);
-        if (lane == 0) p.tail[blockIdx.x] = balance;
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) last = atom_add_acq_rel_gpu(p.ticket, 1u) == gridDim.x - 1;
-        __syncwarp();
-        if (last) {
-            __threadfence();
-            float total = 0.f;
-            for (int i = lane; i < (int)gridDim.x; i += 32) total += __ldcg(p.tail + i);
-            total = row_sum<32>(total);
-            if (lane == 0) {
-                const float z = __ldcg(p.tail + gridDim.x);
-                store_loss(p, total, z);
-            }
-        }
+        if (threadIdx.x % 32 == 0) shares[threadIdx.x / 32] = balance;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float balance = 0.f;
+        for (int w = 0; w < kFinalColumns / 32; ++w) balance += shares[w];
+        st_cluster_f32(in_cta(smem_u32(joined + rank), 0), balance);
+    }
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        float balance = 0.f;
+        for (int b = 0; b < kFinalCluster; ++b) balance += joined[b];
+        store_loss(p, balance, z);
     }
 }
 
@@ -806,8 +808,6 @@ int loss_clusters(const ep_route_desc_t &d) {
     const int64_t want = tokens * d.num_experts <= 1 << 17 ? 1 : (tokens + 127) / 128;
     return (int)(want < 36 ? want : 36);
 }
-
-int final_blocks(const ep_route_desc_t &d) { return d.num_experts / 32 + 1; }
 
 // Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
 // Reductions cost a warp the same for one token or several, so for the losses
@@ -957,8 +957,8 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
 
 ep_status_t ep_balance_loss_workspace(const ep_route_desc_t *d, size_t *bytes) {
     if (!valid(d) || !bytes) return EP_ERR_INVALID_ARGS;
-    // parts of the sums and counts, shares of the loss, z, the ticket
-    *bytes = ((size_t)loss_clusters(*d) * (2 * (size_t)d->num_experts + 1) + final_blocks(*d) + 2) * 4;
+    // parts of the sums and counts
+    *bytes = (size_t)loss_clusters(*d) * (2 * (size_t)d->num_experts + 1) * 4;
     return EP_SUCCESS;
 }
 
@@ -984,9 +984,6 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     p.error = d_error;
     p.part = static_cast<float *>(d_workspace);
     p.part_count = reinterpret_cast<int32_t *>(p.part + (size_t)clusters * (p.E + 1));
-    const int last = final_blocks(*d);
-    p.tail = reinterpret_cast<float *>(p.part_count + (size_t)clusters * p.E);
-    p.ticket = reinterpret_cast<uint32_t *>(p.tail + last + 1);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     with_types<true>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
@@ -1000,7 +997,7 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     });
     if (e != cudaSuccess) return EP_ERR_GPU_OP;
     if (clusters == 1) return EP_SUCCESS;
-    e = launch_after_previous(balance_final_kernel, last, 1024, 0, st, p, clusters);
+    e = launch_after_previous(balance_final_kernel, kFinalCluster, 1024, 0, st, p, clusters);
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
