@@ -415,18 +415,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 // chosen experts' terms are added to the dense part, one choice after the
 // other where an expert was chosen twice.  The experts' loads, the same for
 // all tokens, stay in registers over a warp's tokens.
-template <typename T, int LANES, int VPL>
+template <typename T, int LANES, int VPL, bool WEIGHTS>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const RouteParams p, bool softmax, bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
     constexpr int kTokens = 32 / LANES, kRow = LANES * VPL;
-    __shared__ __align__(16) float rows[kRouteWarps * kTokens][kRow + 4];
-    const bool dense = p.grad_loss || (softmax && !renorm);
+    __shared__ __align__(16) float rows[WEIGHTS ? kRouteWarps * kTokens : 1][kRow + 4];
+    const bool dense = !WEIGHTS || p.grad_loss || (softmax && !renorm);
     const int e0 = (int)(threadIdx.x & 31) % LANES * VPL;
     float f[VPL], gl = 0.f;
     grid_dependency_wait();
     grid_dependents_may_launch();     // the next kernel may count on all before this one
-    if (p.grad_loss) {
+    if (!WEIGHTS || p.grad_loss) {
         gl = *p.grad_loss * p.inv_n;
         const float share = p.inv_n * ((float)p.E / (float)p.k) * p.balance_coef;
 #pragma unroll
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
         for (int q = 0; q < SLOTS; ++q) {
             const int j = q * LANES + at.l;
-            const bool mine = p.grad_w && t < present && j < p.k;
+            const bool mine = WEIGHTS && t < present && j < p.k;
             id_next[q] = mine ? idx[j] : 0;
             g_next[q] = mine ? gw[j] : 0.f;
         }
@@ -475,12 +475,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         if (__any_sync(0xffffffffu, t < present)) {
             const bool is = t < present;
             RowStats st = {0.f, 0.f, 1.f, false};
-            float *r = rows[threadIdx.x / LANES];
+            float *r = rows[WEIGHTS ? threadIdx.x / LANES : 0];
             float c[SLOTS];
             bool mine[SLOTS];
 #pragma unroll
             for (int q = 0; q < SLOTS; ++q) {
-                mine[q] = p.grad_w && is && q * LANES + at.l < p.k;
+                mine[q] = WEIGHTS && is && q * LANES + at.l < p.k;
                 if (mine[q] && (uint32_t)id[q] >= (uint32_t)p.E) {
                     mine[q] = false;
                     g[q] = 0.f;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 c[q] = -INFINITY;
             }
             // the chosen logits: from the row where it is at hand
-            if (p.grad_w && dense) {
+            if (WEIGHTS && dense) {
 #pragma unroll
                 for (int i = 0; i < VPL; i += 4)
                     *reinterpret_cast<float4 *>(r + e0 + i) = make_float4(pr[i], pr[i + 1], pr[i + 2], pr[i + 3]);
@@ -498,12 +498,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 for (int q = 0; q < SLOTS; ++q)
                     if (mine[q]) c[q] = r[id[q]];
                 __syncwarp();
-            } else if (p.grad_w) {
+            } else if (WEIGHTS) {
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q)
                     if (mine[q]) c[q] = sane_logit(to_f32(here[id[q]]));
             }
-            if (p.grad_loss) {
+            if (!WEIGHTS || p.grad_loss) {
                 // p (f - <p, f> + 2 z lse), with p = exp / sum: both sums at once
                 st = row_exps<LANES, VPL>(pr);
                 float sum = lane_sum<VPL>(pr), dot = 0.f;
@@ -517,11 +517,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                 st.inv_sum = inverse(st, sum);
                 const float shift = 2.0f * p.z_coef * st.lse() - dot * st.inv_sum, factor = st.inv_sum * gl;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) d[i] = pr[i] * factor * (f[i] + shift);
+                for (int i = 0; i < VPL; ++i) d[i] = pr[i] * fmaf(f[i], factor, shift * factor);
             } else if (dense) {
                 st = softmax_row<LANES, VPL>(pr);
             }
-            if (p.grad_w) {
+            if constexpr (WEIGHTS) {
                 float v[SLOTS], dv[SLOTS], sum, dot = 0.f;
                 chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
 #pragma unroll
@@ -949,7 +949,9 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
         // enough warps for all SMs (32 each) before a warp takes a second run
         const int64_t runs = (int64_t)p.W * p.T * kLanes / 32;
         p.rounds = (int)(runs < 152 * 32 ? 1 : runs < 4 * 152 * 32 ? runs / (152 * 32) : 4);
-        e = launch(p, route_backward_kernel<decltype(type), kLanes, decltype(vpl)::value>,
+        constexpr int kVpl = decltype(vpl)::value;
+        e = launch(p, d_grad_w ? route_backward_kernel<decltype(type), kLanes, kVpl, true>
+                               : route_backward_kernel<decltype(type), kLanes, kVpl, false>,
                    token_grid<kLanes>(p, p.rounds), kRouteWarps * 32, 0, st, p, softmax, renorm);
     });
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
