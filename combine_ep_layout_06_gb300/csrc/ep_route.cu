@@ -415,13 +415,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 // chosen experts' terms are added to the dense part, one choice after the
 // other where an expert was chosen twice.  The experts' loads, the same for
 // all tokens, stay in registers over a warp's tokens.
-template <typename T, int LANES, int VPL, bool WEIGHTS>
+// What a call differentiates: the loss alone, or weights (and the loss, or
+// not) of one of the scores.
+enum Part { kLossOnly, kSoftmaxChosen, kSoftmaxAll, kSigmoid };
+
+template <typename T, int LANES, int VPL, Part PART>
 __global__ void __launch_bounds__(kRouteWarps * 32)
-    route_backward_kernel(const RouteParams p, bool softmax, bool renorm) {
+    route_backward_kernel(const RouteParams p, bool renorm) {
+    constexpr bool WEIGHTS = PART != kLossOnly, softmax = PART != kSigmoid;
     constexpr int SLOTS = slots_of<LANES>();
     constexpr int kTokens = 32 / LANES, kRow = LANES * VPL;
     __shared__ __align__(16) float rows[WEIGHTS ? kRouteWarps * kTokens : 1][kRow + 4];
-    const bool dense = !WEIGHTS || p.grad_loss || (softmax && !renorm);
+    const bool dense = PART == kLossOnly || PART == kSoftmaxAll || p.grad_loss;
     const int e0 = (int)(threadIdx.x & 31) % LANES * VPL;
     float f[VPL], gl = 0.f;
     grid_dependency_wait();
@@ -523,21 +528,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             }
             if constexpr (WEIGHTS) {
                 float v[SLOTS], dv[SLOTS], sum, dot = 0.f;
-                chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
+                chosen_scores<LANES, SLOTS>(softmax, PART == kSoftmaxChosen || (PART == kSigmoid && renorm), st, c, mine, v, &sum);
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
-                if (softmax || renorm) dot = row_sum<LANES>(dot);
+                if (PART != kSigmoid || renorm) dot = row_sum<LANES>(dot);
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q) {
                     if (softmax) {
-                        dv[q] = renorm ? v[q] * (g[q] - dot) : v[q] * g[q];
+                        dv[q] = PART == kSoftmaxChosen ? v[q] * (g[q] - dot) : v[q] * g[q];
                     } else {
                         float s = g[q];
                         if (renorm) s = sum > 0.f ? (g[q] - dot / sum) / sum : 0.f;
                         dv[q] = s * v[q] * (1.0f - v[q]);
                     }
                 }
-                if (softmax && !renorm) {
+                if (PART == kSoftmaxAll) {
                     const float slope = dot * st.inv_sum;
 #pragma unroll
                     for (int i = 0; i < VPL; ++i) d[i] = fmaf(-pr[i], slope, d[i]);
@@ -950,9 +955,12 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
         const int64_t runs = (int64_t)p.W * p.T * kLanes / 32;
         p.rounds = (int)(runs < 152 * 32 ? 1 : runs < 4 * 152 * 32 ? runs / (152 * 32) : 4);
         constexpr int kVpl = decltype(vpl)::value;
-        e = launch(p, d_grad_w ? route_backward_kernel<decltype(type), kLanes, kVpl, true>
-                               : route_backward_kernel<decltype(type), kLanes, kVpl, false>,
-                   token_grid<kLanes>(p, p.rounds), kRouteWarps * 32, 0, st, p, softmax, renorm);
+        using T = decltype(type);
+        e = launch(p, !d_grad_w          ? route_backward_kernel<T, kLanes, kVpl, kLossOnly>
+                      : !softmax         ? route_backward_kernel<T, kLanes, kVpl, kSigmoid>
+                      : renorm           ? route_backward_kernel<T, kLanes, kVpl, kSoftmaxChosen>
+                                         : route_backward_kernel<T, kLanes, kVpl, kSoftmaxAll>,
+                   token_grid<kLanes>(p, p.rounds), kRouteWarps * 32, 0, st, p, renorm);
     });
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
