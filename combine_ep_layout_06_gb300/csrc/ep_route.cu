@@ -304,9 +304,11 @@ __device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const R
     }
 }
 
-template <typename T, int LANES, int VPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool softmax,
-                                                                 bool renorm) {
+// The scores, each in kernels of its own; and a gradient of the loss alone.
+enum Part { kLossOnly, kSoftmaxChosen, kSoftmaxAll, kSigmoid };
+
+template <typename T, int LANES, int VPL, Part PART>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p, bool renorm) {
     constexpr int SLOTS = slots_of<LANES>();
     const Place<LANES> at(p, kRouteWarps, 1);
     grid_dependency_wait();
@@ -397,12 +399,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
         c[q] = mine[q] ? sane_logit(to_f32(row[id[q]])) : -INFINITY;
     }
     RowStats st = {0.f, 0.f, 1.f, false};
-    if (softmax && !renorm) st = softmax_row<LANES, VPL>(x);
-    chosen_scores<LANES, SLOTS>(softmax, renorm, st, c, mine, v, &sum);
+    if (PART == kSoftmaxAll) st = softmax_row<LANES, VPL>(x);
+    chosen_scores<LANES, SLOTS>(PART != kSigmoid, PART == kSoftmaxChosen || (PART == kSigmoid && renorm), st, c, mine, v,
+                                &sum);
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) {
         const int j = q * LANES + at.l;
-        if (!softmax && renorm) v[q] = sum > 0.f ? v[q] / sum : 0.f;
+        if (PART == kSigmoid && renorm) v[q] = sum > 0.f ? v[q] / sum : 0.f;
         if (at.in && j < p.k) {
             p.w[at.tok * p.k + j] = mine[q] ? v[q] * p.scale : 0.f;
             p.idx_out[at.tok * p.k + j] = mine[q] ? id[q] : -1;
@@ -415,10 +418,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 // chosen experts' terms are added to the dense part, one choice after the
 // other where an expert was chosen twice.  The experts' loads, the same for
 // all tokens, stay in registers over a warp's tokens.
-// What a call differentiates: the loss alone, or weights (and the loss, or
-// not) of one of the scores.
-enum Part { kLossOnly, kSoftmaxChosen, kSoftmaxAll, kSigmoid };
-
 template <typename T, int LANES, int VPL, Part PART>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const RouteParams p, bool renorm) {
@@ -918,8 +917,12 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits, const float
     cudaError_t e = cudaSuccess;
     with_types<false>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
-        e = launch(p, route_kernel<decltype(type), kLanes, decltype(vpl)::value>,
-                   token_grid<kLanes>(p, 1), kRouteWarps * 32, 0, st, p, softmax, renorm);
+        constexpr int kVpl = decltype(vpl)::value;
+        using T = decltype(type);
+        e = launch(p, !softmax ? route_kernel<T, kLanes, kVpl, kSigmoid>
+                      : renorm ? route_kernel<T, kLanes, kVpl, kSoftmaxChosen>
+                               : route_kernel<T, kLanes, kVpl, kSoftmaxAll>,
+                   token_grid<kLanes>(p, 1), kRouteWarps * 32, 0, st, p, renorm);
     });
     return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
