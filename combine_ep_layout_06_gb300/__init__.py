@@ -2,10 +2,10 @@
 combine over W logical ranks held in one GPU's HBM.
 
 The compute path is the CUDA library libep_gb300.so (C ABI in
-include/ep_api.h); ``EpDispatchCombineOp`` is a thin ctypes binding over it,
-and so are the calls around it: top-k routing (``route``), the balance loss
+include/ep_api.h); ``EpDispatchCombineOp`` is a thin ctypes binding over it.
+The calls around it, top-k routing (``route``), the balance loss
 (``balance_loss``) and the experts' matrix products (``expert_product``), each
-with its gradient.
+with its gradient, go through a compiled binding.
 Submodules are imported lazily so that ``combine_ep_layout_06_gb300.inputs``
 (the seeded input generator) can be used without loading the library.
 """

@@ -20,8 +20,12 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
-// Warps of a block of the losses, one block per SM: what the registers allow.
-__host__ __device__ constexpr int loss_warps(int experts_per_lane) { return 256 / experts_per_lane; }
+// Warps of a block of the losses, one block per SM: what the registers and 48
+// KB of shared memory allow (32768 x 256: 24 warps of 16 lanes a token 13.4 us
+// a call, 16 warps 15.0).
+__host__ __device__ constexpr int loss_warps(int lanes, int experts_per_lane) {
+    return experts_per_lane == 8 ? 32 : experts_per_lane == 16 ? (lanes < 32 ? 24 : 16) : 8;
+}
 
 struct RouteParams {
     const void *logits;
@@ -616,10 +620,10 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 constexpr int kLossCluster = 4;
 
 template <typename T, int LANES, int VPL>
-__global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(loss_warps(VPL) * 32)
+__global__ void __cluster_dims__(kLossCluster, 1, 1) __launch_bounds__(loss_warps(LANES, VPL) * 32)
     balance_partial_kernel(const RouteParams p, int tokens_per_warp) {
     extern __shared__ float sh[];                 // [kLossWarps][E + 1], then [E] counts
-    constexpr int kTokens = 32 / LANES, kLossWarps = loss_warps(VPL), SLOTS = slots_of<LANES>();
+    constexpr int kTokens = 32 / LANES, kLossWarps = loss_warps(LANES, VPL), SLOTS = slots_of<LANES>();
     __shared__ float shares[32], joined[kLossCluster + 1];   // of the loss by warp, by block; z
     int32_t *cnt = reinterpret_cast<int32_t *>(sh + kLossWarps * (p.E + 1));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES;
@@ -815,8 +819,8 @@ int loss_clusters(const ep_route_desc_t &d) {
 
 // Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
 // Reductions cost a warp the same for one token or several, so for the losses
-// (WIDE) a lane takes 16 experts of a long row (32768 x 256: 11.2 against 12.3
-// us); top-k, which searches a lane's experts, and the gradient, which needs the
+// (WIDE) a lane takes 16 experts of a long row (32768 x 256: 13.4 against 14.9
+// us a call); top-k, which searches a lane's experts, and the gradient, which needs the
 // registers, take 8 (gradient: 19 against 26 us).
 template <int V> struct Int { static constexpr int value = V; };
 template <bool WIDE, typename T, typename F> void with_row(int E, F f) {
@@ -1000,7 +1004,7 @@ ep_status_t ep_balance_loss(const ep_route_desc_t *d, const void *d_logits, cons
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     with_types<true>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
-        constexpr int kWarps = loss_warps(decltype(vpl)::value);
+        constexpr int kWarps = loss_warps(decltype(lanes)::value, decltype(vpl)::value);
         const size_t sh = ((size_t)kWarps * (p.E + 1) + p.E) * 4;    // 37 KB at most
         const int64_t warps = (int64_t)clusters * kLossCluster * kWarps;
         const int per_warp = (int)(((int64_t)p.W * p.T + warps - 1) / warps);
