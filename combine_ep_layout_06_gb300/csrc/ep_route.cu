@@ -329,10 +329,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     raw.load(p, row, at.l, at.present);
     float x[VPL], y[VPL];
     const int e0 = at.l * VPL;
-    if (p.bias && p.vec_e && e0 < p.E) {
+    if (p.bias && p.vec_e) {          // E is a multiple of 8: every piece is inside or outside
 #pragma unroll
         for (int i = 0; i < VPL; i += 4) {
-            const float4 b = *reinterpret_cast<const float4 *>(p.bias + e0 + i);
+            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e0 + i < p.E) b = *reinterpret_cast<const float4 *>(p.bias + e0 + i);
             y[i] = b.x; y[i + 1] = b.y; y[i + 2] = b.z; y[i + 3] = b.w;
         }
     } else {
