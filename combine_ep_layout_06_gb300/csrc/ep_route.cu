@@ -762,6 +762,7 @@ __global__ void __cluster_dims__(kFinalCluster, 1, 1) __launch_bounds__(1024)
     const int column = threadIdx.x % kFinalColumns, slice = threadIdx.x / kFinalColumns;
     const int per = (p.E + kFinalCluster - 1) / kFinalCluster;
     const int e = column < per && (int)rank * per + column < p.E ? (int)rank * per + column : -1;
+    cluster_sync();              // all 8 blocks run: their shared memory may be written
     grid_dependency_wait();
     float sum = 0.f, z = 0.f;
     int32_t c = 0;
