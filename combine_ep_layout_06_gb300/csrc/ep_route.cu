@@ -201,9 +201,12 @@ struct RowStats {
     float m, scaled, inv_sum;    // scaled: m log2(e)
     bool open;                   // some expert is open
 
-    // Rows of ordinary size take exp(x - m) as 2^(x log2(e) - scaled), one
-    // multiply-add; scaled's rounding is a factor that all terms share.
-    __device__ bool near() const { return fabsf(m) <= 1e30f; }
+    // With |m| <= 2^16, exp(x - m) is taken as 2^(x log2(e) - scaled), one
+    // multiply-add.  What rounding m log2(e) to `scaled` left out, 2^-8 at most
+    // there, is in every term's exponent: a factor that probabilities share and
+    // that lse() takes back out.  It grows with |m| (512 at 2^33: sums of 0 or
+    // infinity), so rows further out subtract first, which is exact at the maximum.
+    __device__ bool near() const { return fabsf(m) <= 65536.f; }
     __device__ float prob(float x) const {
         if (!open) return 0.f;
         return (near() ? exp2_approx(fmaf(x, kLog2e, -scaled)) : exp_diff(x - m)) * inv_sum;
@@ -232,7 +235,7 @@ __device__ __forceinline__ RowStats row_exps(float *x) {
     }
     return st;
 }
-// 1 <= sum <= E for an open row.
+// Of an open row, whose largest term is 1 within 2^-8: 0.99 <= sum <= 1.01 E.
 __device__ __forceinline__ float inverse(const RowStats &st, float sum) {
     return st.open ? __fdividef(1.0f, sum) : 1.f;
 }

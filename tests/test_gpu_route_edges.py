@@ -1,13 +1,25 @@
 """Routing and losses at the edges of their ranges: the last lane's experts,
 few experts over many tokens, logits far from 0.  References and tolerances are
-those of test_gpu_route."""
+those of test_gpu_route; a NaN is never near anything here."""
+import math
+
 import pytest
 import torch
 
 import combine_ep_layout_06_gb300 as ep
-from test_gpu_route import DTYPES, OPTIONS, clean, draw_logits, near, ref_loss, ref_route
+from test_gpu_route import (DTYPES, OPTIONS, TINY, UNIT, clean, draw_logits, ref_loss, ref_route, softmax,
+                            weights_of)
 
 pytestmark = pytest.mark.gpu
+
+
+def near(got, want, scale, dtype=torch.float32):
+    """Within 1e-5 of the largest term `scale` (one, or one per row) and of the
+    result, and half a unit of a 16-bit type's last place."""
+    got, want = got.cpu().double(), want.detach()
+    tol = 1e-5 * scale + (UNIT[dtype] + 1e-5) * want.abs() + TINY[dtype]
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
 
 
 @pytest.mark.parametrize("E", [8, 24, 40, 72, 136, 200, 264, 328, 504, 520, 600, 776, 1000, 1016, 1024])
@@ -43,3 +55,74 @@ def test_losses_over_several_clusters(W, T, E, k):
     near(first[2], rp, 1.0 / E)
     for _ in range(20):
         assert all(torch.equal(p, q) for p, q in zip(ep.balance_loss(*a, balance_coef=0.5, z_coef=0.25, num_tokens=nt), first))
+
+
+LARGE = [6e4, 1e5, 1e9, 1e10, 1e20, 9e29, 3e38]
+
+
+def large_rows(E, dtype, most=3.4e38):
+    """Rows whose largest logit is far from 0, of both signs: all equal, next
+    to closed experts, alone, one of two, and with neighbours a few units away."""
+    rows = []
+    for v in LARGE:
+        v = min(v, float(torch.finfo(dtype).max))
+        if v > most:
+            continue
+        for s in (v, -v):
+            rest = -v if s < 0 else 0.0
+            rows += [[s] * E, [s, -math.inf] * (E // 2) + [s] * (E % 2), [s] + [rest * 2 if s < 0 else rest] * (E - 1),
+                     [rest * 2 if s < 0 else rest] * (E - 2) + [s, s], [s - 0.75 * (j % 7) for j in range(E)]]
+    x = torch.tensor(rows, dtype=torch.float64)
+    return x.clamp(min=-float(torch.finfo(dtype).max)).where(x > -math.inf, x).to(dtype)[None]
+
+
+def largest(want, terms):
+    """A row's largest term: `terms`, or its largest output."""
+    return want.abs().amax(-1, keepdim=True).clamp(min=terms)
+
+
+@pytest.mark.parametrize("E", [12, 256, 600])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_far_from_zero(E, dtype):
+    """Finite logits of any size (a mask's fill value over a whole row, a router
+    that ran away) have finite probabilities, weights and gradients."""
+    x, k = large_rows(E, dtype), 3
+    nt = [x.shape[1]]
+    g = torch.Generator().manual_seed(E)
+    gw = torch.randn((1, nt[0], k), generator=g)
+    cb, cz = 0.5, 0.25
+    for score, renorm, scale in OPTIONS:
+        w, idx = ep.route(x.cuda(), k, score=score, renormalize=renorm, scale=scale)
+        rw, ridx = ref_route(x, k, score, renorm, scale, None, nt)
+        assert torch.equal(idx.cpu(), ridx) and torch.isfinite(w).all()
+        near(w, rw, scale)
+        xs = clean(x).requires_grad_(True)
+        want, = torch.autograd.grad((weights_of(xs, ridx.long(), score, renorm, scale) * gw).sum(), xs)
+        got = ep.route_backward(gw.cuda(), x.cuda(), idx, score=score, renormalize=renorm, scale=scale)
+        want = torch.nan_to_num(want, nan=0.0)
+        near(got, want, largest(want, 4 * scale * float(gw.abs().max())), dtype)
+    idx = torch.argsort(torch.rand((1, nt[0], E), generator=g), -1)[..., :k].to(torch.int32).contiguous()
+    rl, rc, rp = ref_loss(clean(x), idx, nt, cb, cz)
+    loss, counts, probs = ep.balance_loss(x.cuda(), idx.cuda(), balance_coef=cb, z_coef=cz)
+    assert torch.equal(counts.cpu(), rc)
+    near(probs, rp, 1.0 / E)
+    near(loss[1], rl[1], 0.0)
+    # p (cb (f - <p, f>) + 2 cz lse) / n: through autograd of logsumexp even 64 bits lose p where |x| > 1e16
+    p, f = softmax(clean(x)), rc.double() * E / (k * nt[0])
+    lse = torch.logsumexp(clean(x), -1, keepdim=True)
+    want = 1.5 / nt[0] * p * (cb * (f - (p * f).sum(-1, keepdim=True)) + 2 * cz * lse)
+    gl = torch.tensor(1.5).cuda()
+    got = ep.balance_loss_backward(gl, x.cuda(), counts, k, balance_coef=cb, z_coef=cz)
+    near(got, want, largest(want, E * cb * 1.5 / nt[0]), dtype)
+    for score, renorm, scale in OPTIONS:         # and with the weights' gradient in the same pass
+        alone = ep.route_backward(gw.cuda(), x.cuda(), idx.cuda(), score=score, renormalize=renorm, scale=scale)
+        both = ep.route_backward(gw.cuda(), x.cuda(), idx.cuda(), score=score, renormalize=renorm, scale=scale,
+                                 grad_loss=gl, counts=counts, balance_coef=cb, z_coef=cz)
+        assert torch.isfinite(both).all()
+        if dtype == torch.float32:
+            total = want + alone.cpu().double()
+            near(both, total, largest(total, E * cb + 4 * scale * float(gw.abs().max())))
+    few = large_rows(E, dtype, 1e10)             # z, where its squares fit 32 bits
+    i = idx[:, :few.shape[1]].contiguous()
+    loss, _, _ = ep.balance_loss(few.cuda(), i.cuda(), balance_coef=cb, z_coef=cz)
+    near(loss, ref_loss(clean(few), i, [few.shape[1]], cb, cz)[0], 0.0)
