@@ -595,8 +595,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
 }
 
+// Without the z loss its size, past fp32 for |lse| > 2^64, has no part in the
+// total: 0 * infinity would be NaN.
 __device__ __forceinline__ void store_loss(const RouteParams &p, float balance, float z) {
-    p.loss[0] = p.balance_coef * balance + p.z_coef * z;
+    p.loss[0] = p.balance_coef * balance + (p.z_coef != 0.f ? p.z_coef * z : 0.f);
     p.loss[1] = balance;
     p.loss[2] = z;
 }

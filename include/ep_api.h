@@ -453,7 +453,8 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits,
  *   d_loss[1] = sum_e (counts_e * E / (k n)) * probs_e
  *   d_loss[2] = (1/n) sum of (log sum exp x)^2   (0 for a token that sees no
  *               open expert)
- *   d_loss[0] = balance_coef * d_loss[1] + z_coef * d_loss[2]
+ *   d_loss[0] = balance_coef * d_loss[1] + z_coef * d_loss[2]   (z_coef 0: without the
+ *               second term, whatever d_loss[2] is)
  * All 0 when n = 0.  Sums are fp32, in an order that the sizes alone fix.
  * d_idx [W][T][k]; d_loss [3], d_counts [E] int32, d_probs [E] fp32.
  * d_workspace: ep_balance_loss_workspace bytes, 16-byte aligned, any

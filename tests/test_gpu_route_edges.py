@@ -126,3 +126,20 @@ def test_rows_far_from_zero(E, dtype):
     i = idx[:, :few.shape[1]].contiguous()
     loss, _, _ = ep.balance_loss(few.cuda(), i.cuda(), balance_coef=cb, z_coef=cz)
     near(loss, ref_loss(clean(few), i, [few.shape[1]], cb, cz)[0], 0.0)
+
+
+@pytest.mark.parametrize("W,T,E,k", [(1, 6, 8, 2), (2, 40, 77, 3), (4, 3000, 64, 4)])
+def test_without_the_z_loss_its_size_does_not_matter(W, T, E, k):
+    """One token whose whole row is at the type's lowest number: the square of
+    its log-sum-exp is past fp32, and with z_coef 0 it has no part in the total."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x = draw_logits(W, T, E, dtype, seed=E)
+        x[0, 3] = torch.finfo(dtype).min
+        idx = torch.argsort(torch.rand((W, T, E), generator=torch.Generator().manual_seed(T)), -1)[..., :k]
+        idx = idx.to(torch.int32).contiguous()
+        nt = [T] * W
+        rl, rc, rp = ref_loss(clean(x), idx, nt, 0.5, 0.0)
+        loss, counts, probs = ep.balance_loss(x.cuda(), idx.cuda(), balance_coef=0.5, z_coef=0.0)
+        near(loss[:2], rl[:2], 0.0)
+        near(probs, rp, 1.0 / E)
+        assert torch.equal(counts.cpu(), rc)
