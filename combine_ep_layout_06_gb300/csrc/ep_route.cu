@@ -280,10 +280,15 @@ template <int LANES> __host__ __device__ constexpr int slots_of() { return 32 / 
 
 // Scores of the chosen experts from their logits c[] (mine: slot is a choice)
 // and the row's statistics.  v[]: scale 1.  For the sigmoid *sum is what
-// renormalising divides by.
+// renormalising divides by.  Where that sum is below 2^-32 the scores are e^c
+// within 2^-32 of themselves, down to below fp32's range, and only their ratios
+// matter: they are taken relative to the largest instead (the return value).  A
+// token whose largest is below e^-745, the least that 64 bits hold (all at a
+// mask's fill value), has no score.
 template <int LANES, int SLOTS>
-__device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const RowStats &st, const float *c,
+__device__ __forceinline__ bool chosen_scores(bool softmax, bool renorm, const RowStats &st, const float *c,
                                               const bool *mine, float *v, float *sum) {
+    bool relative = false;
     *sum = 0.f;
     if (softmax && renorm) {
         float m = -INFINITY;
@@ -307,8 +312,26 @@ __device__ __forceinline__ void chosen_scores(bool softmax, bool renorm, const R
             v[q] = mine[q] ? sigmoid(c[q]) : 0.f;
             *sum += v[q];
         }
-        if (renorm) *sum = row_sum<LANES>(*sum);
+        if (renorm) {
+            *sum = row_sum<LANES>(*sum);
+            const bool low = *sum < 2.3283064e-10f;      // 2^-32
+            if (__any_sync(0xffffffffu, low)) {
+                float m = -INFINITY, total = 0.f;
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) m = fmaxf(m, mine[q] ? c[q] : -INFINITY);
+                m = row_max<LANES>(m);
+                relative = low && m > -745.f;
+#pragma unroll
+                for (int q = 0; q < SLOTS; ++q) {
+                    if (low) v[q] = relative && mine[q] ? exp_diff(c[q] - m) : 0.f;
+                    total += v[q];
+                }
+                total = row_sum<LANES>(total);
+                if (low) *sum = total;
+            }
+        }
     }
+    return relative;
 }
 
 // The scores, each in kernels of its own; and a gradient of the loss alone.
@@ -535,7 +558,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             }
             if constexpr (WEIGHTS) {
                 float v[SLOTS], dv[SLOTS], sum, dot = 0.f;
-                chosen_scores<LANES, SLOTS>(softmax, PART == kSoftmaxChosen || (PART == kSigmoid && renorm), st, c, mine, v, &sum);
+                const bool relative = chosen_scores<LANES, SLOTS>(
+                    softmax, PART == kSoftmaxChosen || (PART == kSigmoid && renorm), st, c, mine, v, &sum);
 #pragma unroll
                 for (int q = 0; q < SLOTS; ++q) dot += g[q] * v[q];
                 if (PART != kSigmoid || renorm) dot = row_sum<LANES>(dot);
@@ -546,7 +570,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
                     } else {
                         float s = g[q];
                         if (renorm) s = sum > 0.f ? (g[q] - dot / sum) / sum : 0.f;
-                        dv[q] = s * v[q] * (1.0f - v[q]);
+                        dv[q] = s * v[q] * (relative ? 1.0f : 1.0f - v[q]);
                     }
                 }
                 if (PART == kSoftmaxAll) {

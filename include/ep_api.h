@@ -439,7 +439,8 @@ typedef struct {
  *   softmax:  w_j = scale * exp(x_j) / sum exp(x), the sum over the chosen
  *             experts (renormalize) or over all
  *   sigmoid:  w_j = scale * v_j, v_j = 1 / (1 + exp(-x_j)), divided by the sum
- *             of the chosen v (renormalize)
+ *             of the chosen v (renormalize; weights 0 where every chosen x is
+ *             below -745)
  * d_w [W][T][k] fp32 and d_idx [W][T][k] int32, dense, are dispatch's weights
  * and indices.  Tokens that are not present get ids -1 and weights 0. */
 ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits,

@@ -143,3 +143,30 @@ def test_without_the_z_loss_its_size_does_not_matter(W, T, E, k):
         near(loss[:2], rl[:2], 0.0)
         near(probs, rp, 1.0 / E)
         assert torch.equal(counts.cpu(), rc)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (8, 1), (77, 3), (256, 8), (257, 32), (600, 6)])
+def test_renormalised_sigmoid_of_very_low_logits(E, k):
+    """Scores below what fp32 holds still have ratios: weights that sum to the
+    scale, and gradients, as in 64 bits.  A weight's relative error is that of
+    a difference of logits, 2^-23 of up to 10 and of the logit's own size."""
+    rows = 64
+    g = torch.Generator().manual_seed(E)
+    level = torch.linspace(-30.0, -690.0, rows, dtype=torch.float64)
+    level[:8] = torch.tensor([-80.0, -86.0, -87.4, -88.0, -88.5, -88.8, -95.0, -103.0])
+    x = level[:, None] + torch.rand((rows, E), generator=g, dtype=torch.float64) * 5.0
+    x[-6:] = torch.tensor([-2.0, 3.0, -90.0, -60.0, -50.0, -45.0])[:, None] - torch.arange(E) * 7.0    # few of a row low
+    x[-8, 1:] = -math.inf
+    x[-7] = -math.inf
+    for dtype in DTYPES:
+        xt = x.to(dtype)[None]
+        w, idx = ep.route(xt.cuda(), k, score="sigmoid", scale=2.5)
+        rw, ridx = ref_route(xt, k, "sigmoid", True, 2.5, None, [rows])
+        assert torch.equal(idx.cpu(), ridx)
+        near(w, rw, 2.5)
+        gw = torch.randn((1, rows, k), generator=g)
+        xs = clean(xt).requires_grad_(True)
+        want, = torch.autograd.grad((weights_of(xs, ridx.long(), "sigmoid", True, 2.5) * gw).sum(), xs)
+        got = ep.route_backward(gw.cuda(), xt.cuda(), idx, score="sigmoid", scale=2.5)
+        assert torch.isfinite(got).all()
+        near(got, torch.nan_to_num(want, nan=0.0), 4 * 2.5 * float(gw.abs().max()), dtype)
