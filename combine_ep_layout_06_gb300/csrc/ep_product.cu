@@ -210,7 +210,7 @@ __device__ __forceinline__ void activate8(int act, float *v) {
     switch (act) {
     case EP_ACT_RELU:
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaxf(v[i], 0.f);
+        for (int i = 0; i < 8; ++i) v[i] = v[i] <= 0.f ? 0.f : v[i];     // NaN stays (fmaxf would drop it)
         break;
     case EP_ACT_GELU:
 #pragma unroll
