@@ -749,15 +749,16 @@ struct ActGradParams {
 
 constexpr int kActWarps = 8, kActCols = 256, kActRows = 4;
 
-__device__ __forceinline__ float act_slope(int act, float v) {
-    if (act == EP_ACT_RELU) return v > 0.f ? 1.f : 0.f;
+// grad * act'(v).  A closed unit of ReLU takes nothing, an infinite gradient included.
+__device__ __forceinline__ float act_grad(int act, float grad, float v) {
+    if (act == EP_ACT_RELU) return v > 0.f ? grad : 0.f;
     if (act == EP_ACT_GELU)      // Phi(v) + v phi(v), phi(v) = exp(-v^2/2) / sqrt(2 pi)
-        return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+        return grad * (0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f);
     if (act == EP_ACT_SILU) {
         const float s = sigmoidf(v);
-        return s * (1.0f + v * (1.0f - s));
+        return grad * (s * (1.0f + v * (1.0f - s)));
     }
-    return 1.f;
+    return grad;
 }
 
 template <typename T> __device__ __forceinline__ void unpack8(float *v, const uint4 &r) {
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
             } else if (reads_pre) {
                 unpack8<T>(v, v0[u]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d0[j] = y[j] * act_slope(p.act, v[j]);
+                for (int j = 0; j < 8; ++j) d0[j] = act_grad(p.act, y[j], v[j]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d0[j] = y[j];

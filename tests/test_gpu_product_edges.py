@@ -27,3 +27,29 @@ def test_relu_keeps_what_is_not_a_number():
         # 64 products in fp32, one rounding
         tol = u * want[clean].abs() + 64 * 2.0 ** -23 * (x[clean].double().abs() @ w[0].double().abs().T) + 2.0 ** -24
         assert ((y[clean].double() - want[clean]).abs() <= tol).all()
+
+
+def test_relu_gradient_of_a_closed_unit_is_zero():
+    """A unit at or below 0 passes nothing on, not even an infinite gradient; an
+    open one passes it on."""
+    for dtype in (torch.bfloat16, torch.float16):
+        g = torch.Generator().manual_seed(4)
+        pre = torch.randn((24, 72), generator=g).to(dtype)
+        grad = torch.randn((24, 72), generator=g).to(dtype)
+        pre[5], grad[5] = -pre[5].abs() - 0.5, INF
+        pre[6], grad[6] = 0.0, -INF
+        pre[9, 3], grad[9, 3] = 1.0, INF
+        x = torch.ones((24, 64), dtype=dtype)
+        w = (torch.rand((1, 72, 64), generator=g) + 0.5).to(dtype)
+        dx, dw, db = ep.expert_product_backward(grad.cuda(), x.cuda(), w.cuda(), pre=pre.cuda(), activation="relu",
+                                                bias_grad=True)
+        dx, dw, db = dx.cpu().double(), dw.cpu().double(), db.cpu().double()
+        assert (dx[5:7] == 0).all() and (dx[9] == INF).all()
+        assert (dw[0, 3] == INF).all() and db[0, 3] == INF
+        d = torch.where(pre > 0, grad, torch.zeros_like(grad)).double()
+        finite = [j for j in range(72) if j != 3]
+        u = torch.finfo(dtype).eps / 2
+        # 24 terms in fp32, one rounding
+        for got, want in ((dw[0][finite], d.T[finite] @ x.double()), (db[0][finite], d.sum(0)[finite])):
+            tol = u * want.abs() + 24 * 2.0 ** -23 * d[:, finite].abs().sum(0).max() + 2.0 ** -24
+            assert ((got - want).abs() <= tol).all()
