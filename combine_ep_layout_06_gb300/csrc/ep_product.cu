@@ -172,7 +172,7 @@ __device__ __forceinline__ void clear_rows(uint32_t slice, int chunks, int live)
 struct __align__(8) Barriers {
     uint64_t full[kStages], empty[kStages], tail[kStages], peer_tail[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
-    int gave_up;
+    Watch watch;
 };
 
 // Two floats as two 16-bit values.
@@ -339,7 +339,7 @@ struct Cta {
     uint32_t ring, tmem, rank;
     float *turns;
     int64_t pairs;
-    volatile int *gave_up;
+    volatile Watch *watch;
 
     static __device__ uint32_t bar(uint64_t *b) { return smem_u32(b); }
     static __device__ uint32_t first_cta(uint64_t *b) { return in_cta(smem_u32(b), 0); }
@@ -386,7 +386,7 @@ struct Loader {
             const CUtensorMap *mb = narrow ? &w.b32 : &w.b;
             const int m0 = (t.m * 2 + (int)c.rank) * kTileM, n0 = t.n0 + (int)c.rank * half;
             for (int k = 0; k < K; k += kSliceK) {
-                if (!tensor_wait(c.bar(&bars.empty[s]), phase ^ 1u, c.gave_up)) {
+                if (!tensor_wait(c.bar(&bars.empty[s]), phase ^ 1u, c.watch)) {
                     ok = false;
                     break;
                 }
@@ -426,6 +426,7 @@ struct Loader {
                     tails |= 1u << s;
                 }
                 ++issued;
+                if (elected) c.watch->loaded = issued;
                 advance(s, phase);
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -440,14 +441,14 @@ struct Loader {
     __device__ void finish(const Cta &c, bool ok) {
         if ((threadIdx.x & 31) == 0) {
             Barriers &bars = *c.bars;
-            int ignore = 0;
-            volatile int *flag = ok ? c.gave_up : &ignore;
+            Watch ignore = {};
+            volatile Watch *watch = ok ? c.watch : &ignore;
             for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
                 const uint32_t q = j % kStages, round = (j / kStages) & 1u;
-                if (!ok && c.rank == 0) tensor_wait(c.bar(&bars.full[q]), round, flag);
+                if (!ok && c.rank == 0) tensor_wait(c.bar(&bars.full[q]), round, watch);
                 if (!ok && c.rank == 1 && (tails >> q & 1u))
-                    tensor_wait(c.bar(&bars.tail[q]), landed >> q & 1u, flag);
-                tensor_wait(c.bar(&bars.empty[q]), round, flag);
+                    tensor_wait(c.bar(&bars.tail[q]), landed >> q & 1u, watch);
+                tensor_wait(c.bar(&bars.empty[q]), round, watch);
             }
         }
         __syncwarp();
@@ -484,13 +485,13 @@ struct Multiplier {
             if (K == 0) continue;
             const uint32_t idesc = kIdesc | idesc_n(n);
             const uint32_t d = c.tmem + (acc & 1u) * 256;
-            ok = warp_wait<true>(c.bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, c.gave_up);
+            ok = warp_wait<true>(c.bar(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, c.watch);
             tcgen_after_sync();
             // One thread issues everything, and has to queue the next slice's
             // instructions before the last one's end: the loop is kept short.
             const int end = !ok ? 0 : MODE == kGradW ? K / kSliceK * kSliceK : K;
             for (int k = 0; k < end; k += kSliceK) {
-                if (!tensor_wait(c.bar(&bars.full[s]), phase, c.gave_up)) {
+                if (!tensor_wait(c.bar(&bars.full[s]), phase, c.watch)) {
                     ok = false;
                     break;
                 }
@@ -506,10 +507,10 @@ struct Multiplier {
             }
             ok = __all_sync(0xffffffffu, ok);
             if (MODE == kGradW && ok && K % kSliceK) {
-                ok = warp_wait(c.bar(&bars.full[s]), phase, c.gave_up);
+                ok = warp_wait(c.bar(&bars.full[s]), phase, c.watch);
                 if (ok) {
                     clear_rows(c.ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, K % kSliceK);
-                    ok = warp_wait<true>(c.bar(&bars.peer_tail[s]), tails >> s & 1u, c.gave_up);
+                    ok = warp_wait<true>(c.bar(&bars.peer_tail[s]), tails >> s & 1u, c.watch);
                     tails ^= 1u << s;
                 }
                 if (ok && elected) {
@@ -530,7 +531,7 @@ struct Multiplier {
     }
     __device__ void finish(const Cta &c, bool ok) {
         if (ok) return;                                  // else let the matrix unit finish
-        int ignore = 0;
+        Watch ignore = {};
         if (elect_one()) mma_commit(c.bar(&c.bars->drained));
         tensor_wait(c.bar(&c.bars->drained), 0, &ignore);
     }
@@ -556,7 +557,7 @@ struct Clearer {
             if (MODE != kGradW || live == 0) continue;
             const int n = (t.n + 31) & ~31;
             const uint32_t s = (slice - 1) % kStages;
-            ok = warp_wait(c.bar(&bars.tail[s]), tails >> s & 1u, c.gave_up);
+            ok = warp_wait(c.bar(&bars.tail[s]), tails >> s & 1u, c.watch);
             if (!ok) break;
             tails ^= 1u << s;
             clear_rows(c.ring + s * kStageBytes, 2 + (n / 2 + 63) / 64, live);
@@ -598,7 +599,7 @@ struct Finisher {
                 if (m < p.M) bias = f32(b[MODE == kGated && (in & 8) ? p.M + m : m]);
             }
             if (K > 0) {
-                ok = warp_wait(c.bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, c.gave_up);
+                ok = warp_wait(c.bar(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, c.watch);
                 if (!ok) break;
                 tcgen_after_sync();
             }
@@ -648,7 +649,7 @@ __device__ __forceinline__ void run_products(const Work *first, const Work *seco
     c.turns = reinterpret_cast<float *>(smem_raw + (c.ring - smem_u32(smem_raw)) + kRingBytes);
     c.rank = cluster_rank();
     c.pairs = gridDim.x >> 1;
-    c.gave_up = &bars.gave_up;
+    c.watch = &bars.watch;
     const int64_t pair = blockIdx.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -663,7 +664,8 @@ __device__ __forceinline__ void run_products(const Work *first, const Work *seco
             mbar_init(&bars.acc_empty[i], 2 * kEpilogueWarps);   // both CTAs' epilogue warps
         }
         mbar_init(&bars.drained, 1);
-        bars.gave_up = 0;
+        bars.watch.gave_up = 0;
+        bars.watch.loaded = 0;
         mbar_init_fence();
         const Work *w = first ? first : second;
         tma_prefetch_map(&w->a);
@@ -715,7 +717,7 @@ __device__ __forceinline__ void run_products(const Work *first, const Work *seco
     cluster_sync();              // neither CTA's memory is read or signalled any more
     tcgen_after_sync();
     if (warp == 1) tmem_free(c.tmem, 512);
-    if (threadIdx.x == 0 && bars.gave_up && error) atomicOr(error, EP_DEVERR_TIMEOUT);
+    if (threadIdx.x == 0 && bars.watch.gave_up && error) atomicOr(error, EP_DEVERR_TIMEOUT);
 }
 
 template <typename T, Mode MODE>

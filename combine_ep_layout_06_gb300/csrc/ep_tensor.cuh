@@ -30,31 +30,47 @@ __device__ __forceinline__ bool tensor_try(uint32_t bar, uint32_t parity) {
                      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for `parity` of an mbarrier, for a second at most.  `gave_up` is the
-// CTA's shared flag: set by the wait that runs out, and seen by the others.
+// What a CTA's waits share, in its shared memory.  `loaded` moves with every
+// slice that the CTA loads; `gave_up` is set by a wait that runs out, and seen by
+// the others.
+struct Watch {
+    int gave_up;
+    uint32_t loaded;
+};
+// Waits for `parity` of an mbarrier, until a second has passed without another
+// slice loaded.  A limit on the whole wait would end work that goes on: an
+// epilogue waits for all of a tile's slices, 2^23 of them in the weight gradient
+// of a group of 2^30 rows.
 template <bool PEER>
-__device__ __noinline__ bool tensor_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+__device__ __noinline__ bool tensor_wait_long(uint32_t bar, uint32_t parity, volatile Watch *watch) {
     uint64_t t0 = 0;
+    uint32_t seen = 0;
     for (uint32_t it = 0; it < (1u << 26); ++it) {
         if (tensor_try<PEER>(bar, parity)) return true;
         if ((it & 63) == 63) {
-            if (*gave_up) return false;
+            if (watch->gave_up) return false;
             const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > kTensorWaitNs) break;
+            const uint32_t loaded = watch->loaded;
+            if (t0 == 0 || loaded != seen) {
+                t0 = now;
+                seen = loaded;
+                it = 63;
+            } else if (now - t0 > kTensorWaitNs) {
+                break;
+            }
         }
     }
-    *gave_up = 1;
+    watch->gave_up = 1;
     return false;
 }
 template <bool PEER = false>
-__device__ __forceinline__ bool tensor_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    return tensor_try<PEER>(bar, parity) || tensor_wait_long<PEER>(bar, parity, gave_up);
+__device__ __forceinline__ bool tensor_wait(uint32_t bar, uint32_t parity, volatile Watch *watch) {
+    return tensor_try<PEER>(bar, parity) || tensor_wait_long<PEER>(bar, parity, watch);
 }
 // The same by a whole warp, with one answer for all its lanes.
 template <bool PEER = false>
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    return __all_sync(0xffffffffu, tensor_wait<PEER>(bar, parity, gave_up));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile Watch *watch) {
+    return __all_sync(0xffffffffu, tensor_wait<PEER>(bar, parity, watch));
 }
 // One lane of the warp, the same one each time.  Code that only it runs,
 // inside control flow that the whole warp follows, keeps its operands in

@@ -53,3 +53,30 @@ def test_relu_gradient_of_a_closed_unit_is_zero():
         for got, want in ((dw[0][finite], d.T[finite] @ x.double()), (db[0][finite], d.sum(0)[finite])):
             tol = u * want.abs() + 24 * 2.0 ** -23 * d[:, finite].abs().sum(0).max() + 2.0 ** -24
             assert ((got - want).abs() <= tol).all()
+
+
+def test_a_group_of_very_many_rows():
+    """The weight gradient of one group of almost 2^30 rows runs for more than a
+    second in one pair of SMs, and no wait gives up.  Small whole numbers in a few
+    rows, the first and last among them: every sum is exact."""
+    n = (1 << 30) - 5
+    g = torch.Generator().manual_seed(1)
+    at = torch.cat([torch.tensor([0, 1, 63, 127, 128, n - 129, n - 2, n - 1]),
+                    torch.randint(200, n - 200, (300,), generator=g)]).unique()
+    xs, gs = (torch.randint(-2, 3, (len(at), 8), generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.randint(-2, 3, (1, 8, 8), generator=g).to(torch.bfloat16)
+    x, grad = (torch.zeros((n, 8), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[at.cuda()], grad[at.cuda()] = xs.cuda(), gs.cuda()
+    assert ep.moe_error() == 0
+    dx, dw, db = ep.expert_product_backward(grad, x, w.cuda(), bias_grad=True)
+    assert ep.moe_error() == 0
+    want = gs.double() @ w[0].double()
+    assert torch.equal(dx[at.cuda()].cpu().double(), want)
+    assert int(torch.count_nonzero(dx)) == int(torch.count_nonzero(want))
+    total = gs.double().T @ xs.double()
+    assert total.abs().max() <= 256 and torch.equal(dw[0].cpu().double(), total)
+    assert torch.equal(db[0].cpu().double(), gs.double().sum(0))
+    y = ep.expert_product(x, w.cuda())
+    want = xs.double() @ w[0].double().T
+    assert torch.equal(y[at.cuda()].cpu().double(), want)
+    assert int(torch.count_nonzero(y)) == int(torch.count_nonzero(want))
