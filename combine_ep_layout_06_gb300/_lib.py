@@ -189,8 +189,8 @@ def load(build_if_missing: bool = True):
         if _lib is not None:
             return _lib
         path = _build.LIB
-        if build_if_missing and not _build.up_to_date():
-            _build.build()
+        if build_if_missing and not _build.library_up_to_date():
+            _build.build_library()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing; run "
                                "`python -m combine_ep_layout_06_gb300.build`")

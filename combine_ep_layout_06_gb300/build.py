@@ -3,14 +3,16 @@ _moe.so, the Python binding of the routing, loss and product calls.
 
 Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
 one shared library with the CUDA runtime linked statically, so that loading
-it needs only the driver.  The binding is one C++ file against torch's
-headers, compiled next to them and linked to that library.  Usage: ``python -m
+it needs only the driver, and building it only nvcc.  The binding is one C++
+file against torch's headers, compiled next to them and linked to that library;
+without torch, which alone could load it, it is left out.  Usage: ``python -m
 combine_ep_layout_06_gb300.build [--ptxas-verbose]``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -47,12 +49,20 @@ def _deps():
         os.path.join(ROOT, "include", "ep_api.h"), os.path.abspath(__file__)]
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+def library_up_to_date() -> bool:
+    if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps()) and \
+    return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def binding_up_to_date() -> bool:
+    return os.path.exists(BINDING) and \
         os.path.getmtime(BINDING_SRC) <= os.path.getmtime(BINDING)
+
+
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def _run(cmd, what):
@@ -90,10 +100,10 @@ def _link_binding(obj: str):
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, ptxas_verbose: bool = False) -> str:
+def build_library(force: bool = False, ptxas_verbose: bool = False) -> str:
     """EP_NVTX=1 in the environment compiles NVTX ranges around the entry
     points in (for timelines and ncu range filters); they are off otherwise."""
-    if not force and not ptxas_verbose and up_to_date():
+    if not force and not ptxas_verbose and library_up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -103,27 +113,37 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+        return obj, _run([nvcc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj], f"nvcc failed on {src}")
 
-    with cf.ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding)
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         results = list(ex.map(compile_one, sources()))
-        binding = binding.result()
     if ptxas_verbose:
         for _, log in results:
             sys.stderr.write(log)
     tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp,
-           *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for o, _ in results]], "link failed")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    return LIB
+
+
+def build_binding(force: bool = False) -> str:
+    """The binding, for a library that is there."""
+    if force or not binding_up_to_date():
+        _link_binding(_compile_binding())
+    return BINDING
+
+
+def build(force: bool = False, ptxas_verbose: bool = False) -> str:
+    """Both, compiled side by side.  The library is in place before a binding
+    that does not build is an error."""
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding) if _has_torch() and (force or not binding_up_to_date()) else None
+        build_library(force, ptxas_verbose)
+        if binding:
+            _link_binding(binding.result())
+    if not _has_torch():
+        sys.stderr.write("torch is not installed: the Python binding is left out\n")
     return LIB
 
 

@@ -28,7 +28,8 @@ from . import build as _build
 
 
 def _load_binding():
-    _lib.load()                    # builds both if needed; raises if it cannot
+    _lib.load()                    # each is built if needed; raises if it cannot
+    _build.build_binding()
     spec = importlib.util.spec_from_file_location("_moe", _build.BINDING)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
