@@ -56,9 +56,23 @@ def library_up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _binding_made_for() -> str:
+    """What a binding fits besides its sources: one torch, one Python."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}\n"
+
+
 def binding_up_to_date() -> bool:
-    return os.path.exists(BINDING) and \
-        os.path.getmtime(BINDING_SRC) <= os.path.getmtime(BINDING)
+    """Newer than its source, than the structs it shares with the library and
+    than this file, and made for the torch and the Python that run."""
+    try:
+        with open(BINDING + ".for") as f:
+            made_for = f.read()
+        t = os.path.getmtime(BINDING)
+    except OSError:
+        return False
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "ep_api.h"), os.path.abspath(__file__)]
+    return made_for == _binding_made_for() and all(os.path.getmtime(d) <= t for d in deps)
 
 
 def _has_torch() -> bool:
@@ -98,6 +112,8 @@ def _link_binding(obj: str):
           "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"],
          "link of the Python binding failed")
     os.replace(tmp, BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(_binding_made_for())
 
 
 def build_library(force: bool = False, ptxas_verbose: bool = False) -> str:

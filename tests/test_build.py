@@ -59,3 +59,41 @@ def test_the_library_loads_without_the_binding(tmp_path, monkeypatch):
     for name in ("build", "build_library", "build_binding"):
         monkeypatch.setattr(build, name, never, raising=False)
     assert _lib.load().ep_status_str(0)
+
+
+def test_a_stale_binding_is_built_again(compilers, tmp_path, monkeypatch):
+    """A changed header (the structs that binding and library share), binding
+    source or recipe; a link that failed after the new library was in place;
+    another torch."""
+    commands, broken = compilers
+    header = tmp_path / "include" / "ep_api.h"
+    header.parent.mkdir()
+    header.write_text("/* as it was */")
+    monkeypatch.setattr(build, "ROOT", str(tmp_path))
+    src = tmp_path / "moe_binding.cpp"
+    src.write_text("// as it was")
+    monkeypatch.setattr(build, "BINDING_SRC", str(src))
+    build.build()
+    assert build.binding_up_to_date()
+    later = os.path.getmtime(build.BINDING) + 10
+    for changed in (header, src):
+        os.utime(changed, (later, later))
+        broken.add("g++")                                    # the library gets there, the binding does not
+        with pytest.raises(RuntimeError):
+            build.build()
+        broken.clear()
+        assert not build.binding_up_to_date()
+        os.utime(changed, (1, 1))
+        assert build.binding_up_to_date()
+    recipe = tmp_path / "build.py"
+    recipe.write_text("")
+    os.utime(recipe, (later, later))
+    monkeypatch.setattr(build, "__file__", str(recipe))
+    assert not build.binding_up_to_date()
+    os.utime(recipe, (1, 1))
+    import torch
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    assert not build.binding_up_to_date()
+    commands.clear()
+    build.build_binding()
+    assert commands and build.binding_up_to_date()
