@@ -406,6 +406,7 @@ PyObject *expert_product(PyObject *const *a) {
               "ep_expert_product");
     PyObject *result = nullptr;
     if (out) {
+        if (!out->is_inference()) out->unsafeGetTensorImpl()->bump_version();     // whoever saved it sees the change
         result = a[8];
         Py_INCREF(result);
     } else {

@@ -80,3 +80,22 @@ def test_a_group_of_very_many_rows():
     want = xs.double() @ w[0].double().T
     assert torch.equal(y[at.cuda()].cpu().double(), want)
     assert int(torch.count_nonzero(y)) == int(torch.count_nonzero(want))
+
+
+def test_writing_into_out_is_seen_by_autograd():
+    """Another operator that saved `out` for its gradient learns that it changed."""
+    x = torch.randn((16, 64)).to(torch.bfloat16).cuda()
+    w = torch.randn((1, 72, 64)).to(torch.bfloat16).cuda()
+    out = torch.zeros((16, 72), dtype=torch.bfloat16, device="cuda")
+    p = torch.ones((16, 72), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    loss = (p * out).sum()
+    before = out._version
+    assert ep.expert_product(x, w, out=out) is out
+    assert out._version == before + 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        other = torch.zeros_like(out)
+        ep.expert_product(x, w, out=other)
+    ep.expert_product(x, w, out=other)            # has no version to count
+    assert torch.equal(other, out)
