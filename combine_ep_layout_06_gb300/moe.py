@@ -90,11 +90,12 @@ def _backward(stream, logits, *args):
 def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, indices: torch.Tensor, *,
                    score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
                    num_tokens: Optional[Sequence[int]] = None, grad_loss: Optional[torch.Tensor] = None,
-                   counts: Optional[torch.Tensor] = None, balance_coef: float = 0.0, z_coef: float = 0.0,
+                   counts: Optional[torch.Tensor] = None, balance_coef: float = 1.0, z_coef: float = 0.0,
                    stream=None) -> torch.Tensor:
     """Gradient of ``route``'s weights by the logits, dense and in their type.
     With grad_loss (one fp32 value) and counts, the gradient of
-    ``balance_loss`` with these coefficients is added in the same pass."""
+    ``balance_loss`` with these coefficients (its own defaults) is added in the
+    same pass."""
     if grad_weights is None:
         raise ValueError("grad_weights is needed: balance_loss_backward is the loss's gradient alone")
     return _backward(stream, logits, indices.shape[-1], grad_weights, indices, grad_loss, counts, num_tokens,

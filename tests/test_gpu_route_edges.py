@@ -170,3 +170,15 @@ def test_renormalised_sigmoid_of_very_low_logits(E, k):
         got = ep.route_backward(gw.cuda(), xt.cuda(), idx, score="sigmoid", scale=2.5)
         assert torch.isfinite(got).all()
         near(got, torch.nan_to_num(want, nan=0.0), 4 * 2.5 * float(gw.abs().max()), dtype)
+
+
+def test_defaults_of_the_losses_agree():
+    """The combined gradient's loss is balance_loss's own unless told otherwise."""
+    x = draw_logits(2, 30, 24, torch.float32, seed=8).cuda()
+    w, idx = ep.route(x, 4)
+    loss, counts, _ = ep.balance_loss(x, idx)
+    gw, gl = torch.randn_like(w), torch.tensor(0.6).cuda()
+    both = ep.route_backward(gw, x, idx, grad_loss=gl, counts=counts)
+    parts = ep.route_backward(gw, x, idx) + ep.balance_loss_backward(gl, x, counts, 4)
+    near(both, parts.cpu().double(), 4 * float(gw.abs().max()) + 24)
+    assert (both - ep.route_backward(gw, x, idx)).abs().max() > 1e-4
