@@ -20,6 +20,7 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWarps = 4;
+constexpr int kSms = 152;        // of a GB300
 // Warps of a block of the losses, one block per SM: what the registers and 48
 // KB of shared memory allow (32768 x 256: 24 warps of 16 lanes a token 13.4 us
 // a call, 16 warps 15.0).
@@ -203,15 +204,15 @@ struct RowStats {
 
     // With |m| <= 2^16, exp(x - m) is taken as 2^(x log2(e) - scaled), one
     // multiply-add.  What rounding m log2(e) to `scaled` left out, 2^-8 at most
-    // there, is in every term's exponent: a factor that probabilities share and
-    // that lse() takes back out.  It grows with |m| (512 at 2^33: sums of 0 or
-    // infinity), so rows further out subtract first, which is exact at the maximum.
+    // there, is in every term's exponent: a factor that probabilities share, and
+    // in lse() an error of 2^-24 |m|.  It grows with |m| (512 at 2^33: sums of 0
+    // or infinity), so rows further out subtract first, exact at the maximum.
     __device__ bool near() const { return fabsf(m) <= 65536.f; }
     __device__ float prob(float x) const {
         if (!open) return 0.f;
         return (near() ? exp2_approx(fmaf(x, kLog2e, -scaled)) : exp_diff(x - m)) * inv_sum;
     }
-    // |error| of the logarithm: 2^-22, next to an lse of order 1 or more
+    // error of the logarithm: 2^-21.4 where the sum is below 2, else 3 units in the last place of a value of 7 at most
     __device__ float lse() const { return open ? m - __logf(inv_sum) : 0.f; }
 };
 
@@ -841,7 +842,8 @@ __global__ void __cluster_dims__(kFinalCluster, 1, 1) __launch_bounds__(1024)
 }
 
 // Clusters of the losses' first pass.  One, without a second pass, up to 2^17
-// logits; else one per 128 tokens, up to the 36 that fit the SMs.
+// logits; else one per 128 tokens, up to the 36 that run at a time (a block per
+// SM: what cudaOccupancyMaxActiveClusters gives on the 152 SMs).
 int loss_clusters(const ep_route_desc_t &d) {
     const int64_t tokens = (int64_t)d.world_size * d.tokens;
     const int64_t want = tokens * d.num_experts <= 1 << 17 ? 1 : (tokens + 127) / 128;
@@ -850,9 +852,10 @@ int loss_clusters(const ep_route_desc_t &d) {
 
 // Calls f(T(), Int<LANES>, Int<VPL>) for the logits' type and the row length.
 // Reductions cost a warp the same for one token or several, so for the losses
-// (WIDE) a lane takes 16 experts of a long row (32768 x 256: 13.4 against 14.9
+// (WIDE) a lane takes 16 experts of a long row (32768 x 256: 13.7 against 15.0
 // us a call); top-k, which searches a lane's experts, and the gradient, which needs the
-// registers, take 8 (gradient: 19 against 26 us).
+// registers, take 8 (against 16: top-k 14.5 and 15.4 us, gradient of the loss
+// alone 9.1 and 10.1, with the weights' 15.7 and 24.3).
 template <int V> struct Int { static constexpr int value = V; };
 template <bool WIDE, typename T, typename F> void with_row(int E, F f) {
     if (E <= 8) f(T(), Int<1>(), Int<8>());
@@ -911,9 +914,10 @@ bool make_params(const ep_route_desc_t *d, const void *logits, const int32_t *h_
 }
 
 // Launches as a programmatic dependent of the kernel before where the kernel
-// is long enough to gain by it (131072 x 8 logits: 5.8 instead of 6.2 us a
-// call, the gradient of 32768 x 256 18.1 instead of 20.5); a one-token call's
-// time goes by the host, whose launch it makes a microsecond longer.
+// is long enough to gain by it (32768 x 256: top-k 14.5 instead of 16.5 us a
+// call, both gradients 15.7 instead of 17.3; 131072 x 8 the same either way); a
+// one-token call's time goes by the host, whose launch it makes a microsecond
+// longer.
 template <typename... Params, typename... Args>
 cudaError_t launch(const RouteParams &p, void (*kernel)(Params...), dim3 blocks, unsigned threads, size_t dyn,
                    cudaStream_t st, Args &&...args) {
@@ -990,8 +994,9 @@ ep_status_t ep_route_backward(const ep_route_desc_t *d, const void *d_logits,
     with_types<false>(d->dtype, p.E, [&](auto type, auto lanes, auto vpl) {
         constexpr int kLanes = decltype(lanes)::value;
         // enough warps for all SMs (32 each) before a warp takes a second run
+        constexpr int64_t kFull = kSms * 32;
         const int64_t runs = (int64_t)p.W * p.T * kLanes / 32;
-        p.rounds = (int)(runs < 152 * 32 ? 1 : runs < 4 * 152 * 32 ? runs / (152 * 32) : 4);
+        p.rounds = (int)(runs < kFull ? 1 : runs < 4 * kFull ? runs / kFull : 4);
         constexpr int kVpl = decltype(vpl)::value;
         using T = decltype(type);
         e = launch(p, !d_grad_w          ? route_backward_kernel<T, kLanes, kVpl, kLossOnly>

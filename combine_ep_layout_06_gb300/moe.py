@@ -15,6 +15,10 @@ until the call's work is done (``Tensor.record_stream``).  Device-side problems
 (an expert id out of range, a wait that gave up) set bits that ``moe_error``
 reads.  The first call on a device creates its error word and may load device
 code: make it before any stream capture.
+
+Autograd does not follow these calls: whether or not an input requires a
+gradient, the outputs do not, and the ``*_backward`` calls are the gradient (as
+``examples/moe_layer.py`` chains them, or from a ``torch.autograd.Function``).
 """
 from __future__ import annotations
 
@@ -70,8 +74,11 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormaliz
     """Choose every token's ``topk`` experts and weigh them.
 
     logits: bf16, fp16 or fp32 [T][E] or [W][T][E] (rows may be strided).
-    bias: fp32 [E], added to the logits for the choice alone.  An expert whose
-    logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
+    bias: fp32 [E], added to the logits, not to the scores, for the choice alone.
+    (Where a load-balancing bias belongs to the score, as in sigmoid(x) + bias,
+    ``route(torch.sigmoid(logits.float()), topk, bias=bias)`` chooses so; its
+    indices go into ``route_backward`` with the logits as any others do.)  An
+    expert whose logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
     [...][topk], as ``EpDispatchCombineOp.dispatch`` takes them; tokens
     t >= num_tokens[w] get weights 0 and indices -1."""
     if stream is not None:

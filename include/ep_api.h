@@ -435,7 +435,10 @@ typedef struct {
 
 /* Top-k routing.  The k experts with the largest x_e + bias_e (an fp32 add;
  * d_bias NULL: no bias) are chosen, in descending order, ties to the lowest
- * expert id.  The bias takes no part in the weights:
+ * expert id.  The bias takes no part in the weights.  It is one of the logits:
+ * balancing without a loss, as published, adds its bias to the score, which is
+ * another choice wherever scores differ by less than their biases; pass the
+ * scores as d_logits for that one.
  *   softmax:  w_j = scale * exp(x_j) / sum exp(x), the sum over the chosen
  *             experts (renormalize) or over all
  *   sigmoid:  w_j = scale * v_j, v_j = 1 / (1 + exp(-x_j)), divided by the sum
@@ -454,8 +457,8 @@ ep_status_t ep_route(const ep_route_desc_t *d, const void *d_logits,
  *   d_loss[1] = sum_e (counts_e * E / (k n)) * probs_e
  *   d_loss[2] = (1/n) sum of (log sum exp x)^2   (0 for a token that sees no
  *               open expert)
- *   d_loss[0] = balance_coef * d_loss[1] + z_coef * d_loss[2]   (z_coef 0: without the
- *               second term, whatever d_loss[2] is)
+ *   d_loss[0] = balance_coef * d_loss[1] + z_coef * d_loss[2], with z_coef 0
+ *               without the second term, whatever d_loss[2] is
  * All 0 when n = 0.  Sums are fp32, in an order that the sizes alone fix.
  * d_idx [W][T][k]; d_loss [3], d_counts [E] int32, d_probs [E] fp32.
  * d_workspace: ep_balance_loss_workspace bytes, 16-byte aligned, any

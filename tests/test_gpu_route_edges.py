@@ -182,3 +182,21 @@ def test_defaults_of_the_losses_agree():
     parts = ep.route_backward(gw, x, idx) + ep.balance_loss_backward(gl, x, counts, 4)
     near(both, parts.cpu().double(), 4 * float(gw.abs().max()) + 24)
     assert (both - ep.route_backward(gw, x, idx)).abs().max() > 1e-4
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_choice_by_score_plus_bias(dtype):
+    """Scores in place of logits choose by score + bias; the gradient takes those indices."""
+    W, T, E, k = 2, 50, 96, 6
+    x = draw_logits(W, T, E, dtype, seed=12).cuda()
+    bias = (torch.randn(E, generator=torch.Generator().manual_seed(2)) * 0.1).cuda()
+    s = torch.sigmoid(x.float())
+    _, idx = ep.route(s, k, bias=bias)
+    want = torch.sort(s.cpu() + bias.cpu(), dim=-1, descending=True, stable=True).indices[..., :k]
+    assert torch.equal(idx.cpu().long(), want)
+    assert not torch.equal(ep.route(x, k, bias=bias)[1], idx)
+    gw = torch.randn((W, T, k)).cuda()
+    xs = clean(x.cpu()).requires_grad_(True)
+    grad, = torch.autograd.grad((weights_of(xs, want, "sigmoid", True, 2.5) * gw.cpu()).sum(), xs)
+    got = ep.route_backward(gw, x, idx, score="sigmoid", scale=2.5)
+    near(got, grad, 4 * 2.5 * float(gw.abs().max()), dtype)
