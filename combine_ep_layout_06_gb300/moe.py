@@ -76,9 +76,10 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormaliz
     logits: bf16, fp16 or fp32 [T][E] or [W][T][E] (rows may be strided).
     bias: fp32 [E], added to the logits, not to the scores, for the choice alone.
     (Where a load-balancing bias belongs to the score, as in sigmoid(x) + bias,
-    ``route(torch.sigmoid(logits.float()), topk, bias=bias)`` chooses so; its
-    indices go into ``route_backward`` with the logits as any others do.)  An
-    expert whose logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
+    ``route(torch.sigmoid(logits.float()), topk, bias=bias)`` chooses so, with
+    -inf put back for closed experts, whose score is 0 otherwise; its indices go
+    into ``route_backward`` with the logits as any others do.)  An expert whose
+    logit is -inf or NaN is closed.  Returns (weights fp32, indices int32)
     [...][topk], as ``EpDispatchCombineOp.dispatch`` takes them; tokens
     t >= num_tokens[w] get weights 0 and indices -1."""
     if stream is not None:

@@ -438,7 +438,7 @@ typedef struct {
  * expert id.  The bias takes no part in the weights.  It is one of the logits:
  * balancing without a loss, as published, adds its bias to the score, which is
  * another choice wherever scores differ by less than their biases; pass the
- * scores as d_logits for that one.
+ * scores as d_logits for that one, -inf for experts that are to stay closed.
  *   softmax:  w_j = scale * exp(x_j) / sum exp(x), the sum over the chosen
  *             experts (renormalize) or over all
  *   sigmoid:  w_j = scale * v_j, v_j = 1 / (1 + exp(-x_j)), divided by the sum
