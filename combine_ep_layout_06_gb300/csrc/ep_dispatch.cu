@@ -21,12 +21,10 @@
 //  - the bulk path (bf16): one thread drives the Tensor Memory Accelerator
 //    with 1-D cp.async.bulk row copies through a ring of shared-memory
 //    stages, one load per source row and one bulk store per destination.
-#include <cuda_fp8.h>
-
 #include <atomic>
 #include <mutex>
 
-#include "ep_device.cuh"
+#include "ep_fp8.cuh"
 
 namespace ep {
 namespace {
@@ -54,9 +52,6 @@ namespace {
 #endif
 #ifndef EP_DISPATCH_FP8_PREFETCH
 #define EP_DISPATCH_FP8_PREFETCH 1     // FP8: load the next element pair while quantising
-#endif
-#ifndef EP_FP8_RECIP_QUOT
-#define EP_FP8_RECIP_QUOT 1            // FP8: quotients by reciprocal + one FMA correction
 #endif
 #ifndef EP_DISPATCH_PDL
 #define EP_DISPATCH_PDL 1              // launch the copy programmatically after the layout
@@ -281,68 +276,6 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 &v, float f[8]) {
         f[2 * i] = __uint_as_float(w[i] << 16);
         f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-}
-
-// 4 values -> 4 E4M3 codes (byte i = element i) given the block scale.
-__device__ __forceinline__ uint32_t quant4(const float *f, float scale) {
-    uint32_t packed = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float a = f[2 * i] / scale;
-        const float b = f[2 * i + 1] / scale;
-        const __nv_fp8x2_storage_t q =
-            __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        packed |= (uint32_t)q << (16 * i);
-    }
-    return packed;
-}
-
-// fl32(x / scale) from r = RN(1 / scale) and one FMA correction of the
-// product (Markstein's division step: P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
-// Dev. 34(1), 1990).  For scale >= 2^-90 the residual x - q0*scale is exact
-// for every quotient large enough to give a nonzero code, and the E4M3 code
-// of the result equals that of the IEEE quotient for every bf16 x under every
-// bf16 block maximum (fp8_quotient_check_kernel below compares the codes over
-// all 1.07e9 pairs; ep_test_fp8_quotient_check runs it); smaller scales
-// divide.  The
-// residual is formed negated, q0*scale - x (the same magnitude: RN is
-// symmetric), and applied with -r, so that for x = +-0 the sums of zeros
-// keep the sign of x (the code of -0 is 0x80) with no sign fix-up.
-__device__ __forceinline__ float quot_recip(float x, float scale, float r) {
-    const float q0 = __fmul_rn(x, r);
-    const float nres = __fmaf_rn(q0, scale, -x);
-    return __fmaf_rn(nres, -r, q0);
-}
-
-// fl32(a / 448) for a block maximum a > 0 (a bf16 magnitude): the product
-// with RN(1/448) and the same one-FMA correction.  Equal to the IEEE
-// quotient for every finite non-negative bf16 a (proved on the host in exact
-// rational arithmetic, and compared on the device for every positive finite
-// a by fp8_quotient_check_kernel); a = inf gives inf.
-__device__ __forceinline__ float block_scale(float a) {
-#if EP_FP8_RECIP_QUOT
-    constexpr float kInv448 = 0x1.24924ap-9f;   // RN(1/448)
-    const float q0 = __fmul_rn(a, kInv448);
-    const float e = __fmaf_rn(-q0, 448.0f, a);
-    const float q = __fmaf_rn(e, kInv448, q0);
-    return a <= 0x1.fffffep127f ? q : a;
-#else
-    return a / 448.0f;
-#endif
-}
-
-__device__ __forceinline__ uint32_t quant4_recip(const float *f, float scale, float r) {
-    uint32_t packed = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float a = quot_recip(f[2 * i], scale, r);
-        const float b = quot_recip(f[2 * i + 1], scale, r);
-        const __nv_fp8x2_storage_t q =
-            __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        packed |= (uint32_t)q << (16 * i);
-    }
-    return packed;
 }
 
 // ------------------------------------------- quotient check (test harness)

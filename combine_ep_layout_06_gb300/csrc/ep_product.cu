@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "ep_rows.cuh"
 #include "ep_tensor.cuh"
 
 namespace ep {
@@ -45,24 +46,6 @@ constexpr int kTurnBytes = 32 * 32 * 4;            // a warp's transposing buffe
 constexpr size_t kSmemBytes = (size_t)kRingBytes + kEpilogueWarps * kTurnBytes + 1024;
 constexpr int kThreads = 64 + kEpilogueWarps * 32;
 
-struct Groups {
-    const int32_t *count, *offset;
-    int R, per, rows;
-};
-
-// First row and number of rows of group g within its segment.
-__device__ __forceinline__ void group_range(const Groups &gr, int g, int *first, int *n) {
-    if (!gr.count) {
-        *first = 0;
-        *n = gr.rows;
-        return;
-    }
-    const int o = gr.offset[g], c = gr.count[g];
-    const bool none = o < 0 || o >= gr.rows || c <= 0;
-    *first = none ? 0 : o;
-    *n = none ? 0 : min(c, gr.rows - o);
-}
-
 enum Mode { kForward, kGated, kGradX, kGradW, kNone };
 
 struct ProductParams {
@@ -74,17 +57,6 @@ struct ProductParams {
     ep_rows_t residual, out, pre;
     uint32_t *error;
 };
-
-template <typename T> __device__ __forceinline__ float f32(T v);
-template <> __device__ __forceinline__ float f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float f32(__half v) { return __half2float(v); }
-template <typename T> __device__ __forceinline__ T rounded(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 rounded(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half rounded(float v) { return __float2half_rn(v); }
-
-// Within a few units of the last place of fp32 (more of 2^-24 |v|): far below
-// the 16-bit rounding of every result it goes into.
-__device__ __forceinline__ float sigmoidf(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
 template <typename T> struct IsBf16 { static constexpr bool value = false; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
@@ -175,20 +147,6 @@ struct __align__(8) Barriers {
     Watch watch;
 };
 
-// Two floats as two 16-bit values.
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <typename T> __device__ __forceinline__ void store8(T *p, const float *v) {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-}
 template <typename T> __device__ __forceinline__ void add8(float *v, const uint4 &r) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
@@ -206,24 +164,6 @@ __device__ __forceinline__ void read8(float *v, float *turn, int c, int i) {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void activate8(int act, float *v) {
-    switch (act) {
-    case EP_ACT_RELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] <= 0.f ? 0.f : v[i];     // NaN stays (fmaxf would drop it)
-        break;
-    case EP_ACT_GELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
-        break;
-    case EP_ACT_SILU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sigmoidf(v[i]);
-        break;
-    default: break;
-    }
-}
-
 // A quarter of the accumulator's lanes belongs to two warps, which take turns
 // of 32 columns.
 constexpr int kColumnStep = 32 * (kEpilogueWarps / 4);
@@ -754,24 +694,6 @@ struct ActGradParams {
 
 constexpr int kActWarps = 8, kActCols = 256, kActRows = 4;
 
-// grad * act'(v).  A closed unit of ReLU takes nothing, an infinite gradient included.
-__device__ __forceinline__ float act_grad(int act, float grad, float v) {
-    if (act == EP_ACT_RELU) return v > 0.f ? grad : 0.f;
-    if (act == EP_ACT_GELU)      // Phi(v) + v phi(v), phi(v) = exp(-v^2/2) / sqrt(2 pi)
-        return grad * (0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * expf(-0.5f * v * v) * 0.39894228040143268f);
-    if (act == EP_ACT_SILU) {
-        const float s = sigmoidf(v);
-        return grad * (s * (1.0f + v * (1.0f - s)));
-    }
-    return grad;
-}
-
-template <typename T> __device__ __forceinline__ void unpack8(float *v, const uint4 &r) {
-    const T *e = reinterpret_cast<const T *>(&r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f32(e[i]);
-}
-
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradParams p) {
     __shared__ float sums[kActWarps][GATED ? 2 : 1][kActCols + 4];
@@ -868,14 +790,6 @@ int act_splits(const ep_product_desc_t &d) {
     return (int)(parts < 1 ? 1 : parts > 32 ? 32 : parts);
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Rows of `width` elements: 16-byte aligned, dense rows that do not overlap.
-bool valid_rows(const ep_rows_t &r, int64_t width, bool many) {
-    return r.ptr && aligned(r.ptr, 16) && r.row_stride >= width && r.row_stride % 8 == 0 &&
-           (!many || (r.rank_stride > 0 && r.rank_stride % 8 == 0));
-}
-
 int64_t wide_of(const ep_product_desc_t &d) {
     return d.activation == EP_ACT_SWIGLU ? 2 * (int64_t)d.out_features : d.out_features;
 }
@@ -899,85 +813,7 @@ Groups groups_of(const ep_product_desc_t &d) {
     return Groups{d.d_count, d.d_offset, d.ranks, d.groups, d.rows};
 }
 
-template <typename F> void with_type(int dtype, F f) {
-    if (dtype == EP_DT_BF16) f(__nv_bfloat16());
-    else f(__half());
-}
-
-ep_status_t launched() { return cudaGetLastError() == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP; }
-
-// ---- tensor maps
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static std::atomic<EncodeFn> cached{nullptr};
-    EncodeFn f = cached.load(std::memory_order_acquire);
-    if (!f) {
-        void *sym = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess || found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        f = reinterpret_cast<EncodeFn>(sym);
-        cached.store(f, std::memory_order_release);
-    }
-    return f;
-}
-
-bool encode(CUtensorMap *map, int dtype, void *ptr, int rank, const uint64_t *dims, const int64_t *strides,
-            const uint32_t *box) {
-    EncodeFn f = encode_fn();
-    if (!f) return false;
-    cuuint64_t d[5], s[5];
-    cuuint32_t b[5], one[5];
-    for (int i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        b[i] = box[i];
-        one[i] = 1;
-        if (i) s[i - 1] = (cuuint64_t)strides[i] * 2;
-    }
-    return f(map, dtype == EP_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-             (cuuint32_t)rank, ptr, d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [outer][rows][width] with boxes of 64 elements by `box_rows` rows.  Reads
-// past an edge give zeros.
-bool encode_rows(CUtensorMap *map, int dtype, const ep_rows_t &r, int64_t width, int64_t rows, int64_t outer,
-                 uint32_t box_rows) {
-    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)rows, (uint64_t)outer};
-    const int64_t strides[3] = {1, r.row_stride, outer > 1 ? r.rank_stride : r.row_stride};
-    const uint32_t box[3] = {64, box_rows, 1};
-    return encode(map, dtype, r.ptr, 3, dims, strides, box);
-}
-
-// Gated weights [G][2][N][K]: one box is 8 features of the gate, the same 8
-// of the up half, and so on for 64 features.
-bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, int64_t N, int64_t G) {
-    const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)G};
-    const int64_t strides[5] = {1, w.row_stride, N * w.row_stride, 8 * w.row_stride,
-                                G > 1 ? w.rank_stride : w.row_stride};
-    const uint32_t box[5] = {64, 8, 2, 8, 1};
-    return encode(map, dtype, w.ptr, 5, dims, strides, box);
-}
-
 // ---- launch
-
-constexpr int kMaxDevices = 64;
-
-int sm_count(int dev) {
-    static std::atomic<int> cached[kMaxDevices];
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (!n) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
 
 // Tiles of `columns` columns at most: every group's last tile may be a part.
 template <Mode MODE> int64_t most_tiles(const ProductParams &p, int columns) {

@@ -5,7 +5,7 @@
 
 #include <cuda.h>
 
-#include "ep_device.cuh"
+#include "ep_rows.cuh"
 
 namespace ep {
 
@@ -190,6 +190,65 @@ __device__ __forceinline__ void tmem_wait(uint32_t *r) {
 }
 __device__ __forceinline__ void fence_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ------------------------------------------------------ tensor maps (host)
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+inline EncodeFn encode_fn() {
+    static std::atomic<EncodeFn> cached{nullptr};
+    EncodeFn f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        void *sym = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeFn>(sym);
+        cached.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+inline bool encode(CUtensorMap *map, int dtype, void *ptr, int rank, const uint64_t *dims, const int64_t *strides,
+            const uint32_t *box) {
+    EncodeFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t d[5], s[5];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i) s[i - 1] = (cuuint64_t)strides[i] * 2;
+    }
+    return f(map, dtype == EP_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             (cuuint32_t)rank, ptr, d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [outer][rows][width] with boxes of 64 elements by `box_rows` rows.  Reads
+// past an edge give zeros.
+inline bool encode_rows(CUtensorMap *map, int dtype, const ep_rows_t &r, int64_t width, int64_t rows, int64_t outer,
+                 uint32_t box_rows) {
+    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)rows, (uint64_t)outer};
+    const int64_t strides[3] = {1, r.row_stride, outer > 1 ? r.rank_stride : r.row_stride};
+    const uint32_t box[3] = {64, box_rows, 1};
+    return encode(map, dtype, r.ptr, 3, dims, strides, box);
+}
+
+// Gated weights [G][2][N][K]: one box is 8 features of the gate, the same 8
+// of the up half, and so on for 64 features.
+inline bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, int64_t N, int64_t G) {
+    const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)G};
+    const int64_t strides[5] = {1, w.row_stride, N * w.row_stride, 8 * w.row_stride,
+                                G > 1 ? w.rank_stride : w.row_stride};
+    const uint32_t box[5] = {64, 8, 2, 8, 1};
+    return encode(map, dtype, w.ptr, 5, dims, strides, box);
 }
 
 }  // namespace ep
