@@ -34,6 +34,7 @@ EP_DEVERR_TIMEOUT = 0x4
 EP_DEVERR_COMBINE_MISMATCH = 0x8
 EP_DT_BF16, EP_DT_FP8_E4M3, EP_DT_FP32, EP_DT_FP16 = 0, 1, 2, 3
 EP_MAX_WORLD, EP_MAX_TOPK, EP_MAX_ROUTE_EXPERTS = 32, 32, 1024
+EP_MAX_NORM_WIDTH, EP_MAX_FEW_TOKENS = 32768, 64
 
 
 class EpConfigC(ctypes.Structure):
@@ -133,6 +134,49 @@ class EpProductDescC(ctypes.Structure):
     ]
 
 
+class EpNormDescC(ctypes.Structure):
+    _fields_ = [
+        ("ranks", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("x", EpRowsC),
+        ("weight", ctypes.c_void_p),
+    ]
+
+
+class EpCheckpointDescC(ctypes.Structure):
+    _fields_ = [
+        ("ranks", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("features", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("d_count", ctypes.c_void_p),
+        ("d_offset", ctypes.c_void_p),
+    ]
+
+
+class EpFewDescC(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int32),
+        ("experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("hidden", ctypes.c_int32),
+        ("inner", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("up", EpRowsC),
+        ("down", EpRowsC),
+        ("up_bias", ctypes.c_void_p),
+        ("down_bias", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -168,6 +212,14 @@ SIGNATURES = {
     "ep_expert_product": (_S, [_P, _P, _P, _P, _P, _P, _P]),
     "ep_expert_product_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "ep_expert_product_backward": (_S, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "ep_rms_norm": (_S, [_P, _P, _P, _P, _P, _P]),
+    "ep_rms_norm_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "ep_rms_norm_backward": (_S, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "ep_checkpoint_save": (_S, [_P, _P, _P, _P, _P]),
+    "ep_checkpoint_restore": (_S, [_P, _P, _P, _P, _P]),
+    "ep_expert_product_backward_checkpoint": (_S, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "ep_moe_few_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "ep_moe_few": (_S, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "ep_layout_noalloc": (_S, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P]),
 }
 

@@ -20,6 +20,11 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p) {
                  : "l"(p));
     return v;
 }
+__device__ __forceinline__ uint2 ld_stream8(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
 // The same, not allocated in L1: faster for a gather of few tokens
 // (2048-token decode combine: 45.5 against 49.6 us), where the kernel is
 // latency-bound.

@@ -2,6 +2,7 @@
 // the codes of fl32(x / scale), rounded to nearest even and saturated.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "ep_device.cuh"
@@ -72,6 +73,41 @@ __device__ __forceinline__ uint32_t quant4_recip(const float *f, float scale, fl
         packed |= (uint32_t)q << (16 * i);
     }
     return packed;
+}
+
+// A block of 128 values over 16 neighbouring lanes, 8 values a lane: this lane's
+// codes (byte i = value i) and the block's scale.  By whole warps.  The maximum is
+// taken of the magnitudes' bits, above which infinities and NaN stand: such a
+// block is NaN as a whole.
+__device__ __forceinline__ uint2 block_codes(const float *f, float *scale) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (a >= 0x7f800000u) {
+        *scale = __uint_as_float(0x7fffffffu);
+        return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    }
+    const float s = __fdiv_rn(__uint_as_float(a), 448.0f);
+    *scale = s;
+    if (s == 0.f) return make_uint2(0u, 0u);
+    if (s >= 0x1p-90f) {
+        const float r = __frcp_rn(s);
+        return make_uint2(quant4_recip(f, s, r), quant4_recip(f + 4, s, r));
+    }
+    return make_uint2(quant4(f, s), quant4(f + 4, s));
+}
+// 8 codes -> 8 values, code * scale.
+__device__ __forceinline__ void block_values(float *v, const uint2 &q, float scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1)));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        v[2 * i] = f.x * scale;
+        v[2 * i + 1] = f.y * scale;
+    }
 }
 
 }  // namespace ep

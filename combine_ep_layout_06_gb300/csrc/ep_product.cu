@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "ep_fp8.cuh"
 #include "ep_rows.cuh"
 #include "ep_tensor.cuh"
 
@@ -687,6 +688,7 @@ struct ActGradParams {
     Groups gr;
     int N, act, splits;
     ep_rows_t grad, pre, d;
+    ep_rows_t scales;       // ptr: pre is codes with these block scales
     float *part;            // [splits][G][wide] column sums, or null
     void *grad_bias;        // [G][wide], with one part a group
     bool write;
@@ -694,7 +696,26 @@ struct ActGradParams {
 
 constexpr int kActWarps = 8, kActCols = 256, kActRows = 4;
 
-template <typename T, bool GATED>
+// Pre-activations as they were kept, 8 of them: 16-bit values, or codes and
+// their block's scale.
+template <typename T, bool EIGHT> struct Kept {
+    uint4 q;
+    __device__ __forceinline__ void load(const ep_rows_t &pre, const ep_rows_t &, int seg, int64_t row, int64_t c) {
+        q = ld_stream16(static_cast<const T *>(pre.ptr) + seg * pre.rank_stride + row * pre.row_stride + c);
+    }
+    __device__ __forceinline__ void values(float *v) const { unpack8<T>(v, q); }
+};
+template <typename T> struct Kept<T, true> {
+    uint2 q;
+    float scale;
+    __device__ __forceinline__ void load(const ep_rows_t &pre, const ep_rows_t &scales, int seg, int64_t row, int64_t c) {
+        q = ld_stream8(static_cast<const uint8_t *>(pre.ptr) + seg * pre.rank_stride + row * pre.row_stride + c);
+        scale = __ldg(static_cast<const float *>(scales.ptr) + seg * scales.rank_stride + row * scales.row_stride + c / 128);
+    }
+    __device__ __forceinline__ void values(float *v) const { block_values(v, q, scale); }
+};
+
+template <typename T, bool GATED, bool EIGHT>
 __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradParams p) {
     __shared__ float sums[kActWarps][GATED ? 2 : 1][kActCols + 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -707,19 +728,19 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
     const int r1 = first + min(rows, (split + 1) * per);
     grid_dependents_may_launch();
     const T *grad = static_cast<const T *>(p.grad.ptr) + seg * p.grad.rank_stride + c;
-    const T *pre = static_cast<const T *>(p.pre.ptr) + seg * p.pre.rank_stride + c;
     T *d = static_cast<T *>(p.d.ptr) + seg * p.d.rank_stride + c;
     float s0[8] = {}, s1[8] = {};
     const bool reads_pre = p.act != EP_ACT_NONE;
     for (int64_t r = first + split * per + warp; live && r < r1; r += kActWarps * kActRows) {
-        uint4 gv[kActRows], v0[kActRows], v1[kActRows];
+        uint4 gv[kActRows];
+        Kept<T, EIGHT> v0[kActRows], v1[kActRows];
 #pragma unroll
         for (int u = 0; u < kActRows; ++u) {
             const int64_t i = r + u * kActWarps;
             if (i >= r1) continue;
             gv[u] = ld_stream16(grad + i * p.grad.row_stride);
-            if (reads_pre) v0[u] = ld_stream16(pre + i * p.pre.row_stride);
-            if (GATED) v1[u] = ld_stream16(pre + i * p.pre.row_stride + p.N);
+            if (reads_pre) v0[u].load(p.pre, p.scales, seg, i, c);
+            if (GATED) v1[u].load(p.pre, p.scales, seg, i, (int64_t)c + p.N);
         }
 #pragma unroll
         for (int u = 0; u < kActRows; ++u) {
@@ -729,8 +750,8 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
             unpack8<T>(y, gv[u]);
             if (GATED) {
                 float up[8];
-                unpack8<T>(v, v0[u]);
-                unpack8<T>(up, v1[u]);
+                v0[u].values(v);
+                v1[u].values(up);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float s = sigmoidf(v[j]);
@@ -739,7 +760,7 @@ __global__ void __launch_bounds__(kActWarps * 32) act_grad_kernel(const ActGradP
                     s1[j] += d1[j];
                 }
             } else if (reads_pre) {
-                unpack8<T>(v, v0[u]);
+                v0[u].values(v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d0[j] = act_grad(p.act, y[j], v[j]);
             } else {
@@ -882,6 +903,79 @@ size_t part_bytes(const ep_product_desc_t &d) {
     return align256((size_t)act_splits(d) * d.ranks * d.groups * (size_t)wide_of(d) * 4);
 }
 
+// Both gradients; scales: null, or those of pre's codes.
+ep_status_t backward(const ep_product_desc_t *d, const ep_rows_t *grad, const ep_rows_t *pre, const ep_rows_t *scales,
+                     const ep_rows_t *grad_x, void *d_grad_w, void *d_grad_bias, void *d_workspace,
+                     size_t workspace_bytes, uint32_t *d_error, void *stream) {
+    if (!valid(d) || !grad || !pre || !grad_x || !aligned(d_grad_w, 16) || !aligned(d_grad_bias, 16) ||
+        !aligned(d_workspace, 256) || !aligned(d_error, 4))
+        return EP_ERR_INVALID_ARGS;
+    const bool many = d->ranks > 1, act = d->activation != EP_ACT_NONE;
+    const int64_t wide = wide_of(*d);
+    const size_t need = rounded_d_bytes(*d) + part_bytes(*d);
+    if (workspace_bytes < need || (need && !d_workspace)) return EP_ERR_INVALID_ARGS;
+    if (d->rows > 0 && (!valid_rows(*grad, d->out_features, many) ||
+                        (act && !(scales ? valid_codes(*pre, *scales, wide, many) : valid_rows(*pre, wide, many))) ||
+                        (grad_x->ptr && !valid_rows(*grad_x, d->in_features, many))))
+        return EP_ERR_INVALID_ARGS;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Groups gr = groups_of(*d);
+    const ep_rows_t dd = act ? ep_rows_t{d_workspace, d->rows * wide, wide} : *grad;
+    const int splits = act_splits(*d);
+    const int64_t G = (int64_t)d->ranks * d->groups;
+    float *part = d_grad_bias && splits > 1
+                      ? reinterpret_cast<float *>(static_cast<char *>(d_workspace) + rounded_d_bytes(*d)) : nullptr;
+    if (act || d_grad_bias) {
+        const ActGradParams q = {gr, d->out_features, d->activation, splits, *grad, *pre, dd,
+                                 scales ? *scales : ep_rows_t{}, part,
+                                 part ? nullptr : d_grad_bias, act};
+        const dim3 grid((d->out_features + kActCols - 1) / kActCols, (unsigned)G, splits);
+        with_type(d->dtype, [&](auto type) {
+            using T = decltype(type);
+            const bool gated = d->activation == EP_ACT_SWIGLU;
+            if (gated && scales) act_grad_kernel<T, true, true><<<grid, kActWarps * 32, 0, st>>>(q);
+            else if (gated) act_grad_kernel<T, true, false><<<grid, kActWarps * 32, 0, st>>>(q);
+            else if (scales) act_grad_kernel<T, false, true><<<grid, kActWarps * 32, 0, st>>>(q);
+            else act_grad_kernel<T, false, false><<<grid, kActWarps * 32, 0, st>>>(q);
+        });
+    }
+    const bool has_x = grad_x->ptr && d->rows > 0, has_w = d_grad_w && d->rows > 0;
+    if (has_x || has_w) {
+        Work x = {}, w = {};
+        x.p.gr = gr;
+        x.p.M = d->in_features;
+        x.p.N = -1;
+        x.p.K = (int)wide;
+        x.p.out = *grad_x;
+        w.p.gr = gr;
+        w.p.M = d->in_features;
+        w.p.N = (int)wide;
+        w.p.K = -1;
+        w.p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
+        x.p.error = w.p.error = d_error;
+        if ((has_x && (!encode_rows(&x.a, d->dtype, d->weight, d->in_features, wide, G, kSliceK) ||
+                       !encode_rows(&x.b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
+                       !encode_rows(&x.b32, d->dtype, dd, wide, d->rows, d->ranks, 32))) ||
+            (has_w && (!encode_rows(&w.a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kSliceK) ||
+                       !encode_rows(&w.b, d->dtype, dd, wide, d->rows, d->ranks, kSliceK))))
+            return EP_ERR_GPU_OP;
+        const ep_status_t s = d->dtype == EP_DT_BF16 ? launch_gradients<__nv_bfloat16>(x, w, has_x, has_w, st)
+                                                     : launch_gradients<__half>(x, w, has_x, has_w, st);
+        if (s != EP_SUCCESS) return s;
+    } else if (d_grad_w) {
+        if (cudaMemsetAsync(d_grad_w, 0, (size_t)G * wide * d->in_features * 2, st) != cudaSuccess)
+            return EP_ERR_GPU_OP;
+    }
+    if (part)
+        with_type(d->dtype, [&](auto type) {
+            using T = decltype(type);
+            const int64_t n = G * wide;
+            sum_parts_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, splits, n,
+                                                                             static_cast<T *>(d_grad_bias));
+        });
+    return launched();
+}
+
 }  // namespace
 }  // namespace ep
 
@@ -936,70 +1030,17 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d, const ep_rows
                                        void *d_grad_bias, void *d_workspace, size_t workspace_bytes,
                                        uint32_t *d_error, void *stream) {
     EP_RANGE("ep_expert_product_backward");
-    if (!valid(d) || !grad || !pre || !grad_x || !aligned(d_grad_w, 16) || !aligned(d_grad_bias, 16) ||
-        !aligned(d_workspace, 256) || !aligned(d_error, 4))
-        return EP_ERR_INVALID_ARGS;
-    const bool many = d->ranks > 1, act = d->activation != EP_ACT_NONE;
-    const int64_t wide = wide_of(*d);
-    size_t need = 0;
-    ep_expert_product_workspace(d, &need);
-    if (workspace_bytes < need || (need && !d_workspace)) return EP_ERR_INVALID_ARGS;
-    if (d->rows > 0 && (!valid_rows(*grad, d->out_features, many) ||
-                        (act && !valid_rows(*pre, wide, many)) ||
-                        (grad_x->ptr && !valid_rows(*grad_x, d->in_features, many))))
-        return EP_ERR_INVALID_ARGS;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Groups gr = groups_of(*d);
-    const ep_rows_t dd = act ? ep_rows_t{d_workspace, d->rows * wide, wide} : *grad;
-    const int splits = act_splits(*d);
-    const int64_t G = (int64_t)d->ranks * d->groups;
-    float *part = d_grad_bias && splits > 1
-                      ? reinterpret_cast<float *>(static_cast<char *>(d_workspace) + rounded_d_bytes(*d)) : nullptr;
-    if (act || d_grad_bias) {
-        const ActGradParams q = {gr, d->out_features, d->activation, splits, *grad, *pre, dd, part,
-                                 part ? nullptr : d_grad_bias, act};
-        const dim3 grid((d->out_features + kActCols - 1) / kActCols, (unsigned)G, splits);
-        with_type(d->dtype, [&](auto type) {
-            using T = decltype(type);
-            if (d->activation == EP_ACT_SWIGLU) act_grad_kernel<T, true><<<grid, kActWarps * 32, 0, st>>>(q);
-            else act_grad_kernel<T, false><<<grid, kActWarps * 32, 0, st>>>(q);
-        });
-    }
-    const bool has_x = grad_x->ptr && d->rows > 0, has_w = d_grad_w && d->rows > 0;
-    if (has_x || has_w) {
-        Work x = {}, w = {};
-        x.p.gr = gr;
-        x.p.M = d->in_features;
-        x.p.N = -1;
-        x.p.K = (int)wide;
-        x.p.out = *grad_x;
-        w.p.gr = gr;
-        w.p.M = d->in_features;
-        w.p.N = (int)wide;
-        w.p.K = -1;
-        w.p.out = ep_rows_t{d_grad_w, wide * d->in_features, d->in_features};
-        x.p.error = w.p.error = d_error;
-        if ((has_x && (!encode_rows(&x.a, d->dtype, d->weight, d->in_features, wide, G, kSliceK) ||
-                       !encode_rows(&x.b, d->dtype, dd, wide, d->rows, d->ranks, kTileN / 2) ||
-                       !encode_rows(&x.b32, d->dtype, dd, wide, d->rows, d->ranks, 32))) ||
-            (has_w && (!encode_rows(&w.a, d->dtype, d->x, d->in_features, d->rows, d->ranks, kSliceK) ||
-                       !encode_rows(&w.b, d->dtype, dd, wide, d->rows, d->ranks, kSliceK))))
-            return EP_ERR_GPU_OP;
-        const ep_status_t s = d->dtype == EP_DT_BF16 ? launch_gradients<__nv_bfloat16>(x, w, has_x, has_w, st)
-                                                     : launch_gradients<__half>(x, w, has_x, has_w, st);
-        if (s != EP_SUCCESS) return s;
-    } else if (d_grad_w) {
-        if (cudaMemsetAsync(d_grad_w, 0, (size_t)G * wide * d->in_features * 2, st) != cudaSuccess)
-            return EP_ERR_GPU_OP;
-    }
-    if (part)
-        with_type(d->dtype, [&](auto type) {
-            using T = decltype(type);
-            const int64_t n = G * wide;
-            sum_parts_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, splits, n,
-                                                                             static_cast<T *>(d_grad_bias));
-        });
-    return launched();
+    return backward(d, grad, pre, nullptr, grad_x, d_grad_w, d_grad_bias, d_workspace, workspace_bytes, d_error, stream);
+}
+
+ep_status_t ep_expert_product_backward_checkpoint(const ep_product_desc_t *d, const ep_rows_t *grad,
+                                                  const ep_rows_t *codes, const ep_rows_t *scales,
+                                                  const ep_rows_t *grad_x, void *d_grad_w, void *d_grad_bias,
+                                                  void *d_workspace, size_t workspace_bytes, uint32_t *d_error,
+                                                  void *stream) {
+    EP_RANGE("ep_expert_product_backward_checkpoint");
+    if (!scales) return EP_ERR_INVALID_ARGS;
+    return backward(d, grad, codes, scales, grad_x, d_grad_w, d_grad_bias, d_workspace, workspace_bytes, d_error, stream);
 }
 
 }  // extern "C"

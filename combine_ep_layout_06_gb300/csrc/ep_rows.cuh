@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ep_device.cuh"
 
@@ -36,9 +37,11 @@ __device__ __forceinline__ void group_range(const Groups &gr, int g, int *first,
 template <typename T> __device__ __forceinline__ float f32(T v);
 template <> __device__ __forceinline__ float f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <> __device__ __forceinline__ float f32(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float f32(float v) { return v; }
 template <typename T> __device__ __forceinline__ T rounded(float v);
 template <> __device__ __forceinline__ __nv_bfloat16 rounded(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half rounded(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ float rounded(float v) { return v; }
 
 // Two floats as two 16-bit values.
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -104,6 +107,13 @@ inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_
 inline bool valid_rows(const ep_rows_t &r, int64_t width, bool many) {
     return r.ptr && aligned(r.ptr, 16) && r.row_stride >= width && r.row_stride % 8 == 0 &&
            (!many || (r.rank_stride > 0 && r.rank_stride % 8 == 0));
+}
+
+// 8-bit rows of `width` codes, 8-byte aligned, and their blocks' scales.
+inline bool valid_codes(const ep_rows_t &codes, const ep_rows_t &scales, int64_t width, bool many) {
+    return codes.ptr && aligned(codes.ptr, 8) && codes.row_stride >= width && codes.row_stride % 8 == 0 &&
+           (!many || (codes.rank_stride > 0 && codes.rank_stride % 8 == 0)) && scales.ptr && aligned(scales.ptr, 4) &&
+           scales.row_stride >= (width + 127) / 128 && (!many || scales.rank_stride > 0);
 }
 
 template <typename F> void with_type(int dtype, F f) {

@@ -1,4 +1,4 @@
-// Python binding of the routing, loss and product calls: checks of torch
+// Python binding of the calls around dispatch and combine: checks of torch
 // tensors, output allocation on the current stream, and the C entry points of
 // include/ep_api.h.  Marshalling only.  A binding in C++ because a one-token
 // call is a few microseconds on the GPU: through ctypes the host took 10 to
@@ -419,7 +419,31 @@ PyObject *expert_product(PyObject *const *a) {
     return both;
 }
 
-// (grad, x, weight, count, offset, pre, activation, bias_grad)
+// Rows of codes and their blocks' scales, [...][width] and [...][ceil(width / 128)].
+void codes_of(const Tensor &codes, const Tensor &scales, c10::DeviceIndex index, at::IntArrayRef shape, ep_rows_t *q,
+              ep_rows_t *s) {
+    on_device(codes, index, "codes");
+    on_device(scales, index, "scales");
+    const size_t n = shape.size();
+    std::vector<int64_t> blocks(shape.begin(), shape.end());
+    blocks[n - 1] = (blocks[n - 1] + 127) / 128;
+    if ((codes.scalar_type() != at::kFloat8_e4m3fn && codes.scalar_type() != at::kByte) || codes.sizes() != shape)
+        refuse("codes must be float8_e4m3fn or uint8 " + shape_text(shape));
+    if (scales.scalar_type() != at::kFloat || scales.sizes() != at::IntArrayRef(blocks))
+        refuse("scales must be fp32 " + shape_text(blocks));
+    if (!codes.numel()) return;
+    const bool many = n == 3 && shape[0] > 1, rows = shape[n - 2] > 1;
+    const auto cs = codes.strides(), ss = scales.strides();
+    *q = ep_rows_t{codes.data_ptr(), many ? cs[0] : 0, rows ? cs[n - 2] : (shape[n - 1] + 7) / 8 * 8};
+    *s = ep_rows_t{scales.data_ptr(), many ? ss[0] : 0, rows ? ss[n - 2] : blocks[n - 1]};
+    if (cs[n - 1] != 1 || q->row_stride < shape[n - 1] || (q->row_stride | q->rank_stride) % 8 != 0 ||
+        (many && q->rank_stride <= 0) || reinterpret_cast<uintptr_t>(q->ptr) % 8 != 0)
+        refuse("codes: contiguous rows, 8-byte aligned, with strides of a multiple of 8");
+    if ((ss[n - 1] != 1 && blocks[n - 1] > 1) || s->row_stride < blocks[n - 1] || (many && s->rank_stride <= 0))
+        refuse("scales: contiguous rows that do not overlap");
+}
+
+// (grad, x, weight, count, offset, pre, activation, bias_grad, pre_scales)
 PyObject *expert_product_backward(PyObject *const *a) {
     const Tensor &grad = tensor(a[0], "grad"), &x = tensor(a[1], "x"), &weight = tensor(a[2], "weight");
     Here here(x, "x");
@@ -427,8 +451,11 @@ PyObject *expert_product_backward(PyObject *const *a) {
     const auto type = x.scalar_type();
     const Tensor *saved = optional(a[5], "pre");
     if (!saved && p.d.activation != EP_ACT_NONE) refuse("the gradient of this activation needs pre");
-    ep_rows_t g = rows_as(grad, here.index, type, p.y, "grad"), pre{};
-    if (saved) pre = rows_as(*saved, here.index, type, p.pre, "pre");
+    const Tensor *saved_scales = optional(a[8], "pre_scales");
+    if (saved_scales && !saved) refuse("pre_scales needs pre's codes");
+    ep_rows_t g = rows_as(grad, here.index, type, p.y, "grad"), pre{}, scales{};
+    if (saved_scales) codes_of(*saved, *saved_scales, here.index, p.pre, &pre, &scales);
+    else if (saved) pre = rows_as(*saved, here.index, type, p.pre, "pre");
     const int64_t K = p.d.in_features;
     Tensor dx = here.empty(x.sizes(), type), dw = here.empty({p.G, p.wide, K}, type), db;
     if (truth(a[7])) db = here.empty({p.G, p.wide}, type);
@@ -436,10 +463,279 @@ PyObject *expert_product_backward(PyObject *const *a) {
     check(ep_expert_product_workspace(&p.d, &need), "ep_expert_product_workspace");
     Tensor scratch = here.empty({(int64_t)need}, at::kByte);
     const ep_rows_t gx = rows_new(dx, p.rows, K);
-    check(ep_expert_product_backward(&p.d, &g, &pre, &gx, dw.data_ptr(), db.defined() ? db.data_ptr() : nullptr,
-                                     scratch.data_ptr(), need, error_ptr(here.index), here.stream()),
-          "ep_expert_product_backward");
+    void *bias = db.defined() ? db.data_ptr() : nullptr;
+    if (saved_scales)
+        check(ep_expert_product_backward_checkpoint(&p.d, &g, &pre, &scales, &gx, dw.data_ptr(), bias, scratch.data_ptr(),
+                                                    need, error_ptr(here.index), here.stream()),
+              "ep_expert_product_backward_checkpoint");
+    else
+        check(ep_expert_product_backward(&p.d, &g, &pre, &gx, dw.data_ptr(), bias, scratch.data_ptr(), need,
+                                         error_ptr(here.index), here.stream()),
+              "ep_expert_product_backward");
     return pack(dx, dw, db);
+}
+
+// ----------------------------------------------------------- checkpoints
+
+ep_checkpoint_desc_t checkpoint_desc(const Here &here, at::IntArrayRef shape, const Tensor *count, const Tensor *offset,
+                                     int dtype, int act) {
+    ep_checkpoint_desc_t d{};
+    if (shape.size() != 2 && shape.size() != 3) refuse("rows must be [rows][features] or [R][rows][features]");
+    const size_t n = shape.size();
+    const int64_t R = n == 3 ? shape[0] : 1, rows = shape[n - 2], F = shape[n - 1];
+    if (F < 8 || F % 8 || F > 1 << 24) refuse("features must be a multiple of 8");
+    if (!count != !offset) refuse("count and offset come together");
+    int64_t G = R;
+    if (count) {
+        G = count->numel();
+        for (const Tensor *t : {count, offset}) {
+            on_device(*t, here.index, "count and offset");
+            if (t->scalar_type() != at::kInt || t->numel() != G || !t->is_contiguous())
+                refuse("count and offset must be contiguous int32 of the same number of groups");
+        }
+        d.d_count = static_cast<const int32_t *>(count->data_ptr());
+        d.d_offset = static_cast<const int32_t *>(offset->data_ptr());
+    }
+    if (R < 1 || G < 1 || G % R) refuse(std::to_string(G) + " groups do not divide over " + std::to_string(R) + " ranks");
+    if (rows > (int64_t)1 << 30 || G > 65535) refuse("too many rows or groups");
+    d.ranks = (int32_t)R;
+    d.groups = (int32_t)(G / R);
+    d.rows = (int32_t)rows;
+    d.features = (int32_t)F;
+    d.dtype = dtype;
+    d.activation = act;
+    return d;
+}
+
+// (x, count, offset)
+PyObject *checkpoint(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x");
+    Here here(x, "x");
+    if (x.scalar_type() != at::kBFloat16 && x.scalar_type() != at::kHalf) refuse("x must be bf16 or fp16");
+    const ep_checkpoint_desc_t d =
+        checkpoint_desc(here, x.sizes(), optional(a[1], "count"), optional(a[2], "offset"),
+                        x.scalar_type() == at::kBFloat16 ? EP_DT_BF16 : EP_DT_FP16, EP_ACT_NONE);
+    std::vector<int64_t> blocks(x.sizes().begin(), x.sizes().end());
+    const int64_t nb = ((int64_t)d.features + 127) / 128;
+    blocks.back() = nb;
+    Tensor codes = here.empty(x.sizes(), at::kFloat8_e4m3fn), scales = here.empty(blocks, at::kFloat);
+    if (d.rows) {
+        const ep_rows_t from = rows_of(x, "x"), q = rows_new(codes, d.rows, d.features), s = rows_new(scales, d.rows, nb);
+        check(ep_checkpoint_save(&d, &from, &q, &s, here.stream()), "ep_checkpoint_save");
+    }
+    return pack(codes, scales);
+}
+
+// (codes, scales, count, offset, activation, dtype code)
+PyObject *checkpoint_restore(PyObject *const *a) {
+    const Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
+    Here here(codes, "codes");
+    const int act = choice(a[4], "activation", {"none", "relu", "gelu", "silu", "swiglu"});
+    const int64_t dtype = whole(a[5]);
+    const ep_checkpoint_desc_t d = checkpoint_desc(here, codes.sizes(), optional(a[2], "count"), optional(a[3], "offset"),
+                                                   (int)dtype, act);
+    if (act == EP_ACT_SWIGLU && d.features % 16) refuse("swiglu needs a multiple of 16 features");
+    ep_rows_t q{}, s{};
+    codes_of(codes, scales, here.index, codes.sizes(), &q, &s);
+    std::vector<int64_t> shape(codes.sizes().begin(), codes.sizes().end());
+    if (act == EP_ACT_SWIGLU) shape.back() /= 2;
+    Tensor y = here.empty(shape, dtype == EP_DT_BF16 ? at::kBFloat16 : at::kHalf);
+    if (d.rows) {
+        const ep_rows_t to = rows_new(y, d.rows, shape.back());
+        check(ep_checkpoint_restore(&d, &q, &s, &to, here.stream()), "ep_checkpoint_restore");
+    }
+    return THPVariable_Wrap(y);
+}
+
+// ------------------------------------------------------------------ norm
+
+// Rows of a norm: [H], [rows][H] or [R][rows][H] with any strides, or dense of
+// any shape.
+struct Norm {
+    ep_norm_desc_t d{};
+    bool flat;                           // one rank of dense rows
+};
+ep_rows_t norm_rows(const Norm &n, const Tensor &t, const char *name) {
+    const int64_t H = n.d.width;
+    if (n.flat) {
+        if (!t.is_contiguous()) refuse(std::string(name) + ": rows of such a shape must be dense");
+        return ep_rows_t{t.data_ptr(), 0, H};
+    }
+    const auto shape = t.sizes(), strides = t.strides();
+    const size_t k = shape.size();
+    const bool many = n.d.ranks > 1;
+    const ep_rows_t r{t.data_ptr(), many ? strides[0] : 0, n.d.rows > 1 ? strides[k - 2] : H};
+    if ((strides[k - 1] != 1 && H > 1) || r.row_stride < H || (many && r.rank_stride <= 0))
+        refuse(std::string(name) + ": rows must be contiguous and must not overlap");
+    return r;
+}
+ep_rows_t norm_rows_as(const Norm &n, const Tensor &t, const Tensor &like, c10::DeviceIndex index, const char *name) {
+    on_device(t, index, name);
+    if (t.scalar_type() != like.scalar_type() || t.sizes() != like.sizes())
+        refuse(std::string(name) + " must be " + c10::toString(like.scalar_type()) + " " + shape_text(like.sizes()));
+    return t.numel() ? norm_rows(n, t, name) : ep_rows_t{nullptr, 0, 0};
+}
+Norm norm_of(const Here &here, const Tensor &x, const char *name, const Tensor &weight, double eps) {
+    Norm n;
+    const auto shape = x.sizes();
+    const auto type = x.scalar_type(), wt = weight.scalar_type();
+    if (shape.empty() || (type != at::kBFloat16 && type != at::kHalf && type != at::kFloat))
+        refuse(std::string(name) + " must be bf16, fp16 or fp32 [...][H]");
+    const int64_t H = shape.back();
+    if (H < 1 || H > EP_MAX_NORM_WIDTH) refuse("rows of 1 to " + std::to_string(EP_MAX_NORM_WIDTH) + " values, not " + std::to_string(H));
+    on_device(weight, here.index, "weight");
+    if ((wt != type && wt != at::kFloat) || weight.dim() != 1 || weight.size(0) != H || !weight.is_contiguous())
+        refuse("weight must be contiguous [" + std::to_string(H) + "] of the rows' type or fp32");
+    if (!(eps >= 0.0) || eps > 3e38) refuse("eps must be 0 or more");
+    const int64_t rows = x.numel() / H;
+    if (rows > (int64_t)1 << 30) refuse("too many rows");
+    n.flat = shape.size() > 3 || (shape.size() == 3 && shape[0] > 65535) || shape.size() == 1;
+    const bool many = !n.flat && shape.size() == 3 && rows;
+    n.d.ranks = many ? (int32_t)shape[0] : 1;
+    n.d.rows = (int32_t)(rows / n.d.ranks);
+    n.d.width = (int32_t)H;
+    n.d.dtype = type == at::kBFloat16 ? EP_DT_BF16 : type == at::kHalf ? EP_DT_FP16 : EP_DT_FP32;
+    n.d.weight_dtype = wt == type ? n.d.dtype : EP_DT_FP32;
+    n.d.eps = (float)eps;
+    n.d.weight = weight.data_ptr();
+    if (rows) n.d.x = norm_rows(n, x, name);
+    return n;
+}
+
+// (x, weight, residual, eps, quantize)
+PyObject *rms_norm(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight");
+    Here here(x, "x");
+    const Norm n = norm_of(here, x, "x", weight, number(a[3]));
+    const Tensor *residual = optional(a[2], "residual");
+    const bool eight = truth(a[4]);
+    const int64_t H = n.d.width;
+    if (eight && H % 128) refuse("8-bit rows need a multiple of 128 values, not " + std::to_string(H));
+    ep_rows_t res{}, total{}, scales{};
+    Tensor sum, sc, y = here.empty(x.sizes(), eight ? at::kFloat8_e4m3fn : x.scalar_type());
+    const ep_rows_t to{y.data_ptr(), n.d.rows * H, H};
+    if (residual) {
+        res = norm_rows_as(n, *residual, x, here.index, "residual");
+        sum = here.empty(x.sizes(), x.scalar_type());
+        total = ep_rows_t{sum.data_ptr(), n.d.rows * H, H};
+    }
+    if (eight) {
+        std::vector<int64_t> blocks(x.sizes().begin(), x.sizes().end());
+        blocks.back() = H / 128;
+        sc = here.empty(blocks, at::kFloat);
+        scales = ep_rows_t{sc.data_ptr(), n.d.rows * (H / 128), H / 128};
+    }
+    if (n.d.rows) check(ep_rms_norm(&n.d, &res, &total, &to, &scales, here.stream()), "ep_rms_norm");
+    if (eight && residual) return pack(y, sc, sum);
+    if (eight) return pack(y, sc);
+    if (residual) return pack(y, sum);
+    return THPVariable_Wrap(y);
+}
+
+// (grad, total, weight, grad_total, eps)
+PyObject *rms_norm_backward(PyObject *const *a) {
+    const Tensor &grad = tensor(a[0], "grad"), &total = tensor(a[1], "total"), &weight = tensor(a[2], "weight");
+    Here here(total, "total");
+    const Norm n = norm_of(here, total, "total", weight, number(a[4]));
+    const Tensor *more = optional(a[3], "grad_total");
+    const ep_rows_t g = norm_rows_as(n, grad, total, here.index, "grad");
+    const ep_rows_t gt = more ? norm_rows_as(n, *more, total, here.index, "grad_total") : ep_rows_t{nullptr, 0, 0};
+    const int64_t H = n.d.width;
+    Tensor dx = here.empty(total.sizes(), total.scalar_type()), dw = here.empty({H}, weight.scalar_type());
+    size_t need = 0;
+    check(ep_rms_norm_workspace(&n.d, &need), "ep_rms_norm_workspace");
+    Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+    const ep_rows_t to{dx.data_ptr(), n.d.rows * H, H};
+    check(ep_rms_norm_backward(&n.d, &g, &gt, &to, dw.data_ptr(), scratch.data_ptr(), need, here.stream()),
+          "ep_rms_norm_backward");
+    return pack(dx, dw);
+}
+
+// ------------------------------------------------------------ a few tokens
+
+// (x, weights, indices, up, down, activation, up_bias, down_bias, residual)
+PyObject *moe_few_tokens(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weights"), &idx = tensor(a[2], "indices");
+    const Tensor &up = tensor(a[3], "up"), &down = tensor(a[4], "down");
+    Here here(x, "x");
+    const auto shape = x.sizes();
+    const auto type = x.scalar_type();
+    if ((type != at::kBFloat16 && type != at::kHalf) || (shape.size() != 2 && shape.size() != 3))
+        refuse("x must be bf16 or fp16 [T][H] or [W][T][H]");
+    const int64_t H = shape.back(), T = shape.size() == 3 ? shape[0] * shape[1] : shape[0];
+    if (T > EP_MAX_FEW_TOKENS)
+        refuse("at most " + std::to_string(EP_MAX_FEW_TOKENS) + " tokens, not " + std::to_string(T) +
+               ": more of them go through dispatch and expert_product");
+    const int act = choice(a[5], "activation", {"none", "relu", "gelu", "silu", "swiglu"});
+    if (idx.dim() != x.dim()) refuse("indices must be [...][topk]");
+    const int64_t k = idx.size(-1);
+    if (k < 1 || k > EP_MAX_TOPK) refuse("topk must be 1 to " + std::to_string(EP_MAX_TOPK) + ", not " + std::to_string(k));
+    std::vector<int64_t> choices(shape.begin(), shape.end() - 1);
+    choices.push_back(k);
+    on_device(w, here.index, "weights");
+    on_device(idx, here.index, "indices");
+    dense(w, at::kFloat, choices, "weights");
+    dense(idx, at::kInt, choices, "indices");
+    on_device(up, here.index, "up");
+    on_device(down, here.index, "down");
+    if (up.scalar_type() != type || up.dim() != 3 || up.size(2) != H)
+        refuse("up must be " + std::string(c10::toString(type)) + " [experts][features][" + std::to_string(H) + "]");
+    const int64_t E = up.size(0), wide = up.size(1), F = act == EP_ACT_SWIGLU ? wide / 2 : wide;
+    if (E < 1 || E > EP_MAX_ROUTE_EXPERTS)
+        refuse("1 to " + std::to_string(EP_MAX_ROUTE_EXPERTS) + " experts, not " + std::to_string(E));
+    if (H < 8 || H % 8 || H > 1 << 20 || F < 8 || F % 8 || F > 1 << 20 || (act == EP_ACT_SWIGLU && wide % 2))
+        refuse("feature counts must be multiples of 8");
+    if (down.scalar_type() != type || down.sizes() != at::IntArrayRef({E, H, F}))
+        refuse("down must be " + std::string(c10::toString(type)) + " " + shape_text({E, H, F}));
+    const Tensor *up_bias = optional(a[6], "up_bias"), *down_bias = optional(a[7], "down_bias");
+    const Tensor *residual = optional(a[8], "residual");
+    if (up_bias) {
+        on_device(*up_bias, here.index, "up_bias");
+        dense(*up_bias, type, {E, wide}, "up_bias");
+    }
+    if (down_bias) {
+        on_device(*down_bias, here.index, "down_bias");
+        dense(*down_bias, type, {E, H}, "down_bias");
+    }
+    ep_few_desc_t d{};
+    d.tokens = (int32_t)T;
+    d.experts = (int32_t)E;
+    d.topk = (int32_t)k;
+    d.hidden = (int32_t)H;
+    d.inner = (int32_t)F;
+    d.dtype = type == at::kBFloat16 ? EP_DT_BF16 : EP_DT_FP16;
+    d.activation = act;
+    d.up = rows_of(up, "up");
+    d.down = rows_of(down, "down");
+    d.up_bias = up_bias ? up_bias->data_ptr() : nullptr;
+    d.down_bias = down_bias ? down_bias->data_ptr() : nullptr;
+    // the tokens of all ranks as one list
+    auto tokens = [&](const Tensor &t, const char *name) {
+        on_device(t, here.index, name);
+        if (t.scalar_type() != type || t.sizes() != shape)
+            refuse(std::string(name) + " must be " + c10::toString(type) + " " + shape_text(shape));
+        if (!T) return ep_rows_t{nullptr, 0, 0};
+        ep_rows_t r = rows_of(t, name);
+        if (shape.size() == 3 && shape[0] > 1) {
+            if (shape[1] == 1) r.row_stride = r.rank_stride;
+            else if (r.rank_stride != shape[1] * r.row_stride)
+                refuse(std::string(name) + ": the ranks' rows must follow each other");
+            if (r.row_stride < H) refuse(std::string(name) + ": rows must not overlap");
+        }
+        return r;
+    };
+    const ep_rows_t from = tokens(x, "x"), res = residual ? tokens(*residual, "residual") : ep_rows_t{nullptr, 0, 0};
+    Tensor out = here.empty(shape, type);
+    if (T) {
+        size_t need = 0;
+        check(ep_moe_few_workspace(&d, &need), "ep_moe_few_workspace");
+        Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+        const ep_rows_t to{out.data_ptr(), 0, H};
+        check(ep_moe_few(&d, &from, static_cast<const float *>(w.data_ptr()), static_cast<const int32_t *>(idx.data_ptr()),
+                         &res, &to, scratch.data_ptr(), need, error_ptr(here.index), here.stream()),
+              "ep_moe_few");
+    }
+    return THPVariable_Wrap(out);
 }
 
 // ------------------------------------------------------------------ module
@@ -498,7 +794,12 @@ PyMethodDef methods[] = {
     ENTRY("route_backward", route_backward, 12),
     ENTRY("balance_loss", balance_loss, 5),
     ENTRY("expert_product", expert_product, 9),
-    ENTRY("expert_product_backward", expert_product_backward, 8),
+    ENTRY("expert_product_backward", expert_product_backward, 9),
+    ENTRY("checkpoint", checkpoint, 3),
+    ENTRY("checkpoint_restore", checkpoint_restore, 6),
+    ENTRY("rms_norm", rms_norm, 5),
+    ENTRY("rms_norm_backward", rms_norm_backward, 5),
+    ENTRY("moe_few_tokens", moe_few_tokens, 9),
     ENTRY("error_word", error_word_py, 1),
     ENTRY("set_error_class", set_error_class, 1),
     {nullptr, nullptr, 0, nullptr},

@@ -3,7 +3,10 @@
 (the loss that evens out the experts' loads, with per-expert counts) and
 ``expert_product`` (one matrix product per expert over the rows that
 ``moe_group`` leaves, with bias, activation and residual), each with its
-gradient as a ``*_backward`` call.
+gradient as a ``*_backward`` call.  Around them ``rms_norm`` (the norm before
+the layer, in 8 bits where dispatch takes them so), ``checkpoint`` (activations
+kept in 8 bits for the backward pass) and ``moe_few_tokens`` (the whole layer's
+experts at decode).
 
 Names, defaults and streams only: the checks of the tensors, the allocation of
 outputs and the calls into libep_gb300.so are in the compiled binding (_moe.so,
@@ -152,13 +155,89 @@ def expert_product(x: torch.Tensor, weight: torch.Tensor, count: Optional[torch.
 
 def expert_product_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                             count: Optional[torch.Tensor] = None, offset: Optional[torch.Tensor] = None, *,
-                            pre: Optional[torch.Tensor] = None, activation: str = "none",
-                            bias_grad: bool = False, stream=None):
+                            pre: Optional[torch.Tensor] = None, pre_scales: Optional[torch.Tensor] = None,
+                            activation: str = "none", bias_grad: bool = False, stream=None):
     """Gradients of ``expert_product``: (grad_x, grad_weight, grad_bias or
-    None) from grad = dL/dy.  pre: the forward's (not needed for "none").  The
-    residual's gradient is grad itself.  Rows of grad_x outside every group
+    None) from grad = dL/dy.  pre: the forward's (not needed for "none"), or its
+    codes with pre_scales, as ``checkpoint`` keeps them.  The residual's
+    gradient is grad itself.  Rows of grad_x outside every group
     are unspecified; a group without rows gets zero gradients."""
     if stream is not None:
         with _on(x, stream):
-            return _moe.expert_product_backward(grad, x, weight, count, offset, pre, activation, bias_grad)
-    return _moe.expert_product_backward(grad, x, weight, count, offset, pre, activation, bias_grad)
+            return _moe.expert_product_backward(grad, x, weight, count, offset, pre, activation, bias_grad, pre_scales)
+    return _moe.expert_product_backward(grad, x, weight, count, offset, pre, activation, bias_grad, pre_scales)
+
+
+def checkpoint(x: torch.Tensor, count: Optional[torch.Tensor] = None, offset: Optional[torch.Tensor] = None, *,
+               stream=None):
+    """Keep activations in 8 bits until the backward pass: (codes float8_e4m3fn,
+    scales fp32 [...][ceil(F / 128)]) of the rows x [rows][F] or [R][rows][F], bf16
+    or fp16, in every group (count, offset as for ``expert_product``).  One scale
+    for every 128 values of a row, as dispatch quantises; a block with an infinity
+    or a NaN is NaN as a whole.  Rows outside every group are unspecified."""
+    if stream is not None:
+        with _on(x, stream):
+            return _moe.checkpoint(x, count, offset)
+    return _moe.checkpoint(x, count, offset)
+
+
+def checkpoint_restore(codes: torch.Tensor, scales: torch.Tensor, count: Optional[torch.Tensor] = None,
+                       offset: Optional[torch.Tensor] = None, *, activation: str = "none",
+                       dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """act(code * scale) of the rows of every group, bf16 or fp16: what was kept
+    (activation "none"), or the activations of kept pre-activations, recomputed
+    ("swiglu": half as many features).  codes: float8_e4m3fn or uint8, so the
+    grouped rows of an FP8 dispatch as well."""
+    if dtype not in _CODES:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    if stream is not None:
+        with _on(codes, stream):
+            return _moe.checkpoint_restore(codes, scales, count, offset, activation, _CODES[dtype])
+    return _moe.checkpoint_restore(codes, scales, count, offset, activation, _CODES[dtype])
+
+
+_CODES = {torch.bfloat16: _lib.EP_DT_BF16, torch.float16: _lib.EP_DT_FP16}
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             quantize: bool = False, stream=None):
+    """y = total / sqrt(mean(total^2) + eps) * weight, total = x + residual.
+
+    x: bf16, fp16 or fp32 [...][H], H to 32768; weight [H] in x's type or fp32.
+    Returns y; with a residual (y, total), total rounded to x's type, whose norm
+    it is.  quantize: in y's place codes (float8_e4m3fn) and scales (fp32
+    [...][H/128]), H a multiple of 128: ``EpDispatchCombineOp.dispatch`` takes
+    them as pre-quantised input."""
+    if stream is not None:
+        with _on(x, stream):
+            return _moe.rms_norm(x, weight, residual, eps, quantize)
+    return _moe.rms_norm(x, weight, residual, eps, quantize)
+
+
+def rms_norm_backward(grad: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, *,
+                      grad_total: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """Gradients of ``rms_norm`` from grad = dL/dy: (grad_x, grad_weight).
+    total: the forward's, or x where there was no residual.  grad_total: what
+    reaches total by other ways, added.  grad_x is the residual's gradient too."""
+    if stream is not None:
+        with _on(total, stream):
+            return _moe.rms_norm_backward(grad, total, weight, grad_total, eps)
+    return _moe.rms_norm_backward(grad, total, weight, grad_total, eps)
+
+
+def moe_few_tokens(x: torch.Tensor, weights: torch.Tensor, indices: torch.Tensor, up: torch.Tensor,
+                   down: torch.Tensor, *, activation: str = "swiglu", up_bias: Optional[torch.Tensor] = None,
+                   down_bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The experts of at most 64 tokens, without dispatch: out[t] = residual[t] +
+    sum over j of weights[t][j] * y(t, indices[t][j]), y(t, e) = act(x[t] up[e]^T
+    + up_bias[e]) down[e]^T + down_bias[e].
+
+    x, residual: bf16 or fp16 [T][H] or [W][T][H]; weights fp32 and indices int32
+    [...][topk] as ``route`` returns them (a negative index: no expert, so absent tokens
+    get their residual or 0); up: [E][F][H], or [E][2F][H] for "swiglu" (the
+    gate's features first); down: [E][H][F].  Sums are fp32, out is rounded once."""
+    if stream is not None:
+        with _on(x, stream):
+            return _moe.moe_few_tokens(x, weights, indices, up, down, activation, up_bias, down_bias, residual)
+    return _moe.moe_few_tokens(x, weights, indices, up, down, activation, up_bias, down_bias, residual)

@@ -553,6 +553,125 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d,
                                        size_t workspace_bytes, uint32_t *d_error,
                                        void *stream);
 
+/* ---------------------------------------------------------------------
+ * Norm, checkpoints in 8 bits, and the experts of a few tokens: no handle,
+ * asynchronous on `stream`, as the calls above.
+ *
+ * 8 bits are E4M3 codes with one fp32 scale for every block of 128 values of a
+ * row (the last block of a row may be a part), as dispatch quantises:
+ * a = max|v|, scale = fl32(a / 448), code = the E4M3 value nearest to
+ * fl32(v / scale), ties to even; the quotient is the IEEE one for bf16 values and
+ * within a unit of fp32's last place for others.  A block of zeros has scale 0
+ * and codes 0; a block that holds an infinity or a NaN has scale NaN and every
+ * code NaN (0x7F), so that all of it comes back as NaN. */
+
+#define EP_MAX_NORM_WIDTH 32768
+#define EP_MAX_FEW_TOKENS 64
+
+/* Rows here are contiguous, aligned to their element alone, with any strides >=
+ * width (rank_stride > 0), in elements; 16-byte aligned ones are read faster. */
+typedef struct {
+    int32_t ranks;        /* R, 1..65535 */
+    int32_t rows;         /* rows per rank, 0..2^30, R * rows <= 2^30 */
+    int32_t width;        /* H, 1..EP_MAX_NORM_WIDTH */
+    int32_t dtype;        /* EP_DT_BF16, EP_DT_FP16 or EP_DT_FP32, of every row */
+    int32_t weight_dtype; /* dtype or EP_DT_FP32 */
+    float   eps;          /* >= 0 */
+    ep_rows_t x;          /* [R][rows][H] */
+    const void *weight;   /* [H] */
+} ep_norm_desc_t;
+
+/* Root-mean-square norm of every row, after the residual's addition:
+ *   total = x + residual, rounded once to dtype (residual->ptr NULL: x itself)
+ *   r = 1 / sqrt(mean(total^2) + eps),  y = total * r * weight
+ * The norm is that of the rounded total, which is what the next block adds to
+ * and what the gradient sees.  Sums in fp32, y rounded once.  total->ptr NULL:
+ * not written.  total may be x or the residual itself; y overlaps nothing that is
+ * read.  scales->ptr NULL: y has dtype; else y gets codes (one byte each) and scales the
+ * [R][rows][H/128] fp32 block scales, with H a multiple of 128: what a
+ * pre-quantised dispatch takes. */
+ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual,
+                        const ep_rows_t *total, const ep_rows_t *y,
+                        const ep_rows_t *scales, void *stream);
+
+/* The gradient, d->x being the forward's total, grad = dL/dy:
+ *   u = grad * weight
+ *   grad_x = r * (u - total * r^2 * mean(u * total)) + grad_total
+ *   grad_weight = sum over rows of grad * total * r
+ * grad_total (ptr NULL: none) is what comes to total from elsewhere, the residual
+ * stream.  grad_x is the gradient of x and of the residual alike, and may be
+ * grad_total itself.  d_grad_weight [H] in weight_dtype; rows are summed in an
+ * order that the sizes alone fix.  d_workspace: ep_rms_norm_workspace bytes, 16-byte
+ * aligned, any contents. */
+ep_status_t ep_rms_norm_workspace(const ep_norm_desc_t *d, size_t *bytes);
+ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
+                                 const ep_rows_t *grad_total,
+                                 const ep_rows_t *grad_x, void *d_grad_weight,
+                                 void *d_workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Activations kept in 8 bits between forward and backward, over rows grouped as in
+ * ep_product_desc_t.  Rows outside every group are neither read nor written. */
+typedef struct {
+    int32_t ranks, groups, rows;    /* as in ep_product_desc_t */
+    int32_t features;     /* values of a kept row, multiple of 8, <= 2^24 */
+    int32_t dtype;        /* EP_DT_BF16 or EP_DT_FP16, of x and y */
+    int32_t activation;   /* of restore */
+    const int32_t *d_count, *d_offset;
+} ep_checkpoint_desc_t;
+
+/* x [R][rows][features] -> codes (one byte each, strides in bytes, multiples of 8)
+ * and scales [R][rows][ceil(features / 128)] fp32. */
+ep_status_t ep_checkpoint_save(const ep_checkpoint_desc_t *d, const ep_rows_t *x,
+                               const ep_rows_t *codes, const ep_rows_t *scales,
+                               void *stream);
+/* y = act(code * scale), the product in fp32, rounded once; with EP_ACT_SWIGLU
+ * features is a multiple of 16 and y has half of them.  Also turns the grouped 8-bit rows of
+ * an FP8 dispatch into rows that ep_expert_product takes. */
+ep_status_t ep_checkpoint_restore(const ep_checkpoint_desc_t *d, const ep_rows_t *codes,
+                                  const ep_rows_t *scales, const ep_rows_t *y,
+                                  void *stream);
+/* ep_expert_product_backward with pre = code * scale (in fp32, not rounded to
+ * the tensors' type), codes [R][rows][wide] and scales [R][rows][ceil(wide /
+ * 128)] as ep_checkpoint_save leaves them. */
+ep_status_t ep_expert_product_backward_checkpoint(
+    const ep_product_desc_t *d, const ep_rows_t *grad, const ep_rows_t *codes,
+    const ep_rows_t *scales, const ep_rows_t *grad_x, void *d_grad_w,
+    void *d_grad_bias, void *d_workspace, size_t workspace_bytes,
+    uint32_t *d_error, void *stream);
+
+/* A whole MoE layer's experts for a few tokens, without dispatch:
+ *   out[t] = residual[t] + sum over j of w[t][j] * y(t, e), e = idx[t][j],
+ *   y(t, e) = act(x[t] up_e^T + up_bias_e) down_e^T + down_bias_e
+ * Every sum is fp32; the activations between the products are kept in two 16-bit
+ * halves (a value and what its rounding left), and out is rounded once.
+ * The experts of a token are added in ascending order; one that is named
+ * twice has the sum of its weights.  idx < 0: no expert (ep_route's -1); idx >=
+ * experts: skipped, and sets BAD_INDEX.  A token without experts gets its
+ * residual, or 0. */
+typedef struct {
+    int32_t tokens;       /* T, 0..EP_MAX_FEW_TOKENS */
+    int32_t experts;      /* E, 1..EP_MAX_ROUTE_EXPERTS */
+    int32_t topk;         /* k, 1..32 */
+    int32_t hidden;       /* H, multiple of 8, <= 2^20 */
+    int32_t inner;        /* F, multiple of 8, <= 2^20 */
+    int32_t dtype;        /* EP_DT_BF16 or EP_DT_FP16, of every tensor but w */
+    int32_t activation;   /* ep_activation_t; SWIGLU: up has 2F features, the gate's first */
+    int32_t reserved;     /* 0 */
+    ep_rows_t up;         /* [E][wide][H]; rows as in ep_product_desc_t */
+    ep_rows_t down;       /* [E][H][F] */
+    const void *up_bias, *down_bias;    /* [E][wide], [E][H] dense, or NULL */
+} ep_few_desc_t;
+
+/* x, residual (ptr NULL: none), out: [T][H] (rank_stride unused).  out may be the
+ * residual itself and overlaps nothing else.  d_workspace: ep_moe_few_workspace bytes,
+ * 256-byte aligned, any contents. */
+ep_status_t ep_moe_few_workspace(const ep_few_desc_t *d, size_t *bytes);
+ep_status_t ep_moe_few(const ep_few_desc_t *d, const ep_rows_t *x, const float *d_w,
+                       const int32_t *d_idx, const ep_rows_t *residual,
+                       const ep_rows_t *out, void *d_workspace,
+                       size_t workspace_bytes, uint32_t *d_error, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
