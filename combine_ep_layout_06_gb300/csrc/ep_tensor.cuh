@@ -84,6 +84,9 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+}
 
 // ------------------------------------------------------------ pairs of CTAs
 // Two CTAs of a cluster share each matrix instruction.
@@ -91,20 +94,34 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-// ------------------------------------------------------------------ TMA tiles
-// `bar` is in the shared memory of either CTA of the pair.
 
+// ------------------------------------------------------------------ TMA tiles
+// For a pair (PAIR) `bar` is in the shared memory of either CTA; for a single
+// CTA in its own.
+
+template <bool PAIR = true>
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
                                           int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-                 "[%0], [%1, {%3, %4, %5}], [%2];"
-                 :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%3, %4, %5}], [%2];"
+                     :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%3, %4, %5}], [%2];"
+                     :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
+template <bool PAIR = true>
 __device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
                                           int y, int z, int u, int v) {
-    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
-                 :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                     "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+                     :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                     "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];"
+                     :: "r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
@@ -137,6 +154,12 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
+// One instruction of a single CTA: m = 128.
+__device__ __forceinline__ void mma_f16_single(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
 // Arrives on the mbarrier once every matrix instruction issued so far by
 // this thread is complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -147,6 +170,20 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
                  "[%0], %1;" :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void mma_commit_single(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(bar) : "memory");
+}
+// Taken and freed by one warp of a CTA.
+__device__ __forceinline__ void tmem_alloc_single(uint32_t smem_slot, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_slot), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_single(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "r"(columns)
+                 : "memory");
 }
 // Taken and freed by one warp of each CTA of the pair together.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t columns) {
@@ -186,6 +223,23 @@ __device__ __forceinline__ void tmem_wait(uint32_t *r) {
           "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
           "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
           "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :: "memory");
+}
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+          "+r"(r[15])
         :: "memory");
 }
 __device__ __forceinline__ void fence_async_smem() {
@@ -242,12 +296,13 @@ inline bool encode_rows(CUtensorMap *map, int dtype, const ep_rows_t &r, int64_t
 }
 
 // Gated weights [G][2][N][K]: one box is 8 features of the gate, the same 8
-// of the up half, and so on for 64 features.
-inline bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, int64_t N, int64_t G) {
+// of the up half, and so on for 8 * `eights` features.
+inline bool encode_gated(CUtensorMap *map, int dtype, const ep_rows_t &w, int64_t K, int64_t N, int64_t G,
+                         uint32_t eights = 8) {
     const uint64_t dims[5] = {(uint64_t)K, 8, 2, (uint64_t)(N / 8), (uint64_t)G};
     const int64_t strides[5] = {1, w.row_stride, N * w.row_stride, 8 * w.row_stride,
                                 G > 1 ? w.rank_stride : w.row_stride};
-    const uint32_t box[5] = {64, 8, 2, 8, 1};
+    const uint32_t box[5] = {64, 8, 2, eights, 1};
     return encode(map, dtype, w.ptr, 5, dims, strides, box);
 }
 
