@@ -8,9 +8,9 @@
 // else is small, so the kernels are built to keep memory busy.  The weights are the
 // 128-wide operand of the matrix instructions and the tokens the other
 // (16 columns at least), so that few tokens cost narrow instructions.  One
-// CTA per SM: a warp loads 128-deep slices of weights and tokens by TMA into a
-// ring in shared memory, tile after tile without a pause; one thread issues the
-// instructions; four warps finish one accumulator while the other fills.
+// CTA per SM: two warps in turn load 128-deep slices of weights and tokens by TMA
+// into a ring in shared memory, tile after tile without a pause; one thread issues
+// the instructions; four warps finish one accumulator while the other fills.
 //
 // Up takes all tokens as columns and keeps those that chose the expert: no
 // gather.  Down has a CTA go through all experts for its outputs, which it sums in
@@ -30,8 +30,9 @@ namespace {
 
 constexpr int kSlice = 128;                  // k of a slice: two halves of 64, 128 bytes each
 constexpr int kMaxStages = 12;
-constexpr int kFinishers = 4;
-constexpr int kThreads = 64 + kFinishers * 32;
+constexpr int kLoaders = 2, kFinishers = 4;    // warps
+constexpr int kMostRows = 32;                // of h in an accumulator of down
+constexpr int kThreads = (kLoaders + 1 + kFinishers) * 32;
 constexpr int kSmemMost = 227 * 1024 - 1024; // of a CTA, less what is static
 
 struct FewParams {
@@ -39,6 +40,7 @@ struct FewParams {
     int act, rows;               // rows of weights a tile
     int box;                     // up: token rows a copy brings
     int stages, stage_bytes, columns;
+    int split;                   // down: CTAs that share a tile, each a part of K
     int off_acc, off_mask, off_weight, off_first, off_list, off_token;    // in shared memory, after the ring
     const float *w;
     const int32_t *idx;
@@ -54,7 +56,7 @@ struct FewWork {
 };
 
 struct __align__(8) FewBarriers {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], joined, drained;
     uint32_t tmem;
     int present;
     Watch watch;
@@ -125,11 +127,17 @@ template <bool DOWN> __device__ void make_plan(const FewParams &p, unsigned char
     if (DOWN) __syncthreads();
 }
 
-// The accumulators that a CTA fills, one after the other: tile m of the i-th
-// chosen expert.  Up: a tile of one expert; down: a tile of outputs, all experts.
+// The accumulators that a CTA fills, one after the other.  Up: tile m of the
+// i-th chosen expert.  Down: tile m of the outputs for all experts, at most
+// kMostRows rows of h at a time (an expert with more has its weights come again, from
+// L2), so that the ring need not be laid out for all tokens.
 template <bool DOWN> struct Walk {
-    int tiles, present, u, i, m;
-    __device__ Walk(const FewParams &p, int n) : tiles((p.M + per_tile(p) - 1) / per_tile(p)), present(n), u(blockIdx.x), i(0), m(0) {
+    const FewParams &p;
+    const Plan &plan;
+    int tiles, u, i, m, row;     // row: first of the expert's rows
+    __device__ Walk(const FewParams &params, const Plan &pl)
+        : p(params), plan(pl), tiles((params.M + per_tile(params) - 1) / per_tile(params)),
+          u(DOWN ? blockIdx.x / params.split : blockIdx.x), i(0), m(0), row(0) {
         place();
     }
     static __device__ int per_tile(const FewParams &p) { return !DOWN && p.act == EP_ACT_SWIGLU ? p.rows / 2 : p.rows; }
@@ -141,20 +149,48 @@ template <bool DOWN> struct Walk {
             m = u - i * tiles;
         }
     }
-    __device__ bool more() const { return DOWN ? u < tiles && present > 0 : u < tiles * present; }
-    __device__ bool last_expert() const { return !DOWN || i + 1 == present; }
+    __device__ bool more() const { return DOWN ? u < tiles && plan.present > 0 : u < tiles * plan.present; }
+    __device__ int expert() const { return plan.list[i]; }
+    __device__ int rows_from(int at) const { return __popcll(plan.mask[expert()]) - at; }
+    __device__ int rows() const { return min(rows_from(row), kMostRows); }
+    __device__ bool last_of_tile() const { return i + 1 == plan.present && rows_from(row) <= kMostRows; }
     __device__ void next() {
-        if (DOWN && ++i < present) return;
-        if (DOWN) i = 0;
-        u += gridDim.x;
+        if constexpr (DOWN) {
+            if (rows_from(row) > kMostRows) {
+                row += kMostRows;
+                return;
+            }
+            row = 0;
+            if (++i < plan.present) return;
+            i = 0;
+            u += gridDim.x / p.split;
+        } else {
+            u += gridDim.x;
+        }
         place();
+    }
+};
+
+// This CTA's part of K, in slices.
+template <bool DOWN> struct Depth {
+    int first, n;
+    __device__ explicit Depth(const FewParams &p) {
+        const int all = (p.K + kSlice - 1) / kSlice;
+        if constexpr (DOWN) {
+            const int r = blockIdx.x % p.split;          // the CTA's rank in its cluster
+            first = r * all / p.split;
+            n = (r + 1) * all / p.split - first;
+        } else {
+            first = 0;
+            n = all;
+        }
     }
 };
 
 // Columns of an accumulator.  Up: all tokens.  Down: for every 8 rows of h 8 of
 // upper and 8 of lower halves.
-template <bool DOWN> __device__ __forceinline__ int columns_of(const FewParams &p, int rows) {
-    return DOWN ? (rows + 7) / 8 * 16 : (p.T + 15) & ~15;
+template <bool DOWN> __device__ __forceinline__ int columns_of(const FewParams &p, const Walk<DOWN> &at) {
+    return DOWN ? (at.rows() + 7) / 8 * 16 : (p.T + 15) & ~15;
 }
 
 // Tensor memory for two accumulators: a power of two of at least 32 columns.
@@ -164,7 +200,7 @@ __device__ __forceinline__ uint32_t tmem_columns(int columns) {
     return n;
 }
 
-// ---- warp 0: copies
+// ---- the first warps: copies
 
 template <bool DOWN, bool GATED> struct FewLoader {
     const FewWork &w;
@@ -176,18 +212,18 @@ template <bool DOWN, bool GATED> struct FewLoader {
     __device__ void weights(uint32_t s, const Walk<DOWN> &at, int k) const {
         const FewParams &p = w.p;
         const uint32_t bar = smem_u32(&bars.full[s]), half = p.rows * 128;
-        const int e = plan.list[at.i];
+        const int e = at.expert();
         for (int h = 0; h < (p.K - k > 64 ? 2 : 1); ++h) {
             if constexpr (GATED) tma_load5<false>(stage(s) + h * half, &w.a, bar, k + h * 64, 0, 0, at.m * (p.rows / 16), e);
             else tma_load3<false>(stage(s) + h * half, &w.a, bar, k + h * 64, at.m * p.rows, e);
         }
     }
     // Boxes of tokens in a half slice, and where the halves start.
-    __device__ int boxes(const Walk<DOWN> &at) const { return DOWN ? (__popcll(plan.mask[plan.list[at.i]]) + 7) / 8 : 1; }
+    __device__ int boxes(const Walk<DOWN> &at) const { return DOWN ? (at.rows() + 7) / 8 : 1; }
     __device__ void tokens(uint32_t s, const Walk<DOWN> &at, int k, int n) const {
         const FewParams &p = w.p;
         const uint32_t bar = smem_u32(&bars.full[s]), to = stage(s) + p.rows * 256;
-        const int first = DOWN ? plan.first[plan.list[at.i]] : 0;
+        const int first = DOWN ? plan.first[at.expert()] + at.row : 0;
         for (int h = 0; h < (p.K - k > 64 ? 2 : 1); ++h)
             for (int j = 0; j < n; ++j)
                 tma_load3<false>(to + (h * n + j) * p.box * 128, &w.b, bar, k + h * 64, first + j * 8, 0);
@@ -197,53 +233,69 @@ template <bool DOWN, bool GATED> struct FewLoader {
         mbar_expect(smem_u32(&bars.full[s]), (p.K - k > 64 ? 2 : 1) * (p.rows + n * p.box) * 128);
     }
 
-    __device__ void run() {
+    // This warp's slices: every kLoaders-th one, from its own number on.
+    struct Slices {
+        Walk<DOWN> at;
+        Depth<DOWN> depth;
+        int n, ks;                                       // slice, its place in the accumulator
+        __device__ Slices(const FewParams &p, const Plan &plan, int mine) : at(p, plan), depth(p), n(mine), ks(mine) { settle(); }
+        __device__ void settle() {
+            for (; at.more() && ks >= depth.n; at.next()) ks -= depth.n;
+        }
+        __device__ bool more() const { return at.more(); }
+        __device__ int k() const { return (depth.first + ks) * kSlice; }
+        __device__ void next() {
+            n += kLoaders;
+            ks += kLoaders;
+            settle();
+        }
+    };
+
+    __device__ void run(int mine) {
         const FewParams &p = w.p;
         const bool elected = elect_one();
-        uint32_t issued = 0, s = 0, phase = 0;
+        const int S = p.stages;
         bool ok = true;
-        int early = 0;
         if constexpr (DOWN) {                            // weights for a whole ring, ahead of h
-            Walk<DOWN> at(p, plan.present);
-            for (; at.more() && early < p.stages; at.next())
-                for (int k = 0; k < p.K && early < p.stages; k += kSlice, ++early)
-                    if (elected) {
-                        expect(early, k, boxes(at));
-                        weights(early, at, k);
-                    }
+            for (Slices it(p, plan, mine); it.more() && it.n < S; it.next()) {
+                if (elected) {
+                    expect(it.n, it.k(), boxes(it.at));
+                    weights(it.n, it.at, it.k());
+                }
+                __syncwarp();
+            }
             grid_dependency_wait();
         }
-        for (Walk<DOWN> at(p, plan.present); ok && at.more(); at.next()) {
-            const int n = boxes(at);
-            for (int k = 0; k < p.K; k += kSlice) {
-                if (!tensor_wait(smem_u32(&bars.empty[s]), phase ^ 1u, &bars.watch)) {
-                    ok = false;
-                    break;
+        int s = mine % S, last = -1;
+        uint32_t phase = mine / S & 1u;
+        Slices it(p, plan, mine);
+        for (; it.more(); it.next()) {
+            // by the whole warp, which stays together: a lane that fell two
+            // rounds behind would wait for a phase that has passed
+            ok = warp_wait(smem_u32(&bars.empty[s]), phase ^ 1u, &bars.watch);
+            if (!ok) break;
+            if (elected) {
+                const int n = boxes(it.at);
+                if (!DOWN || it.n >= S) {
+                    expect(s, it.k(), n);
+                    weights(s, it.at, it.k());
                 }
-                if (elected) {
-                    if ((int)issued >= early) {
-                        expect(s, k, n);
-                        weights(s, at, k);
-                    }
-                    tokens(s, at, k, n);
-                }
-                ++issued;
-                if (elected) *(volatile uint32_t *)&bars.watch.loaded = issued;
-                if (++s == (uint32_t)p.stages) {
-                    s = 0;
-                    phase ^= 1u;
-                }
+                tokens(s, it.at, it.k(), n);
+                *(volatile uint32_t *)&bars.watch.loaded = it.n + 1;
             }
-            ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();
+            last = it.n;
+            for (s += kLoaders; s >= S; s -= S) phase ^= 1u;
         }
-        // the CTA ends no earlier than its copies and its stages' last signals;
-        // after a wait that ran out, as far as they come within another wait each
+        // The CTA ends no earlier than its copies and its stages' last signals (of
+        // the last S slices of all warps: earlier ones' phases have passed);
+        // after a wait that ran out, as far as they come within another wait each.
         if ((threadIdx.x & 31) == 0) {
             Watch ignore = {};
             volatile Watch *watch = ok ? (volatile Watch *)&bars.watch : &ignore;
-            const uint32_t S = p.stages;
-            for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) {
-                const uint32_t q = j % S, round = (j / S) & 1u;
+            const int all = ok ? it.n - it.ks : last + 1;
+            for (int n = last; n >= 0 && n >= all - S; n -= kLoaders) {
+                const uint32_t q = n % S, round = n / S & 1u;
                 if (!ok) tensor_wait(smem_u32(&bars.full[q]), round, watch);
                 tensor_wait(smem_u32(&bars.empty[q]), round, watch);
             }
@@ -252,7 +304,7 @@ template <bool DOWN, bool GATED> struct FewLoader {
     }
 };
 
-// ---- warp 1: matrix instructions
+// ---- the next warp: matrix instructions
 
 template <typename T, bool DOWN>
 __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &bars, uint32_t ring, uint32_t tmem) {
@@ -260,17 +312,16 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
     constexpr uint32_t kIdesc = f16_idesc(std::is_same<T, __nv_bfloat16>::value, false, false, 128);
     uint32_t s = 0, phase = 0, acc = 0;
     bool ok = true;
-    for (Walk<DOWN> at(p, plan.present); ok && at.more(); at.next()) {
-        const int rows = DOWN ? __popcll(plan.mask[plan.list[at.i]]) : 0;
-        const int n = columns_of<DOWN>(p, rows), boxes = DOWN ? (rows + 7) / 8 : 1;
+    const Depth<DOWN> depth(p);
+    for (Walk<DOWN> at(p, plan); ok && at.more(); at.next()) {
+        const int n = columns_of<DOWN>(p, at), boxes = DOWN ? n / 16 : 1;
         const uint32_t idesc = kIdesc | idesc_n(n), d = tmem + (acc & 1u) * p.columns;
         ok = warp_wait(smem_u32(&bars.acc_empty[acc & 1u]), ((acc >> 1) & 1u) ^ 1u, &bars.watch);
         tcgen_after_sync();
-        for (int k = 0; ok && k < p.K; k += kSlice) {
-            if (!tensor_wait(smem_u32(&bars.full[s]), phase, &bars.watch)) {
-                ok = false;
-                break;
-            }
+        for (int ks = 0; ks < depth.n; ++ks) {
+            const int k = (depth.first + ks) * kSlice;
+            ok = ok && warp_wait(smem_u32(&bars.full[s]), phase, &bars.watch);
+            if (!ok) break;
             if (elected) {
                 // rows of weights past p.rows are whatever follows in shared
                 // memory: their lanes of the accumulator are not read
@@ -281,15 +332,15 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
 #pragma unroll
                 for (int j = 0; j < kSlice / 16; ++j)
                     if (j == 0 || k + j * 16 < p.K)
-                        mma_f16_single(d, (j < 4 ? a0 : a1) + j % 4 * 2, (j < 4 ? b0 : b1) + j % 4 * 2, idesc, k > 0 || j > 0);
+                        mma_f16_single(d, (j < 4 ? a0 : a1) + j % 4 * 2, (j < 4 ? b0 : b1) + j % 4 * 2, idesc, ks > 0 || j > 0);
                 mma_commit_single(smem_u32(&bars.empty[s]));
             }
+            __syncwarp();
             if (++s == (uint32_t)p.stages) {
                 s = 0;
                 phase ^= 1u;
             }
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (ok && elected) mma_commit_single(smem_u32(&bars.acc_full[acc & 1u]));
         ++acc;
     }
@@ -300,7 +351,7 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
     }
 }
 
-// ---- warps 2..5: outputs.  A lane has a row of weights, a register a column.
+// ---- the last four warps: outputs.  A lane has a row of weights, a register a column.
 
 template <typename T, bool GATED>
 __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers &bars, uint32_t tmem) {
@@ -309,7 +360,7 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
     const bool upper = GATED && (r & 8);                 // 8 rows of the gate, 8 of the up half
     const int in = GATED ? (r >> 4) * 8 + (r & 7) : r;
     uint32_t acc = 0;
-    for (Walk<false> at(p, plan.present); at.more(); at.next(), ++acc) {
+    for (Walk<false> at(p, plan); at.more(); at.next(), ++acc) {
         const int e = plan.list[at.i], f = at.m * Walk<false>::per_tile(p) + in;
         const bool live = f < p.M && r < p.rows;
         const unsigned long long mask = plan.mask[e];
@@ -318,7 +369,7 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
         if (!warp_wait(smem_u32(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, &bars.watch)) return;
         tcgen_after_sync();
         const uint32_t d = tmem + (acc & 1u) * p.columns + ((uint32_t)(quarter * 32) << 16);
-        const int n = columns_of<false>(p, 0);
+        const int n = columns_of<false>(p, at);
         T *h = static_cast<T *>(p.h) + (int64_t)plan.first[e] * p.M + f;
         for (int c0 = 0; c0 < n; c0 += 16) {
             uint32_t raw[16];
@@ -354,39 +405,70 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
     }
 }
 
+// Reads a float of another CTA's shared memory.
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 template <typename T>
 __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarriers &bars, float *sums, uint32_t tmem) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
     if (quarter * 32 >= p.rows) return;
+    const int rank = blockIdx.x % p.split;
     float *mine = sums + r;                              // [T][rows], a column for each thread
     for (int t = 0; t < p.T; ++t) mine[t * p.rows] = 0.f;
-    auto write = [&](int m) {
-        if (m >= p.M) return;
-        const T *res = static_cast<const T *>(p.residual.ptr);
-        T *out = static_cast<T *>(p.out.ptr) + m;
+    // A meeting of these warps of all CTAs that share the tile.
+    uint32_t phase = 0;
+    auto meet = [&]() -> bool {
+        if (p.split == 1) return true;
+        __syncwarp();
+        if (lane < p.split) cluster_arrive(in_cta(smem_u32(&bars.joined), lane));
+        const bool ok = __all_sync(0xffffffffu, tensor_wait<true>(smem_u32(&bars.joined), phase, &bars.watch));
+        phase ^= 1u;
+        return ok;
+    };
+    // The tile's outputs; with other CTAs every split-th token of them, the
+    // parts added in order of rank.
+    auto write = [&](int m) -> bool {
+        if (!meet()) return false;
+        if (m < p.M) {
+            const T *res = static_cast<const T *>(p.residual.ptr);
+            T *out = static_cast<T *>(p.out.ptr) + m;
 #pragma unroll 4
-        for (int t = 0; t < p.T; ++t) {
-            float v = mine[t * p.rows];
-            if (res) v += f32(res[t * p.residual.row_stride + m]);
-            out[t * p.out.row_stride] = rounded<T>(v);
-            mine[t * p.rows] = 0.f;
+            for (int t = rank; t < p.T; t += p.split) {
+                float v;
+                if (p.split == 1) {
+                    v = mine[t * p.rows];
+                } else {
+                    v = 0.f;
+                    for (int q = 0; q < p.split; ++q) v += ld_cluster(in_cta(smem_u32(mine + t * p.rows), q));
+                }
+                if (res) v += f32(res[t * p.residual.row_stride + m]);
+                out[t * p.out.row_stride] = rounded<T>(v);
+            }
         }
+        if (!meet()) return false;                       // the others have read
+        for (int t = 0; t < p.T; ++t) mine[t * p.rows] = 0.f;
+        return true;
     };
     if (plan.present == 0) {
-        for (int u = blockIdx.x; u * p.rows < p.M; u += gridDim.x) write(u * p.rows + r);
+        for (int u = blockIdx.x / p.split; u * p.rows < p.M; u += gridDim.x / p.split)
+            if (!write(u * p.rows + r)) return;
         return;
     }
     uint32_t acc = 0;
-    for (Walk<true> at(p, plan.present); at.more(); at.next(), ++acc) {
-        const int e = plan.list[at.i], m = at.m * p.rows + r;
-        const int rows = __popcll(plan.mask[e]), n = columns_of<true>(p, rows);
+    for (Walk<true> at(p, plan); at.more(); at.next(), ++acc) {
+        const int e = at.expert(), m = at.m * p.rows + r;
+        const int rows = at.rows(), n = columns_of<true>(p, at);
         float bias = 0.f;
-        if (p.bias && m < p.M) bias = f32(static_cast<const T *>(p.bias)[(int64_t)e * p.M + m]);
+        if (p.bias && m < p.M && rank == 0) bias = f32(static_cast<const T *>(p.bias)[(int64_t)e * p.M + m]);
         if (!warp_wait(smem_u32(&bars.acc_full[acc & 1u]), (acc >> 1) & 1u, &bars.watch)) return;
         tcgen_after_sync();
         const uint32_t d = tmem + (acc & 1u) * p.columns + ((uint32_t)(quarter * 32) << 16);
-        const float *weight = plan.weight + plan.first[e];
-        const uint8_t *token = plan.token + plan.first[e];
+        const float *weight = plan.weight + plan.first[e] + at.row;
+        const uint8_t *token = plan.token + plan.first[e] + at.row;
         for (int c0 = 0; c0 < n; c0 += 16) {
             uint32_t raw[16];
             tmem_load16(d + c0, raw);
@@ -404,7 +486,7 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
                 mine[token[j] * p.rows] += weight[j] * v;
             }
         }
-        if (at.last_expert()) write(m);
+        if (at.last_of_tile() && !write(m)) return;
     }
 }
 
@@ -426,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             mbar_init(&bars.acc_full[i], 1);
             mbar_init(&bars.acc_empty[i], (p.rows + 31) / 32);
         }
+        mbar_init(&bars.joined, DOWN ? p.split * ((p.rows + 31) / 32) : 1);
         mbar_init(&bars.drained, 1);
         bars.watch.gave_up = 0;
         bars.watch.loaded = 0;
@@ -434,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         tma_prefetch_map(&w.b);
     }
     __syncwarp();
-    if (warp == 1) tmem_alloc_single(smem_u32(&bars.tmem), tmem_columns(p.columns));
+    if (DOWN && p.split > 1) cluster_sync();             // the barriers stand before another CTA signals
+    if (warp == kLoaders) tmem_alloc_single(smem_u32(&bars.tmem), tmem_columns(p.columns));
     tcgen_before_sync();
     __syncthreads();
     tcgen_after_sync();
@@ -448,11 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     }
     Plan plan;
     make_plan<DOWN>(p, smem, &bars.present, &plan);
-    if (warp == 0) {
-        FewLoader<DOWN, GATED>{w, plan, bars, ring}.run();
+    if (warp < kLoaders) {
+        FewLoader<DOWN, GATED>{w, plan, bars, ring}.run(warp);
     } else {
         if (DOWN) grid_dependency_wait();
-        if (warp == 1) few_multiply<T, DOWN>(p, plan, bars, ring, tmem);
+        if (warp == kLoaders) few_multiply<T, DOWN>(p, plan, bars, ring, tmem);
         else if constexpr (DOWN) few_finish_down<T>(p, plan, bars, reinterpret_cast<float *>(smem + p.off_acc), tmem);
         else few_finish_up<T, GATED>(p, plan, bars, tmem);
     }
@@ -461,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     tcgen_before_sync();
     __syncthreads();
     tcgen_after_sync();
-    if (warp == 1) tmem_free_single(tmem, tmem_columns(p.columns));
+    if (DOWN && p.split > 1) cluster_sync();             // nobody reads or signals here any more
+    if (warp == kLoaders) tmem_free_single(tmem, tmem_columns(p.columns));
     if (threadIdx.x == 0 && bars.watch.gave_up && p.error) atomicOr(p.error, EP_DEVERR_TIMEOUT);
 }
 
@@ -488,7 +573,8 @@ size_t workspace(const ep_few_desc_t &d) { return (size_t)h_rows(d) * d.inner * 
 // 16 KB at least: instructions read 128 rows of weights whatever a tile has.
 bool lay_out(FewParams *p, bool down, size_t *bytes) {
     const int rows_most = p->T * p->k;
-    p->stage_bytes = p->rows * 256 + (down ? (p->T + 7) / 8 * 16 : p->box) * 256;
+    const int most = p->T < kMostRows ? p->T : kMostRows;
+    p->stage_bytes = p->rows * 256 + (down ? (most + 7) / 8 * 16 : p->box) * 256;
     int at = 0;
     auto take = [&](int size) {
         const int was = at;
@@ -500,7 +586,7 @@ bool lay_out(FewParams *p, bool down, size_t *bytes) {
     if (at < 16384) at = 16384;
     p->stages = (kSmemMost - 1024 - at) / p->stage_bytes;
     if (p->stages > kMaxStages) p->stages = kMaxStages;
-    if (p->stages < 2) return false;
+    if (p->stages < kLoaders) return false;      // see FewLoader: a warp counts on slices a ring behind its last one
     const int ring = p->stages * p->stage_bytes;
     p->off_acc = ring + acc;
     p->off_mask = ring + mask;
@@ -525,9 +611,21 @@ template <typename T, bool DOWN, bool GATED> ep_status_t launch_few(FewWork &w, 
             return EP_ERR_GPU_OP;
         configured[dev].store(true, std::memory_order_release);
     }
-    return launch_after_previous(few_kernel<T, DOWN, GATED>, (unsigned)(tiles < sms ? tiles : sms), kThreads, bytes, st, w) ==
-                   cudaSuccess
-               ? EP_SUCCESS : EP_ERR_GPU_OP;
+    const int64_t clusters = sms / w.p.split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles < clusters ? tiles : clusters) * w.p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = w.p.split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, few_kernel<T, DOWN, GATED>, w) == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 template <typename T>
@@ -585,7 +683,7 @@ ep_status_t ep_moe_few(const ep_few_desc_t *d, const ep_rows_t *x, const float *
     down.p.K = F;
     down.p.bias = d->down_bias;
     down.p.box = 16;
-    down.p.columns = (T + 7) / 8 * 16;
+    down.p.columns = ((T < kMostRows ? T : kMostRows) + 7) / 8 * 16;
     down.p.residual = *residual;
     down.p.out = *out;
 
@@ -593,7 +691,9 @@ ep_status_t ep_moe_few(const ep_few_desc_t *d, const ep_rows_t *x, const float *
     up.p.rows = 128;
     while (up.p.rows > 32 && most * ((wide + up.p.rows - 1) / up.p.rows) < 300) up.p.rows /= 2;
     down.p.rows = 128;
-    while (down.p.rows > 32 && (H + down.p.rows - 1) / down.p.rows < 150) down.p.rows /= 2;
+    const int slices = (F + kSlice - 1) / kSlice, tiles = (H + 127) / 128;
+    up.p.split = down.p.split = 1;
+    while (down.p.split < 8 && 2 * down.p.split <= slices && tiles * down.p.split * 2 <= 144) down.p.split *= 2;
     const int64_t up_tiles = most * ((wide + up.p.rows - 1) / up.p.rows), down_tiles = (H + down.p.rows - 1) / down.p.rows;
 
     const ep_rows_t tokens = {x->ptr, 0, x->row_stride};
