@@ -643,10 +643,10 @@ ep_status_t ep_expert_product_backward_checkpoint(
 /* A whole MoE layer's experts for a few tokens, without dispatch:
  *   out[t] = residual[t] + sum over j of w[t][j] * y(t, e), e = idx[t][j],
  *   y(t, e) = act(x[t] up_e^T + up_bias_e) down_e^T + down_bias_e
- * Every sum is fp32; the activations between the products are kept in two 16-bit
- * halves (a value and what its rounding left), and out is rounded once.
- * The experts of a token are added in ascending order; one that is named
- * twice has the sum of its weights.  idx < 0: no expert (ep_route's -1); idx >=
+ * Every sum is fp32; the activations between the products are kept in fp32 or in
+ * two 16-bit halves (a value and what its rounding left), and out is rounded
+ * once.  Sums are in an order that sizes and indices alone fix; an expert that is
+ * named twice counts twice.  idx < 0: no expert (ep_route's -1); idx >=
  * experts: skipped, and sets BAD_INDEX.  A token without experts gets its
  * residual, or 0. */
 typedef struct {
