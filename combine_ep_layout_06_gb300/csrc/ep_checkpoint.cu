@@ -49,8 +49,8 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) save_kernel
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int64_t i = r + u * kWarps;
-            float f[8], scale;
-            unpack8<T>(f, v[u]);
+            const float2 f[4] = {unpack2<T>(v[u].x), unpack2<T>(v[u].y), unpack2<T>(v[u].z), unpack2<T>(v[u].w)};
+            float scale;
             const uint2 q = block_codes(f, &scale);
             if (!live || i >= part.end) continue;
             *reinterpret_cast<uint2 *>(codes + i * p.codes.row_stride) = q;

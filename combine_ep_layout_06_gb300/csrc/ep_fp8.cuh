@@ -49,7 +49,9 @@ __device__ __forceinline__ float quot_recip(float x, float scale, float r) {
 // with RN(1/448) and the same one-FMA correction.  Equal to the IEEE
 // quotient for every finite non-negative bf16 a (proved on the host in exact
 // rational arithmetic, and compared on the device for every positive finite
-// a by fp8_quotient_check_kernel); a = inf gives inf.
+// a by fp8_quotient_check_kernel), and for other a that are far from underflow by
+// the theorem of the paper above (1/448 is rounded correctly, the first product is
+// within a unit of the quotient); a = inf gives inf.
 __device__ __forceinline__ float block_scale(float a) {
 #if EP_FP8_RECIP_QUOT
     constexpr float kInv448 = 0x1.24924ap-9f;   // RN(1/448)
@@ -75,28 +77,49 @@ __device__ __forceinline__ uint32_t quant4_recip(const float *f, float scale, fl
     return packed;
 }
 
-// A block of 128 values over 16 neighbouring lanes, 8 values a lane: this lane's
-// codes (byte i = value i) and the block's scale.  By whole warps.  The maximum is
-// taken of the magnitudes' bits, above which infinities and NaN stand: such a
-// block is NaN as a whole.
-__device__ __forceinline__ uint2 block_codes(const float *f, float *scale) {
-    uint32_t a = 0;
+// 4 values, as two pairs: quot_recip's steps two at a time.
+__device__ __forceinline__ uint32_t quant4_recip(const float2 *f, float scale, float r) {
+    uint32_t packed = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
+    for (int i = 0; i < 2; ++i) {
+        const float2 q0 = mul2_rn(f[i], both(r));
+        const float2 res = fma2_rn(q0, both(scale), make_float2(-f[i].x, -f[i].y));
+        const __nv_fp8x2_storage_t q =
+            __nv_cvt_float2_to_fp8x2(fma2_rn(res, both(-r), q0), __NV_SATFINITE, __NV_E4M3);
+        packed |= (uint32_t)q << (16 * i);
+    }
+    return packed;
+}
+// The larger magnitude; NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// A block of 128 values over 16 neighbouring lanes, 4 pairs a lane: this lane's
+// codes (byte i = value i) and the block's scale.  By whole warps.  A block with
+// a NaN or an infinity is NaN as a whole.
+__device__ __forceinline__ uint2 block_codes(const float2 *f, float *scale) {
+    float a = max_nan(fabsf(f[0].x), fabsf(f[0].y));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (a >= 0x7f800000u) {
+    for (int i = 1; i < 4; ++i) a = max_nan(max_nan(a, fabsf(f[i].x)), fabsf(f[i].y));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (a >= 0x1p-80f && a <= 0x1.fffffep127f) { // so that the scale is past 2^-90
+        const float s = block_scale(a), r = __frcp_rn(s);
+        *scale = s;
+        return make_uint2(quant4_recip(f, s, r), quant4_recip(f + 2, s, r));
+    }
+    if (!(a <= 0x1.fffffep127f)) {
         *scale = __uint_as_float(0x7fffffffu);
         return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
     }
-    const float s = __fdiv_rn(__uint_as_float(a), 448.0f);
+    const float s = __fdiv_rn(a, 448.0f);
     *scale = s;
     if (s == 0.f) return make_uint2(0u, 0u);
-    if (s >= 0x1p-90f) {
-        const float r = __frcp_rn(s);
-        return make_uint2(quant4_recip(f, s, r), quant4_recip(f + 4, s, r));
-    }
-    return make_uint2(quant4(f, s), quant4(f + 4, s));
+    const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    return make_uint2(quant4(v, s), quant4(v + 4, s));
 }
 // 8 codes -> 8 values, code * scale.
 __device__ __forceinline__ void block_values(float *v, const uint2 &q, float scale) {
@@ -104,9 +127,9 @@ __device__ __forceinline__ void block_values(float *v, const uint2 &q, float sca
     for (int i = 0; i < 4; ++i) {
         const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1)));
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        v[2 * i] = f.x * scale;
-        v[2 * i + 1] = f.y * scale;
+        const float2 f = mul2_rn(__half22float2(__half2(h)), both(scale));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
     }
 }
 

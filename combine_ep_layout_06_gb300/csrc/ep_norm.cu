@@ -30,38 +30,48 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw<T> load_chunk(con
     }
     return r;
 }
-template <typename T> __device__ __forceinline__ void values(float *f, const Raw<T> &r) {
-    const T *e = reinterpret_cast<const T *>(r.q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f32(e[i]);
-}
-template <typename T, bool VEC> __device__ __forceinline__ void store_chunk(T *p, const float *f, int n) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        store8<T>(p, f);
-    } else if constexpr (VEC) {
-        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+// As pairs: sums and scalings are two-wide instructions.
+template <typename T> __device__ __forceinline__ void values(float2 *f, const Raw<T> &r) {
+    if constexpr (sizeof(T) == 2) {
+        f[0] = unpack2<T>(r.q[0].x);
+        f[1] = unpack2<T>(r.q[0].y);
+        f[2] = unpack2<T>(r.q[0].z);
+        f[3] = unpack2<T>(r.q[0].w);
     } else {
 #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[2 * i] = make_float2(__uint_as_float(r.q[i].x), __uint_as_float(r.q[i].y));
+            f[2 * i + 1] = make_float2(__uint_as_float(r.q[i].z), __uint_as_float(r.q[i].w));
+        }
+    }
+}
+template <typename T> __device__ __forceinline__ Raw<T> packed(const float2 *f) {
+    Raw<T> r;
+    if constexpr (sizeof(T) == 2) {
+        r.q[0] = make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            r.q[i] = make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y), __float_as_uint(f[2 * i + 1].x),
+                                __float_as_uint(f[2 * i + 1].y));
+    }
+    return r;
+}
+template <typename T, bool VEC> __device__ __forceinline__ void store_chunk(T *p, const Raw<T> &r, int n) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.q[i];
+    } else {
+        const T *e = reinterpret_cast<const T *>(r.q);
+#pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = rounded<T>(f[i]);
+            if (i < n) p[i] = e[i];
     }
 }
 // 8 weights, in the rows' type or fp32.
-template <typename T, bool VEC> __device__ __forceinline__ void load_weights(float *f, const void *w, bool w32, int c, int n) {
-    if (w32) {
-        const float *p = static_cast<const float *>(w) + c;
-        if constexpr (VEC) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = i < n ? __ldg(p + i) : 0.f;
-        }
-    } else {
-        values<T>(f, load_chunk<T, VEC>(static_cast<const T *>(w) + c, n));
-    }
+template <typename T, bool VEC> __device__ __forceinline__ void load_weights(float2 *f, const void *w, bool w32, int c, int n) {
+    if (w32) values<float>(f, load_chunk<float, VEC>(static_cast<const float *>(w) + c, n));
+    else values<T>(f, load_chunk<T, VEC>(static_cast<const T *>(w) + c, n));
 }
 
 // Sums over the threads that share a row: a warp, or the whole block.
@@ -102,70 +112,64 @@ __device__ __forceinline__ int64_t row_at(const ep_rows_t &r, int seg, int row) 
     return seg * r.rank_stride + row * r.row_stride;
 }
 
-template <typename T, int CH, bool VEC, bool EIGHT>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p, int tpr) {
-    __shared__ float part[1][32];
-    const int t = threadIdx.x % tpr;
-    const int64_t index = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    if (index >= (int64_t)p.R * p.rows) return;  // the whole warp: more warps a block only with a warp a row
-    const int seg = (int)(index / p.rows), row = (int)(index - (int64_t)seg * p.rows);
-    const T *x = static_cast<const T *>(p.x.ptr) + row_at(p.x, seg, row);
-    const T *res = p.residual.ptr ? static_cast<const T *>(p.residual.ptr) + row_at(p.residual, seg, row) : nullptr;
-    T *total = p.total.ptr ? static_cast<T *>(p.total.ptr) + row_at(p.total, seg, row) : nullptr;
-    float h[CH][8];
-    {
-        Raw<T> a[CH], b[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-            if (c < p.H) {
-                a[i] = load_chunk<T, VEC>(x + c, p.H - c);
-                if (res) b[i] = load_chunk<T, VEC>(res + c, p.H - c);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-            if (c < p.H) {
-                values<T>(h[i], a[i]);
-                if (res) {
-                    float f[8];
-                    values<T>(f, b[i]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[i][j] = f32(rounded<T>(h[i][j] + f[j]));
-                }
-                if (total) store_chunk<T, VEC>(total + c, h[i], p.H - c);
-            }
-        }
-    }
-    float s[1] = {0.f};
+// 1 / sqrt(mean(h^2) + eps) from the sum of squares.
+template <int CH> __device__ __forceinline__ float inverse_root(const float2 (*h)[4], float sum, int H, float eps, int tpr, float (*part)[32]) {
+    if (sum != __int_as_float(0x7f800000)) return rsqrtf(sum / H + eps);
+    float s[1] = {0.f};                          // the same for the whole row
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += h[i][j] * h[i][j];
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = mul2_rn(h[i][j], both(kShrink));
+            s[0] += v.x * v.x + v.y * v.y;
+        }
     row_sums<1>(s, tpr, part);
-    float r = rsqrtf(s[0] / p.H + p.eps);
-    if (s[0] == __int_as_float(0x7f800000)) {    // the same for the whole row
-        s[0] = 0.f;
+    return rsqrtf(s[0] / H) * kShrink;
+}
+
+// A row's chunks, `t` of `tpr` threads: total = x + residual, written if wanted,
+// and its squares' sum so far.
+template <typename T, int CH, bool VEC>
+__device__ __forceinline__ float make_total(float2 (*h)[4], const Raw<T> *a, const Raw<T> *b, bool add, T *total, int H, int t, int tpr) {
+    float2 s = both(0.f);
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < CH; ++i) {
+        const int c = (t + i * tpr) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += (h[i][j] * kShrink) * (h[i][j] * kShrink);
-        row_sums<1>(s, tpr, part);
-        r = rsqrtf(s[0] / p.H) * kShrink;
+        for (int j = 0; j < 4; ++j) h[i][j] = both(0.f);
+        if (c < H) {
+            values<T>(h[i], a[i]);
+            Raw<T> sum = a[i];
+            if (add) {
+                float2 f[4];
+                values<T>(f, b[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = add2_rn(h[i][j], f[j]);
+                sum = packed<T>(f);
+                values<T>(h[i], sum);
+            }
+            if (total) store_chunk<T, VEC>(total + c, sum, H - c);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma2_rn(h[i][j], h[i][j], s);
     }
+    return s.x + s.y;
+}
+
+// y, or its codes and scales.
+template <typename T, int CH, bool VEC, bool EIGHT>
+__device__ __forceinline__ void write_normed(const NormParams &p, int seg, int row, const float2 (*h)[4], float r, int t, int tpr) {
     if constexpr (EIGHT) {
         uint8_t *y = static_cast<uint8_t *>(p.y.ptr) + row_at(p.y, seg, row);
         float *scales = static_cast<float *>(p.scales.ptr) + row_at(p.scales, seg, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (t + i * tpr) * 8;
-            float f[8], w[8] = {};
+            if (c - t % 32 * 8 >= p.H) continue; // the whole warp: a block's codes need all its lanes
+            float2 f[4], w[4] = {};
             if (c < p.H) load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = c < p.H ? h[i][j] * r * w[j] : 0.f;
+            for (int j = 0; j < 4; ++j) f[j] = c < p.H ? mul2_rn(mul2_rn(h[i][j], both(r)), w[j]) : both(0.f);
             float scale;
             const uint2 q = block_codes(f, &scale);
             if (c >= p.H) continue;
@@ -183,20 +187,50 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p, i
         for (int i = 0; i < CH; ++i) {
             const int c = (t + i * tpr) * 8;
             if (c >= p.H) continue;
-            float w[8];
+            float2 w[4];
             load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= h[i][j] * r;
-            store_chunk<T, VEC>(y + c, w, p.H - c);
+            for (int j = 0; j < 4; ++j) w[j] = mul2_rn(mul2_rn(h[i][j], both(r)), w[j]);
+            store_chunk<T, VEC>(y + c, packed<T>(w), p.H - c);
         }
     }
+}
+
+// ---- a row a block (or a warp), straight from memory
+
+template <typename T, int CH, bool VEC, bool EIGHT, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int tpr) {
+    __shared__ float part[1][32];
+    grid_dependency_wait();
+    grid_dependents_may_launch();
+    const int t = threadIdx.x % tpr;
+    const int64_t index = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    if (index >= (int64_t)p.R * p.rows) return;  // the whole warp: more warps a block only with a warp a row
+    const int seg = (int)(index / p.rows), row = (int)(index - (int64_t)seg * p.rows);
+    const T *x = static_cast<const T *>(p.x.ptr) + row_at(p.x, seg, row);
+    const T *res = p.residual.ptr ? static_cast<const T *>(p.residual.ptr) + row_at(p.residual, seg, row) : nullptr;
+    Raw<T> a[CH], b[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = (t + i * tpr) * 8;
+        if (c < p.H) {
+            a[i] = load_chunk<T, VEC>(x + c, p.H - c);
+            if (res) b[i] = load_chunk<T, VEC>(res + c, p.H - c);
+        }
+    }
+    float2 h[CH][4];
+    float s[1] = {make_total<T, CH, VEC>(h, a, b, res, p.total.ptr ? static_cast<T *>(p.total.ptr) + row_at(p.total, seg, row) : nullptr,
+                                         p.H, t, tpr)};
+    row_sums<1>(s, tpr, part);
+    write_normed<T, CH, VEC, EIGHT>(p, seg, row, h, inverse_root<CH>(h, s[0], p.H, p.eps, tpr, part), t, tpr);
 }
 
 // ---------------------------------------------------------------- gradient
 // A block takes every gridDim-th row and keeps its sums for grad_weight in
 // registers; column_kernel joins the blocks' sums in order.
 
-constexpr int kParts = 304;                      // blocks at most, two for each SM
+constexpr int kSms = 152, kParts = 2 * kSms;     // blocks at most where a block keeps no rows ahead
+constexpr int kMostBlocks = 8 * kSms;
 
 struct NormGradParams {
     int R, rows, H;
@@ -207,103 +241,257 @@ struct NormGradParams {
     float *part;                                 // [rows taken at a time][H]
 };
 
-template <typename T, int CH, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const NormGradParams p, int tpr) {
+// A row's sums, h^2 and u h, and what its outputs need of them.
+struct RowGrad {
+    float2 squares = {0.f, 0.f}, inner = {0.f, 0.f};
+    float r, mean;               // mean(u n), n = h r the normed row
+
+    __device__ __forceinline__ void add(const float2 *h, const float2 *g, const float2 *w) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            squares = fma2_rn(h[j], h[j], squares);
+            inner = fma2_rn(mul2_rn(g[j], w[j]), h[j], inner);
+        }
+    }
+    __device__ __forceinline__ void sums(float *s) const {
+        s[0] = squares.x + squares.y;
+        s[1] = inner.x + inner.y;
+    }
+    // From the sums of h (or of h * kShrink, where those of h do not fit).
+    __device__ __forceinline__ void set(const float *s, int H, float eps, bool shrunk) {
+        r = rsqrtf(s[0] / H + (shrunk ? 0.f : eps));
+        mean = s[1] / H * r;
+        if (shrunk) r *= kShrink;
+    }
+    // 8 values of the row's gradient, added to f; the weight's is added to dw.
+    __device__ __forceinline__ void out(float2 *f, float2 *dw, const float2 *h, const float2 *g, const float2 *w) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 n = mul2_rn(h[j], both(r));
+            dw[j] = fma2_rn(g[j], n, dw[j]);
+            f[j] = fma2_rn(fma2_rn(n, both(-mean), mul2_rn(g[j], w[j])), both(r), f[j]);
+        }
+    }
+};
+__device__ __forceinline__ void shrink8(float2 *h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(kShrink));
+}
+template <int CH> __device__ __forceinline__ void write_part(const NormGradParams &p, int64_t place, const float2 (*dw)[4], int t, int tpr) {
+    float *mine = p.part + place * p.H;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = (t + i * tpr) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < p.H) mine[c + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+    }
+}
+
+template <typename T, int CH, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradParams p, int tpr) {
     __shared__ float part[2][32];
+    grid_dependency_wait();
+    grid_dependents_may_launch();
     const int t = threadIdx.x % tpr, per = blockDim.x / tpr;
     const int64_t first = (int64_t)blockIdx.x * per + threadIdx.x / tpr, step = (int64_t)gridDim.x * per;
-    float dw[CH][8] = {};
+    float2 dw[CH][4] = {};
     for (int64_t index = first; index < (int64_t)p.R * p.rows; index += step) {
         const int seg = (int)(index / p.rows), row = (int)(index - (int64_t)seg * p.rows);
         const T *x = static_cast<const T *>(p.x.ptr) + row_at(p.x, seg, row);
         const T *grad = static_cast<const T *>(p.grad.ptr) + row_at(p.grad, seg, row);
-        float h[CH][8], u[CH][8];
-        float s[2] = {0.f, 0.f};
-        Raw<T> a[CH], b[CH];
+        const T *total = p.grad_total.ptr ? static_cast<const T *>(p.grad_total.ptr) + row_at(p.grad_total, seg, row) : nullptr;
+        T *out = static_cast<T *>(p.grad_x.ptr) + row_at(p.grad_x, seg, row);
+        Raw<T> a[CH], b[CH], more[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (t + i * tpr) * 8;
             if (c < p.H) {
                 a[i] = load_chunk<T, VEC>(x + c, p.H - c);
                 b[i] = load_chunk<T, VEC>(grad + c, p.H - c);
+                if (total) more[i] = load_chunk<T, VEC>(total + c, p.H - c);      // before grad_x, perhaps the same rows, is written
             }
         }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = u[i][j] = 0.f;
-            if (c < p.H) {
-                float w[8];
-                values<T>(h[i], a[i]);
-                values<T>(u[i], b[i]);
-                load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[0] += h[i][j] * h[i][j];
-                    s[1] += u[i][j] * w[j] * h[i][j];
-                }
-            }
-        }
-        row_sums<2>(s, tpr, part);
-        float shrink = 1.f;
-        float r = rsqrtf(s[0] / p.H + p.eps);
-        if (s[0] == __int_as_float(0x7f800000)) {        // the same for the whole row
-            shrink = kShrink;
-            s[0] = s[1] = 0.f;
+        float s[2];
+        RowGrad rg;
+        bool shrunk = false;
+        for (;;) {
+            RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int c = (t + i * tpr) * 8;
-                float w[8] = {};
-                if (c < p.H) load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float v = h[i][j] * kShrink;
-                    s[0] += v * v;
-                    s[1] += u[i][j] * w[j] * v;
-                }
+                if (c >= p.H) continue;
+                float2 h[4], g[4], w[4];
+                values<T>(h, a[i]);
+                values<T>(g, b[i]);
+                load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
+                if (shrunk) shrink8(h);
+                sum.add(h, g, w);
             }
+            sum.sums(s);
             row_sums<2>(s, tpr, part);
-            r = rsqrtf(s[0] / p.H);
+            if (shrunk || s[0] != __int_as_float(0x7f800000)) break;      // the same for the whole row
+            shrunk = true;
         }
-        const float mean = s[1] / p.H * r;               // mean(u * n), n = total * r the normed row
-        T *out = static_cast<T *>(p.grad_x.ptr) + row_at(p.grad_x, seg, row);
-        const T *more = p.grad_total.ptr
-                            ? static_cast<const T *>(p.grad_total.ptr) + row_at(p.grad_total, seg, row) : nullptr;
+        rg.set(s, p.H, p.eps, shrunk);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int c = (t + i * tpr) * 8;
             if (c >= p.H) continue;
-            float w[8], f[8] = {};
+            float2 h[4], g[4], w[4], f[4] = {};
+            values<T>(h, a[i]);
+            values<T>(g, b[i]);
             load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
-            if (more) {
-                // plain loads: grad_x may be the same rows
-                if constexpr (VEC) {
-                    Raw<T> m;
-#pragma unroll
-                    for (int k = 0; k < (int)sizeof(T) / 2; ++k) m.q[k] = reinterpret_cast<const uint4 *>(more + c)[k];
-                    values<T>(f, m);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = c + j < p.H ? f32(more[c + j]) : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = h[i][j] * shrink * r;
-                dw[i][j] += u[i][j] * n;
-                f[j] += (u[i][j] * w[j] - n * mean) * r * shrink;
-            }
-            store_chunk<T, VEC>(out + c, f, p.H - c);
+            if (total) values<T>(f, more[i]);
+            rg.out(f, dw[i], h, g, w);
+            store_chunk<T, VEC>(out + c, packed<T>(f), p.H - c);
         }
     }
-    float *mine = p.part + first * p.H;
+    write_part<CH>(p, first, dw, t, tpr);
+}
+
+// ---- many rows: a block goes from row to row and has the next ones brought into
+// shared memory by bulk copies meanwhile, so that reads never pause.
+
+constexpr int kMaxRing = 8;
+constexpr uint64_t kRingWaitNs = 1000000000ull;
+
+struct Ring {
+    uint64_t *full;
+    unsigned char *rows;
+    int stages, tensors, bytes;                  // bytes of a row
+    int *gave_up;
+
+    __device__ unsigned char *at(int s, int tensor) const { return rows + ((size_t)s * tensors + tensor) * bytes; }
+    // By one thread: rows of all tensors into stage s.
+    __device__ void load(int s, const void *const *from) const {
+        mbar_expect_tx(&full[s], tensors * bytes);
+        for (int i = 0; i < tensors; ++i) bulk_load<false>(at(s, i), from[i], bytes, &full[s], 0);
+    }
+    // By one thread, after a wait that gave up: as many of the last loads as come.
+    __device__ void drain(int64_t loads) const {
+        for (int64_t n = loads > stages ? loads - stages : 0; n < loads; ++n)
+            mbar_wait(&full[n % stages], (uint32_t)(n / stages) & 1u, kRingWaitNs);
+    }
+    // By every thread: a row is there.  After a wait of a second all others end at once.
+    __device__ void wait(int s, uint32_t phase) const {
+        if (mbar_try_wait(&full[s], phase) || *(volatile int *)gave_up) return;
+        if (!mbar_wait(&full[s], phase, kRingWaitNs)) *(volatile int *)gave_up = 1;
+    }
+};
+template <typename T> __device__ __forceinline__ Raw<T> ring_chunk(const unsigned char *row, int c) {
+    Raw<T> r;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = (t + i * tpr) * 8;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4 *>(row + (size_t)c * sizeof(T))[i];
+    return r;
+}
+// A block's sums with one barrier: `slot` alternates.
+template <int N> __device__ __forceinline__ void block_sums(float *v, float (*part)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < p.H) mine[c + j] = dw[i][j];
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (lane == 0) part[i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = lane < warps ? part[i][lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+}
+
+constexpr int kGradRingThreads = 512;
+template <typename T, int CH, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGradParams p, int stages, uint32_t *error) {
+    extern __shared__ __align__(128) unsigned char ring_rows[];
+    __shared__ uint64_t full[kMaxRing];
+    __shared__ float part[3][2][32];
+    __shared__ int gave_up;
+    const int t = threadIdx.x, tpr = blockDim.x;
+    const Ring ring = {full, ring_rows, stages, p.grad_total.ptr ? 3 : 2, p.H * (int)sizeof(T), &gave_up};
+    if (t == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        mbar_init_fence();
+        gave_up = 0;
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_dependents_may_launch();
+    const int all = p.R * p.rows;
+    int64_t loads = 0, next = blockIdx.x;        // of thread 0
+    int to = 0;
+    auto load = [&]() {
+        if (t != 0 || next >= all || *(volatile int *)&gave_up) return;
+        const int seg = (int)next / p.rows, row = (int)next - seg * p.rows;
+        const void *from[3] = {static_cast<const T *>(p.x.ptr) + row_at(p.x, seg, row),
+                               static_cast<const T *>(p.grad.ptr) + row_at(p.grad, seg, row),
+                               static_cast<const T *>(p.grad_total.ptr) + row_at(p.grad_total, seg, row)};
+        ring.load(to, from);
+        ++loads;
+        next += gridDim.x;
+        if (++to == stages) to = 0;
+    };
+    for (int s = 0; s < stages - 1; ++s) load();
+    float2 dw[CH][4] = {};
+    int s = 0;
+    uint32_t phase = 0, turn = 0;
+    for (int64_t index = blockIdx.x; index < all; index += gridDim.x) {
+        const int seg = (int)index / p.rows, row = (int)index - seg * p.rows;
+        T *out = static_cast<T *>(p.grad_x.ptr) + row_at(p.grad_x, seg, row);
+        ring.wait(s, phase);
+        // The row is read twice, before and after its sums are known, so that
+        // registers suffice for two blocks an SM.
+        float v[2];
+        auto sums = [&](bool shrunk) {
+            RowGrad sum;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int c = (t + i * tpr) * 8;
+                if (c >= p.H) continue;
+                float2 h[4], g[4], w[4];
+                values<T>(h, ring_chunk<T>(ring.at(s, 0), c));
+                values<T>(g, ring_chunk<T>(ring.at(s, 1), c));
+                load_weights<T, true>(w, p.weight, p.w32, c, p.H - c);
+                if (shrunk) shrink8(h);
+                sum.add(h, g, w);
+            }
+            sum.sums(v);
+        };
+        sums(false);
+        block_sums<2>(v, part[turn]);            // and every thread is done with the row before
+        load();
+        const bool shrunk = v[0] == __int_as_float(0x7f800000);      // the same for the whole row
+        if (shrunk) {
+            sums(true);
+            row_sums<2>(v, tpr, part[2]);
+        }
+        RowGrad rg;
+        rg.set(v, p.H, p.eps, shrunk);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = (t + i * tpr) * 8;
+            if (c >= p.H) continue;
+            float2 h[4], g[4], w[4], f[4] = {};
+            values<T>(h, ring_chunk<T>(ring.at(s, 0), c));
+            values<T>(g, ring_chunk<T>(ring.at(s, 1), c));
+            load_weights<T, true>(w, p.weight, p.w32, c, p.H - c);
+            if (p.grad_total.ptr) values<T>(f, ring_chunk<T>(ring.at(s, 2), c));
+            rg.out(f, dw[i], h, g, w);
+            store_chunk<T, true>(out + c, packed<T>(f), p.H - c);
+        }
+        turn ^= 1u;
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+    write_part<CH>(p, blockIdx.x, dw, t, tpr);
+    if (t == 0 && *(volatile int *)&gave_up) {
+        ring.drain(loads);
+        if (error) atomicOr(error, EP_DEVERR_TIMEOUT);
     }
 }
 
@@ -311,6 +499,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const NormGradPa
 constexpr int kColumnRows = 16;
 template <typename T> __global__ void __launch_bounds__(32 * kColumnRows) column_kernel(const float *part, int n, int H, T *out) {
     __shared__ float sums[kColumnRows][32];
+    grid_dependency_wait();
+    grid_dependents_may_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < H)
@@ -357,34 +547,70 @@ bool vectors(const ep_rows_t &r, int ranks, int64_t size, int64_t bytes = 16) {
                       (ranks == 1 || r.rank_stride * size % bytes == 0));
 }
 
-// Threads a row, chunks a thread, rows a block.
+// Threads a row, chunks a thread, rows a block.  A warp a row where `most`
+// chunks a lane hold it, else a block.
 struct Shape {
     int chunks, tpr, per;
 };
 Shape shape_of(int H, int most) {
     const int all = (H + 7) / 8;
-    Shape s;
-    s.chunks = all <= 32 ? 1 : all <= 64 ? 2 : all <= 32 * most ? most : 1;
-    if (all <= 32 * most) {
-        s.tpr = 32;
-        s.per = 8;
-        return s;
-    }
-    while (s.chunks < most || (all + s.chunks - 1) / s.chunks > kMaxThreads) {
-        if (s.chunks == kMaxChunks) break;
-        s.chunks *= 2;
-    }
+    if (all <= 32 * most) return Shape{all <= 32 ? 1 : all <= 64 ? 2 : 4, 32, 8};
+    Shape s = {most, 0, 1};
+    while ((all + s.chunks - 1) / s.chunks > kMaxThreads) s.chunks *= 2;
     s.tpr = ((all + s.chunks - 1) / s.chunks + 31) / 32 * 32;
-    s.per = 1;
     return s;
 }
 
+// Stages of rows in `bytes` of shared memory, at most kMaxRing.
+int ring_stages(int64_t row_bytes, int tensors, int64_t bytes) {
+    const int64_t n = bytes / (row_bytes * tensors);
+    return (int)(n < kMaxRing ? n : kMaxRing);
+}
+constexpr int64_t kRingMost = 220 * 1024;
+constexpr int64_t kRingRow = 1024;               // bytes of a row at least
+
+template <typename... Params, typename... Args>
+cudaError_t launch_ring(void (*kernel)(Params...), std::atomic<bool> *configured, int blocks, int threads, size_t bytes, cudaStream_t st,
+                        Args &&...args) {
+    int dev;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[dev].load(std::memory_order_acquire)) {         // the attribute is per device
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingMost);
+        if (e != cudaSuccess) return e;
+        configured[dev].store(true, std::memory_order_release);
+    }
+    return launch_after_previous(kernel, blocks, threads, bytes, st, static_cast<Args &&>(args)...);
+}
+
+// How a norm of many rows goes through the ring; stages 0: it does not.
+struct RingShape {
+    int stages, chunks, threads, blocks;
+};
+RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
+    const int64_t row = d.width * size_of(d.dtype), rows = (int64_t)d.ranks * d.rows;
+    RingShape r = {0, 2, 0, 0};
+    r.threads = ((d.width / 8 + 1) / 2 + 31) / 32 * 32;
+    if (!vec || row < kRingRow || r.threads > kGradRingThreads) return r;
+    int blocks = 1024 / r.threads;                               // an SM's, by registers
+    if (blocks > 8) blocks = 8;
+    while (blocks > 1 && ring_stages(row, total ? 3 : 2, kRingMost / blocks) < 3) --blocks;
+    if (blocks == 1 && ring_stages(row, total ? 3 : 2, kRingMost / 2) == 2) blocks = 2;
+    const int stages = ring_stages(row, total ? 3 : 2, kRingMost / blocks);
+    r.blocks = kSms * blocks;
+    if (stages >= 2 && rows >= 4 * r.blocks) r.stages = stages < 4 ? stages : 4;
+    return r;
+}
+
 Shape grad_shape(const ep_norm_desc_t &d) { return shape_of(d.width, 2); }
-// Rows that the gradient's blocks take at a time.
+// Parts of the weight's gradient at most: rows that the blocks take at a time.
 int64_t grad_parts(const ep_norm_desc_t &d) {
     const Shape s = grad_shape(d);
     const int64_t rows = (int64_t)d.ranks * d.rows, blocks = (rows + s.per - 1) / s.per;
     return (blocks < kParts ? blocks : kParts) * s.per;
+}
+int64_t most_parts(const ep_norm_desc_t &d) {
+    const int64_t rows = (int64_t)d.ranks * d.rows, n = grad_parts(d);
+    return rows < kMostBlocks ? n < rows ? rows : n : n < kMostBlocks ? kMostBlocks : n;
 }
 
 }  // namespace
@@ -395,9 +621,9 @@ using namespace ep;
 extern "C" {
 
 ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, const ep_rows_t *total,
-                        const ep_rows_t *y, const ep_rows_t *scales, void *stream) {
+                        const ep_rows_t *y, const ep_rows_t *scales, uint32_t *d_error, void *stream) {
     EP_RANGE("ep_rms_norm");
-    if (!valid(d) || !residual || !total || !y || !scales) return EP_ERR_INVALID_ARGS;
+    if (!valid(d) || !residual || !total || !y || !scales || !aligned(d_error, 4)) return EP_ERR_INVALID_ARGS;
     if (d->rows == 0) return EP_SUCCESS;
     const bool eight = scales->ptr != nullptr;
     const int64_t size = size_of(d->dtype);
@@ -411,34 +637,40 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, cons
     const bool vec = d->width % 8 == 0 && aligned(d->weight, 16) && vectors(d->x, d->ranks, size) &&
                      vectors(*residual, d->ranks, size) && vectors(*total, d->ranks, size) &&
                      vectors(*y, d->ranks, eight ? 1 : size, eight ? 8 : 16);
-    const Shape s = shape_of(d->width, kMaxChunks);
     const int64_t rows = (int64_t)d->ranks * d->rows;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    // few rows: more threads for each, so that all of it is on its way at once
+    const Shape s = shape_of(d->width, rows <= 304 ? 1 : kMaxChunks);
     const unsigned blocks = (unsigned)((rows + s.per - 1) / s.per), threads = s.tpr * s.per;
     with_any_type(d->dtype, [&](auto type) {
         using T = decltype(type);
         with_chunks(s.chunks, [&](auto chunks) {
             constexpr int CH = decltype(chunks)::value;
-            if (eight && vec) norm_kernel<T, CH, true, true><<<blocks, threads, 0, st>>>(p, s.tpr);
-            else if (eight) norm_kernel<T, CH, false, true><<<blocks, threads, 0, st>>>(p, s.tpr);
-            else if (vec) norm_kernel<T, CH, true, false><<<blocks, threads, 0, st>>>(p, s.tpr);
-            else norm_kernel<T, CH, false, false><<<blocks, threads, 0, st>>>(p, s.tpr);
+            auto go = [&](auto most) {
+                constexpr int N = decltype(most)::value;
+                auto kernel = eight ? (vec ? norm_kernel<T, CH, true, true, N> : norm_kernel<T, CH, false, true, N>)
+                                    : (vec ? norm_kernel<T, CH, true, false, N> : norm_kernel<T, CH, false, false, N>);
+                e = launch_after_previous(kernel, blocks, threads, 0, st, p, s.tpr);
+            };
+            if (threads <= 256) go(std::integral_constant<int, 256>());
+            else go(std::integral_constant<int, kMaxThreads>());
         });
     });
-    return launched();
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 ep_status_t ep_rms_norm_workspace(const ep_norm_desc_t *d, size_t *bytes) {
     if (!valid(d) || !bytes) return EP_ERR_INVALID_ARGS;
-    *bytes = (size_t)grad_parts(*d) * d->width * 4;
+    *bytes = (size_t)most_parts(*d) * d->width * 4;
     return EP_SUCCESS;
 }
 
 ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad, const ep_rows_t *grad_total,
                                  const ep_rows_t *grad_x, void *d_grad_weight, void *d_workspace,
-                                 size_t workspace_bytes, void *stream) {
+                                 size_t workspace_bytes, uint32_t *d_error, void *stream) {
     EP_RANGE("ep_rms_norm_backward");
-    if (!valid(d) || !grad || !grad_total || !grad_x || !d_grad_weight || !aligned(d_workspace, 16) ||
+    if (!valid(d) || !aligned(d_error, 4) || !grad || !grad_total || !grad_x || !d_grad_weight || !aligned(d_workspace, 16) ||
         !aligned(d_grad_weight, size_of(d->weight_dtype)))
         return EP_ERR_INVALID_ARGS;
     const int64_t size = size_of(d->dtype);
@@ -451,29 +683,48 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool w32 = d->weight_dtype == EP_DT_FP32;
     const Shape s = grad_shape(*d);
-    const int n = (int)grad_parts(*d);
+    int n = (int)grad_parts(*d);
     float *part = static_cast<float *>(d_workspace);
+    cudaError_t e = cudaSuccess;
     if (d->rows > 0) {
         const NormGradParams p = {d->ranks, d->rows, d->width, d->eps, w32 && d->dtype != EP_DT_FP32, d->weight,
                                   d->x, *grad, *grad_total, *grad_x, part};
         const bool vec = d->width % 8 == 0 && aligned(d->weight, 16) && vectors(d->x, d->ranks, size) &&
                          vectors(*grad, d->ranks, size) && vectors(*grad_total, d->ranks, size) &&
                          vectors(*grad_x, d->ranks, size);
+        const RingShape ring = grad_ring(*d, vec, grad_total->ptr);
         with_any_type(d->dtype, [&](auto type) {
             using T = decltype(type);
+            if (ring.stages) {
+                static std::atomic<bool> configured[2][kMaxDevices];
+                const size_t bytes = (size_t)ring.stages * (grad_total->ptr ? 3 : 2) * d->width * size;
+                n = ring.blocks;
+                e = ring.threads <= 448      // 72 registers a thread, else 64
+                        ? launch_ring(norm_grad_ring_kernel<T, 2, 448>, configured[0], n, ring.threads, bytes, st, p, ring.stages, d_error)
+                        : launch_ring(norm_grad_ring_kernel<T, 2, kGradRingThreads>, configured[1], n, ring.threads, bytes, st, p,
+                                      ring.stages, d_error);
+                return;
+            }
             with_chunks(s.chunks, [&](auto chunks) {
                 constexpr int CH = decltype(chunks)::value;
-                if (vec) norm_grad_kernel<T, CH, true><<<n / s.per, s.tpr * s.per, 0, st>>>(p, s.tpr);
-                else norm_grad_kernel<T, CH, false><<<n / s.per, s.tpr * s.per, 0, st>>>(p, s.tpr);
+                auto go = [&](auto most) {
+                    constexpr int N = decltype(most)::value;
+                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, true, N> : norm_grad_kernel<T, CH, false, N>, n / s.per,
+                                              s.tpr * s.per, 0, st, p, s.tpr);
+                };
+                if (s.tpr * s.per <= 256) go(std::integral_constant<int, 256>());
+                else if (s.tpr * s.per <= 512) go(std::integral_constant<int, 512>());
+                else go(std::integral_constant<int, kMaxThreads>());
             });
         });
     }
+    if (e != cudaSuccess) return EP_ERR_GPU_OP;
     with_any_type(d->weight_dtype, [&](auto type) {
         using T = decltype(type);
-        column_kernel<T><<<(d->width + 31) / 32, 32 * kColumnRows, 0, st>>>(part, n, d->width,
-                                                                           static_cast<T *>(d_grad_weight));
+        e = launch_after_previous(column_kernel<T>, (d->width + 31) / 32, 32 * kColumnRows, 0, st, part, n, d->width,
+                                  static_cast<T *>(d_grad_weight));
     });
-    return launched();
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 }  // extern "C"

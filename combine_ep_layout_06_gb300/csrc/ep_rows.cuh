@@ -57,6 +57,14 @@ template <typename T> __device__ __forceinline__ void store8(T *p, const float *
     *reinterpret_cast<uint4 *>(p) =
         make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
+// Two 16-bit values as two floats.
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t q);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t q) {
+    return make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t q) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&q));
+}
 template <typename T> __device__ __forceinline__ void unpack8(float *v, const uint4 &r) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll

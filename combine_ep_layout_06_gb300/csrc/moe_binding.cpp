@@ -625,7 +625,7 @@ PyObject *rms_norm(PyObject *const *a) {
         sc = here.empty(blocks, at::kFloat);
         scales = ep_rows_t{sc.data_ptr(), n.d.rows * (H / 128), H / 128};
     }
-    if (n.d.rows) check(ep_rms_norm(&n.d, &res, &total, &to, &scales, here.stream()), "ep_rms_norm");
+    if (n.d.rows) check(ep_rms_norm(&n.d, &res, &total, &to, &scales, error_ptr(here.index), here.stream()), "ep_rms_norm");
     if (eight && residual) return pack(y, sc, sum);
     if (eight) return pack(y, sc);
     if (residual) return pack(y, sum);
@@ -646,7 +646,8 @@ PyObject *rms_norm_backward(PyObject *const *a) {
     check(ep_rms_norm_workspace(&n.d, &need), "ep_rms_norm_workspace");
     Tensor scratch = here.empty({(int64_t)need}, at::kByte);
     const ep_rows_t to{dx.data_ptr(), n.d.rows * H, H};
-    check(ep_rms_norm_backward(&n.d, &g, &gt, &to, dw.data_ptr(), scratch.data_ptr(), need, here.stream()),
+    check(ep_rms_norm_backward(&n.d, &g, &gt, &to, dw.data_ptr(), scratch.data_ptr(), need,
+                               error_ptr(here.index), here.stream()),
           "ep_rms_norm_backward");
     return pack(dx, dw);
 }

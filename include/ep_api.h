@@ -592,7 +592,7 @@ typedef struct {
  * pre-quantised dispatch takes. */
 ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual,
                         const ep_rows_t *total, const ep_rows_t *y,
-                        const ep_rows_t *scales, void *stream);
+                        const ep_rows_t *scales, uint32_t *d_error, void *stream);
 
 /* The gradient, d->x being the forward's total, grad = dL/dy:
  *   u = grad * weight
@@ -608,7 +608,7 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
                                  const ep_rows_t *grad_total,
                                  const ep_rows_t *grad_x, void *d_grad_weight,
                                  void *d_workspace, size_t workspace_bytes,
-                                 void *stream);
+                                 uint32_t *d_error, void *stream);
 
 /* Activations kept in 8 bits between forward and backward, over rows grouped as in
  * ep_product_desc_t.  Rows outside every group are neither read nor written. */
