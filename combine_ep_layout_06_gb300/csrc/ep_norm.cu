@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int t
 // A block takes every gridDim-th row and keeps its sums for grad_weight in
 // registers; column_kernel joins the blocks' sums in order.
 
-constexpr int kSms = 152, kParts = 2 * kSms;     // blocks at most where a block keeps no rows ahead
+constexpr int kSms = 152, kParts = 3 * kSms;     // blocks at most where a block keeps no rows ahead
 constexpr int kMostBlocks = 8 * kSms;
 
 struct NormGradParams {
@@ -238,7 +238,7 @@ struct NormGradParams {
     bool w32;
     const void *weight;
     ep_rows_t x, grad, grad_total, grad_x;
-    float *part;                                 // [rows taken at a time][H]
+    float *part;                                 // [blocks][H]
 };
 
 // A row's sums, h^2 and u h, and what its outputs need of them.
@@ -277,19 +277,18 @@ __device__ __forceinline__ void shrink8(float2 *h) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(kShrink));
 }
-template <int CH> __device__ __forceinline__ void write_part(const NormGradParams &p, int64_t place, const float2 (*dw)[4], int t, int tpr) {
-    float *mine = p.part + place * p.H;
+template <int CH> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = (t + i * tpr) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c + j < p.H) mine[c + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+            if (c + j < H) to[c + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
     }
 }
 
 template <typename T, int CH, bool VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradParams p, int tpr) {
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) norm_grad_kernel(const NormGradParams p, int tpr) {
     __shared__ float part[2][32];
     grid_dependency_wait();
     grid_dependents_may_launch();
@@ -347,7 +346,23 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradParams
             store_chunk<T, VEC>(out + c, packed<T>(f), p.H - c);
         }
     }
-    write_part<CH>(p, first, dw, t, tpr);
+    float *mine = p.part + (int64_t)blockIdx.x * p.H;
+    if (tpr > 32) {
+        write_part<CH>(mine, p.H, dw, t, tpr);
+        return;
+    }
+    // a warp a row: the block's warps add theirs, in order
+    __shared__ float sums[THREADS == 256 ? 8 : 1][CH * 256];
+    const int warp = threadIdx.x / 32;
+    if constexpr (THREADS == 256) {
+        write_part<CH>(sums[warp], p.H, dw, t, tpr);
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.H; c += 256) {
+            float v = 0.f;
+            for (int w = 0; w < 8; ++w) v += sums[w][c];
+            mine[c] = v;
+        }
+    }
 }
 
 // ---- many rows: a block goes from row to row and has the next ones brought into
@@ -488,15 +503,15 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
             phase ^= 1u;
         }
     }
-    write_part<CH>(p, blockIdx.x, dw, t, tpr);
+    write_part<CH>(p.part + (int64_t)blockIdx.x * p.H, p.H, dw, t, tpr);
     if (t == 0 && *(volatile int *)&gave_up) {
         ring.drain(loads);
         if (error) atomicOr(error, EP_DEVERR_TIMEOUT);
     }
 }
 
-// Column sums of part [n][H]: 32 columns a block, 16 rows at a time.
-constexpr int kColumnRows = 16;
+// Column sums of part [n][H]: 32 columns a block, 32 rows at a time.
+constexpr int kColumnRows = 32;
 template <typename T> __global__ void __launch_bounds__(32 * kColumnRows) column_kernel(const float *part, int n, int H, T *out) {
     __shared__ float sums[kColumnRows][32];
     grid_dependency_wait();
@@ -504,7 +519,7 @@ template <typename T> __global__ void __launch_bounds__(32 * kColumnRows) column
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < H)
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < n; i += kColumnRows) s += part[(int64_t)i * H + c];
     sums[warp][lane] = s;
     __syncthreads();
@@ -590,7 +605,7 @@ RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
     const int64_t row = d.width * size_of(d.dtype), rows = (int64_t)d.ranks * d.rows;
     RingShape r = {0, 2, 0, 0};
     r.threads = ((d.width / 8 + 1) / 2 + 31) / 32 * 32;
-    if (!vec || row < kRingRow || r.threads > kGradRingThreads) return r;
+    if (!vec || row < kRingRow || r.threads < 64 || r.threads > kGradRingThreads) return r;
     int blocks = 1024 / r.threads;                               // an SM's, by registers
     if (blocks > 8) blocks = 8;
     while (blocks > 1 && ring_stages(row, total ? 3 : 2, kRingMost / blocks) < 3) --blocks;
@@ -602,15 +617,15 @@ RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
 }
 
 Shape grad_shape(const ep_norm_desc_t &d) { return shape_of(d.width, 2); }
-// Parts of the weight's gradient at most: rows that the blocks take at a time.
+// Parts of the weight's gradient, one a block.
 int64_t grad_parts(const ep_norm_desc_t &d) {
     const Shape s = grad_shape(d);
     const int64_t rows = (int64_t)d.ranks * d.rows, blocks = (rows + s.per - 1) / s.per;
-    return (blocks < kParts ? blocks : kParts) * s.per;
+    return blocks < kParts ? blocks : kParts;
 }
 int64_t most_parts(const ep_norm_desc_t &d) {
-    const int64_t rows = (int64_t)d.ranks * d.rows, n = grad_parts(d);
-    return rows < kMostBlocks ? n < rows ? rows : n : n < kMostBlocks ? kMostBlocks : n;
+    const int64_t rows = (int64_t)d.ranks * d.rows;
+    return rows < kMostBlocks ? rows : kMostBlocks;
 }
 
 }  // namespace
@@ -640,8 +655,9 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, cons
     const int64_t rows = (int64_t)d->ranks * d->rows;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    // few rows: more threads for each, so that all of it is on its way at once
-    const Shape s = shape_of(d->width, rows <= 304 ? 1 : kMaxChunks);
+    // Chunks a thread: 4 of 16 bits (32768 x 7168 to 8 bits 259 us, with 2 348) or 2 of fp32 (4096 x
+    // 16384 168 us, with 4 205); few rows: one, all of a row on its way at once (1.1 us less).
+    const Shape s = shape_of(d->width, rows <= 304 ? 1 : d->dtype == EP_DT_FP32 ? 2 : kMaxChunks);
     const unsigned blocks = (unsigned)((rows + s.per - 1) / s.per), threads = s.tpr * s.per;
     with_any_type(d->dtype, [&](auto type) {
         using T = decltype(type);
@@ -709,7 +725,7 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
                 constexpr int CH = decltype(chunks)::value;
                 auto go = [&](auto most) {
                     constexpr int N = decltype(most)::value;
-                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, true, N> : norm_grad_kernel<T, CH, false, N>, n / s.per,
+                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, true, N> : norm_grad_kernel<T, CH, false, N>, n,
                                               s.tpr * s.per, 0, st, p, s.tpr);
                 };
                 if (s.tpr * s.per <= 256) go(std::integral_constant<int, 256>());
