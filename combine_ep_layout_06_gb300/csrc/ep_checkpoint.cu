@@ -31,75 +31,98 @@ __device__ __forceinline__ Part part_of(const CheckpointParams &p) {
     return Part{g / p.gr.per, first + (int)(a < rows ? a : rows), first + (int)(b < rows ? b : rows)};
 }
 
-template <typename T> __global__ void __launch_bounds__(kWarps * 32) save_kernel(const CheckpointParams p) {
+// The largest magnitude among 8 16-bit values, NaN above all: the bits without
+// their signs stand in that order.
+template <typename T> __device__ __forceinline__ float largest(const uint4 &q) {
+    const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu), __vmaxu2(q.z & 0x7fff7fffu, q.w & 0x7fff7fffu));
+    const uint16_t top = (uint16_t)max(m >> 16, m & 0xffffu);
+    return f32(*reinterpret_cast<const T *>(&top));
+}
+
+template <typename T> __global__ void __launch_bounds__(kWarps * 32, 4) save_kernel(const CheckpointParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * kCols + lane * 8;
     const bool live = c < p.F;
+    grid_dependency_wait();
+    grid_dependents_may_launch();
     const Part part = part_of(p);
-    const T *x = static_cast<const T *>(p.x.ptr) + part.seg * p.x.rank_stride + c;
-    uint8_t *codes = static_cast<uint8_t *>(p.codes.ptr) + part.seg * p.codes.rank_stride + c;
-    float *scales = static_cast<float *>(p.scales.ptr) + part.seg * p.scales.rank_stride + c / 128;
-    for (int64_t r = part.first + warp; r < part.end; r += kWarps * kRows) {
+    const int64_t r0 = part.first + warp;
+    const T *x = static_cast<const T *>(p.x.ptr) + part.seg * p.x.rank_stride + r0 * p.x.row_stride + c;
+    uint8_t *codes = static_cast<uint8_t *>(p.codes.ptr) + part.seg * p.codes.rank_stride + r0 * p.codes.row_stride + c;
+    float *scales = static_cast<float *>(p.scales.ptr) + part.seg * p.scales.rank_stride + r0 * p.scales.row_stride + c / 128;
+    const int64_t xs = kWarps * p.x.row_stride, cs = kWarps * p.codes.row_stride, ss = kWarps * p.scales.row_stride;
+    for (int left = part.end - (int)r0; left > 0; left -= kWarps * kRows) {
         uint4 v[kRows];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t i = r + u * kWarps;
-            v[u] = live && i < part.end ? ld_stream16(x + i * p.x.row_stride) : make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < kRows; ++u)
+            v[u] = live && u * kWarps < left ? ld_stream16(x + u * xs) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int64_t i = r + u * kWarps;
+            if (u * kWarps >= left) break;       // the same for the warp
             const float2 f[4] = {unpack2<T>(v[u].x), unpack2<T>(v[u].y), unpack2<T>(v[u].z), unpack2<T>(v[u].w)};
             float scale;
-            const uint2 q = block_codes(f, &scale);
-            if (!live || i >= part.end) continue;
-            *reinterpret_cast<uint2 *>(codes + i * p.codes.row_stride) = q;
-            if ((lane & 15) == 0) scales[i * p.scales.row_stride] = scale;
+            const uint2 q = block_codes(f, largest<T>(v[u]), &scale);
+            if (!live) continue;
+            *reinterpret_cast<uint2 *>(codes + u * cs) = q;
+            if ((lane & 15) == 0) scales[u * ss] = scale;
         }
+        x += kRows * xs;
+        codes += kRows * cs;
+        scales += kRows * ss;
     }
 }
 
 template <typename T, bool GATED>
-__global__ void __launch_bounds__(kWarps * 32) restore_kernel(const CheckpointParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) restore_kernel(const CheckpointParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int N = GATED ? p.F / 2 : p.F;
     const int c = blockIdx.x * kCols + lane * 8;
+    grid_dependency_wait();
+    grid_dependents_may_launch();
     if (c >= N) return;
     const Part part = part_of(p);
-    T *y = static_cast<T *>(p.x.ptr) + part.seg * p.x.rank_stride + c;
-    const uint8_t *codes = static_cast<const uint8_t *>(p.codes.ptr) + part.seg * p.codes.rank_stride + c;
-    const float *scales = static_cast<const float *>(p.scales.ptr) + part.seg * p.scales.rank_stride;
-    const int b0 = c / 128, b1 = (c + N) / 128;      // 8 neighbours from a multiple of 8 on share a block
-    for (int64_t r = part.first + warp; r < part.end; r += kWarps * kRows) {
+    const int64_t r0 = part.first + warp;
+    T *y = static_cast<T *>(p.x.ptr) + part.seg * p.x.rank_stride + r0 * p.x.row_stride + c;
+    const uint8_t *codes = static_cast<const uint8_t *>(p.codes.ptr) + part.seg * p.codes.rank_stride + r0 * p.codes.row_stride + c;
+    // 8 neighbours from a multiple of 8 on share a block
+    const float *scales = static_cast<const float *>(p.scales.ptr) + part.seg * p.scales.rank_stride + r0 * p.scales.row_stride + c / 128;
+    const int up = (c + N) / 128 - c / 128;
+    const int64_t ys = kWarps * p.x.row_stride, cs = kWarps * p.codes.row_stride, ss = kWarps * p.scales.row_stride;
+    for (int left = part.end - (int)r0; left > 0; left -= kWarps * kRows) {
         uint2 q0[kRows], q1[kRows];
         float s0[kRows], s1[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int64_t i = r + u * kWarps;
-            if (i >= part.end) continue;
-            q0[u] = ld_stream8(codes + i * p.codes.row_stride);
-            s0[u] = __ldg(scales + i * p.scales.row_stride + b0);
+            if (u * kWarps >= left) break;
+            q0[u] = ld_stream8(codes + u * cs);
+            s0[u] = __ldg(scales + u * ss);
             if (GATED) {
-                q1[u] = ld_stream8(codes + i * p.codes.row_stride + N);
-                s1[u] = __ldg(scales + i * p.scales.row_stride + b1);
+                q1[u] = ld_stream8(codes + u * cs + N);
+                s1[u] = __ldg(scales + u * ss + up);
             }
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int64_t i = r + u * kWarps;
-            if (i >= part.end) continue;
-            float f[8];
+            if (u * kWarps >= left) break;
+            float2 f[4];
             block_values(f, q0[u], s0[u]);
             if (GATED) {
-                float up[8];
-                block_values(up, q1[u], s1[u]);
+                float2 w[4];
+                block_values(w, q1[u], s1[u]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = f[j] * sigmoidf(f[j]) * up[j];
-            } else {
-                activate8(p.act, f);
+                for (int j = 0; j < 4; ++j) f[j] = mul2_rn(silu2(f[j]), w[j]);
+            } else if (p.act != EP_ACT_NONE) {
+                float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+                activate8(p.act, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
             }
-            store8<T>(y + i * p.x.row_stride, f);
+            *reinterpret_cast<uint4 *>(y + u * ys) =
+                make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
         }
+        y += kRows * ys;
+        codes += kRows * cs;
+        scales += kRows * ss;
     }
 }
 
@@ -136,10 +159,11 @@ ep_status_t ep_checkpoint_save(const ep_checkpoint_desc_t *d, const ep_rows_t *x
         return EP_ERR_INVALID_ARGS;
     const CheckpointParams p = params(*d, *x, *codes, *scales);
     const dim3 grid((d->features + kCols - 1) / kCols, d->ranks * d->groups, p.splits);
+    cudaError_t e = cudaSuccess;
     with_type(d->dtype, [&](auto type) {
-        save_kernel<decltype(type)><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        e = launch_after_previous(save_kernel<decltype(type)>, grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream), p);
     });
-    return launched();
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 ep_status_t ep_checkpoint_restore(const ep_checkpoint_desc_t *d, const ep_rows_t *codes, const ep_rows_t *scales,
@@ -154,13 +178,13 @@ ep_status_t ep_checkpoint_restore(const ep_checkpoint_desc_t *d, const ep_rows_t
         return EP_ERR_INVALID_ARGS;
     const CheckpointParams p = params(*d, *y, *codes, *scales);
     const dim3 grid((N + kCols - 1) / kCols, d->ranks * d->groups, p.splits);
+    cudaError_t e = cudaSuccess;
     with_type(d->dtype, [&](auto type) {
         using T = decltype(type);
-        cudaStream_t st = static_cast<cudaStream_t>(stream);
-        if (gated) restore_kernel<T, true><<<grid, kWarps * 32, 0, st>>>(p);
-        else restore_kernel<T, false><<<grid, kWarps * 32, 0, st>>>(p);
+        e = launch_after_previous(gated ? restore_kernel<T, true> : restore_kernel<T, false>, grid, kWarps * 32, 0,
+                                  static_cast<cudaStream_t>(stream), p);
     });
-    return launched();
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 }  // extern "C"

@@ -77,37 +77,37 @@ __device__ __forceinline__ uint32_t quant4_recip(const float *f, float scale, fl
     return packed;
 }
 
-// 4 values, as two pairs: quot_recip's steps two at a time.
-__device__ __forceinline__ uint32_t quant4_recip(const float2 *f, float scale, float r) {
+// 4 values, as two pairs: quot_recip's steps two at a time, on the negated
+// quotient: with q = -x r the residual x + q scale and the correction q - res r
+// need no value's negative, and zeros keep their sign (x = -0: q = +0, res = +0,
+// q - 0 = +0).  The codes' signs are turned at the end.
+__device__ __forceinline__ uint32_t quant4_recip(const float2 *f, float scale, float minus_r) {
     uint32_t packed = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float2 q0 = mul2_rn(f[i], both(r));
-        const float2 res = fma2_rn(q0, both(scale), make_float2(-f[i].x, -f[i].y));
+        const float2 q0 = mul2_rn(f[i], both(minus_r));
+        const float2 res = fma2_rn(q0, both(scale), f[i]);
         const __nv_fp8x2_storage_t q =
-            __nv_cvt_float2_to_fp8x2(fma2_rn(res, both(-r), q0), __NV_SATFINITE, __NV_E4M3);
+            __nv_cvt_float2_to_fp8x2(fma2_rn(res, both(minus_r), q0), __NV_SATFINITE, __NV_E4M3);
         packed |= (uint32_t)q << (16 * i);
     }
-    return packed;
+    return packed ^ 0x80808080u;
 }
-// The larger magnitude; NaN where one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The largest magnitude; NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float m;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
     return m;
 }
 
 // A block of 128 values over 16 neighbouring lanes, 4 pairs a lane: this lane's
 // codes (byte i = value i) and the block's scale.  By whole warps.  A block with
-// a NaN or an infinity is NaN as a whole.
-__device__ __forceinline__ uint2 block_codes(const float2 *f, float *scale) {
-    float a = max_nan(fabsf(f[0].x), fabsf(f[0].y));
+// a NaN or an infinity is NaN as a whole.  a: the lane's largest magnitude.
+__device__ __forceinline__ uint2 block_codes(const float2 *f, float a, float *scale) {
 #pragma unroll
-    for (int i = 1; i < 4; ++i) a = max_nan(max_nan(a, fabsf(f[i].x)), fabsf(f[i].y));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o), 0.f);
     if (a >= 0x1p-80f && a <= 0x1.fffffep127f) { // so that the scale is past 2^-90
-        const float s = block_scale(a), r = __frcp_rn(s);
+        const float s = block_scale(a), r = -__frcp_rn(s);
         *scale = s;
         return make_uint2(quant4_recip(f, s, r), quant4_recip(f + 2, s, r));
     }
@@ -121,15 +121,28 @@ __device__ __forceinline__ uint2 block_codes(const float2 *f, float *scale) {
     const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
     return make_uint2(quant4(v, s), quant4(v + 4, s));
 }
+__device__ __forceinline__ uint2 block_codes(const float2 *f, float *scale) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = max_nan(a, f[i].x, f[i].y);
+    return block_codes(f, a, scale);
+}
 // 8 codes -> 8 values, code * scale.
-__device__ __forceinline__ void block_values(float *v, const uint2 &q, float scale) {
+__device__ __forceinline__ void block_values(float2 *v, const uint2 &q, float scale) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1)));
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        const float2 f = mul2_rn(__half22float2(__half2(h)), both(scale));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[i] = mul2_rn(__half22float2(__half2(h)), both(scale));
+    }
+}
+__device__ __forceinline__ void block_values(float *v, const uint2 &q, float scale) {
+    float2 f[4];
+    block_values(f, q, scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = f[i].x;
+        v[2 * i + 1] = f[i].y;
     }
 }
 

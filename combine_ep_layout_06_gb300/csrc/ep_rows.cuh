@@ -77,6 +77,18 @@ template <typename T> __device__ __forceinline__ void unpack8(float *v, const ui
 // the 16-bit rounding of every result it goes into.
 __device__ __forceinline__ float sigmoidf(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
+// v sigmoid(v) of two values, with the same error.
+__device__ __forceinline__ float2 silu2(float2 v) {
+    const float2 t = mul2_rn(v, both(-1.4426950408889634f));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = add2_rn(e, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    return mul2_rn(v, e);
+}
+
 __device__ __forceinline__ void activate8(int act, float *v) {
     switch (act) {
     case EP_ACT_RELU:
