@@ -36,7 +36,8 @@ constexpr int kMaxStages = 12;
 constexpr int kLoaders = 2, kFinishers = 4;    // warps
 constexpr int kMostRows = 32;                // of h in an accumulator of down
 constexpr int kMostCtas = 160;
-constexpr int kLeastSlices = 8;              // of a CTA of down, while there are more CTAs than one
+constexpr int kEvenTenths = 7;
+constexpr int kLeastSlices = 4;              // of a CTA of down, while there are more CTAs than one
 constexpr int kThreads = (kLoaders + 1 + kFinishers) * 32;
 constexpr int kSmemMost = 227 * 1024 - 1024; // of a CTA, less what is static
 
@@ -166,7 +167,11 @@ template <> struct Walk<true> {
     int m, i, ks, n;
     __device__ Walk(const FewParams &p, const Plan &pl) : plan(pl), per((p.K + kSlice - 1) / kSlice) {
         total = (int64_t)((p.M + kTile - 1) / kTile) * plan.present * per;
-        const int64_t most = total / kLeastSlices;
+        // A CTA's slices cost 0.4 us each where weights come fast, a part T / 100 us to the
+        // one that joins a tile's: both are least at the root of their product.
+        const int tile_slices = plan.present * per;
+        const int least = max(kLeastSlices, (int)sqrtf((float)tile_slices * p.T * (1.0f / 40)));
+        const int64_t most = total / least;
         ctas = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
         const int c = blockIdx.x;
         const int64_t lo = start(c);
@@ -783,6 +788,10 @@ template <typename T, bool DOWN, bool GATED> ep_status_t launch_few(FewWork &w, 
         configured[dev].store(true, std::memory_order_release);
     }
     const int most = sms < kMostCtas ? sms : kMostCtas;
+    if (DOWN && ctas > most) {                           // whole tiles for equally many CTAs each, where that leaves few SMs out
+        const int tiles = (w.p.M + kTile - 1) / kTile, even = tiles <= most ? most / tiles * tiles : 0;
+        ctas = even * 10 >= most * kEvenTenths ? even : most;
+    }
     return launch_after_previous(few_kernel<T, DOWN, GATED>, (unsigned)(ctas < most ? ctas : most), kThreads, bytes, st, w) ==
                    cudaSuccess
                ? EP_SUCCESS : EP_ERR_GPU_OP;

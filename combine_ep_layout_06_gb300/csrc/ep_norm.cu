@@ -616,7 +616,8 @@ RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
     return r;
 }
 
-Shape grad_shape(const ep_norm_desc_t &d) { return shape_of(d.width, 2); }
+// Chunks a thread as in the norm: fewer where a row is all that a block has.
+Shape grad_shape(const ep_norm_desc_t &d) { return shape_of(d.width, (int64_t)d.ranks * d.rows <= kParts ? 1 : 2); }
 // Parts of the weight's gradient, one a block.
 int64_t grad_parts(const ep_norm_desc_t &d) {
     const Shape s = grad_shape(d);
