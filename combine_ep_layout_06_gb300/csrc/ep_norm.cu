@@ -13,20 +13,37 @@ namespace {
 constexpr int kMaxChunks = 4, kMaxThreads = EP_MAX_NORM_WIDTH / (kMaxChunks * 8);
 
 // ------------------------------------------------------------ rows' chunks
-// 8 values of a row.  VEC: one or two 16-byte accesses; else value by value,
-// `n` of them (a row's end, or rows that are not 16-byte aligned).
+// How a thread's chunk of 8 values stands in its row.  kVector: neighbours, one or
+// two 16-byte accesses.  Rows that these do not reach go value by value:
+// kStrided, every tpr-th value, so that a warp's accesses are next to each other
+// (2332 x 4333 fp16: neighbours 56 us); kNeighbours where a block's codes need 16
+// lanes to hold 128 neighbours.
+enum Access { kStrided, kNeighbours, kVector };
+
+struct Span {
+    int c, step, n;              // first value, distance, how many there are
+};
+template <Access A> __device__ __forceinline__ Span span_of(int i, int t, int tpr, int H) {
+    if constexpr (A == kStrided) {
+        const int c = i * tpr * 8 + t;
+        return Span{c, tpr, c < H ? (H - 1 - c) / tpr + 1 : 0};
+    } else {
+        const int c = (t + i * tpr) * 8;
+        return Span{c, 1, H - c};
+    }
+}
 
 template <typename T> struct Raw { uint4 q[sizeof(T) / 2]; };
 
-template <typename T, bool VEC> __device__ __forceinline__ Raw<T> load_chunk(const T *p, int n) {
+template <typename T, Access A> __device__ __forceinline__ Raw<T> load_chunk(const T *row, const Span &s) {
     Raw<T> r;
-    if constexpr (VEC) {
+    if constexpr (A == kVector) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = ld_stream16(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = ld_stream16(reinterpret_cast<const uint4 *>(row + s.c) + i);
     } else {
         T *e = reinterpret_cast<T *>(r.q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : rounded<T>(0.f);
+        for (int i = 0; i < 8; ++i) e[i] = i < s.n ? row[s.c + i * s.step] : rounded<T>(0.f);
     }
     return r;
 }
@@ -57,21 +74,21 @@ template <typename T> __device__ __forceinline__ Raw<T> packed(const float2 *f) 
     }
     return r;
 }
-template <typename T, bool VEC> __device__ __forceinline__ void store_chunk(T *p, const Raw<T> &r, int n) {
-    if constexpr (VEC) {
+template <typename T, Access A> __device__ __forceinline__ void store_chunk(T *row, const Raw<T> &r, const Span &s) {
+    if constexpr (A == kVector) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = r.q[i];
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(row + s.c)[i] = r.q[i];
     } else {
         const T *e = reinterpret_cast<const T *>(r.q);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = e[i];
+            if (i < s.n) row[s.c + i * s.step] = e[i];
     }
 }
 // 8 weights, in the rows' type or fp32.
-template <typename T, bool VEC> __device__ __forceinline__ void load_weights(float2 *f, const void *w, bool w32, int c, int n) {
-    if (w32) values<float>(f, load_chunk<float, VEC>(static_cast<const float *>(w) + c, n));
-    else values<T>(f, load_chunk<T, VEC>(static_cast<const T *>(w) + c, n));
+template <typename T, Access A> __device__ __forceinline__ void load_weights(float2 *f, const void *w, bool w32, const Span &s) {
+    if (w32) values<float>(f, load_chunk<float, A>(static_cast<const float *>(w), s));
+    else values<T>(f, load_chunk<T, A>(static_cast<const T *>(w), s));
 }
 
 // Sums over the threads that share a row: a warp, or the whole block.
@@ -129,15 +146,15 @@ template <int CH> __device__ __forceinline__ float inverse_root(const float2 (*h
 
 // A row's chunks, `t` of `tpr` threads: total = x + residual, written if wanted,
 // and its squares' sum so far.
-template <typename T, int CH, bool VEC>
+template <typename T, int CH, Access A>
 __device__ __forceinline__ float make_total(float2 (*h)[4], const Raw<T> *a, const Raw<T> *b, bool add, T *total, int H, int t, int tpr) {
     float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = (t + i * tpr) * 8;
+        const Span at = span_of<A>(i, t, tpr, H);
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[i][j] = both(0.f);
-        if (c < H) {
+        if (at.n > 0) {
             values<T>(h[i], a[i]);
             Raw<T> sum = a[i];
             if (add) {
@@ -148,7 +165,7 @@ __device__ __forceinline__ float make_total(float2 (*h)[4], const Raw<T> *a, con
                 sum = packed<T>(f);
                 values<T>(h[i], sum);
             }
-            if (total) store_chunk<T, VEC>(total + c, sum, H - c);
+            if (total) store_chunk<T, A>(total, sum, at);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) s = fma2_rn(h[i][j], h[i][j], s);
@@ -157,23 +174,24 @@ __device__ __forceinline__ float make_total(float2 (*h)[4], const Raw<T> *a, con
 }
 
 // y, or its codes and scales.
-template <typename T, int CH, bool VEC, bool EIGHT>
+template <typename T, int CH, Access A, bool EIGHT>
 __device__ __forceinline__ void write_normed(const NormParams &p, int seg, int row, const float2 (*h)[4], float r, int t, int tpr) {
     if constexpr (EIGHT) {
         uint8_t *y = static_cast<uint8_t *>(p.y.ptr) + row_at(p.y, seg, row);
         float *scales = static_cast<float *>(p.scales.ptr) + row_at(p.scales, seg, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
+            const Span at = span_of<A>(i, t, tpr, p.H);
+            const int c = at.c;
             if (c - t % 32 * 8 >= p.H) continue; // the whole warp: a block's codes need all its lanes
             float2 f[4], w[4] = {};
-            if (c < p.H) load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
+            if (c < p.H) load_weights<T, A>(w, p.weight, p.w32, at);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = c < p.H ? mul2_rn(mul2_rn(h[i][j], both(r)), w[j]) : both(0.f);
             float scale;
             const uint2 q = block_codes(f, &scale);
             if (c >= p.H) continue;
-            if constexpr (VEC) {
+            if constexpr (A == kVector) {
                 *reinterpret_cast<uint2 *>(y + c) = q;
             } else {
 #pragma unroll
@@ -185,20 +203,20 @@ __device__ __forceinline__ void write_normed(const NormParams &p, int seg, int r
         T *y = static_cast<T *>(p.y.ptr) + row_at(p.y, seg, row);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-            if (c >= p.H) continue;
+            const Span at = span_of<A>(i, t, tpr, p.H);
+            if (at.n <= 0) continue;
             float2 w[4];
-            load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
+            load_weights<T, A>(w, p.weight, p.w32, at);
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = mul2_rn(mul2_rn(h[i][j], both(r)), w[j]);
-            store_chunk<T, VEC>(y + c, packed<T>(w), p.H - c);
+            store_chunk<T, A>(y, packed<T>(w), at);
         }
     }
 }
 
 // ---- a row a block (or a warp), straight from memory
 
-template <typename T, int CH, bool VEC, bool EIGHT, int THREADS>
+template <typename T, int CH, Access A, bool EIGHT, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int tpr) {
     __shared__ float part[1][32];
     grid_dependency_wait();
@@ -212,17 +230,17 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int t
     Raw<T> a[CH], b[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = (t + i * tpr) * 8;
-        if (c < p.H) {
-            a[i] = load_chunk<T, VEC>(x + c, p.H - c);
-            if (res) b[i] = load_chunk<T, VEC>(res + c, p.H - c);
+        const Span at = span_of<A>(i, t, tpr, p.H);
+        if (at.n > 0) {
+            a[i] = load_chunk<T, A>(x, at);
+            if (res) b[i] = load_chunk<T, A>(res, at);
         }
     }
     float2 h[CH][4];
-    float s[1] = {make_total<T, CH, VEC>(h, a, b, res, p.total.ptr ? static_cast<T *>(p.total.ptr) + row_at(p.total, seg, row) : nullptr,
+    float s[1] = {make_total<T, CH, A>(h, a, b, res, p.total.ptr ? static_cast<T *>(p.total.ptr) + row_at(p.total, seg, row) : nullptr,
                                          p.H, t, tpr)};
     row_sums<1>(s, tpr, part);
-    write_normed<T, CH, VEC, EIGHT>(p, seg, row, h, inverse_root<CH>(h, s[0], p.H, p.eps, tpr, part), t, tpr);
+    write_normed<T, CH, A, EIGHT>(p, seg, row, h, inverse_root<CH>(h, s[0], p.H, p.eps, tpr, part), t, tpr);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -277,17 +295,17 @@ __device__ __forceinline__ void shrink8(float2 *h) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(kShrink));
 }
-template <int CH> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
+template <int CH, Access A> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = (t + i * tpr) * 8;
+        const Span at = span_of<A>(i, t, tpr, H);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (c + j < H) to[c + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+            if (j < at.n) to[at.c + j * at.step] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
     }
 }
 
-template <typename T, int CH, bool VEC, int THREADS>
+template <typename T, int CH, Access A, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) norm_grad_kernel(const NormGradParams p, int tpr) {
     __shared__ float part[2][32];
     grid_dependency_wait();
@@ -304,11 +322,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
         Raw<T> a[CH], b[CH], more[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-            if (c < p.H) {
-                a[i] = load_chunk<T, VEC>(x + c, p.H - c);
-                b[i] = load_chunk<T, VEC>(grad + c, p.H - c);
-                if (total) more[i] = load_chunk<T, VEC>(total + c, p.H - c);      // before grad_x, perhaps the same rows, is written
+            const Span at = span_of<A>(i, t, tpr, p.H);
+            if (at.n > 0) {
+                a[i] = load_chunk<T, A>(x, at);
+                b[i] = load_chunk<T, A>(grad, at);
+                if (total) more[i] = load_chunk<T, A>(total, at);      // before grad_x, perhaps the same rows, is written
             }
         }
         float s[2];
@@ -318,12 +336,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
             RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int c = (t + i * tpr) * 8;
-                if (c >= p.H) continue;
+                const Span at = span_of<A>(i, t, tpr, p.H);
+                if (at.n <= 0) continue;
                 float2 h[4], g[4], w[4];
                 values<T>(h, a[i]);
                 values<T>(g, b[i]);
-                load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
+                load_weights<T, A>(w, p.weight, p.w32, at);
                 if (shrunk) shrink8(h);
                 sum.add(h, g, w);
             }
@@ -335,27 +353,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
         rg.set(s, p.H, p.eps, shrunk);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-            if (c >= p.H) continue;
+            const Span at = span_of<A>(i, t, tpr, p.H);
+            if (at.n <= 0) continue;
             float2 h[4], g[4], w[4], f[4] = {};
             values<T>(h, a[i]);
             values<T>(g, b[i]);
-            load_weights<T, VEC>(w, p.weight, p.w32, c, p.H - c);
+            load_weights<T, A>(w, p.weight, p.w32, at);
             if (total) values<T>(f, more[i]);
             rg.out(f, dw[i], h, g, w);
-            store_chunk<T, VEC>(out + c, packed<T>(f), p.H - c);
+            store_chunk<T, A>(out, packed<T>(f), at);
         }
     }
     float *mine = p.part + (int64_t)blockIdx.x * p.H;
     if (tpr > 32) {
-        write_part<CH>(mine, p.H, dw, t, tpr);
+        write_part<CH, A>(mine, p.H, dw, t, tpr);
         return;
     }
     // a warp a row: the block's warps add theirs, in order
     __shared__ float sums[THREADS == 256 ? 8 : 1][CH * 256];
     const int warp = threadIdx.x / 32;
     if constexpr (THREADS == 256) {
-        write_part<CH>(sums[warp], p.H, dw, t, tpr);
+        write_part<CH, A>(sums[warp], p.H, dw, t, tpr);
         __syncthreads();
         for (int c = threadIdx.x; c < p.H; c += 256) {
             float v = 0.f;
@@ -464,12 +482,12 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
             RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int c = (t + i * tpr) * 8;
-                if (c >= p.H) continue;
+                const Span at = span_of<kVector>(i, t, tpr, p.H);
+                if (at.n <= 0) continue;
                 float2 h[4], g[4], w[4];
-                values<T>(h, ring_chunk<T>(ring.at(s, 0), c));
-                values<T>(g, ring_chunk<T>(ring.at(s, 1), c));
-                load_weights<T, true>(w, p.weight, p.w32, c, p.H - c);
+                values<T>(h, ring_chunk<T>(ring.at(s, 0), at.c));
+                values<T>(g, ring_chunk<T>(ring.at(s, 1), at.c));
+                load_weights<T, kVector>(w, p.weight, p.w32, at);
                 if (shrunk) shrink8(h);
                 sum.add(h, g, w);
             }
@@ -487,15 +505,15 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
         rg.set(v, p.H, p.eps, shrunk);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int c = (t + i * tpr) * 8;
-            if (c >= p.H) continue;
+            const Span at = span_of<kVector>(i, t, tpr, p.H);
+            if (at.n <= 0) continue;
             float2 h[4], g[4], w[4], f[4] = {};
-            values<T>(h, ring_chunk<T>(ring.at(s, 0), c));
-            values<T>(g, ring_chunk<T>(ring.at(s, 1), c));
-            load_weights<T, true>(w, p.weight, p.w32, c, p.H - c);
-            if (p.grad_total.ptr) values<T>(f, ring_chunk<T>(ring.at(s, 2), c));
+            values<T>(h, ring_chunk<T>(ring.at(s, 0), at.c));
+            values<T>(g, ring_chunk<T>(ring.at(s, 1), at.c));
+            load_weights<T, kVector>(w, p.weight, p.w32, at);
+            if (p.grad_total.ptr) values<T>(f, ring_chunk<T>(ring.at(s, 2), at.c));
             rg.out(f, dw[i], h, g, w);
-            store_chunk<T, true>(out + c, packed<T>(f), p.H - c);
+            store_chunk<T, kVector>(out, packed<T>(f), at);
         }
         turn ^= 1u;
         if (++s == stages) {
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
             phase ^= 1u;
         }
     }
-    write_part<CH>(p.part + (int64_t)blockIdx.x * p.H, p.H, dw, t, tpr);
+    write_part<CH, kVector>(p.part + (int64_t)blockIdx.x * p.H, p.H, dw, t, tpr);
     if (t == 0 && *(volatile int *)&gave_up) {
         ring.drain(loads);
         if (error) atomicOr(error, EP_DEVERR_TIMEOUT);
@@ -666,8 +684,8 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, cons
             constexpr int CH = decltype(chunks)::value;
             auto go = [&](auto most) {
                 constexpr int N = decltype(most)::value;
-                auto kernel = eight ? (vec ? norm_kernel<T, CH, true, true, N> : norm_kernel<T, CH, false, true, N>)
-                                    : (vec ? norm_kernel<T, CH, true, false, N> : norm_kernel<T, CH, false, false, N>);
+                auto kernel = eight ? (vec ? norm_kernel<T, CH, kVector, true, N> : norm_kernel<T, CH, kNeighbours, true, N>)
+                                    : (vec ? norm_kernel<T, CH, kVector, false, N> : norm_kernel<T, CH, kStrided, false, N>);
                 e = launch_after_previous(kernel, blocks, threads, 0, st, p, s.tpr);
             };
             if (threads <= 256) go(std::integral_constant<int, 256>());
@@ -726,7 +744,7 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
                 constexpr int CH = decltype(chunks)::value;
                 auto go = [&](auto most) {
                     constexpr int N = decltype(most)::value;
-                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, true, N> : norm_grad_kernel<T, CH, false, N>, n,
+                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, kVector, N> : norm_grad_kernel<T, CH, kStrided, N>, n,
                                               s.tpr * s.per, 0, st, p, s.tpr);
                 };
                 if (s.tpr * s.per <= 256) go(std::integral_constant<int, 256>());
