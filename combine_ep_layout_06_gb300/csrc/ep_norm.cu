@@ -295,17 +295,17 @@ __device__ __forceinline__ void shrink8(float2 *h) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(kShrink));
 }
-template <int CH, Access A> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
+template <int CH> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const Span at = span_of<A>(i, t, tpr, H);
+        const int c = (t + i * tpr) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < at.n) to[at.c + j * at.step] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
+            if (c + j < H) to[c + j] = j & 1 ? dw[i][j / 2].y : dw[i][j / 2].x;
     }
 }
 
-template <typename T, int CH, Access A, int THREADS>
+template <typename T, int CH, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) norm_grad_kernel(const NormGradParams p, int tpr) {
     __shared__ float part[2][32];
     grid_dependency_wait();
@@ -322,11 +322,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
         Raw<T> a[CH], b[CH], more[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const Span at = span_of<A>(i, t, tpr, p.H);
+            const Span at = span_of<kVector>(i, t, tpr, p.H);
             if (at.n > 0) {
-                a[i] = load_chunk<T, A>(x, at);
-                b[i] = load_chunk<T, A>(grad, at);
-                if (total) more[i] = load_chunk<T, A>(total, at);      // before grad_x, perhaps the same rows, is written
+                a[i] = load_chunk<T, kVector>(x, at);
+                b[i] = load_chunk<T, kVector>(grad, at);
+                if (total) more[i] = load_chunk<T, kVector>(total, at);      // before grad_x, perhaps the same rows, is written
             }
         }
         float s[2];
@@ -336,12 +336,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
             RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const Span at = span_of<A>(i, t, tpr, p.H);
+                const Span at = span_of<kVector>(i, t, tpr, p.H);
                 if (at.n <= 0) continue;
                 float2 h[4], g[4], w[4];
                 values<T>(h, a[i]);
                 values<T>(g, b[i]);
-                load_weights<T, A>(w, p.weight, p.w32, at);
+                load_weights<T, kVector>(w, p.weight, p.w32, at);
                 if (shrunk) shrink8(h);
                 sum.add(h, g, w);
             }
@@ -353,33 +353,102 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
         rg.set(s, p.H, p.eps, shrunk);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const Span at = span_of<A>(i, t, tpr, p.H);
+            const Span at = span_of<kVector>(i, t, tpr, p.H);
             if (at.n <= 0) continue;
             float2 h[4], g[4], w[4], f[4] = {};
             values<T>(h, a[i]);
             values<T>(g, b[i]);
-            load_weights<T, A>(w, p.weight, p.w32, at);
+            load_weights<T, kVector>(w, p.weight, p.w32, at);
             if (total) values<T>(f, more[i]);
             rg.out(f, dw[i], h, g, w);
-            store_chunk<T, A>(out, packed<T>(f), at);
+            store_chunk<T, kVector>(out, packed<T>(f), at);
         }
     }
     float *mine = p.part + (int64_t)blockIdx.x * p.H;
     if (tpr > 32) {
-        write_part<CH, A>(mine, p.H, dw, t, tpr);
+        write_part<CH>(mine, p.H, dw, t, tpr);
         return;
     }
     // a warp a row: the block's warps add theirs, in order
     __shared__ float sums[THREADS == 256 ? 8 : 1][CH * 256];
     const int warp = threadIdx.x / 32;
     if constexpr (THREADS == 256) {
-        write_part<CH, A>(sums[warp], p.H, dw, t, tpr);
+        write_part<CH>(sums[warp], p.H, dw, t, tpr);
         __syncthreads();
         for (int c = threadIdx.x; c < p.H; c += 256) {
             float v = 0.f;
             for (int w = 0; w < 8; ++w) v += sums[w][c];
             mine[c] = v;
         }
+    }
+}
+
+// Rows that 16-byte accesses do not reach: a thread has every tpr-th value, reads it
+// again (from L1) once the row's sums are known, and keeps the weight's sums in
+// shared memory, all of it in loops of few registers (in registers, unrolled, 629 us
+// for 16384 x 5001 bf16).
+template <typename T>
+__global__ void __launch_bounds__(512, 3) norm_grad_strided_kernel(const NormGradParams p, int tpr) {
+    extern __shared__ __align__(16) float weight_sums[];
+    __shared__ float part[2][32];
+    grid_dependency_wait();
+    grid_dependents_may_launch();
+    const int t = threadIdx.x % tpr, per = blockDim.x / tpr;
+    const int64_t first = (int64_t)blockIdx.x * per + threadIdx.x / tpr, step = (int64_t)gridDim.x * per;
+    float *dw = weight_sums + threadIdx.x / tpr * p.H;
+    auto weight = [&](int c) {
+        return p.w32 ? __ldg(static_cast<const float *>(p.weight) + c) : f32(static_cast<const T *>(p.weight)[c]);
+    };
+    for (int c = t; c < p.H; c += tpr) dw[c] = 0.f;
+    for (int64_t index = first; index < (int64_t)p.R * p.rows; index += step) {
+        const int seg = (int)(index / p.rows), row = (int)(index - (int64_t)seg * p.rows);
+        const T *x = static_cast<const T *>(p.x.ptr) + row_at(p.x, seg, row);
+        const T *grad = static_cast<const T *>(p.grad.ptr) + row_at(p.grad, seg, row);
+        const T *total = p.grad_total.ptr ? static_cast<const T *>(p.grad_total.ptr) + row_at(p.grad_total, seg, row) : nullptr;
+        T *out = static_cast<T *>(p.grad_x.ptr) + row_at(p.grad_x, seg, row);
+        float s[2];
+        float shrink = 1.f;
+        for (;;) {
+            s[0] = s[1] = 0.f;
+#pragma unroll 4
+            for (int c = t; c < p.H; c += tpr) {
+                const float h = f32(x[c]) * shrink;
+                s[0] += h * h;
+                s[1] += f32(grad[c]) * weight(c) * h;
+            }
+            row_sums<2>(s, tpr, part);
+            if (shrink != 1.f || s[0] != __int_as_float(0x7f800000)) break;      // the same for the whole row
+            shrink = kShrink;
+        }
+        RowGrad rg;
+        rg.set(s, p.H, p.eps, shrink != 1.f);
+        if (total) {
+#pragma unroll 4
+            for (int c = t; c < p.H; c += tpr) {
+                const float g = f32(grad[c]), n = f32(x[c]) * rg.r, more = f32(total[c]);     // before grad_x, perhaps the same row
+                dw[c] += g * n;
+                out[c] = rounded<T>((g * weight(c) - n * rg.mean) * rg.r + more);
+            }
+        } else {
+#pragma unroll 4
+            for (int c = t; c < p.H; c += tpr) {
+                const float g = f32(grad[c]), n = f32(x[c]) * rg.r;
+                dw[c] += g * n;
+                out[c] = rounded<T>((g * weight(c) - n * rg.mean) * rg.r);
+            }
+        }
+    }
+    float *mine = p.part + (int64_t)blockIdx.x * p.H;
+    if (tpr > 32) {
+        for (int c = t; c < p.H; c += tpr) mine[c] = dw[c];
+        return;
+    }
+    // a warp a row: the block's warps add theirs, in order
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+        float v = 0.f;
+        for (int w = 0; w < per; ++w) v += weight_sums[w * p.H + c];
+        mine[c] = v;
     }
 }
 
@@ -521,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
             phase ^= 1u;
         }
     }
-    write_part<CH, kVector>(p.part + (int64_t)blockIdx.x * p.H, p.H, dw, t, tpr);
+    write_part<CH>(p.part + (int64_t)blockIdx.x * p.H, p.H, dw, t, tpr);
     if (t == 0 && *(volatile int *)&gave_up) {
         ring.drain(loads);
         if (error) atomicOr(error, EP_DEVERR_TIMEOUT);
@@ -636,6 +705,24 @@ RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
 
 // Chunks a thread as in the norm: fewer where a row is all that a block has.
 Shape grad_shape(const ep_norm_desc_t &d) { return shape_of(d.width, (int64_t)d.ranks * d.rows <= kParts ? 1 : 2); }
+// Rows that vectors do not reach: a warp a row, or more threads the longer it is;
+// blocks by registers and shared memory.
+struct StridedShape {
+    int tpr, per, blocks;
+};
+StridedShape strided_shape(const ep_norm_desc_t &d) {
+    const int64_t rows = (int64_t)d.ranks * d.rows;
+    StridedShape s = {d.width <= 512 ? 32 : d.width <= 1024 ? 64 : d.width <= 2048 ? 128 : d.width <= 8192 ? 256 : 512, 1, 0};
+    if (rows <= kParts) s.tpr = d.width <= 64 ? 32 : d.width <= 256 ? 128 : 512;    // all of a row at once
+    else if (s.tpr == 32) s.per = 8;
+    int64_t an_sm = kRingMost / ((int64_t)s.per * d.width * 4 + 1024);
+    if (an_sm > 1536 / (s.tpr * s.per)) an_sm = 1536 / (s.tpr * s.per);
+    if (an_sm > 8) an_sm = 8;
+    const int64_t blocks = (rows + s.per - 1) / s.per;
+    s.blocks = (int)(blocks < an_sm * kSms ? blocks : an_sm * kSms);
+    return s;
+}
+
 // Parts of the weight's gradient, one a block.
 int64_t grad_parts(const ep_norm_desc_t &d) {
     const Shape s = grad_shape(d);
@@ -740,12 +827,18 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
                                       ring.stages, d_error);
                 return;
             }
+            if (!vec) {
+                static std::atomic<bool> configured[kMaxDevices];
+                const StridedShape q = strided_shape(*d);
+                n = q.blocks;
+                e = launch_ring(norm_grad_strided_kernel<T>, configured, n, q.tpr * q.per, (size_t)q.per * d->width * 4, st, p, q.tpr);
+                return;
+            }
             with_chunks(s.chunks, [&](auto chunks) {
                 constexpr int CH = decltype(chunks)::value;
                 auto go = [&](auto most) {
                     constexpr int N = decltype(most)::value;
-                    e = launch_after_previous(vec ? norm_grad_kernel<T, CH, kVector, N> : norm_grad_kernel<T, CH, kStrided, N>, n,
-                                              s.tpr * s.per, 0, st, p, s.tpr);
+                    e = launch_after_previous(norm_grad_kernel<T, CH, N>, n, s.tpr * s.per, 0, st, p, s.tpr);
                 };
                 if (s.tpr * s.per <= 256) go(std::integral_constant<int, 256>());
                 else if (s.tpr * s.per <= 512) go(std::integral_constant<int, 512>());

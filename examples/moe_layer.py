@@ -7,7 +7,9 @@ training step.
 and back, through the same calls: the gradient of combine is a dispatch of the
 output's gradient along the cached layout, the gradient of dispatch is a
 combine.  The router's own product and the per-row scalings between the calls
-are plain torch.
+are plain torch.  With ``checkpoints`` the pre-activations are kept in 8 bits and
+the activations recomputed; ``decode`` takes a few tokens through norm, routing
+and experts without dispatch.
 
     python examples/moe_layer.py            # a few steps on random data, loss printed
 """
@@ -25,17 +27,18 @@ class MoeLayer:
     size F, top-k routing with renormalised softmax weights."""
 
     def __init__(self, W=2, E=8, k=2, T=128, H=256, F=192, dtype=torch.bfloat16, balance_coef=0.01, z_coef=0.001,
-                 device="cuda", seed=0):
+                 device="cuda", seed=0, checkpoints=False):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def param(*shape):
             return (torch.randn(shape, generator=g, device=device) * shape[-1] ** -0.5).to(dtype)
 
-        self.k, self.balance_coef, self.z_coef = k, balance_coef, z_coef
+        self.k, self.balance_coef, self.z_coef, self.checkpoints = k, balance_coef, z_coef, checkpoints
         self.router = param(E, H)
         self.gate_up = param(E, 2 * F, H)            # the experts of rank r are r * E/W ...
         self.down = param(E, H, F)
         self.down_bias = torch.zeros(E, H, dtype=dtype, device=device)
+        self.norm = torch.ones(H, dtype=dtype, device=device)     # of decode
         self.op = ep.EpDispatchCombineOp(ep.EpDispatchCombineConfig(
             world_size=W, num_experts=E, topk=k, hidden=H, max_tokens_per_rank=T,
             max_grouped_rows_per_rank=W * T * k))
@@ -55,6 +58,8 @@ class MoeLayer:
         ep.expert_product(h, self.down, count, offset, bias=self.down_bias, out=op.moe_y)
         op.moe_ungroup()
         out, _ = op.combine()
+        if self.checkpoints:                          # 8 bits in place of h and pre
+            h, pre = None, ep.checkpoint(pre, count, offset)
         self.saved = (x, logits, ids, indices, counts, num_tokens, rows, h, pre, count, offset)
         return out, loss[0]
 
@@ -80,9 +85,13 @@ class MoeLayer:
         grad_weights = torch.zeros(ids.shape, dtype=torch.float32, device=x.device)
         grad_weights.view(-1)[place] = (g_rows.float() * y.float()).sum(-1)[used]
         g_y = (g_rows.float() * torch.where(used, g_w, 0.0)[..., None]).to(x.dtype)
+        scales = None
+        if self.checkpoints:
+            pre, scales = pre
+            h = ep.checkpoint_restore(pre, scales, count, offset, activation="swiglu", dtype=x.dtype)
         g_h, g_down, g_bias = ep.expert_product_backward(g_y, h, self.down, count, offset, bias_grad=True)
         g_x, g_gate_up, _ = ep.expert_product_backward(g_h, rows, self.gate_up, count, offset, pre=pre,
-                                                       activation="swiglu")
+                                                       pre_scales=scales, activation="swiglu")
         op.moe_ungroup(g_x)
         grad_x, _ = op.combine()
         g_logits = ep.route_backward(grad_weights, logits, ids, num_tokens=num_tokens, grad_loss=grad_loss,
@@ -91,6 +100,14 @@ class MoeLayer:
         grad_x = torch.where(here, grad_x, zero) + torch.matmul(g_logits, self.router)
         g_router = torch.matmul(g_logits.flatten(0, 1).T, torch.where(here, x, zero).flatten(0, 1))
         return grad_x, g_router, g_gate_up, g_down, g_bias
+
+    def decode(self, x, residual):
+        """x: what the block before adds to the residual stream, [T][H], a few
+        tokens.  Returns (the layer's output, the residual stream): the next
+        block's pair."""
+        y, total = ep.rms_norm(x, self.norm, residual=residual)
+        weights, indices = ep.route(torch.matmul(y, self.router.T), self.k)
+        return ep.moe_few_tokens(y, weights, indices, self.gate_up, self.down, down_bias=self.down_bias), total
 
 
 def main():

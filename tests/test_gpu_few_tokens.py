@@ -1,7 +1,7 @@
 """The experts of a few tokens against 64 bits.
 
 Tolerance.  Sums are fp32, activations between the products are exact to 2^-16 of
-their value (two 16-bit halves), and out is rounded once: finfo.eps / 2 of each
+their value (fp32, or two 16-bit halves), and out is rounded once: finfo.eps / 2 of each
 value, and 2^-14 of the sum of magnitudes |w| |down| (|x| |up|) (at most 2^10 terms of
 2^-24 each for both products, and the activation's few units)."""
 import math
@@ -29,6 +29,11 @@ def make(T, E, k, H, F, act="swiglu", dtype=BF, bias=False, residual=False, seed
     c["weights"] = torch.softmax(torch.randn((T, k), generator=g, device="cuda"), -1)
     c["indices"] = torch.rand((T, E), generator=g, device="cuda").argsort(-1)[:, :k].to(torch.int32).contiguous()
     return c
+
+
+# Layers of both kinds: little work (up to 32 MB of weights over all choices)
+# and the kernels on tensor cores.
+LAYERS = [(128, 64), (1032, 520)]
 
 
 def call(c, **kw):
@@ -77,7 +82,8 @@ def check(got, c):
 @pytest.mark.parametrize("T,E,k,H,F", [
     (1, 1, 1, 8, 8), (1, 8, 2, 256, 192), (2, 3, 3, 64, 40), (3, 16, 4, 264, 136), (7, 40, 8, 512, 72), (8, 4, 1, 1024, 8),
     (9, 5, 5, 128, 1000), (16, 64, 6, 136, 128), (17, 300, 2, 72, 64), (31, 9, 9, 200, 88), (33, 2, 2, 640, 320), (64, 8, 2, 384, 256),
-    (64, 1, 1, 264, 248), (64, 1024, 32, 16, 16), (5, 6, 2, 1000, 1000)])
+    (64, 1, 1, 264, 248), (64, 1024, 32, 16, 16), (5, 6, 2, 1000, 1000), (64, 1, 1, 776, 264), (64, 1024, 32, 72, 64),
+    (63, 40, 30, 136, 40), (33, 33, 32, 8, 968), (34, 3, 3, 1024, 56), (1, 40, 32, 1000, 392), (48, 300, 8, 264, 72)])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_against_the_formula(T, E, k, H, F, dtype):
     c = make(T, E, k, H, F, dtype=dtype, bias=T % 2 == 0, residual=T % 3 == 0, seed=T)
@@ -85,9 +91,9 @@ def test_against_the_formula(T, E, k, H, F, dtype):
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
-@pytest.mark.parametrize("T", [1, 20])
-def test_activations(act, T):
-    c = make(T, 6, 3, 320, 168, act=act, bias=True, residual=True, seed=5)
+@pytest.mark.parametrize("T,H,F", [(1, 320, 168), (20, 320, 168), (3, 1032, 776), (40, 520, 264)])
+def test_activations(act, T, H, F):
+    c = make(T, 6, 3, H, F, act=act, bias=True, residual=True, seed=5)
     check(call(c), c)
 
 
@@ -100,8 +106,9 @@ def test_wider_layers():
         assert float((got.double() - want).norm()) <= float(want.norm()) * (torch.finfo(BF).eps / 2 + 2.0 ** -13)
 
 
-def test_absent_repeated_and_wrong_experts():
-    c = make(9, 7, 4, 256, 64, bias=True, residual=True)
+@pytest.mark.parametrize("H,F", LAYERS)
+def test_absent_repeated_and_wrong_experts(H, F):
+    c = make(9, 7, 4, H, F, bias=True, residual=True)
     idx = c["indices"]
     idx[0] = -1                                     # an absent token
     idx[1, 2:] = -1
@@ -120,10 +127,20 @@ def test_absent_repeated_and_wrong_experts():
     assert bool((got == 0).all()) and ep.moe_error() == _lib.EP_DEVERR_BAD_INDEX
 
 
-def test_rows_do_not_meet():
+@pytest.mark.parametrize("T", [9, 40, 64])
+def test_an_expert_with_every_token(T):
+    """More rows of one expert than an accumulator takes, next to experts of one."""
+    c = make(T, 12, 3, 520, 392, bias=True)
+    c["indices"][:, 1] = 5
+    c["indices"][T // 2:, 2] = 5
+    check(call(c), c)
+
+
+@pytest.mark.parametrize("H,F", LAYERS)
+def test_rows_do_not_meet(H, F):
     """NaN and infinities of one token, of an expert that nobody chose and of
     choices that are closed reach no other row."""
-    c = make(12, 6, 2, 192, 64, residual=True)
+    c = make(12, 6, 2, H, F, residual=True)
     c["indices"][c["indices"] == 4] = 3
     clean = call(c)
     c["x"][5] = math.nan
@@ -139,13 +156,14 @@ def test_rows_do_not_meet():
     assert torch.equal(got[8], c["residual"][8])
 
 
-def test_layouts():
+@pytest.mark.parametrize("H,F", [(128, 64), (1032, 640)])
+def test_layouts(H, F):
     """Ranks of tokens, strided rows and experts' slices of a larger tensor have the bits of dense ones."""
-    c = make(6, 5, 2, 128, 64, residual=True)
+    c = make(6, 5, 2, H, F, residual=True)
     want = call(c)
-    r = dict(c, x=c["x"].view(3, 2, 128), residual=c["residual"].view(3, 2, 128), weights=c["weights"].view(3, 2, 2),
+    r = dict(c, x=c["x"].view(3, 2, H), residual=c["residual"].view(3, 2, H), weights=c["weights"].view(3, 2, 2),
              indices=c["indices"].view(3, 2, 2))
-    assert torch.equal(call(r).view(6, 128), want)
+    assert torch.equal(call(r).view(6, H), want)
     wide = dict(c)
     for name, pad in (("x", 16), ("residual", 8), ("up", 24), ("down", 8)):
         t = c[name]
@@ -153,13 +171,13 @@ def test_layouts():
         big[..., :t.shape[-1]] = t
         wide[name] = big[..., :t.shape[-1]]
     assert torch.equal(call(wide), want)
-    assert torch.equal(call(dict(c, up=c["up"].repeat(1, 2, 1)[:, :128])), want)
+    assert torch.equal(call(dict(c, up=c["up"].repeat(1, 2, 1)[:, :2 * F])), want)
     none = dict(c, x=c["x"][:0], residual=None, weights=c["weights"][:0], indices=c["indices"][:0])
-    assert call(none).shape == (0, 128)
+    assert call(none).shape == (0, H)
 
 
 def test_streams_graphs_and_two_at_once():
-    cases = [make(T, 16, 4, 512, 256, seed=T, residual=True) for T in (1, 5, 40)]
+    cases = [make(T, 16, 4, 512, 256, seed=T, residual=True) for T in (1, 5, 40)]       # little work and tensor cores
     want = [call(c) for c in cases]
     torch.cuda.synchronize()
     sides = [torch.cuda.Stream() for _ in cases]
@@ -183,16 +201,17 @@ def test_streams_graphs_and_two_at_once():
     assert torch.equal(got[0], call(cases[0]))
 
 
-def test_a_chain_of_layers():
+@pytest.mark.parametrize("T,H,F", [(4, 256, 128), (12, 1024, 512)])
+def test_a_chain_of_layers(T, H, F):
     """Each call starts while the one before it ends: every layer must see the
     last one's output."""
-    layers = [make(4, 8, 2, 256, 128, seed=s) for s in range(6)]
+    layers = [make(T, 8, 2, H, F, seed=s) for s in range(6)]
 
     def chain(wait):
         x = layers[0]["x"]
         for c in layers * 5:
             x = call(dict(c, x=x, residual=x))
-            x = ep.rms_norm(x, torch.ones(256, dtype=BF, device="cuda"))
+            x = ep.rms_norm(x, torch.ones(H, dtype=BF, device="cuda"))
             if wait:
                 torch.cuda.synchronize()
         return x
