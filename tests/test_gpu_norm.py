@@ -5,12 +5,14 @@ fp32 additions in a row, so it is within 44 * 2^-24 of its value, its reciprocal
 root within half of that and two units of rsqrt: R = 2^-18 bounds every product
 of it.  On top comes the output's rounding, finfo.eps / 2 of the value (or half
 a step of its subnormals).  E4M3 is off by 2^-4 of the value or 2^-10 scales."""
+import ctypes
 import math
 
 import pytest
 import torch
 
 import combine_ep_layout_06_gb300 as ep
+from combine_ep_layout_06_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -151,6 +153,60 @@ def test_gradient(rows, H, dtype, wtype):
     dx, again = ep.rms_norm_backward(g, x, w, grad_total=more)
     close(dx, want + more.double(), size + R * more.double().abs())
     assert torch.equal(dw, again)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("rows,H", [(5000, 1032), (2500, 4096), (2000, 8192), (20000, 264), (3000, 77), (2000, 1537)])
+def test_gradient_of_many_rows(rows, H, dtype):
+    """Rows that come through shared memory ahead of their use, and rows strided by
+    threads; some whose squares do not fit fp32, some with NaN."""
+    x, g, w = rand(rows, H, dtype=dtype), rand(rows, H, dtype=dtype, seed=1), rand(H, dtype=dtype, seed=2)
+    more = rand(rows, H, dtype=dtype, seed=3)
+    x[7::100] *= 2.0 ** 100
+    x[rows - 1] = math.nan
+    ok = torch.arange(rows, device="cuda") != rows - 1
+    h = x[ok].double().requires_grad_(True)
+    want, = torch.autograd.grad(reference(h, w, 1e-6), h, g[ok].double())
+    u = (g[ok].double() * w.double()).abs()
+    r = 1 / torch.sqrt(x[ok].double().square().mean(-1, keepdim=True) + 1e-6)
+    n = x[ok].double().abs() * r
+    size = R * r * (u + n * (u * n).mean(-1, keepdim=True))
+    dx, dw = ep.rms_norm_backward(g, x, w)
+    close(dx[ok], want, size + 2.0 ** -133)
+    assert bool(dx[rows - 1].isnan().all()) and bool(dw.isnan().all())
+    dx, _ = ep.rms_norm_backward(g, x, w, grad_total=more)
+    close(dx[ok], want + more[ok].double(), size + R * more[ok].double().abs())
+    x[rows - 1] = 1.0
+    n = x.double() / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+    _, dw = ep.rms_norm_backward(g, x, w)
+    close(dw, (g.double() * n).sum(0), ((rows + 32) * 2.0 ** -24 + R) * (g.double() * n).abs().sum(0))
+    assert ep.moe_error() == 0
+
+
+@pytest.mark.parametrize("rows,H", [(6, 256), (3000, 1024), (5, 77), (2000, 300)])
+def test_in_place(rows, H):
+    """total over x or over the residual, grad_x over grad_total: the bits of separate ones."""
+    x, res, g, w = rand(rows, H, dtype=BF), rand(rows, H, dtype=BF, seed=1), rand(rows, H, dtype=BF, seed=2), rand(H, dtype=BF, seed=3)
+    L, ref, none = _lib.load(), ctypes.byref, _lib.EpRowsC(None, 0, 0)
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def at(t):
+        return _lib.EpRowsC(t.data_ptr(), 0, H)
+
+    def desc(t):
+        return _lib.EpNormDescC(1, rows, H, 0, 0, 1e-6, at(t), w.data_ptr())
+    want, total = ep.rms_norm(x, w, residual=res)
+    for over in (0, 1):
+        a, b, y = x.clone(), res.clone(), torch.empty_like(x)
+        assert L.ep_rms_norm(ref(desc(a)), ref(at(b)), ref(at((a, b)[over])), ref(at(y)), ref(none), None, st) == 0
+        assert torch.equal(y, want) and torch.equal((a, b)[over], total)
+    want, dw = ep.rms_norm_backward(g, total, w, grad_total=res)
+    n = ctypes.c_size_t(0)
+    assert L.ep_rms_norm_workspace(ref(desc(total)), ref(n)) == 0
+    scratch, got_w, both = torch.empty(n.value, dtype=torch.uint8, device="cuda"), torch.empty_like(w), res.clone()
+    assert L.ep_rms_norm_backward(ref(desc(total)), ref(at(g)), ref(at(both)), ref(at(both)), got_w.data_ptr(), scratch.data_ptr(),
+                                  n.value, None, st) == 0
+    assert torch.equal(both, want) and torch.equal(got_w, dw)
 
 
 def test_gradient_against_differences():
