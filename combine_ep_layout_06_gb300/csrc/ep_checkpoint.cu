@@ -1,9 +1,8 @@
 // Activations kept in block-scaled 8 bits between forward and backward: saved,
 // and restored through the activation.
 //
-// Element-wise over the rows of every group and bound by memory.  A lane takes 8
-// neighbouring values, so 16 lanes hold a block of 128; a warp takes 256
-// values of a row, a block's warps take rows in turn.
+// Element-wise over the rows of every group.  A lane takes 8 (restored) or 16 (saved)
+// neighbouring values, a warp 256 or 512 of a row; a block's warps take rows in turn.
 #include "ep_fp8.cuh"
 #include "ep_rows.cuh"
 
@@ -31,18 +30,20 @@ __device__ __forceinline__ Part part_of(const CheckpointParams &p) {
     return Part{g / p.gr.per, first + (int)(a < rows ? a : rows), first + (int)(b < rows ? b : rows)};
 }
 
-// The largest magnitude among 8 16-bit values, NaN above all: the bits without
-// their signs stand in that order.
-template <typename T> __device__ __forceinline__ float largest(const uint4 &q) {
-    const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu), __vmaxu2(q.z & 0x7fff7fffu, q.w & 0x7fff7fffu));
-    const uint16_t top = (uint16_t)max(m >> 16, m & 0xffffu);
-    return f32(*reinterpret_cast<const T *>(&top));
+// The larger magnitudes of 16-bit values, pair by pair, NaN above all: the bits
+// without their signs stand in that order.
+__device__ __forceinline__ uint32_t larger(const uint4 &q) {
+    return __vmaxu2(__vmaxu2(q.x & 0x7fff7fffu, q.y & 0x7fff7fffu), __vmaxu2(q.z & 0x7fff7fffu, q.w & 0x7fff7fffu));
 }
 
+// A lane takes 16 neighbouring values, so that 8 lanes share a block's scale: the
+// kernel is bound by instructions (16 lanes of 8 values: 64 us where this takes
+// 54, for 32768 x 3584).
+constexpr int kSaveCols = 512, kSaveRows = 2;
 template <typename T> __global__ void __launch_bounds__(kWarps * 32, 4) save_kernel(const CheckpointParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * kCols + lane * 8;
-    const bool live = c < p.F;
+    const int c = blockIdx.x * kSaveCols + lane * 16;
+    const bool live = c < p.F, second = c + 8 < p.F;
     grid_dependency_wait();
     grid_dependents_may_launch();
     const Part part = part_of(p);
@@ -51,24 +52,31 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32, 4) save_ker
     uint8_t *codes = static_cast<uint8_t *>(p.codes.ptr) + part.seg * p.codes.rank_stride + r0 * p.codes.row_stride + c;
     float *scales = static_cast<float *>(p.scales.ptr) + part.seg * p.scales.rank_stride + r0 * p.scales.row_stride + c / 128;
     const int64_t xs = kWarps * p.x.row_stride, cs = kWarps * p.codes.row_stride, ss = kWarps * p.scales.row_stride;
-    for (int left = part.end - (int)r0; left > 0; left -= kWarps * kRows) {
-        uint4 v[kRows];
+    for (int left = part.end - (int)r0; left > 0; left -= kWarps * kSaveRows) {
+        uint4 v[kSaveRows][2];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u)
-            v[u] = live && u * kWarps < left ? ld_stream16(x + u * xs) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (u * kWarps >= left) break;       // the same for the warp
-            const float2 f[4] = {unpack2<T>(v[u].x), unpack2<T>(v[u].y), unpack2<T>(v[u].z), unpack2<T>(v[u].w)};
-            float scale;
-            const uint2 q = block_codes(f, largest<T>(v[u]), &scale);
-            if (!live) continue;
-            *reinterpret_cast<uint2 *>(codes + u * cs) = q;
-            if ((lane & 15) == 0) scales[u * ss] = scale;
+        for (int u = 0; u < kSaveRows; ++u) {
+            v[u][0] = live && u * kWarps < left ? ld_stream16(x + u * xs) : make_uint4(0, 0, 0, 0);
+            v[u][1] = second && u * kWarps < left ? ld_stream16(x + u * xs + 8) : make_uint4(0, 0, 0, 0);
         }
-        x += kRows * xs;
-        codes += kRows * cs;
-        scales += kRows * ss;
+#pragma unroll
+        for (int u = 0; u < kSaveRows; ++u) {
+            if (u * kWarps >= left) break;       // the same for the warp
+            uint32_t m = __vmaxu2(larger(v[u][0]), larger(v[u][1]));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const uint16_t top = (uint16_t)max(m >> 16, m & 0xffffu);
+            const float2 f[8] = {unpack2<T>(v[u][0].x), unpack2<T>(v[u][0].y), unpack2<T>(v[u][0].z), unpack2<T>(v[u][0].w),
+                                 unpack2<T>(v[u][1].x), unpack2<T>(v[u][1].y), unpack2<T>(v[u][1].z), unpack2<T>(v[u][1].w)};
+            uint2 q[2];
+            const float scale = scaled_codes<2>(f, f32(*reinterpret_cast<const T *>(&top)), q);
+            if (live) *reinterpret_cast<uint2 *>(codes + u * cs) = q[0];
+            if (second) *reinterpret_cast<uint2 *>(codes + u * cs + 8) = q[1];
+            if (live && (lane & 7) == 0) scales[u * ss] = scale;
+        }
+        x += kSaveRows * xs;
+        codes += kSaveRows * cs;
+        scales += kSaveRows * ss;
     }
 }
 
@@ -112,10 +120,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) restore_kernel(const Checkpoin
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j] = mul2_rn(silu2(f[j]), w[j]);
             } else if (p.act != EP_ACT_NONE) {
-                float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-                activate8(p.act, v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = make_float2(v[2 * j], v[2 * j + 1]);
+                for (int j = 0; j < 4; ++j)
+                    f[j] = p.act == EP_ACT_GELU   ? gelu2(f[j])
+                           : p.act == EP_ACT_SILU ? silu2(f[j])
+                                                  : make_float2(f[j].x <= 0.f ? 0.f : f[j].x, f[j].y <= 0.f ? 0.f : f[j].y);
             }
             *reinterpret_cast<uint4 *>(y + u * ys) =
                 make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
@@ -158,7 +167,7 @@ ep_status_t ep_checkpoint_save(const ep_checkpoint_desc_t *d, const ep_rows_t *x
     if (!valid_rows(*x, d->features, d->ranks > 1) || !valid_codes(*codes, *scales, d->features, d->ranks > 1))
         return EP_ERR_INVALID_ARGS;
     const CheckpointParams p = params(*d, *x, *codes, *scales);
-    const dim3 grid((d->features + kCols - 1) / kCols, d->ranks * d->groups, p.splits);
+    const dim3 grid((d->features + kSaveCols - 1) / kSaveCols, d->ranks * d->groups, p.splits);
     cudaError_t e = cudaSuccess;
     with_type(d->dtype, [&](auto type) {
         e = launch_after_previous(save_kernel<decltype(type)>, grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream), p);

@@ -100,32 +100,40 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return m;
 }
 
-// A block of 128 values over 16 neighbouring lanes, 4 pairs a lane: this lane's
-// codes (byte i = value i) and the block's scale.  By whole warps.  A block with
-// a NaN or an infinity is NaN as a whole.  a: the lane's largest magnitude.
-__device__ __forceinline__ uint2 block_codes(const float2 *f, float a, float *scale) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o), 0.f);
+// A lane's N times 8 values of a block whose largest magnitude is a: their codes (byte i =
+// value i); returns the block's scale.  A block with a NaN or an infinity is NaN as a
+// whole.
+template <int N> __device__ __forceinline__ float scaled_codes(const float2 *f, float a, uint2 *q) {
     if (a >= 0x1p-80f && a <= 0x1.fffffep127f) { // so that the scale is past 2^-90
         const float s = block_scale(a), r = -__frcp_rn(s);
-        *scale = s;
-        return make_uint2(quant4_recip(f, s, r), quant4_recip(f + 2, s, r));
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i] = make_uint2(quant4_recip(f + 4 * i, s, r), quant4_recip(f + 4 * i + 2, s, r));
+        return s;
     }
     if (!(a <= 0x1.fffffep127f)) {
-        *scale = __uint_as_float(0x7fffffffu);
-        return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+        for (int i = 0; i < N; ++i) q[i] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+        return __uint_as_float(0x7fffffffu);
     }
     const float s = __fdiv_rn(a, 448.0f);
-    *scale = s;
-    if (s == 0.f) return make_uint2(0u, 0u);
-    const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
-    return make_uint2(quant4(v, s), quant4(v + 4, s));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 *g = f + 4 * i;
+        const float v[8] = {g[0].x, g[0].y, g[1].x, g[1].y, g[2].x, g[2].y, g[3].x, g[3].y};
+        q[i] = s == 0.f ? make_uint2(0u, 0u) : make_uint2(quant4(v, s), quant4(v + 4, s));
+    }
+    return s;
 }
+// A block of 128 values over 16 neighbouring lanes, 4 pairs a lane.  By whole warps.
 __device__ __forceinline__ uint2 block_codes(const float2 *f, float *scale) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a = max_nan(a, f[i].x, f[i].y);
-    return block_codes(f, a, scale);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o), 0.f);
+    uint2 q;
+    *scale = scaled_codes<1>(f, a, &q);
+    return q;
 }
 // 8 codes -> 8 values, code * scale.
 __device__ __forceinline__ void block_values(float2 *v, const uint2 &q, float scale) {

@@ -89,6 +89,25 @@ __device__ __forceinline__ float2 silu2(float2 v) {
     return mul2_rn(v, e);
 }
 
+// v Phi(v) of two values, Phi(v) = erfc(-v / sqrt(2)) / 2 by the rational approximation
+// 7.1.26 of Abramowitz and Stegun (erf within 1.5e-7).
+__device__ __forceinline__ float2 gelu2(float2 v) {
+    const float2 x = make_float2(fabsf(v.x), fabsf(v.y));
+    float2 t = fma2_rn(x, both(0.3275911f * 0.70710678118654752f), both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(t.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(t.y));
+    float2 q = fma2_rn(t, both(1.061405429f), both(-1.453152027f));
+    q = fma2_rn(q, t, both(1.421413741f));
+    q = fma2_rn(q, t, both(-0.284496736f));
+    q = fma2_rn(q, t, both(0.254829592f));
+    const float2 a = mul2_rn(mul2_rn(v, v), both(-0.72134752044448170f));       // -v^2 / 2 in powers of two
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(a.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(a.y));
+    q = mul2_rn(mul2_rn(q, mul2_rn(t, both(0.5f))), e);                         // Phi(-|v|)
+    return mul2_rn(v, make_float2(v.x < 0.f ? q.x : 1.0f - q.x, v.y < 0.f ? q.y : 1.0f - q.y));
+}
+
 __device__ __forceinline__ void activate8(int act, float *v) {
     switch (act) {
     case EP_ACT_RELU:

@@ -70,14 +70,16 @@ bool truth(PyObject *o) {
     return v != 0;
 }
 // The place of a name among `names`.
-int choice(PyObject *o, const char *what, const std::vector<const char *> &names) {
+int choice(PyObject *o, const char *what, std::initializer_list<const char *> names) {
     const char *s = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
-    std::string all;
-    for (size_t i = 0; i < names.size(); ++i) {
-        if (s && !std::strcmp(s, names[i])) return (int)i;
-        all += std::string(i ? ", " : "") + names[i];
+    int i = 0;
+    for (const char *name : names) {
+        if (s && !std::strcmp(s, name)) return i;
+        ++i;
     }
     if (PyErr_Occurred()) throw PythonError{};
+    std::string all;
+    for (const char *name : names) all += std::string(all.empty() ? "" : ", ") + name;
     refuse(std::string(what) + ": one of " + all);
 }
 
