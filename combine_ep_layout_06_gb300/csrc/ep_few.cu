@@ -45,7 +45,7 @@ struct FewParams {
     int T, E, k, M, K;           // M: outputs of this product (gated: of a half); K: its depth
     int act;
     int box;                     // up: token rows a copy brings
-    int stages, stage_bytes, columns;
+    int ring_bytes, columns;
     int off_acc, off_mask, off_weight, off_first, off_list, off_token;    // in shared memory, after the ring
     const float *w;
     const int32_t *idx;
@@ -65,7 +65,7 @@ struct FewWork {
 struct __align__(8) FewBarriers {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
-    int present;
+    int present, most;
     Watch watch;
 };
 
@@ -79,13 +79,14 @@ struct Plan {
     uint16_t *first, *list;      // [E], [entries]; an entry is an expert, from bit kChunkBit on the number of its kMostRows rows
     uint8_t *token;              // [rows], down only
     int present;                 // entries of list
+    int stages, stage_bytes;     // of the ring: down's stages hold the rows that its entries have at most
 };
 constexpr int kChunkBit = 12;
 static_assert(EP_MAX_ROUTE_EXPERTS <= 1 << kChunkBit, "an entry holds an expert and its chunk");
 
 __device__ __forceinline__ int bits_below(unsigned long long mask, int t) { return __popcll(mask & ((1ull << t) - 1)); }
 
-template <bool DOWN> __device__ void make_plan(const FewParams &p, unsigned char *smem, int *present, Plan *plan) {
+template <bool DOWN> __device__ void make_plan(const FewParams &p, unsigned char *smem, FewBarriers *bars, Plan *plan) {
     plan->mask = reinterpret_cast<unsigned long long *>(smem + p.off_mask);
     plan->weight = reinterpret_cast<float *>(smem + p.off_weight);
     plan->first = reinterpret_cast<uint16_t *>(smem + p.off_first);
@@ -101,10 +102,11 @@ template <bool DOWN> __device__ void make_plan(const FewParams &p, unsigned char
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int rows = 0, n = 0;
+        int rows = 0, n = 0, most = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int mine = e0 + lane < p.E ? __popcll(plan->mask[e0 + lane]) : 0;
             const int chunks = DOWN ? (mine + kMostRows - 1) / kMostRows : mine > 0;
+            most = max(most, min(mine, kMostRows));
             int upto = mine << 16 | chunks;              // both running sums at once
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -118,12 +120,18 @@ template <bool DOWN> __device__ void make_plan(const FewParams &p, unsigned char
             rows += upto >> 16;
             n += upto & 0xffff;
         }
-        if (lane == 0) *present = n;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            bars->present = n;
+            bars->most = most;
+        }
         if (DOWN)
             for (int r = lane; r < rows; r += 32) plan->weight[r] = 0.f;
     }
     __syncthreads();
-    plan->present = *present;
+    plan->present = bars->present;
+    plan->stage_bytes = kTile * 256 + (DOWN ? max(1, (bars->most + 7) / 8) * 16 : p.box) * 256;
+    plan->stages = min(p.ring_bytes / plan->stage_bytes, kMaxStages);
     if (DOWN && threadIdx.x < p.T) {         // a thread for each token: one that names an expert twice adds in order
         const int t = threadIdx.x;
         for (int j = 0; j < p.k; ++j) {
@@ -228,7 +236,7 @@ template <bool DOWN, bool GATED> struct FewLoader {
     FewBarriers &bars;
     uint32_t ring;
 
-    __device__ uint32_t stage(uint32_t s) const { return ring + s * w.p.stage_bytes; }
+    __device__ uint32_t stage(uint32_t s) const { return ring + s * plan.stage_bytes; }
     __device__ void weights(uint32_t s, const Walk<DOWN> &at, int k) const {
         const FewParams &p = w.p;
         const uint32_t bar = smem_u32(&bars.full[s]), half = kTile * 128;
@@ -277,7 +285,7 @@ template <bool DOWN, bool GATED> struct FewLoader {
     __device__ void run(int mine) {
         const FewParams &p = w.p;
         const bool elected = elect_one();
-        const int S = p.stages;
+        const int S = plan.stages;
         bool ok = true;
         if constexpr (DOWN) {                            // weights for a whole ring, ahead of h
             for (Slices it(p, plan, mine); it.more() && it.n < S; it.next()) {
@@ -347,7 +355,7 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
             if (elected) {
                 // columns past the tokens that were loaded are whatever follows in
                 // shared memory: they are not read
-                const uint32_t base = ring + s * p.stage_bytes;
+                const uint32_t base = ring + s * plan.stage_bytes;
                 const uint64_t a0 = smem_desc(base, 16, 1024), a1 = smem_desc(base + kTile * 128, 16, 1024);
                 const uint64_t b0 = smem_desc(base + kTile * 256, 16, 1024);
                 const uint64_t b1 = smem_desc(base + kTile * 256 + boxes * p.box * 128, 16, 1024);
@@ -358,7 +366,7 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
                 mma_commit_single(smem_u32(&bars.empty[s]));
             }
             __syncwarp();
-            if (++s == (uint32_t)p.stages) {
+            if (++s == (uint32_t)plan.stages) {
                 s = 0;
                 phase ^= 1u;
             }
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             for (int i = threadIdx.x; i < kMostCtas * kFinishers; i += kThreads) p.tickets[i] = 0;
     }
     Plan plan;
-    make_plan<DOWN>(p, smem, &bars.present, &plan);
+    make_plan<DOWN>(p, smem, &bars, &plan);
     if (warp < kLoaders) {
         FewLoader<DOWN, GATED>{w, plan, bars, ring}.run(warp);
     } else {
@@ -748,8 +756,6 @@ size_t workspace(const ep_few_desc_t &d) { return h_bytes(d) + part_bytes(d) + k
 // at least: instructions read 16 columns where 8 tokens were loaded.
 bool lay_out(FewParams *p, bool down, size_t *bytes) {
     const int rows_most = p->T * p->k;
-    const int most = p->T < kMostRows ? p->T : kMostRows;
-    p->stage_bytes = kTile * 256 + (down ? (most + 7) / 8 * 16 : p->box) * 256;
     int at = 0;
     auto take = [&](int size) {
         const int was = at;
@@ -760,10 +766,11 @@ bool lay_out(FewParams *p, bool down, size_t *bytes) {
     const int first = take(p->E * 2), list = take(p->E * 2 * (down ? (p->T + kMostRows - 1) / kMostRows : 1));
     const int token = take(down ? rows_most : 0);
     if (at < 2048) at = 2048;
-    p->stages = (kSmemMost - 1024 - at) / p->stage_bytes;
-    if (p->stages > kMaxStages) p->stages = kMaxStages;
-    if (p->stages < kLoaders) return false;      // see FewLoader: a warp counts on slices a ring behind its last one
-    const int ring = p->stages * p->stage_bytes;
+    const int rows = p->T < kMostRows ? p->T : kMostRows;
+    const int stage = kTile * 256 + (down ? (rows + 7) / 8 * 16 : p->box) * 256;       // at most
+    const int ring = (kSmemMost - 1024 - at) / 1024 * 1024;
+    if (ring < kLoaders * stage) return false;           // see FewLoader: a warp counts on slices a ring behind its last one
+    p->ring_bytes = ring;
     p->off_acc = ring + acc;
     p->off_mask = ring + mask;
     p->off_weight = ring + weight;
