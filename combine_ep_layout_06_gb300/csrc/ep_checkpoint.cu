@@ -145,9 +145,14 @@ bool valid(const ep_checkpoint_desc_t *d) {
     return aligned(d->d_count, 4) && aligned(d->d_offset, 4);
 }
 
+// About 64 rows a block, or 16 where that leaves SMs without a few of them (4346 x 1672 in
+// 8 groups, saved: 64 rows 10.6 us, 16 rows 6.2).
 CheckpointParams params(const ep_checkpoint_desc_t &d, const ep_rows_t &x, const ep_rows_t &codes,
-                        const ep_rows_t &scales) {
-    const int64_t parts = ((int64_t)d.rows / d.groups + 63) / 64;      // about 64 rows each
+                        const ep_rows_t &scales, int columns) {
+    const int64_t rows = (int64_t)d.rows / d.groups, blocks = (int64_t)columns * d.ranks * d.groups;
+    int64_t each = 64;
+    while (each > 16 && blocks * ((rows + each - 1) / each) < 1216) each /= 2;
+    const int64_t parts = (rows + each - 1) / each;
     return CheckpointParams{Groups{d.d_count, d.d_offset, d.ranks, d.groups, d.rows}, d.features, d.activation,
                             (int)(parts < 1 ? 1 : parts > 256 ? 256 : parts), x, codes, scales};
 }
@@ -166,8 +171,9 @@ ep_status_t ep_checkpoint_save(const ep_checkpoint_desc_t *d, const ep_rows_t *x
     if (d->rows == 0) return EP_SUCCESS;
     if (!valid_rows(*x, d->features, d->ranks > 1) || !valid_codes(*codes, *scales, d->features, d->ranks > 1))
         return EP_ERR_INVALID_ARGS;
-    const CheckpointParams p = params(*d, *x, *codes, *scales);
-    const dim3 grid((d->features + kSaveCols - 1) / kSaveCols, d->ranks * d->groups, p.splits);
+    const int columns = (d->features + kSaveCols - 1) / kSaveCols;
+    const CheckpointParams p = params(*d, *x, *codes, *scales, columns);
+    const dim3 grid(columns, d->ranks * d->groups, p.splits);
     cudaError_t e = cudaSuccess;
     with_type(d->dtype, [&](auto type) {
         e = launch_after_previous(save_kernel<decltype(type)>, grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream), p);
@@ -185,8 +191,9 @@ ep_status_t ep_checkpoint_restore(const ep_checkpoint_desc_t *d, const ep_rows_t
     if (d->rows == 0) return EP_SUCCESS;
     if (!valid_rows(*y, N, d->ranks > 1) || !valid_codes(*codes, *scales, d->features, d->ranks > 1))
         return EP_ERR_INVALID_ARGS;
-    const CheckpointParams p = params(*d, *y, *codes, *scales);
-    const dim3 grid((N + kCols - 1) / kCols, d->ranks * d->groups, p.splits);
+    const int columns = (N + kCols - 1) / kCols;
+    const CheckpointParams p = params(*d, *y, *codes, *scales, columns);
+    const dim3 grid(columns, d->ranks * d->groups, p.splits);
     cudaError_t e = cudaSuccess;
     with_type(d->dtype, [&](auto type) {
         using T = decltype(type);

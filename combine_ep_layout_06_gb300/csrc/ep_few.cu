@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------- little work
-// A warp for each choice and feature, then for each token and output: every
+// A warp for each choice and feature, then for each output and choice: every
 // choice reads its expert's weights anew (from L2 after the first), but
 // nothing stands between a launch and its loads.
 
@@ -681,12 +681,22 @@ template <typename T, bool GATED> __global__ void __launch_bounds__(kSmallWarps 
     if (lane == 0) p.h[(int64_t)pair * p.F + f] = v;
 }
 
+// Outputs of a block: its warps share an output's choices, up to 8 of them (one token,
+// 8 choices of 512 x 512: 12.4 -> 8.1 us), unless there are outputs enough (64 tokens of
+// 256: 18.1 us, shared 20.0).
+__host__ __device__ inline int small_outputs(int k, int tokens, int outputs) {
+    return tokens * outputs >= 8192 ? 8 : k >= 8 ? 1 : k >= 4 ? 2 : k >= 2 ? 4 : 8;
+}
+
 template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_down_kernel(const SmallParams p) {
-    const int lane = threadIdx.x & 31, m = blockIdx.x * kSmallWarps + (threadIdx.x >> 5), t = blockIdx.y;
+    __shared__ float parts[kSmallWarps];
+    const int outputs = small_outputs(p.k, p.T, p.H), share = kSmallWarps / outputs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.y;
+    const int m = blockIdx.x * outputs + warp / share, j0 = warp % share;
     // Indices and weights were there before the first kernel began: the weights'
     // lines are on their way while it ends.
     if (m < p.H)
-        for (int j = 0; j < p.k; ++j) {
+        for (int j = j0; j < p.k; j += share) {
             const int e = p.idx[t * p.k + j];
             if ((unsigned)e >= (unsigned)p.E) continue;
             const T *w = static_cast<const T *>(p.down.ptr) + e * p.down.rank_stride + m * p.down.row_stride;
@@ -694,9 +704,8 @@ template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_
         }
     grid_dependency_wait();
     grid_dependents_may_launch();
-    if (m >= p.H) return;
     float sum = 0.f;
-    for (int j = 0; j < p.k; ++j) {
+    for (int j = j0; m < p.H && j < p.k; j += share) {
         const int pair = t * p.k + j, e = p.idx[pair];
         if ((unsigned)e >= (unsigned)p.E) continue;
         const T *w = static_cast<const T *>(p.down.ptr) + e * p.down.rank_stride + m * p.down.row_stride;
@@ -725,7 +734,10 @@ template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_
         if (p.down_bias) v += f32(static_cast<const T *>(p.down_bias)[(int64_t)e * p.H + m]);
         sum += p.w[pair] * v;
     }
-    if (lane == 0) {
+    if (lane == 0) parts[warp] = sum;
+    __syncthreads();
+    if (lane == 0 && j0 == 0 && m < p.H) {
+        for (int q = 1; q < share; ++q) sum += parts[warp + q];
         if (p.residual.ptr) sum += f32(static_cast<const T *>(p.residual.ptr)[t * p.residual.row_stride + m]);
         static_cast<T *>(p.out.ptr)[t * p.out.row_stride + m] = rounded<T>(sum);
     }
@@ -812,7 +824,8 @@ ep_status_t launch(const ep_few_desc_t &d, FewWork &up, FewWork &down, int64_t u
 }
 
 template <typename T> ep_status_t launch_small(const SmallParams &p, cudaStream_t st) {
-    const dim3 up((p.F + kSmallWarps - 1) / kSmallWarps, p.T * p.k), down((p.H + kSmallWarps - 1) / kSmallWarps, p.T);
+    const int outputs = small_outputs(p.k, p.T, p.H);
+    const dim3 up((p.F + kSmallWarps - 1) / kSmallWarps, p.T * p.k), down((p.H + outputs - 1) / outputs, p.T);
     const cudaError_t e =
         p.act == EP_ACT_SWIGLU ? launch_after_previous(small_up_kernel<T, true>, up, kSmallWarps * 32, 0, st, p)
                                : launch_after_previous(small_up_kernel<T, false>, up, kSmallWarps * 32, 0, st, p);
@@ -822,9 +835,9 @@ template <typename T> ep_status_t launch_small(const SmallParams &p, cudaStream_
 }
 
 // Bytes of weights that the choices read, each its own, up to which the kernels for
-// little work are faster: 1.8 MB 4.5 against 10.2 us, 12.6 MB 8.8 against 14.1,
-// 25 MB 10.6 to 14.6 against 14.1 to 16.8 (with 128 choices 22 against 21); 52 MB
-// 27 against 21.
+// little work are faster: 1.8 MB 3.8 against 11.6 us, 12.6 MB 7.0 against 13.0,
+// 25 MB 10.7 to 12.1 against 15.6 to 16.7 (with 128 choices 23 against 21); 52 MB
+// 25 against 23.
 constexpr int64_t kSmallBytes = 32 << 20;
 
 }  // namespace
