@@ -36,6 +36,8 @@ constexpr int kMaxStages = 12;
 constexpr int kLoaders = 2, kFinishers = 4;    // warps
 constexpr int kMostRows = 32;                // of h in an accumulator of down
 constexpr int kMostCtas = 160;
+// Down gives every tile to equally many CTAs where that uses this many tenths of the
+// SMs (one token 102.5 us, 7168 outputs on 112 CTAs; in equal parts of all 152 104.8).
 constexpr int kEvenTenths = 7;
 constexpr int kLeastSlices = 4;              // of a CTA of down, while there are more CTAs than one
 constexpr int kThreads = (kLoaders + 1 + kFinishers) * 32;
@@ -176,7 +178,8 @@ template <> struct Walk<true> {
     __device__ Walk(const FewParams &p, const Plan &pl) : plan(pl), per((p.K + kSlice - 1) / kSlice) {
         total = (int64_t)((p.M + kTile - 1) / kTile) * plan.present * per;
         // A CTA's slices cost 0.4 us each where weights come fast, a part T / 100 us to the
-        // one that joins a tile's: both are least at the root of their product.
+        // one that joins a tile's: both are least at the root of their product (64 tokens of
+        // 64 experts, 512 x 256: 30 us, with 4 slices at least 46).
         const int tile_slices = plan.present * per;
         const int least = max(kLeastSlices, (int)sqrtf((float)tile_slices * p.T * (1.0f / 40)));
         const int64_t most = total / least;
@@ -381,6 +384,17 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
     }
 }
 
+// A value in two halves.  One that T's range does not reach has T's largest number
+// as its upper half, and the rest (infinite past twice that) as its lower one.
+template <typename T> __device__ __forceinline__ void store_halves(T *upper, T *lower, float y) {
+    constexpr float kLargest = std::is_same<T, __half>::value ? 65504.f : 0x1.fep127f;
+    const bool finite = fabsf(y) <= 0x1.fffffep127f;
+    float hi = f32(rounded<T>(y));
+    if (finite && fabsf(hi) > kLargest) hi = copysignf(kLargest, y);
+    *upper = rounded<T>(hi);
+    *lower = rounded<T>(finite ? y - hi : 0.f);
+}
+
 // ---- the last four warps: outputs.  A lane has a row of weights, a register a column.
 
 template <typename T, bool GATED>
@@ -422,12 +436,7 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
                 if (!(chosen >> c & 1u)) continue;       // the same for the warp
                 float y = v[c];
                 if constexpr (GATED) y = y * sigmoidf(y) * __shfl_xor_sync(0xffffffffu, y, 8);
-                const T hi = rounded<T>(y);
-                const float left = y - f32(hi);
-                if (live && !upper) {
-                    h[0] = hi;
-                    h[p.h_half] = rounded<T>(left == left ? left : 0.f);       // 0 where y is not finite
-                }
+                if (live && !upper) store_halves<T>(h, h + p.h_half, y);
                 h += p.M;
             }
         }
@@ -476,15 +485,15 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
             there = __shfl_sync(0xffffffffu, there, 0);
             if (there == (uint32_t)(z - a)) {            // the last one
                 __threadfence();
-                constexpr int kAhead = 4;                // tokens, and parts, on their way at a time
+                constexpr int kAhead = 4, kParts = 4;    // tokens and parts on their way at a time
                 for (int t = t0; t < p.T; t += 4 * kAhead) {
                     float4 v[kAhead];
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c = a; c <= z; c += kAhead) {
-                        float4 w[kAhead][kAhead];
+                    for (int c = a; c <= z; c += kParts) {
+                        float4 w[kParts][kAhead];
 #pragma unroll
-                        for (int q = 0; q < kAhead; ++q)
+                        for (int q = 0; q < kParts; ++q)
 #pragma unroll
                             for (int j = 0; j < kAhead; ++j)
                                 w[q][j] = c + q <= z && t + 4 * j < p.T
@@ -492,7 +501,7 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
                                                     p.parts + ((c + q) * 2 + (c + q == a)) * part + (t + 4 * j) * kTile + col))
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int q = 0; q < kAhead; ++q)
+                        for (int q = 0; q < kParts; ++q)
 #pragma unroll
                             for (int j = 0; j < kAhead; ++j) {
                                 v[j].x += w[q][j].x;
@@ -508,7 +517,8 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
             }
         }
         __syncwarp();
-        for (int t = 0; t < p.T; ++t) mine[t * kTile] = 0.f;
+        if (at.n < at.left)                              // more tiles to come
+            for (int t = 0; t < p.T; ++t) mine[t * kTile] = 0.f;
     };
     if (plan.present == 0) {
         for (int u = blockIdx.x; u * kTile < p.M; u += gridDim.x)

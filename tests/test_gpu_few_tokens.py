@@ -156,6 +156,24 @@ def test_rows_do_not_meet(H, F):
     assert torch.equal(got[8], c["residual"][8])
 
 
+@pytest.mark.parametrize("H,F", [(128, 64), (1032, 776)])
+def test_activations_past_the_type(H, F):
+    """Between the products values may pass what fp16 holds (up to 131008), and
+    infinite ones stay infinite."""
+    c = make(8, 4, 3, H, F, act="none", dtype=HF)
+    c["up"] *= 100.0
+    c["x"] *= 300.0
+    c["down"] *= 2.0 ** -10
+    v = torch.einsum("th,efh->tef", c["x"].double(), c["up"].double()).abs()
+    c["x"] *= float(100000.0 / v.max())
+    v = torch.einsum("th,efh->tef", c["x"].double(), c["up"].double()).abs()
+    assert 65504 < float(v.max()) < 131008
+    check(call(c), c)
+    c["x"][3, 1] = math.inf
+    got = call(c)
+    assert not bool(got[3].isfinite().any()) and bool(got[torch.arange(8, device="cuda") != 3].isfinite().all())
+
+
 @pytest.mark.parametrize("H,F", [(128, 64), (1032, 640)])
 def test_layouts(H, F):
     """Ranks of tokens, strided rows and experts' slices of a larger tensor have the bits of dense ones."""
