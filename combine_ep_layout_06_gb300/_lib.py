@@ -212,7 +212,7 @@ SIGNATURES = {
     "ep_expert_product": (_S, [_P, _P, _P, _P, _P, _P, _P]),
     "ep_expert_product_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "ep_expert_product_backward": (_S, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
-    "ep_rms_norm": (_S, [_P, _P, _P, _P, _P, _P, _P]),
+    "ep_rms_norm": (_S, [_P, _P, _P, _P, _P, _P]),
     "ep_rms_norm_workspace": (_S, [_P, ctypes.POINTER(ctypes.c_size_t)]),
     "ep_rms_norm_backward": (_S, [_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "ep_checkpoint_save": (_S, [_P, _P, _P, _P, _P]),

@@ -3,7 +3,9 @@
 //
 // A row stays in registers from its one read to its one write: a thread holds
 // up to 4 chunks of 8 neighbouring values, the row's sums meet by shuffles and,
-// where more than a warp shares the row, in shared memory.  Bound by memory.
+// where more than a warp shares the row, in shared memory.  Bound by memory:
+// 32768 x 7168 bf16 with a residual 264 us (7.1 TB/s), to 8 bits 259 (6.35 TB/s; 64 %
+// issue, with arithmetic one value at a time 413 us).
 #include "ep_fp8.cuh"
 #include "ep_rows.cuh"
 
@@ -245,7 +247,9 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int t
 
 // ---------------------------------------------------------------- gradient
 // A block takes every gridDim-th row and keeps its sums for grad_weight in
-// registers; column_kernel joins the blocks' sums in order.
+// registers; column_kernel joins the blocks' sums in order.  Bound by memory and, at
+// 63 % issue, by instructions: 16384 x 7168 bf16 with grad_total 162 us and 5 for the
+// sums, at 83 % of the copy rate.
 
 constexpr int kSms = 152, kParts = 3 * kSms;     // blocks at most where a block keeps no rows ahead
 constexpr int kMostBlocks = 8 * kSms;
@@ -684,13 +688,13 @@ cudaError_t launch_ring(void (*kernel)(Params...), std::atomic<bool> *configured
     return launch_after_previous(kernel, blocks, threads, bytes, st, static_cast<Args &&>(args)...);
 }
 
-// How a norm of many rows goes through the ring; stages 0: it does not.
+// How the gradient of many rows goes through the ring; stages 0: it does not.
 struct RingShape {
-    int stages, chunks, threads, blocks;
+    int stages, threads, blocks;
 };
 RingShape grad_ring(const ep_norm_desc_t &d, bool vec, bool total) {
     const int64_t row = d.width * size_of(d.dtype), rows = (int64_t)d.ranks * d.rows;
-    RingShape r = {0, 2, 0, 0};
+    RingShape r = {0, 0, 0};
     r.threads = ((d.width / 8 + 1) / 2 + 31) / 32 * 32;
     if (!vec || row < kRingRow || r.threads < 64 || r.threads > kGradRingThreads) return r;
     int blocks = 1024 / r.threads;                               // an SM's, by registers
@@ -742,9 +746,9 @@ using namespace ep;
 extern "C" {
 
 ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, const ep_rows_t *total,
-                        const ep_rows_t *y, const ep_rows_t *scales, uint32_t *d_error, void *stream) {
+                        const ep_rows_t *y, const ep_rows_t *scales, void *stream) {
     EP_RANGE("ep_rms_norm");
-    if (!valid(d) || !residual || !total || !y || !scales || !aligned(d_error, 4)) return EP_ERR_INVALID_ARGS;
+    if (!valid(d) || !residual || !total || !y || !scales) return EP_ERR_INVALID_ARGS;
     if (d->rows == 0) return EP_SUCCESS;
     const bool eight = scales->ptr != nullptr;
     const int64_t size = size_of(d->dtype);
@@ -840,9 +844,11 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
                     constexpr int N = decltype(most)::value;
                     e = launch_after_previous(norm_grad_kernel<T, CH, N>, n, s.tpr * s.per, 0, st, p, s.tpr);
                 };
-                if (s.tpr * s.per <= 256) go(std::integral_constant<int, 256>());
-                else if (s.tpr * s.per <= 512) go(std::integral_constant<int, 512>());
-                else go(std::integral_constant<int, kMaxThreads>());
+                if constexpr (CH <= 2) {             // 4 only where 2 would take more threads than there are
+                    if (s.tpr * s.per <= 256) return go(std::integral_constant<int, 256>());
+                    if (s.tpr * s.per <= 512) return go(std::integral_constant<int, 512>());
+                }
+                go(std::integral_constant<int, kMaxThreads>());
             });
         });
     }

@@ -627,7 +627,7 @@ PyObject *rms_norm(PyObject *const *a) {
         sc = here.empty(blocks, at::kFloat);
         scales = ep_rows_t{sc.data_ptr(), n.d.rows * (H / 128), H / 128};
     }
-    if (n.d.rows) check(ep_rms_norm(&n.d, &res, &total, &to, &scales, error_ptr(here.index), here.stream()), "ep_rms_norm");
+    if (n.d.rows) check(ep_rms_norm(&n.d, &res, &total, &to, &scales, here.stream()), "ep_rms_norm");
     if (eight && residual) return pack(y, sc, sum);
     if (eight) return pack(y, sc);
     if (residual) return pack(y, sum);

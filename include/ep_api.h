@@ -555,7 +555,10 @@ ep_status_t ep_expert_product_backward(const ep_product_desc_t *d,
 
 /* ---------------------------------------------------------------------
  * Norm, checkpoints in 8 bits, and the experts of a few tokens: no handle,
- * asynchronous on `stream`, as the calls above.
+ * asynchronous on `stream`, as the calls above; every kernel is launched as a
+ * programmatic dependent of the one before it on the stream and waits for it
+ * before it reads or writes what that one may (ep_moe_few's second kernel reads the
+ * call's inputs, which its first has waited for, ahead of that).
  *
  * 8 bits are E4M3 codes with one fp32 scale for every block of 128 values of a
  * row (the last block of a row may be a part), as dispatch quantises:
@@ -592,7 +595,7 @@ typedef struct {
  * pre-quantised dispatch takes. */
 ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual,
                         const ep_rows_t *total, const ep_rows_t *y,
-                        const ep_rows_t *scales, uint32_t *d_error, void *stream);
+                        const ep_rows_t *scales, void *stream);
 
 /* The gradient, d->x being the forward's total, grad = dL/dy:
  *   u = grad * weight
@@ -601,7 +604,7 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual,
  * grad_total (ptr NULL: none) is what comes to total from elsewhere, the residual
  * stream.  grad_x is the gradient of x and of the residual alike, and may be
  * grad_total itself.  d_grad_weight [H] in weight_dtype; rows are summed in an
- * order that the sizes alone fix.  d_workspace: ep_rms_norm_workspace bytes, 16-byte
+ * order that sizes, strides and alignment fix.  d_workspace: ep_rms_norm_workspace bytes, 16-byte
  * aligned, any contents. */
 ep_status_t ep_rms_norm_workspace(const ep_norm_desc_t *d, size_t *bytes);
 ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,

@@ -198,7 +198,7 @@ def test_in_place(rows, H):
     want, total = ep.rms_norm(x, w, residual=res)
     for over in (0, 1):
         a, b, y = x.clone(), res.clone(), torch.empty_like(x)
-        assert L.ep_rms_norm(ref(desc(a)), ref(at(b)), ref(at((a, b)[over])), ref(at(y)), ref(none), None, st) == 0
+        assert L.ep_rms_norm(ref(desc(a)), ref(at(b)), ref(at((a, b)[over])), ref(at(y)), ref(none), st) == 0
         assert torch.equal(y, want) and torch.equal((a, b)[over], total)
     want, dw = ep.rms_norm_backward(g, total, w, grad_total=res)
     n = ctypes.c_size_t(0)

@@ -40,7 +40,7 @@ def norm(**kw):
 def test_norm_descriptors(L, bad):
     n = ctypes.c_size_t(0)
     d = ref(norm(**bad))
-    assert L.ep_rms_norm(d, ref(NONE), ref(NONE), ref(rows(256)), ref(NONE), None, None) == INVALID
+    assert L.ep_rms_norm(d, ref(NONE), ref(NONE), ref(rows(256)), ref(NONE), None) == INVALID
     assert L.ep_rms_norm_workspace(d, ref(n)) == INVALID
     assert L.ep_rms_norm_backward(d, ref(rows(256)), ref(NONE), ref(rows(256)), P, P, 1 << 40, None, None) == INVALID
 
@@ -51,25 +51,25 @@ def test_norm_rows(L):
         for at in range(3):
             a = [none, none, y]
             a[at] = ref(bad)
-            assert L.ep_rms_norm(d, *a, none, None, None) == INVALID
-    assert L.ep_rms_norm(d, none, none, none, none, None, None) == INVALID
-    assert L.ep_rms_norm(d, none, none, y, none, ctypes.c_void_p(0x10002), None) == INVALID
-    assert L.ep_rms_norm(None, none, none, y, none, None, None) == INVALID
+            assert L.ep_rms_norm(d, *a, none, None) == INVALID
+    assert L.ep_rms_norm(d, none, none, none, none, None) == INVALID
+    assert L.ep_rms_norm(None, none, none, y, none, None) == INVALID
     for at in range(4):
         a = [none, none, y, none]
         a[at] = None
-        assert L.ep_rms_norm(d, *a, None, None) == INVALID
+        assert L.ep_rms_norm(d, *a, None) == INVALID
     # codes: whole blocks, and scales' rows
-    assert L.ep_rms_norm(ref(norm(width=200)), none, none, y, ref(rows(2)), None, None) == INVALID
+    assert L.ep_rms_norm(ref(norm(width=200)), none, none, y, ref(rows(2)), None) == INVALID
     for bad in (rows(1), rows(2, ptr=0x10002), rows(2, rank=0)):
-        assert L.ep_rms_norm(d, none, none, y, ref(bad), None, None) == INVALID
+        assert L.ep_rms_norm(d, none, none, y, ref(bad), None) == INVALID
     n = ctypes.c_size_t(0)
     assert L.ep_rms_norm_workspace(d, ref(n)) == 0 and n.value >= 256 * 4
     for a in ([ref(rows(255)), none, y, P, P, n.value], [y, ref(rows(255)), y, P, P, n.value], [y, none, ref(rows(255)), P, P, n.value],
               [y, none, y, None, P, n.value], [y, none, y, P, None, n.value], [y, none, y, P, P, n.value - 1],
               [y, none, y, ctypes.c_void_p(0x10001), P, n.value], [y, none, y, P, ctypes.c_void_p(0x10004), n.value]):
         assert L.ep_rms_norm_backward(d, *a, None, None) == INVALID
-    assert L.ep_rms_norm(ref(norm(rows=0, x=NONE)), none, none, none, none, None, None) == 0
+    assert L.ep_rms_norm_backward(d, y, none, y, P, P, n.value, ctypes.c_void_p(0x10002), None) == INVALID
+    assert L.ep_rms_norm(ref(norm(rows=0, x=NONE)), none, none, none, none, None) == 0
 
 
 def checkpoint(**kw):
