@@ -109,7 +109,7 @@ def _compile_binding() -> str:
 def _link_binding(obj: str):
     tmp = BINDING + f".{os.getpid()}.tmp"
     _run([shutil.which("g++"), "-shared", "-o", tmp, obj, f"-L{os.path.join(_torch_dir(), 'lib')}", "-ltorch_python",
-          "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"],
+          "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"],
          "link of the Python binding failed")
     os.replace(tmp, BINDING)
     with open(BINDING + ".for", "w") as f:

@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -109,7 +109,8 @@ struct Here {
     }
     void *stream() const { return c10::cuda::getCurrentCUDAStream(index).stream(); }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-        return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, index)));
+        // past the dispatcher, 0.4 us sooner; made on the current stream like any other
+        return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, index), std::nullopt));
     }
 };
 
@@ -122,7 +123,7 @@ const Tensor &error_word(c10::DeviceIndex index) {
     std::lock_guard<std::mutex> hold(word_lock);
     if (!words[index]) {
         c10::cuda::CUDAGuard guard(index);
-        Tensor t = at::empty({1}, at::TensorOptions().dtype(at::kInt).device(c10::Device(c10::kCUDA, index)));
+        Tensor t = at::detail::empty_cuda({1}, at::kInt, c10::Device(c10::kCUDA, index), std::nullopt);
         t.zero_();
         c10::cuda::getCurrentCUDAStream(index).synchronize();       // zero for every stream
         words[index] = new Tensor(t);
