@@ -384,6 +384,10 @@ __device__ void few_multiply(const FewParams &p, const Plan &plan, FewBarriers &
     }
 }
 
+__device__ __forceinline__ float activated(int act, float v) {
+    return act == EP_ACT_GELU ? gelu2(both(v)).x : act == EP_ACT_SILU ? silu2(both(v)).x : act == EP_ACT_RELU && v <= 0.f ? 0.f : v;
+}
+
 // A value in two halves.  One that T's range does not reach has T's largest number
 // as its upper half, and the rest (infinite past twice that) as its lower one.
 template <typename T> __device__ __forceinline__ void store_halves(T *upper, T *lower, float y) {
@@ -415,31 +419,24 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
         const int n = columns_of<false>(p, at);
         T *h = static_cast<T *>(p.h) + (int64_t)plan.first[e] * p.M + f;
         for (int c0 = 0; c0 < n; c0 += 16) {
+            const uint32_t chosen = (uint32_t)(mask >> c0) & 0xffffu;
+            if (!chosen) continue;                       // of most columns few are the expert's
             uint32_t raw[16];
             tmem_load16(d + c0, raw);
             tmem_wait16(raw);
-            if (c0 + 16 >= n) {                          // the accumulator may be filled again
-                tcgen_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars.acc_empty[acc & 1u]));
-            }
-            const uint32_t chosen = (uint32_t)(mask >> c0) & 0xffffu;
-            float v[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(raw[c]) + bias;
-            if constexpr (!GATED) {
-                activate8(p.act, v);
-                activate8(p.act, v + 8);
-            }
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
                 if (!(chosen >> c & 1u)) continue;       // the same for the warp
-                float y = v[c];
-                if constexpr (GATED) y = y * sigmoidf(y) * __shfl_xor_sync(0xffffffffu, y, 8);
+                float y = __uint_as_float(raw[c]) + bias;
+                if constexpr (GATED) y = silu2(both(y)).x * __shfl_xor_sync(0xffffffffu, y, 8);
+                else y = activated(p.act, y);
                 if (live && !upper) store_halves<T>(h, h + p.h_half, y);
                 h += p.M;
             }
         }
+        tcgen_before_sync();                             // the accumulator may be filled again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.acc_empty[acc & 1u]));
     }
 }
 
