@@ -90,8 +90,21 @@ def test_against_the_formula(T, E, k, H, F, dtype):
     check(call(c), c)
 
 
+@pytest.mark.parametrize("T,E,k,H,F", [(17, 7, 1, 4168, 128), (6, 43, 3, 4000, 96), (64, 3, 1, 5000, 72), (33, 2, 2, 1032, 520)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_tiles_of_a_deep_product(T, E, k, H, F, dtype):
+    """Sums of more than 2^10 terms: only the whole is compared."""
+    c = make(T, E, k, H, F, dtype=dtype, bias=T % 2 == 0, residual=True, seed=T)
+    c["indices"][0] = -1
+    got, (want, _) = call(c), reference(c)
+    assert float((got.double() - want).norm()) <= float(want.norm()) * (torch.finfo(dtype).eps / 2 + 2.0 ** -13)
+    for _ in range(20):
+        assert torch.equal(call(c), got)
+    assert ep.moe_error() == 0
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
-@pytest.mark.parametrize("T,H,F", [(1, 320, 168), (20, 320, 168), (3, 1032, 776), (40, 520, 264)])
+@pytest.mark.parametrize("T,H,F", [(1, 320, 168), (20, 320, 168), (3, 1032, 776), (40, 520, 264), (20, 2056, 136)])
 def test_activations(act, T, H, F):
     c = make(T, 6, 3, H, F, act=act, bias=True, residual=True, seed=5)
     check(call(c), c)
