@@ -402,10 +402,11 @@ template <typename T> __device__ __forceinline__ void store_halves(T *upper, T *
 // ---- the last four warps: outputs.  A lane has a row of weights, a register a column.
 
 template <typename T, bool GATED>
-__device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers &bars, uint32_t tmem) {
+__device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers &bars, float *turn, uint32_t tmem) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
     const bool upper = GATED && (r & 8);                 // 8 rows of the gate, 8 of the up half
     const int in = GATED ? (r >> 4) * 8 + (r & 7) : r;
+    float *mine = turn + r;                              // [16][kTile], a column for each thread
     uint32_t acc = 0;
     for (Walk<false> at(p, plan); at.more(); at.next(), ++acc) {
         const int e = plan.list[at.i], f = at.m * Walk<false>::per_tile(p) + in;
@@ -424,10 +425,13 @@ __device__ void few_finish_up(const FewParams &p, const Plan &plan, FewBarriers 
             uint32_t raw[16];
             tmem_load16(d + c0, raw);
             tmem_wait16(raw);
+            // by way of shared memory, so that one piece of code serves every column: most
+            // of a short kernel's time is its first way through its code
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                if (!(chosen >> c & 1u)) continue;       // the same for the warp
-                float y = __uint_as_float(raw[c]) + bias;
+            for (int c = 0; c < 16; ++c) mine[c * kTile] = __uint_as_float(raw[c]);
+#pragma unroll 1
+            for (uint32_t left = chosen; left; left &= left - 1) {
+                float y = mine[(__ffs(left) - 1) * kTile] + bias;
                 if constexpr (GATED) y = silu2(both(y)).x * __shfl_xor_sync(0xffffffffu, y, 8);
                 else y = activated(p.act, y);
                 if (live && !upper) store_halves<T>(h, h + p.h_half, y);
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (DOWN) grid_dependency_wait();
         if (warp == kLoaders) few_multiply<T, DOWN>(p, plan, bars, ring, tmem);
         else if constexpr (DOWN) few_finish_down<T>(p, plan, bars, reinterpret_cast<float *>(smem + p.off_acc), tmem);
-        else few_finish_up<T, GATED>(p, plan, bars, tmem);
+        else few_finish_up<T, GATED>(p, plan, bars, reinterpret_cast<float *>(smem + p.off_acc), tmem);
     }
     if (DOWN) grid_dependents_may_launch();
     __syncwarp();
@@ -771,8 +775,9 @@ size_t h_bytes(const ep_few_desc_t &d) { return ((size_t)h_rows(d) * d.inner * 4
 size_t part_bytes(const ep_few_desc_t &d) { return (size_t)kMostCtas * 2 * d.tokens * kTile * 4; }
 size_t workspace(const ep_few_desc_t &d) { return h_bytes(d) + part_bytes(d) + kMostCtas * kFinishers * 4; }
 
-// The ring takes what the rest leaves.  Behind it stand the sums and the plan, 2 KB
-// at least: instructions read 16 columns where 8 tokens were loaded.
+// The ring takes what the rest leaves.  Behind it stand the sums (or what turns a
+// column) and the plan, 2 KB at least: instructions read 16 columns where 8 tokens were
+// loaded.
 bool lay_out(FewParams *p, bool down, size_t *bytes) {
     const int rows_most = p->T * p->k;
     int at = 0;
@@ -781,7 +786,7 @@ bool lay_out(FewParams *p, bool down, size_t *bytes) {
         at = (at + size + 15) & ~15;
         return was;
     };
-    const int acc = take(down ? p->T * kTile * 4 : 0), mask = take(p->E * 8), weight = take(down ? rows_most * 4 : 0);
+    const int acc = take((down ? p->T : 16) * kTile * 4), mask = take(p->E * 8), weight = take(down ? rows_most * 4 : 0);
     const int first = take(p->E * 2), list = take(p->E * 2 * (down ? (p->T + kMostRows - 1) / kMostRows : 1));
     const int token = take(down ? rows_most : 0);
     if (at < 2048) at = 2048;
