@@ -452,49 +452,52 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
     // What goes to memory: each warp its own 32 rows, a lane 4 neighbouring
     // outputs of every fourth token.
     const int col = quarter * 32 + lane % 8 * 4, t0 = lane / 8;
-    auto put = [&](int t, int m, float4 v) {
-        if (m >= p.M) return;
-        if (p.residual.ptr) {
-            const T *res = static_cast<const T *>(p.residual.ptr) + t * p.residual.row_stride + m;
-            const uint2 q = *reinterpret_cast<const uint2 *>(res);
-            const T *e = reinterpret_cast<const T *>(&q);
-            v.x += f32(e[0]);
-            v.y += f32(e[1]);
-            v.z += f32(e[2]);
-            v.w += f32(e[3]);
-        }
-        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out.ptr) + t * p.out.row_stride + m) =
-            make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+    auto output = [&](int m) {
+        __syncwarp();
+        if (m < p.M)
+#pragma unroll 2
+            for (int t = t0; t < p.T; t += 4) {
+                float4 v = *reinterpret_cast<const float4 *>(sums + t * kTile + col);
+                if (p.residual.ptr) {
+                    const T *res = static_cast<const T *>(p.residual.ptr) + t * p.residual.row_stride + m;
+                    const uint2 q = *reinterpret_cast<const uint2 *>(res);
+                    const float2 x = unpack2<T>(q.x), y = unpack2<T>(q.y);
+                    v = make_float4(v.x + x.x, v.y + x.y, v.z + y.x, v.w + y.y);
+                }
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out.ptr) + t * p.out.row_stride + m) =
+                    make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+            }
     };
     // A tile's outputs, or this CTA's part of them.
     auto write = [&](const Walk<true> &at) {
-        const int m = at.m * kTile + col, a = at.first_cta(), z = at.last_cta();
+        const int a = at.first_cta(), z = at.last_cta();
         const int64_t part = (int64_t)p.T * kTile;
+        bool last = true;
         __syncwarp();
-        if (a == z) {
-#pragma unroll 4
-            for (int t = t0; t < p.T; t += 4) put(t, m, *reinterpret_cast<const float4 *>(sums + t * kTile + col));
-        } else {
+        if (a != z) {
             // a CTA has at most one part that is not a tile's first, and one that is
             float *to = p.parts + (blockIdx.x * 2 + (blockIdx.x == a)) * part + col;
+#pragma unroll 2
             for (int t = t0; t < p.T; t += 4)
                 __stcg(reinterpret_cast<float4 *>(to + t * kTile), *reinterpret_cast<const float4 *>(sums + t * kTile + col));
             __threadfence();
             __syncwarp();
             uint32_t there = 0;
             if (lane == 0) there = atom_add_acq_rel_gpu(p.tickets + a * kFinishers + quarter, 1u);
-            there = __shfl_sync(0xffffffffu, there, 0);
-            if (there == (uint32_t)(z - a)) {            // the last one
+            last = __shfl_sync(0xffffffffu, there, 0) == (uint32_t)(z - a);
+            if (last) {
                 __threadfence();
-                constexpr int kAhead = 4, kParts = 4;    // tokens and parts on their way at a time
+                constexpr int kAhead = 4;                // tokens, and parts, on their way at a time
+#pragma unroll 1
                 for (int t = t0; t < p.T; t += 4 * kAhead) {
                     float4 v[kAhead];
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c = a; c <= z; c += kParts) {
-                        float4 w[kParts][kAhead];
+#pragma unroll 1
+                    for (int c = a; c <= z; c += kAhead) {
+                        float4 w[kAhead][kAhead];
 #pragma unroll
-                        for (int q = 0; q < kParts; ++q)
+                        for (int q = 0; q < kAhead; ++q)
 #pragma unroll
                             for (int j = 0; j < kAhead; ++j)
                                 w[q][j] = c + q <= z && t + 4 * j < p.T
@@ -502,7 +505,7 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
                                                     p.parts + ((c + q) * 2 + (c + q == a)) * part + (t + 4 * j) * kTile + col))
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int q = 0; q < kParts; ++q)
+                        for (int q = 0; q < kAhead; ++q)
 #pragma unroll
                             for (int j = 0; j < kAhead; ++j) {
                                 v[j].x += w[q][j].x;
@@ -513,17 +516,17 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
                     }
 #pragma unroll
                     for (int j = 0; j < kAhead; ++j)
-                        if (t + 4 * j < p.T) put(t + 4 * j, m, v[j]);
+                        if (t + 4 * j < p.T) *reinterpret_cast<float4 *>(sums + (t + 4 * j) * kTile + col) = v[j];
                 }
             }
         }
+        if (last) output(at.m * kTile + col);
         __syncwarp();
         if (at.n < at.left)                              // more tiles to come
             for (int t = 0; t < p.T; ++t) mine[t * kTile] = 0.f;
     };
     if (plan.present == 0) {
-        for (int u = blockIdx.x; u * kTile < p.M; u += gridDim.x)
-            for (int t = t0; t < p.T; t += 4) put(t, u * kTile + col, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int u = blockIdx.x; u * kTile < p.M; u += gridDim.x) output(u * kTile + col);
         return;
     }
     uint32_t acc = 0;
