@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------- little work
-// A warp for each choice and feature, then for each output and choice: every
-// choice reads its expert's weights anew (from L2 after the first), but
-// nothing stands between a launch and its loads.
+// A warp (or a part of it) for each choice and feature, then for each output and
+// choice: every choice reads its expert's weights anew (from L2 after the first),
+// but nothing stands between a launch and its loads.
 
 struct SmallParams {
     int T, E, k, H, F, wide, act;
@@ -644,31 +644,37 @@ template <typename T> __device__ __forceinline__ float dot8(const uint4 &a, cons
     for (int i = 0; i < 8; ++i) s += x[i] * y[i];
     return s;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+// Lanes of a warp that share a product of depth K, 8 values each at a time: the others
+// have products of their own (64 tokens, 2 of 8 experts 512 x 64: 24 us with a warp a
+// product, so 8.5; 128 x 128, 60 tokens, 4 of 20: 20.6 and 10.1).
+inline int small_lanes(int K) { return K <= 64 ? 8 : K <= 128 ? 16 : 32; }
+template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-template <typename T, bool GATED> __global__ void __launch_bounds__(kSmallWarps * 32) small_up_kernel(const SmallParams p) {
-    const int lane = threadIdx.x & 31, f = blockIdx.x * kSmallWarps + (threadIdx.x >> 5), pair = blockIdx.y;
+template <typename T, bool GATED, int LANES>
+__global__ void __launch_bounds__(kSmallWarps * 32) small_up_kernel(const SmallParams p) {
+    const int lane = threadIdx.x % LANES, f = (blockIdx.x * kSmallWarps * 32 + threadIdx.x) / LANES, pair = blockIdx.y;
     grid_dependency_wait();
     grid_dependents_may_launch();
-    if (f >= p.F) return;
     const int e = p.idx[pair];
     if ((unsigned)e >= (unsigned)p.E) {
         if (e >= p.E && f == 0 && lane == 0 && p.error) atomicOr(p.error, EP_DEVERR_BAD_INDEX);
         return;
     }
+    const bool live = f < p.F;
     const T *x = static_cast<const T *>(p.x.ptr) + (pair / p.k) * p.x.row_stride;
     const T *w = static_cast<const T *>(p.up.ptr) + e * p.up.rank_stride + f * p.up.row_stride;
     const int64_t half = p.F * p.up.row_stride;
+    constexpr int step = LANES * 8;
     float v = 0.f, u = 0.f;
-    for (int c0 = lane * 8; c0 < p.H; c0 += 256 * kAtOnce) {
+    for (int c0 = lane * 8; live && c0 < p.H; c0 += step * kAtOnce) {
         uint4 a[kAtOnce], b[kAtOnce], d[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int c = c0 + i * 256;
+            const int c = c0 + i * step;
             const bool in = c < p.H;
             b[i] = in ? ld_stream16(w + c) : make_uint4(0, 0, 0, 0);
             if (GATED) d[i] = in ? ld_stream16(w + half + c) : make_uint4(0, 0, 0, 0);
@@ -680,17 +686,16 @@ template <typename T, bool GATED> __global__ void __launch_bounds__(kSmallWarps 
             if (GATED) u += dot8<T>(a[i], d[i]);
         }
     }
-    v = warp_sum(v);
+    v = lanes_sum<LANES>(v);
+    if (GATED) u = lanes_sum<LANES>(u);
+    if (!live) return;
     const T *bias = p.up_bias ? static_cast<const T *>(p.up_bias) + (int64_t)e * p.wide + f : nullptr;
     if (bias) v += f32(bias[0]);
     if constexpr (GATED) {
-        u = warp_sum(u);
         if (bias) u += f32(bias[p.F]);
         v = v * sigmoidf(v) * u;
     } else {
-        float a[8] = {v};
-        activate8(p.act, a);
-        v = a[0];
+        v = activated(p.act, v);
     }
     if (lane == 0) p.h[(int64_t)pair * p.F + f] = v;
 }
@@ -702,11 +707,12 @@ __host__ __device__ inline int small_outputs(int k, int tokens, int outputs) {
     return tokens * outputs >= 8192 ? 8 : k >= 8 ? 1 : k >= 4 ? 2 : k >= 2 ? 4 : 8;
 }
 
-template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_down_kernel(const SmallParams p) {
-    __shared__ float parts[kSmallWarps];
+template <typename T, int LANES> __global__ void __launch_bounds__(kSmallWarps * 32) small_down_kernel(const SmallParams p) {
+    __shared__ float parts[kSmallWarps][4];
     const int outputs = small_outputs(p.k, p.T, p.H), share = kSmallWarps / outputs;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.y;
-    const int m = blockIdx.x * outputs + warp / share, j0 = warp % share;
+    constexpr int each = 32 / LANES, step = LANES * 8;            // outputs of a warp
+    const int lane = threadIdx.x % LANES, which = (threadIdx.x & 31) / LANES, warp = threadIdx.x >> 5, t = blockIdx.y;
+    const int m = (blockIdx.x * outputs + warp / share) * each + which, j0 = warp % share;
     // Indices and weights were there before the first kernel began: the weights'
     // lines are on their way while it ends.
     if (m < p.H)
@@ -714,23 +720,23 @@ template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_
             const int e = p.idx[t * p.k + j];
             if ((unsigned)e >= (unsigned)p.E) continue;
             const T *w = static_cast<const T *>(p.down.ptr) + e * p.down.rank_stride + m * p.down.row_stride;
-            for (int c = lane * 64; c < p.F; c += 2048) asm volatile("prefetch.global.L2 [%0];" :: "l"(w + c));
+            for (int c = lane * 64; c < p.F; c += LANES * 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(w + c));
         }
     grid_dependency_wait();
     grid_dependents_may_launch();
     float sum = 0.f;
-    for (int j = j0; m < p.H && j < p.k; j += share) {
+    for (int j = j0; j < p.k; j += share) {
         const int pair = t * p.k + j, e = p.idx[pair];
         if ((unsigned)e >= (unsigned)p.E) continue;
         const T *w = static_cast<const T *>(p.down.ptr) + e * p.down.rank_stride + m * p.down.row_stride;
         const float *h = p.h + (int64_t)pair * p.F;
         float v = 0.f;
-        for (int c0 = lane * 8; c0 < p.F; c0 += 256 * kAtOnce) {
+        for (int c0 = lane * 8; m < p.H && c0 < p.F; c0 += step * kAtOnce) {
             uint4 b[kAtOnce];
             float4 a[kAtOnce][2];
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                const int c = c0 + i * 256;
+                const int c = c0 + i * step;
                 const bool in = c < p.F;
                 b[i] = in ? ld_stream16(w + c) : make_uint4(0, 0, 0, 0);
                 a[i][0] = in ? __ldcg(reinterpret_cast<const float4 *>(h + c)) : make_float4(0, 0, 0, 0);
@@ -744,14 +750,14 @@ template <typename T> __global__ void __launch_bounds__(kSmallWarps * 32) small_
                 v += f[4] * a[i][1].x + f[5] * a[i][1].y + f[6] * a[i][1].z + f[7] * a[i][1].w;
             }
         }
-        v = warp_sum(v);
-        if (p.down_bias) v += f32(static_cast<const T *>(p.down_bias)[(int64_t)e * p.H + m]);
+        v = lanes_sum<LANES>(v);
+        if (p.down_bias && m < p.H) v += f32(static_cast<const T *>(p.down_bias)[(int64_t)e * p.H + m]);
         sum += p.w[pair] * v;
     }
-    if (lane == 0) parts[warp] = sum;
+    if (lane == 0) parts[warp][which] = sum;
     __syncthreads();
     if (lane == 0 && j0 == 0 && m < p.H) {
-        for (int q = 1; q < share; ++q) sum += parts[warp + q];
+        for (int q = 1; q < share; ++q) sum += parts[warp + q][which];
         if (p.residual.ptr) sum += f32(static_cast<const T *>(p.residual.ptr)[t * p.residual.row_stride + m]);
         static_cast<T *>(p.out.ptr)[t * p.out.row_stride + m] = rounded<T>(sum);
     }
@@ -838,22 +844,36 @@ ep_status_t launch(const ep_few_desc_t &d, FewWork &up, FewWork &down, int64_t u
     return s == EP_SUCCESS ? launch_few<T, true, false>(down, down_ctas, st) : s;
 }
 
+template <typename F> void with_lanes(int K, F f) {
+    const int n = small_lanes(K);
+    if (n == 8) f(std::integral_constant<int, 8>());
+    else if (n == 16) f(std::integral_constant<int, 16>());
+    else f(std::integral_constant<int, 32>());
+}
+
 template <typename T> ep_status_t launch_small(const SmallParams &p, cudaStream_t st) {
-    const int outputs = small_outputs(p.k, p.T, p.H);
-    const dim3 up((p.F + kSmallWarps - 1) / kSmallWarps, p.T * p.k), down((p.H + outputs - 1) / outputs, p.T);
-    const cudaError_t e =
-        p.act == EP_ACT_SWIGLU ? launch_after_previous(small_up_kernel<T, true>, up, kSmallWarps * 32, 0, st, p)
-                               : launch_after_previous(small_up_kernel<T, false>, up, kSmallWarps * 32, 0, st, p);
-    if (e != cudaSuccess) return EP_ERR_GPU_OP;
-    return launch_after_previous(small_down_kernel<T>, down, kSmallWarps * 32, 0, st, p) == cudaSuccess ? EP_SUCCESS
-                                                                                                        : EP_ERR_GPU_OP;
+    const int outputs = small_outputs(p.k, p.T, p.H);           // warps' worth
+    const int features = kSmallWarps * 32 / small_lanes(p.H), block = outputs * 32 / small_lanes(p.F);
+    const dim3 up((p.F + features - 1) / features, p.T * p.k), down((p.H + block - 1) / block, p.T);
+    cudaError_t e = cudaSuccess;
+    with_lanes(p.H, [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        e = launch_after_previous(p.act == EP_ACT_SWIGLU ? small_up_kernel<T, true, L> : small_up_kernel<T, false, L>, up,
+                                  kSmallWarps * 32, 0, st, p);
+    });
+    if (e == cudaSuccess)
+        with_lanes(p.F, [&](auto lanes) {
+            e = launch_after_previous(small_down_kernel<T, decltype(lanes)::value>, down, kSmallWarps * 32, 0, st, p);
+        });
+    return e == cudaSuccess ? EP_SUCCESS : EP_ERR_GPU_OP;
 }
 
 // Bytes of weights that the choices read, each its own, up to which the kernels for
-// little work are faster: 1.8 MB 3.8 against 11.6 us, 12.6 MB 7.0 against 13.0,
-// 25 MB 10.7 to 12.1 against 15.6 to 16.7 (with 128 choices 23 against 21); 52 MB
-// 25 against 23.
-constexpr int64_t kSmallBytes = 32 << 20;
+// little work are faster: 1.8 MB 3.7 against 11.1 us, 12.6 MB 7.1 against 12.7,
+// 25 MB 10.1 against 16.1 (with 128 choices 8.5 to 18 against 19 to 20), 50 MB 16.7
+// against 19.3 (with 16 choices of 8 experts 14.7 against 13.7); 63 MB 23.8
+// against 19.3, 100 MB 25 to 34 against 15 to 29.
+constexpr int64_t kSmallBytes = 48 << 20;
 
 }  // namespace
 }  // namespace ep

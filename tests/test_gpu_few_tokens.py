@@ -31,7 +31,7 @@ def make(T, E, k, H, F, act="swiglu", dtype=BF, bias=False, residual=False, seed
     return c
 
 
-# Layers of both kinds: little work (up to 32 MB of weights over all choices)
+# Layers of both kinds: little work (up to 48 MB of weights over all choices)
 # and the kernels on tensor cores.
 LAYERS = [(128, 64), (1032, 520)]
 
