@@ -114,10 +114,10 @@ template <int N> __device__ __forceinline__ void row_sums(float *v, int tpr, flo
     }
 }
 
-// Past this factor's use the squares of a row's largest finite values fit fp32.
-// Rows need it where their sum of squares does not (some |v| > 2^56), which makes eps
-// vanish next to it.
-constexpr float kShrink = 0x1p-70f;
+// Rows whose sum of squares passes fp32 (some |v| > 2^56) are summed times this factor:
+// their largest finite values are then below 2^48, and 2^15 squares of them below 2^111.
+// r goes down to 2^-128 then, where fp32 still has 21 bits.
+constexpr float kShrink = 0x1p-80f;
 
 struct NormParams {
     int R, rows, H;
@@ -143,7 +143,7 @@ template <int CH> __device__ __forceinline__ float inverse_root(const float2 (*h
             s[0] += v.x * v.x + v.y * v.y;
         }
     row_sums<1>(s, tpr, part);
-    return rsqrtf(s[0] / H) * kShrink;
+    return rsqrtf(s[0] / H + eps * kShrink * kShrink) * kShrink;
 }
 
 // A row's chunks, `t` of `tpr` threads: total = x + residual, written if wanted,
@@ -281,7 +281,7 @@ struct RowGrad {
     }
     // From the sums of h (or of h * kShrink, where those of h do not fit).
     __device__ __forceinline__ void set(const float *s, int H, float eps, bool shrunk) {
-        r = rsqrtf(s[0] / H + (shrunk ? 0.f : eps));
+        r = rsqrtf(s[0] / H + (shrunk ? eps * kShrink * kShrink : eps));
         mean = s[1] / H * r;
         if (shrunk) r *= kShrink;
     }
