@@ -114,14 +114,27 @@ template <int N> __device__ __forceinline__ void row_sums(float *v, int tpr, flo
     }
 }
 
-// Rows whose sum of squares passes fp32 (some |v| > 2^56) are summed times this factor:
-// their largest finite values are then below 2^48, and 2^15 squares of them below 2^111.
-// r goes down to 2^-128 then, where fp32 still has 21 bits.
-constexpr float kShrink = 0x1p-80f;
+// A row's values are summed times a factor where their squares leave fp32's range.  Where the
+// sum passes it (some |v| > 2^56): the largest finite values are then below 2^48, and 2^15
+// squares of them below 2^111; r goes down to 2^-128, where fp32 still has 21 bits.
+// Where it is below 2^-100, so that squares may have lost bits or vanished, and eps,
+// below 2^-75, does not make up for them: the values are then between 2^-49 and 2^50.
+constexpr float kShrink = 0x1p-80f, kGrow = 0x1p100f;
+constexpr float kLeastSum = 0x1p-100f, kLeastEps = 0x1p-75f;
+
+// The factor, from the sum without one; least: kLeastSum, or 0 where eps suffices.
+__device__ __forceinline__ float factor_of(float sum, float least) {
+    return sum == __int_as_float(0x7f800000) ? kShrink : sum < least ? kGrow : 1.f;
+}
+// 1 / sqrt(mean(h^2) + eps) from the sum of (h * factor)^2: without the factor, or with.
+__device__ __forceinline__ float root_of(float sum, int H, float eps) { return rsqrtf(sum / H + eps); }
+__device__ __forceinline__ float root_of(float sum, int H, float eps, float factor) {
+    return rsqrtf(sum / H + eps * factor * factor);      // times factor: that of h
+}
 
 struct NormParams {
     int R, rows, H;
-    float eps;
+    float eps, least;            // least: of factor_of
     bool w32;
     const void *weight;
     ep_rows_t x, residual, total, y, scales;
@@ -132,18 +145,20 @@ __device__ __forceinline__ int64_t row_at(const ep_rows_t &r, int seg, int row) 
 }
 
 // 1 / sqrt(mean(h^2) + eps) from the sum of squares.
-template <int CH> __device__ __forceinline__ float inverse_root(const float2 (*h)[4], float sum, int H, float eps, int tpr, float (*part)[32]) {
-    if (sum != __int_as_float(0x7f800000)) return rsqrtf(sum / H + eps);
-    float s[1] = {0.f};                          // the same for the whole row
+template <int CH>
+__device__ __forceinline__ float inverse_root(const float2 (*h)[4], float sum, const NormParams &p, int tpr, float (*part)[32]) {
+    const float factor = factor_of(sum, p.least);        // the same for the whole row
+    if (factor == 1.f) return root_of(sum, p.H, p.eps);
+    float s[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 v = mul2_rn(h[i][j], both(kShrink));
+            const float2 v = mul2_rn(h[i][j], both(factor));
             s[0] += v.x * v.x + v.y * v.y;
         }
     row_sums<1>(s, tpr, part);
-    return rsqrtf(s[0] / H + eps * kShrink * kShrink) * kShrink;
+    return root_of(s[0], p.H, p.eps, factor) * factor;
 }
 
 // A row's chunks, `t` of `tpr` threads: total = x + residual, written if wanted,
@@ -242,7 +257,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int t
     float s[1] = {make_total<T, CH, A>(h, a, b, res, p.total.ptr ? static_cast<T *>(p.total.ptr) + row_at(p.total, seg, row) : nullptr,
                                          p.H, t, tpr)};
     row_sums<1>(s, tpr, part);
-    write_normed<T, CH, A, EIGHT>(p, seg, row, h, inverse_root<CH>(h, s[0], p.H, p.eps, tpr, part), t, tpr);
+    write_normed<T, CH, A, EIGHT>(p, seg, row, h, inverse_root<CH>(h, s[0], p, tpr, part), t, tpr);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -256,7 +271,7 @@ constexpr int kMostBlocks = 8 * kSms;
 
 struct NormGradParams {
     int R, rows, H;
-    float eps;
+    float eps, least;            // least: of factor_of
     bool w32;
     const void *weight;
     ep_rows_t x, grad, grad_total, grad_x;
@@ -279,11 +294,11 @@ struct RowGrad {
         s[0] = squares.x + squares.y;
         s[1] = inner.x + inner.y;
     }
-    // From the sums of h (or of h * kShrink, where those of h do not fit).
-    __device__ __forceinline__ void set(const float *s, int H, float eps, bool shrunk) {
-        r = rsqrtf(s[0] / H + (shrunk ? eps * kShrink * kShrink : eps));
+    // From the sums of h * factor.
+    __device__ __forceinline__ void set(const float *s, int H, float eps, float factor) {
+        r = factor == 1.f ? root_of(s[0], H, eps) : root_of(s[0], H, eps, factor);
         mean = s[1] / H * r;
-        if (shrunk) r *= kShrink;
+        r *= factor;
     }
     // 8 values of the row's gradient, added to f; the weight's is added to dw.
     __device__ __forceinline__ void out(float2 *f, float2 *dw, const float2 *h, const float2 *g, const float2 *w) const {
@@ -295,9 +310,9 @@ struct RowGrad {
         }
     }
 };
-__device__ __forceinline__ void shrink8(float2 *h) {
+__device__ __forceinline__ void scale8(float2 *h, float factor) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(kShrink));
+    for (int j = 0; j < 4; ++j) h[j] = mul2_rn(h[j], both(factor));
 }
 template <int CH> __device__ __forceinline__ void write_part(float *to, int H, const float2 (*dw)[4], int t, int tpr) {
 #pragma unroll
@@ -334,9 +349,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
             }
         }
         float s[2];
-        RowGrad rg;
-        bool shrunk = false;
-        for (;;) {
+        auto sums = [&](float factor) {
             RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -346,15 +359,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
                 values<T>(h, a[i]);
                 values<T>(g, b[i]);
                 load_weights<T, kVector>(w, p.weight, p.w32, at);
-                if (shrunk) shrink8(h);
+                if (factor != 1.f) scale8(h, factor);
                 sum.add(h, g, w);
             }
             sum.sums(s);
             row_sums<2>(s, tpr, part);
-            if (shrunk || s[0] != __int_as_float(0x7f800000)) break;      // the same for the whole row
-            shrunk = true;
-        }
-        rg.set(s, p.H, p.eps, shrunk);
+        };
+        sums(1.f);
+        const float factor = factor_of(s[0], p.least);               // the same for the whole row
+        if (factor != 1.f) sums(factor);
+        RowGrad rg;
+        rg.set(s, p.H, p.eps, factor);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const Span at = span_of<kVector>(i, t, tpr, p.H);
@@ -411,21 +426,22 @@ __global__ void __launch_bounds__(512, 3) norm_grad_strided_kernel(const NormGra
         const T *total = p.grad_total.ptr ? static_cast<const T *>(p.grad_total.ptr) + row_at(p.grad_total, seg, row) : nullptr;
         T *out = static_cast<T *>(p.grad_x.ptr) + row_at(p.grad_x, seg, row);
         float s[2];
-        float shrink = 1.f;
+        float factor = 1.f;
         for (;;) {
             s[0] = s[1] = 0.f;
 #pragma unroll 4
             for (int c = t; c < p.H; c += tpr) {
-                const float h = f32(x[c]) * shrink;
+                const float h = f32(x[c]) * factor;
                 s[0] += h * h;
                 s[1] += f32(grad[c]) * weight(c) * h;
             }
             row_sums<2>(s, tpr, part);
-            if (shrink != 1.f || s[0] != __int_as_float(0x7f800000)) break;      // the same for the whole row
-            shrink = kShrink;
+            if (factor != 1.f) break;
+            factor = factor_of(s[0], p.least);                       // the same for the whole row
+            if (factor == 1.f) break;
         }
         RowGrad rg;
-        rg.set(s, p.H, p.eps, shrink != 1.f);
+        rg.set(s, p.H, p.eps, factor);
         if (total) {
 #pragma unroll 4
             for (int c = t; c < p.H; c += tpr) {
@@ -551,7 +567,7 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
         // The row is read twice, before and after its sums are known, so that
         // registers suffice for two blocks an SM.
         float v[2];
-        auto sums = [&](bool shrunk) {
+        auto sums = [&](float factor) {
             RowGrad sum;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -561,21 +577,21 @@ __global__ void __launch_bounds__(THREADS, 2) norm_grad_ring_kernel(const NormGr
                 values<T>(h, ring_chunk<T>(ring.at(s, 0), at.c));
                 values<T>(g, ring_chunk<T>(ring.at(s, 1), at.c));
                 load_weights<T, kVector>(w, p.weight, p.w32, at);
-                if (shrunk) shrink8(h);
+                if (factor != 1.f) scale8(h, factor);
                 sum.add(h, g, w);
             }
             sum.sums(v);
         };
-        sums(false);
+        sums(1.f);
         block_sums<2>(v, part[turn]);            // and every thread is done with the row before
         load();
-        const bool shrunk = v[0] == __int_as_float(0x7f800000);      // the same for the whole row
-        if (shrunk) {
-            sums(true);
+        const float factor = factor_of(v[0], p.least);               // the same for the whole row
+        if (factor != 1.f) {
+            sums(factor);
             row_sums<2>(v, tpr, part[2]);
         }
         RowGrad rg;
-        rg.set(v, p.H, p.eps, shrunk);
+        rg.set(v, p.H, p.eps, factor);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const Span at = span_of<kVector>(i, t, tpr, p.H);
@@ -646,6 +662,8 @@ bool valid(const ep_norm_desc_t *d) {
     return d->weight && aligned(d->weight, size_of(d->weight_dtype)) &&
            (d->rows == 0 || valid_norm_rows(d->x, *d, d->width, size_of(d->dtype)));
 }
+
+float least_sum(const ep_norm_desc_t &d) { return d.eps < kLeastEps ? kLeastSum : 0.f; }
 
 // Whether 16-byte accesses (8-byte ones of codes) reach all of the rows.
 bool vectors(const ep_rows_t &r, int ranks, int64_t size, int64_t bytes = 16) {
@@ -757,7 +775,7 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual, cons
         (residual->ptr && !valid_norm_rows(*residual, *d, d->width, size)) ||
         (total->ptr && !valid_norm_rows(*total, *d, d->width, size)))
         return EP_ERR_INVALID_ARGS;
-    const NormParams p = {d->ranks, d->rows, d->width, d->eps, d->weight_dtype == EP_DT_FP32 && d->dtype != EP_DT_FP32,
+    const NormParams p = {d->ranks, d->rows, d->width, d->eps, least_sum(*d), d->weight_dtype == EP_DT_FP32 && d->dtype != EP_DT_FP32,
                           d->weight, d->x, *residual, *total, *y, *scales};
     const bool vec = d->width % 8 == 0 && aligned(d->weight, 16) && vectors(d->x, d->ranks, size) &&
                      vectors(*residual, d->ranks, size) && vectors(*total, d->ranks, size) &&
@@ -813,7 +831,7 @@ ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
     float *part = static_cast<float *>(d_workspace);
     cudaError_t e = cudaSuccess;
     if (d->rows > 0) {
-        const NormGradParams p = {d->ranks, d->rows, d->width, d->eps, w32 && d->dtype != EP_DT_FP32, d->weight,
+        const NormGradParams p = {d->ranks, d->rows, d->width, d->eps, least_sum(*d), w32 && d->dtype != EP_DT_FP32, d->weight,
                                   d->x, *grad, *grad_total, *grad_x, part};
         const bool vec = d->width % 8 == 0 && aligned(d->weight, 16) && vectors(d->x, d->ranks, size) &&
                          vectors(*grad, d->ranks, size) && vectors(*grad_total, d->ranks, size) &&

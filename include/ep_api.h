@@ -579,7 +579,7 @@ typedef struct {
     int32_t width;        /* H, 1..EP_MAX_NORM_WIDTH */
     int32_t dtype;        /* EP_DT_BF16, EP_DT_FP16 or EP_DT_FP32, of every row */
     int32_t weight_dtype; /* dtype or EP_DT_FP32 */
-    float   eps;          /* >= 0 */
+    float   eps;          /* >= 0; with 0 a row's root mean square has to be 2^-127 or more, or its r passes fp32 */
     ep_rows_t x;          /* [R][rows][H] */
     const void *weight;   /* [H] */
 } ep_norm_desc_t;

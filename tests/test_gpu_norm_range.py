@@ -1,5 +1,5 @@
 """rms_norm and its gradient over fp32's whole range, against 64 bits: rows whose
-squares or their sum pass fp32.
+squares or their sum pass fp32, and rows whose squares vanish in it.
 
 Tolerances are those of test_gpu_norm.py: R = 2^-18 for the sums and the root, and the
 output's own rounding; on top come steps of fp32's subnormals (2^-149), one for each
@@ -66,6 +66,34 @@ def test_largest_values(H, dtype):
             check_codes(*ep.rms_norm(x, w, eps=eps, quantize=True), reference(x, w, eps))
 
 
+def root_fits(x, eps):
+    """Rows whose 1 / root is an fp32 number: with eps 0 those of a root mean square of 2^-127 or more."""
+    rms = x.double().square().mean(-1).sqrt()
+    return rms >= 2.0 ** -127 if eps == 0 else rms >= 0
+
+
+# Rows of every magnitude under every eps: from one that is all, by one that is next to the
+# squares, to one that is nothing.
+EPS = [0.0, 2.0 ** -149, 2.0 ** -130, 2.0 ** -101, 2.0 ** -76, 2.0 ** -75, 2.0 ** -74, 1e-6, 1.0, 2.0 ** 60, 2.0 ** 120, 2.0 ** 127]
+
+
+def magnitudes(H, dtype):
+    e = torch.arange(-148 if dtype == F else -132, 126, device="cuda")
+    x = rand(len(e), H, seed=4).clamp(-3.9, 3.9).double() * torch.pow(2.0, e.double())[:, None]
+    x[:, 0] = torch.pow(2.0, e.double())                    # no row of zeros
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("H", [1, 96, 2056, 2057])
+def test_magnitudes(H, dtype):
+    x, w = magnitudes(H, dtype), rand(H, dtype=dtype, seed=5)
+    for eps in EPS:
+        want = reference(x, w, torch.tensor(eps, dtype=F).double().item())
+        ok = root_fits(x, eps)
+        close(ep.rms_norm(x, w, eps=eps)[ok], want[ok], STEP * (1 + w.double().abs()))
+
+
 def gradient_check(x, g, w, more, eps):
     h, v = x.double().requires_grad_(True), w.double().requires_grad_(True)
     want, want_w = torch.autograd.grad(reference(h, v, eps), (h, v), g.double())
@@ -73,6 +101,9 @@ def gradient_check(x, g, w, more, eps):
     r = 1 / torch.sqrt(x.double().square().mean(-1, keepdim=True) + eps)
     n = x.double().abs() * r
     size = R * r * (u + n * (u * n).mean(-1, keepdim=True))
+    fits = root_fits(x, eps)
+    x, g, more, want, size, n = (t[fits] for t in (x, g, more, want, size, n))
+    want_w = (g.double() * n * x.double().sign()).sum(0)
     fits = (want.abs() + size).amax(-1) < 2.0 ** 127         # others' gradients are past fp32
     extra = size + 4 * STEP
     dx, dw = ep.rms_norm_backward(g, x, w, eps=eps)
@@ -95,4 +126,25 @@ def test_gradient_of_largest_values(rows, H, dtype):
     more = rand(rows, H, dtype=dtype, std=2.0 ** -60, seed=8)
     assert gradient_check(x, g, w, more, 1e-6) == rows
     assert gradient_check(x, g, w, more, 2.0 ** 120) == rows
+    assert ep.moe_error() == 0
+
+
+@pytest.mark.parametrize("H", [1, 96, 520, 2056, 2057])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gradient_of_magnitudes(H, dtype):
+    x = magnitudes(H, dtype)
+    g = rand(len(x), H, dtype=dtype, std=2.0 ** -30, seed=9)
+    w, more = rand(H, dtype=dtype, seed=10), rand(len(x), H, dtype=dtype, std=2.0 ** -60, seed=11)
+    for eps in EPS:
+        if H == 1 and eps < 1e-6:
+            continue                    # the gradient is a difference of equal numbers: nothing of it is left
+        assert gradient_check(x, g, w, more, torch.tensor(eps, dtype=F).double().item()) > 150
+
+
+def test_gradient_of_small_rows_through_the_ring():
+    x, g, w = rand(5000, 1032, seed=12), rand(5000, 1032, std=2.0 ** -40, seed=13), rand(1032, seed=14)
+    more = rand(5000, 1032, seed=15)
+    x[::2] *= 2.0 ** -70
+    x[1::4] *= 2.0 ** -100
+    assert gradient_check(x, g, w, more, 0.0) == 5000
     assert ep.moe_error() == 0
