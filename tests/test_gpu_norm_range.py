@@ -148,3 +148,11 @@ def test_gradient_of_small_rows_through_the_ring():
     x[1::4] *= 2.0 ** -100
     assert gradient_check(x, g, w, more, 0.0) == 5000
     assert ep.moe_error() == 0
+
+
+@pytest.mark.parametrize("rows,H", [(1000, 1024), (2000, 2048), (600, 16392), (600, 32768), (5000, 32), (6, 256)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_gradient_in_blocks_that_take_several_rows(rows, H, dtype):
+    """A block a row where rows are too few for the ring, or too wide."""
+    x, g, w = rand(rows, H, dtype=dtype), rand(rows, H, dtype=dtype, seed=1), rand(H, dtype=dtype, seed=2)
+    assert gradient_check(x, g, w, rand(rows, H, dtype=dtype, seed=3), 1e-6) == rows
