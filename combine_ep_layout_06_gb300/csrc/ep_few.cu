@@ -18,7 +18,7 @@
 // in shared memory.  Where a tile falls to several CTAs, the warp that finishes its
 // rows last adds their parts, in the sequence's order: who is last does not show.
 // h stands grouped by expert, in two 16-bit halves (a value and what its rounding
-// left) that are columns of their own, because 16 columns cost what 8 do.
+// left, see Halves) that are columns of their own, because 16 columns cost what 8 do.
 //
 // Down is launched programmatically: its CTAs start as up's end, and fill their
 // rings with weights before they wait for h.
@@ -388,15 +388,28 @@ __device__ __forceinline__ float activated(int act, float v) {
     return act == EP_ACT_GELU ? gelu2(both(v)).x : act == EP_ACT_SILU ? silu2(both(v)).x : act == EP_ACT_RELU && v <= 0.f ? 0.f : v;
 }
 
-// A value in two halves.  One that T's range does not reach has T's largest number
-// as its upper half, and the rest (infinite past twice that) as its lower one.
+// A value in two halves: value = (upper + lower * kLower) * kUnit.  bf16 has fp32's range
+// and needs no factors; 8 + 8 bits keep the value within 2^-17.  fp16 is taken in units of
+// 16, and its lower half, the rest of at most 2^-11 of the value, 2^11 times as large: so values
+// from 2^-16 on are within 2^-16, smaller ones within 2^-32 (without the factors 2^-25), and
+// those from 2^20 on (without, 131008) are infinite.  A larger unit would move both ends up.
+template <typename T> struct Halves {
+    static constexpr float kUnit = 1.f, kLower = 1.f, kLargest = 0x1.fep127f;
+};
+template <> struct Halves<__half> {
+    static constexpr float kUnit = 16.f, kLower = 0x1p-11f, kLargest = 65504.f;
+};
 template <typename T> __device__ __forceinline__ void store_halves(T *upper, T *lower, float y) {
-    constexpr float kLargest = std::is_same<T, __half>::value ? 65504.f : 0x1.fep127f;
+    using H = Halves<T>;
+    y *= 1.f / H::kUnit;
     const bool finite = fabsf(y) <= 0x1.fffffep127f;
     float hi = f32(rounded<T>(y));
-    if (finite && fabsf(hi) > kLargest) hi = copysignf(kLargest, y);
+    if (finite && fabsf(hi) > H::kLargest) hi = copysignf(H::kLargest, y);       // the lower half has the rest
     *upper = rounded<T>(hi);
-    *lower = rounded<T>(finite ? y - hi : 0.f);
+    *lower = rounded<T>(finite ? (y - hi) * (1.f / H::kLower) : 0.f);
+}
+template <typename T> __device__ __forceinline__ float joined_halves(float upper, float lower) {
+    return (upper + lower * Halves<T>::kLower) * Halves<T>::kUnit;
 }
 
 // ---- the last four warps: outputs.  A lane has a row of weights, a register a column.
@@ -553,7 +566,7 @@ __device__ void few_finish_down(const FewParams &p, const Plan &plan, FewBarrier
             for (int c = 0; c < 8; ++c) {
                 const int j = c0 / 2 + c;
                 if (j >= rows) break;
-                const float v = __uint_as_float(raw[c]) + __uint_as_float(raw[c + 8]) + bias;
+                const float v = joined_halves<T>(__uint_as_float(raw[c]), __uint_as_float(raw[c + 8])) + bias;
                 mine[token[j] * kTile] += weight[j] * v;
             }
         }

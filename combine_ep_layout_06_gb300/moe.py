@@ -236,7 +236,9 @@ def moe_few_tokens(x: torch.Tensor, weights: torch.Tensor, indices: torch.Tensor
     x, residual: bf16 or fp16 [T][H] or [W][T][H]; weights fp32 and indices int32
     [...][topk] as ``route`` returns them (a negative index: no expert, so absent tokens
     get their residual or 0); up: [E][F][H], or [E][2F][H] for "swiglu" (the
-    gate's features first); down: [E][H][F].  Sums are fp32, out is rounded once."""
+    gate's features first); down: [E][H][F].  Sums are fp32, out is rounded once.
+    fp16 activations between the products hold values up to 2^20 where the weights
+    over all choices are more than 48 MB, and all of fp32's below."""
     if stream is not None:
         with _on(x, stream):
             return _moe.moe_few_tokens(x, weights, indices, up, down, activation, up_bias, down_bias, residual)

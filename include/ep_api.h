@@ -646,9 +646,10 @@ ep_status_t ep_expert_product_backward_checkpoint(
 /* A whole MoE layer's experts for a few tokens, without dispatch:
  *   out[t] = residual[t] + sum over j of w[t][j] * y(t, e), e = idx[t][j],
  *   y(t, e) = act(x[t] up_e^T + up_bias_e) down_e^T + down_bias_e
- * Every sum is fp32; the activations between the products are kept in fp32 or in
- * two 16-bit halves (a value and what its rounding left), and out is rounded
- * once.  Sums are in an order that sizes and indices alone fix; an expert that is
+ * Every sum is fp32; the activations between the products are kept in fp32 (little
+ * work: up to 48 MB of weights over all choices) or in two 16-bit halves (a value and what
+ * its rounding left), and out is rounded once.  Halves are within 2^-16 of the value; those of
+ * fp16 only from 2^-16 on, within 2^-32 below, and infinite from 2^20 on.  Sums are in an order that sizes and indices alone fix; an expert that is
  * named twice counts twice.  idx < 0: no expert (ep_route's -1); idx >=
  * experts: skipped, and sets BAD_INDEX.  A token without experts gets its
  * residual, or 0. */

@@ -1,0 +1,98 @@
+"""moe_few_tokens on each of its two ways, the kernels for little work and those on
+tensor cores: every case says which one it is meant for, by the rule that the library
+chooses by, so that another rule fails here and does not move cases from one to the other.
+
+Tolerance.  test_gpu_few_tokens.py's, or where a test says so: fp32 sums of K terms are
+within K * 2^-24 of the sum of magnitudes, and activations between the products within
+2^-16 of their value, in fp16 on tensor cores at least within 2^-32."""
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import combine_ep_layout_06_gb300 as ep
+from test_gpu_few_tokens import call, check, make, reference
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+SOURCE = os.path.join(os.path.dirname(ep.__file__), "csrc", "ep_few.cu")
+SMALL = eval(re.search(r"kSmallBytes = ([0-9 <*]+);", open(SOURCE).read()).group(1))
+
+
+def on(way, c):
+    """c, whose weights over all choices are few bytes ("little") or not ("tensor")."""
+    choices = c["indices"].numel()
+    E, wide, H = c["up"].shape
+    size = choices * H * (wide + c["down"].shape[2]) * 2
+    assert (size > SMALL) == (way == "tensor"), (size, SMALL)
+    return c
+
+
+SIZES = {"little": (5, 4, 2, 256, 192), "tensor": (12, 6, 3, 1032, 776)}       # T, E, k, H, F
+
+
+def one_hot_layer(way, values, x):
+    """A layer in fp16 whose activations between the products are known without a
+    sum: products of x and fp16 numbers near values / x, in some order for every expert."""
+    T, E, k, H, F = SIZES[way]
+    c = on(way, make(T, E, k, H, F, act="none", dtype=HF))
+    g = torch.Generator(device="cuda").manual_seed(7)
+    c["x"].zero_()
+    c["x"][:, 3] = x
+    pick = torch.randint(len(values), (E, F), generator=g, device="cuda")
+    sign = torch.randint(0, 2, (E, F), generator=g, device="cuda") * 2 - 1
+    c["up"].zero_()
+    c["up"][:, :, 3] = (values.to("cuda")[pick] / x * sign).to(HF)
+    return c
+
+
+def one_hot_check(c, way):
+    h = c["up"][:, :, 3].double() * c["x"][0, 3].double()  # [E][F], exact in fp32
+    want = torch.zeros(c["x"].shape, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(want)
+    F = h.shape[1]
+    for t, ids in enumerate(c["indices"].tolist()):
+        for j, e in enumerate(ids):
+            w, down = float(c["weights"][t, j]), c["down"][e].double()
+            want[t] += w * (down @ h[e])
+            off = h[e].abs() * 2.0 ** -16
+            if way == "tensor":
+                off = off.clamp_min(2.0 ** -32)
+            tol[t] += abs(w) * (down.abs() @ (off + h[e].abs() * (F + 64) * 2.0 ** -24))
+    got = call(c)
+    off = (got.double() - want).abs()
+    tol += want.abs() * torch.finfo(HF).eps / 2 + 2.0 ** -25
+    assert bool((off <= tol).all()), float((off / tol).nan_to_num(math.inf).max())
+    return got
+
+
+@pytest.mark.parametrize("way", ["little", "tensor"])
+@pytest.mark.parametrize("at", [2.0 ** -21, 2.0 ** -17, 2.0 ** -13, 2.0 ** -6])
+def test_small_activations_of_fp16(way, at):
+    c = one_hot_layer(way, at * torch.linspace(0.5, 1.0, 37), max(at, 2.0 ** -14) * 1.37)
+    c["down"] *= min(2.0 ** -6 / at, 4096.0)                # outputs far from fp16's smallest
+    one_hot_check(c, way)
+
+
+@pytest.mark.parametrize("way", ["little", "tensor"])
+@pytest.mark.parametrize("most", [60000.0, 131008.0, 1040000.0])
+def test_large_activations_of_fp16(way, most):
+    c = one_hot_layer(way, most * torch.linspace(0.3, 1.0, 37), 23.0)
+    c["down"] *= 2.0 ** -7
+    assert bool(one_hot_check(c, way).isfinite().all())
+
+
+def test_where_activations_of_fp16_become_infinite():
+    """Up to 2^20 on tensor cores; the kernels for little work keep fp32."""
+    for way in ("little", "tensor"):
+        c = one_hot_layer(way, torch.tensor([2.0 ** 20]), 256.0)
+        c["down"] = (c["down"].abs() + 2.0 ** -6) * 2.0 ** -10
+        c["up"].abs_()
+        got = call(c)
+        assert bool((got.isinf() if way == "tensor" else got.isfinite()).all())
+        c["x"][:, 3] = 255.0
+        assert bool(call(c).isfinite().all())
+    assert ep.moe_error() == 0
