@@ -408,8 +408,11 @@ template <typename T> __device__ __forceinline__ void store_halves(T *upper, T *
     *upper = rounded<T>(hi);
     *lower = rounded<T>(finite ? (y - hi) * (1.f / H::kLower) : 0.f);
 }
+// The sums over both.  Where an infinite weight made the upper one infinite the lower one,
+// of rests that are 0 or of another sign, is NaN or infinite the other way: it counts no more.
 template <typename T> __device__ __forceinline__ float joined_halves(float upper, float lower) {
-    return (upper + lower * Halves<T>::kLower) * Halves<T>::kUnit;
+    const float rest = fabsf(upper) <= 0x1.fffffep127f ? lower * Halves<T>::kLower : 0.f;
+    return (upper + rest) * Halves<T>::kUnit;
 }
 
 // ---- the last four warps: outputs.  A lane has a row of weights, a register a column.

@@ -96,3 +96,20 @@ def test_where_activations_of_fp16_become_infinite():
         c["x"][:, 3] = 255.0
         assert bool(call(c).isfinite().all())
     assert ep.moe_error() == 0
+
+
+@pytest.mark.parametrize("way", ["little", "tensor"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_infinite_weights(way, dtype):
+    """An infinite weight of down makes its outputs infinite, by the activation's sign,
+    in 64 bits as in both ways; the others stay."""
+    T, E, k, H, F = SIZES[way]
+    c = on(way, make(T, E, k, H, F, act="gelu", dtype=dtype))
+    clean = call(c)
+    c["down"][1, 5, 7], c["down"][2, 6, 8] = math.inf, -math.inf
+    c["down"][3 % E, 9, 1], c["down"][3 % E, 9, 2] = math.inf, math.nan
+    got, (want, _) = call(c), reference(c)
+    assert torch.equal(got.isnan(), want.isnan()) and bool(want.isnan().any())
+    assert torch.equal(got.isinf(), want.isinf()) and int(want.isinf().sum()) > 2
+    assert torch.equal(got[want.isinf()].sign().double(), want[want.isinf()].sign())
+    assert torch.equal(got[want.isfinite()], clean[want.isfinite()])
