@@ -19,7 +19,8 @@ pytestmark = pytest.mark.gpu
 
 BF, HF = torch.bfloat16, torch.float16
 SOURCE = os.path.join(os.path.dirname(ep.__file__), "csrc", "ep_few.cu")
-SMALL = eval(re.search(r"kSmallBytes = ([0-9 <*]+);", open(SOURCE).read()).group(1))
+SMALL, SHIFT = map(int, re.search(r"kSmallBytes = (\d+) << (\d+);", open(SOURCE).read()).groups())
+SMALL <<= SHIFT
 
 
 def on(way, c):
@@ -113,3 +114,68 @@ def test_infinite_weights(way, dtype):
     assert torch.equal(got.isinf(), want.isinf()) and int(want.isinf().sum()) > 2
     assert torch.equal(got[want.isinf()].sign().double(), want[want.isinf()].sign())
     assert torch.equal(got[want.isfinite()], clean[want.isfinite()])
+
+
+def padded(t, pad):
+    """t's values as a slice of a tensor with longer rows, NaN around them."""
+    big = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), math.nan, dtype=t.dtype, device="cuda")
+    big[..., :t.shape[-1]] = t
+    return big[..., :t.shape[-1]]
+
+
+@pytest.mark.parametrize("way", ["little", "tensor"])
+@pytest.mark.parametrize("act,dtype", [("swiglu", BF), ("gelu", HF)])
+def test_layouts_of_both_ways(way, act, dtype):
+    """Ranks of tokens, strided rows, ranks of strided rows, and experts' slices of
+    larger tensors have the bits of dense ones."""
+    T, E, k, H, F = (6, 5, 2, 256, 64) if way == "little" else (12, 5, 4, 1032, 776)
+    c = on(way, make(T, E, k, H, F, act=act, dtype=dtype, bias=True, residual=True))
+    want = call(c)
+    check(want, c)
+    ranks = {n: c[n].view(3, T // 3, -1) for n in ("x", "residual", "weights", "indices")}
+    assert torch.equal(call(dict(c, **ranks)).view(T, H), want)
+    single = {n: c[n].view(T, 1, -1) for n in ("x", "residual", "weights", "indices")}
+    assert torch.equal(call(dict(c, **single)).view(T, H), want)
+    pads = dict(x=16, residual=8, up=24, down=8)
+    for names in [[n] for n in pads] + [list(pads)]:
+        assert torch.equal(call(dict(c, **{n: padded(c[n], pads[n]) for n in names})), want), names
+    for n in ("x", "residual"):                            # ranks whose rows are padded
+        ranks[n] = padded(c[n], pads[n]).view(3, T // 3, H)
+    assert torch.equal(call(dict(c, **ranks)).view(T, H), want)
+    wide = c["up"].shape[1]
+    more = dict(up=torch.cat([c["up"], torch.full_like(c["up"], math.nan)], 1)[:, :wide],
+                down=torch.cat([c["down"], torch.full_like(c["down"], math.nan)], 1)[:, :H])
+    assert torch.equal(call(dict(c, **more)), want)
+
+
+# As in test_gpu_few_tokens.py, but on tensor cores: fewest features and deepest inner size, narrow
+# layers of many experts, tiles of 3 and 9 features, small depths of both products.
+@pytest.mark.parametrize("T,E,k,H,F", [(64, 40, 32, 8, 968), (64, 300, 32, 264, 72), (48, 300, 30, 264, 96), (8, 6, 3, 1032, 776),
+                                       (20, 5, 4, 2056, 136), (63, 40, 30, 136, 264)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_formula_on_tensor_cores(T, E, k, H, F, dtype):
+    c = on("tensor", make(T, E, k, H, F, dtype=dtype, bias=T % 2 == 0, residual=T % 3 == 0, seed=T))
+    if H > 1024:                                           # more terms than the bound is for: the whole
+        got, (want, _) = call(c), reference(c)
+        assert float((got.double() - want).norm()) <= float(want.norm()) * (torch.finfo(dtype).eps / 2 + 2.0 ** -13)
+    else:
+        check(call(c), c)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_activations_on_tensor_cores(act, dtype):
+    c = on("tensor", make(16, 6, 3, 1000, 776, act=act, dtype=dtype, bias=True, residual=True, seed=5))
+    check(call(c), c)
+
+
+@pytest.mark.parametrize("T,E,k,H,F", [(9, 43, 3, 4000, 96), (17, 7, 1, 4168, 136)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_tiles_of_a_deep_product_on_tensor_cores(T, E, k, H, F, dtype):
+    c = on("tensor", make(T, E, k, H, F, dtype=dtype, bias=T % 2 == 0, residual=True, seed=T))
+    c["indices"][0] = -1
+    got, (want, _) = call(c), reference(c)
+    assert float((got.double() - want).norm()) <= float(want.norm()) * (torch.finfo(dtype).eps / 2 + 2.0 ** -13)
+    for _ in range(20):
+        assert torch.equal(call(c), got)
+    assert ep.moe_error() == 0
