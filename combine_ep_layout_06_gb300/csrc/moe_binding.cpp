@@ -9,8 +9,10 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -109,8 +111,15 @@ struct Here {
     }
     void *stream() const { return c10::cuda::getCurrentCUDAStream(index).stream(); }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+        // at::empty fills under deterministic algorithms, if torch is told to
+        if (at::globalContext().deterministicAlgorithms())
+            return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, index)));
         // past the dispatcher, 0.4 us sooner; made on the current stream like any other
         return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, index), std::nullopt));
+    }
+    // Bytes that no caller sees.
+    Tensor scratch(size_t bytes) const {
+        return Tensor(at::detail::empty_cuda({(int64_t)bytes}, at::kByte, c10::Device(c10::kCUDA, index), std::nullopt));
     }
 };
 
@@ -286,7 +295,7 @@ PyObject *balance_loss(PyObject *const *a) {
     if (r.d.tokens) {
         size_t need = 0;
         check(ep_balance_loss_workspace(&r.d, &need), "ep_balance_loss_workspace");
-        Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+        Tensor scratch = here.scratch(need);
         check(ep_balance_loss(&r.d, x.data_ptr(), static_cast<const int32_t *>(idx.data_ptr()), r.counts,
                               static_cast<float *>(loss.data_ptr()), static_cast<int32_t *>(counts.data_ptr()),
                               static_cast<float *>(probs.data_ptr()), scratch.data_ptr(), need,
@@ -464,7 +473,7 @@ PyObject *expert_product_backward(PyObject *const *a) {
     if (truth(a[7])) db = here.empty({p.G, p.wide}, type);
     size_t need = 0;
     check(ep_expert_product_workspace(&p.d, &need), "ep_expert_product_workspace");
-    Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+    Tensor scratch = here.scratch(need);
     const ep_rows_t gx = rows_new(dx, p.rows, K);
     void *bias = db.defined() ? db.data_ptr() : nullptr;
     if (saved_scales)
@@ -647,7 +656,7 @@ PyObject *rms_norm_backward(PyObject *const *a) {
     Tensor dx = here.empty(total.sizes(), total.scalar_type()), dw = here.empty({H}, weight.scalar_type());
     size_t need = 0;
     check(ep_rms_norm_workspace(&n.d, &need), "ep_rms_norm_workspace");
-    Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+    Tensor scratch = here.scratch(need);
     const ep_rows_t to{dx.data_ptr(), n.d.rows * H, H};
     check(ep_rms_norm_backward(&n.d, &g, &gt, &to, dw.data_ptr(), scratch.data_ptr(), need,
                                error_ptr(here.index), here.stream()),
@@ -733,7 +742,7 @@ PyObject *moe_few_tokens(PyObject *const *a) {
     if (T) {
         size_t need = 0;
         check(ep_moe_few_workspace(&d, &need), "ep_moe_few_workspace");
-        Tensor scratch = here.empty({(int64_t)need}, at::kByte);
+        Tensor scratch = here.scratch(need);
         const ep_rows_t to{out.data_ptr(), 0, H};
         check(ep_moe_few(&d, &from, static_cast<const float *>(w.data_ptr()), static_cast<const int32_t *>(idx.data_ptr()),
                          &res, &to, scratch.data_ptr(), need, error_ptr(here.index), here.stream()),
