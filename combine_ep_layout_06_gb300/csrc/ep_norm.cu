@@ -266,8 +266,9 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p, int t
 // 63 % issue, by instructions: 16384 x 7168 bf16 with grad_total 162 us and 5 for the
 // sums, at 83 % of the copy rate.
 
+// The number of SMs is fixed here, not asked for: it sets the order of the sums and the
+// size of the workspace, which do not depend on the device then.
 constexpr int kSms = 152, kParts = 3 * kSms;     // blocks at most where a block keeps no rows ahead
-constexpr int kMostBlocks = 8 * kSms;
 
 struct NormGradParams {
     int R, rows, H;
@@ -751,9 +752,22 @@ int64_t grad_parts(const ep_norm_desc_t &d) {
     const int64_t rows = (int64_t)d.ranks * d.rows, blocks = (rows + s.per - 1) / s.per;
     return blocks < kParts ? blocks : kParts;
 }
+// Of the kernel with most blocks, as other tensors' alignment may choose any; and never fewer
+// than for fewer rows (some shapes have a warp a row only where rows are many), so that
+// a workspace for the largest batch does for all.
 int64_t most_parts(const ep_norm_desc_t &d) {
     const int64_t rows = (int64_t)d.ranks * d.rows;
-    return rows < kMostBlocks ? rows : kMostBlocks;
+    int64_t most = 0;
+    for (const int64_t n : {rows < kParts ? rows : (int64_t)kParts, rows}) {
+        ep_norm_desc_t e = d;
+        e.ranks = 1;
+        e.rows = (int32_t)n;
+        const RingShape with = grad_ring(e, true, true), without = grad_ring(e, true, false);
+        for (const int64_t parts : {grad_parts(e), (int64_t)strided_shape(e).blocks, (int64_t)(with.stages ? with.blocks : 0),
+                                    (int64_t)(without.stages ? without.blocks : 0)})
+            if (parts > most) most = parts;
+    }
+    return most;
 }
 
 }  // namespace
