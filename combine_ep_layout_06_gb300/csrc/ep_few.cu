@@ -324,6 +324,8 @@ template <bool DOWN, bool GATED> struct FewLoader {
         // The CTA ends no earlier than its copies and its stages' last signals (of
         // the last S slices of all warps: earlier ones' phases have passed);
         // after a wait that ran out, as far as they come within another wait each.
+        // (Weights that went ahead of h have their tokens by then: a stage's first slice
+        // waits for nothing, so that a wait runs out after the first ring only.)
         if ((threadIdx.x & 31) == 0) {
             Watch ignore = {};
             volatile Watch *watch = ok ? (volatile Watch *)&bars.watch : &ignore;
