@@ -18,8 +18,9 @@ constexpr int kMaxChunks = 4, kMaxThreads = EP_MAX_NORM_WIDTH / (kMaxChunks * 8)
 // How a thread's chunk of 8 values stands in its row.  kVector: neighbours, one or
 // two 16-byte accesses.  Rows that these do not reach go value by value:
 // kStrided, every tpr-th value, so that a warp's accesses are next to each other
-// (2332 x 4333 fp16: neighbours 56 us); kNeighbours where a block's codes need 16
-// lanes to hold 128 neighbours.
+// (2332 x 4333 fp16: neighbours 56 us, so 27, bound by instructions: its 40 MB
+// are 6 us of memory); kNeighbours where a block's codes need 16 lanes to hold 128
+// neighbours.
 enum Access { kStrided, kNeighbours, kVector };
 
 struct Span {
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && CH < 4 ? 3 : 1) nor
 
 // Rows that 16-byte accesses do not reach: a thread has every tpr-th value, reads it
 // again (from L1) once the row's sums are known, and keeps the weight's sums in
-// shared memory, all of it in loops of few registers (in registers, unrolled, 629 us
-// for 16384 x 5001 bf16).
+// shared memory, all of it in loops of few registers: 16384 x 5001 bf16 313 us, bound by
+// instructions (its bytes are 72 us of memory); in registers, unrolled, 629.
 template <typename T>
 __global__ void __launch_bounds__(512, 3) norm_grad_strided_kernel(const NormGradParams p, int tpr) {
     extern __shared__ __align__(16) float weight_sums[];

@@ -604,7 +604,7 @@ ep_status_t ep_rms_norm(const ep_norm_desc_t *d, const ep_rows_t *residual,
  * grad_total (ptr NULL: none) is what comes to total from elsewhere, the residual
  * stream.  grad_x is the gradient of x and of the residual alike, and may be
  * grad_total itself.  d_grad_weight [H] in weight_dtype; rows are summed in an
- * order that sizes, strides and alignment fix.  d_workspace: ep_rms_norm_workspace bytes, 16-byte
+ * order that sizes, strides, alignment and whether there is a grad_total fix.  d_workspace: ep_rms_norm_workspace bytes, 16-byte
  * aligned, any contents. */
 ep_status_t ep_rms_norm_workspace(const ep_norm_desc_t *d, size_t *bytes);
 ep_status_t ep_rms_norm_backward(const ep_norm_desc_t *d, const ep_rows_t *grad,
