@@ -205,7 +205,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.
 
     x: bf16, fp16 or fp32 [...][H], H to 32768; weight [H] in x's type or fp32.
     Returns y; with a residual (y, total), total rounded to x's type, whose norm
-    it is.  quantize: in y's place codes (float8_e4m3fn) and scales (fp32
+    it is.  eps: 0 or more (with 0, rows of a root mean square of 2^-127 or more).
+    quantize: in y's place codes (float8_e4m3fn) and scales (fp32
     [...][H/128]), H a multiple of 128: ``EpDispatchCombineOp.dispatch`` takes
     them as pre-quantised input."""
     if stream is not None:
